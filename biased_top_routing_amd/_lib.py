@@ -17,12 +17,12 @@ HEADER = os.path.join(os.path.dirname(PKG), "include", "moe.h")
 
 MOE_OK, MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_LAUNCH = 0, -1, -2, -3, -4, -5
 MOE_ERR_SCRATCH = -6
-MOE_F32, MOE_BF16, MOE_FP8_E4M3 = 0, 1, 2
+MOE_F32, MOE_BF16, MOE_FP8_E4M3, MOE_MXFP4 = 0, 1, 2, 3
 MOE_SCORES_IN = 1
 MOE_FFN_ALL, MOE_FFN_GATE_UP, MOE_FFN_DOWN = 0, 1, 2
 MOE_WS_DISPATCH, MOE_WS_FFN, MOE_WS_FFN_BWD, MOE_WS_ROUTE_BWD, MOE_WS_ROUTE = 1, 2, 3, 4, 5
 MOE_WSP_H, MOE_WSP_H_SCALE, MOE_WSP_H_SHARED, MOE_WSP_H_SHARED_SCALE = 0, 1, 2, 3
-_DTYPES = {"f32": MOE_F32, "bf16": MOE_BF16, "fp8_e4m3": MOE_FP8_E4M3}
+_DTYPES = {"f32": MOE_F32, "bf16": MOE_BF16, "fp8_e4m3": MOE_FP8_E4M3, "mxfp4": MOE_MXFP4}
 
 
 class MoeError(RuntimeError):
@@ -84,6 +84,8 @@ def lib() -> ctypes.CDLL:
             "moe_dispatch_backward": [cfgp, vp, vp, vp, vp, vp, vp],
             "moe_update_bias": [cfgp, vp, vp, f32, vp],
             "moe_quantize_fp8": [vp, i32, i32, i32, i32, vp, vp, vp],
+            "moe_quantize_fp4": [vp, i32, i32, i32, vp, vp, vp],
+            "moe_dequantize_fp4": [vp, vp, i32, i32, i32, vp, vp],
             "moe_ffn_workspace_part": [cfgp, ctypes.c_int, ctypes.POINTER(sz), ctypes.POINTER(sz)],
         }
         for name, args in sig.items():
@@ -130,6 +132,19 @@ def _p(t) -> int | None:
     if isinstance(t, int):
         return t
     return t.data_ptr()
+
+
+def _c(t) -> int | None:
+    """_p for the entry points that check what they are given: a tensor has to be dense,
+    and on the current device when it is on a GPU (its stream and kernels are)."""
+    if t is not None and not isinstance(t, int):
+        if not t.is_contiguous():
+            raise ValueError(f"tensor of shape {tuple(t.shape)} with strides {t.stride()} is not contiguous")
+        if t.is_cuda:
+            import torch
+            if t.device.index != torch.cuda.current_device():
+                raise ValueError(f"tensor on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+    return _p(t)
 
 
 def _s(stream) -> int | None:
@@ -247,6 +262,17 @@ def moe_update_bias(cfg, counts, bias, gamma, stream=None):
 def moe_quantize_fp8(src, n_mat, rows, cols, block_rows, dst, scales, stream=None):
     _check("moe_quantize_fp8", lib().moe_quantize_fp8(_p(src), n_mat, rows, cols, block_rows, _p(dst),
                                                       _p(scales), _s(stream)))
+
+
+def moe_quantize_fp4(src, n_mat, rows, cols, dst, scales, stream=None):
+    """bf16 [n_mat, rows, cols] -> MXFP4 codes [n_mat, rows, cols/2] and scale bytes [n_mat, cols/128, rows, 4]."""
+    _check("moe_quantize_fp4", lib().moe_quantize_fp4(_c(src), n_mat, rows, cols, _c(dst), _c(scales), _s(stream)))
+
+
+def moe_dequantize_fp4(codes, scales, n_mat, rows, cols, dst, stream=None):
+    """The bf16 values [n_mat, rows, cols] of MXFP4 codes and scale bytes."""
+    _check("moe_dequantize_fp4", lib().moe_dequantize_fp4(_c(codes), _c(scales), n_mat, rows, cols, _c(dst),
+                                                          _s(stream)))
 
 
 def moe_ffn_workspace_part(cfg, part) -> tuple:

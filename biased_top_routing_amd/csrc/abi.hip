@@ -10,7 +10,8 @@ namespace moe {
 
 bool gemm_dtype_ok(const moe_cfg* c) {
   if (c->act == MOE_F32 && c->wgt == MOE_F32) return true;
-  if (c->act == MOE_BF16 && (c->wgt == MOE_BF16 || c->wgt == MOE_FP8_E4M3)) return true;
+  if (c->act == MOE_BF16 && (c->wgt == MOE_BF16 || c->wgt == MOE_FP8_E4M3 || c->wgt == MOE_MXFP4))
+    return true;
   return false;
 }
 
@@ -42,6 +43,11 @@ moe_status validate_cfg(const moe_cfg* c) {
     if (c->H % 4 || c->I % 4) return MOE_ERR_SHAPE;
   } else if (c->wgt == MOE_BF16) {
     if (c->H % 64 || c->I % 128) return MOE_ERR_SHAPE;
+  } else if (c->wgt == MOE_MXFP4) {  // whole 128-wide K steps; 32-bit offsets into the scale words of the rows
+    if (c->H % 128 || c->I % 128) return MOE_ERR_SHAPE;
+    if ((int64_t)c->T * c->k * std::max(c->H, c->I) / 32 >= ((int64_t)1 << 31) ||
+        (int64_t)c->T * std::max<int64_t>(c->H, (int64_t)c->S * c->I) / 32 >= ((int64_t)1 << 31))
+      return MOE_ERR_SHAPE;
   } else {  // fp8 experts: K of every GEMM at most kFp8MaxKC chunks of 128
     if (c->H % 128 || c->I % 128) return MOE_ERR_SHAPE;
     if (c->H > 128 * kFp8MaxKC || (int64_t)(c->S > 1 ? c->S : 1) * c->I > 128 * kFp8MaxKC)

@@ -32,6 +32,8 @@ inline size_t act_bytes(const moe_cfg* c) { return c->act == MOE_F32 ? 4 : 2; }
 inline moe_status launch_status() {
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH;
 }
+// whether a device address is no multiple of a (a power of two)
+inline bool misaligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) & (a - 1); }
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 // moe_route's workspace: room for the [T, E] fp32 affinities when the caller
 // passes no `scores` (at least 256 bytes, so that a size of 0 means an invalid cfg)

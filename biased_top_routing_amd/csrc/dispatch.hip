@@ -16,6 +16,7 @@
 
 #include "common.h"
 #include "ffn_layout.h"
+#include "fp4.h"
 #include "kernels.h"
 
 namespace moe {
@@ -271,6 +272,47 @@ __global__ __launch_bounds__(256) void permute_rows_fp8_kernel(const uint4* __re
   }
 }
 
+// MXFP4 dispatch (format: fp4.h): quantise the token's bf16 row once, then store
+// the codes and the scale words of its 128-column groups to each of its k
+// destination rows (a row's scale words lie ntile planes of T*k words apart).
+template <int CPL>
+__global__ __launch_bounds__(256) void permute_rows_fp4_kernel(const uint4* __restrict__ src,
+                                                               const int32_t* __restrict__ inv,
+                                                               int T, int k, int H,
+                                                               uint32_t* __restrict__ dst,
+                                                               uint32_t* __restrict__ dst_scale) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const int lane = threadIdx.x & 63;
+  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (t >= T) return;      // whole wavefront exits together
+  const int64_t nchunk = H / 8, P = (int64_t)T * k;
+  const int32_t myp = lane < k ? inv[t * k + lane] : 0;
+  for (int64_t c0 = 0; c0 < nchunk; c0 += (int64_t)CPL * kWave) {
+    uint32_t q[CPL], sw[CPL];
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) {
+      const int64_t c = c0 + i * kWave + lane;
+      // a 16-lane group of 128 columns is wholly inside or outside the row (H % 128 == 0)
+      const uint4 raw = c < nchunk ? src[t * nchunk + c] : make_uint4(0, 0, 0, 0);
+      uint32_t e;
+      q[i] = mx_quant_chunk(raw, &e);
+      sw[i] = mx_scale_word(e);
+    }
+    for (int j = 0; j < k; ++j) {
+      const int64_t p = __shfl(myp, j);
+#pragma unroll
+      for (int i = 0; i < CPL; ++i) {
+        const int64_t c = c0 + i * kWave + lane;
+        if (c < nchunk) {
+          dst[p * nchunk + c] = q[i];
+          if ((lane & 15) == 0) dst_scale[c / 16 * P + p] = sw[i];
+        }
+      }
+    }
+  }
+#endif
+}
+
 // Row quantisation without permutation (shared-expert input, tests).
 __global__ __launch_bounds__(256) void quantize_rows_kernel(const uint4* __restrict__ src,
                                                             int64_t rows, int cols,
@@ -354,7 +396,7 @@ static moe_status dispatch_launch(const moe_cfg* cfg, const int32_t* topk_idx, c
                                   int32_t* offsets, int32_t* perm, int32_t* inv, void* x_perm, float* x_perm_scale,
                                   int32_t* segc, hipStream_t s) {
   moe_status st;
-  const bool fp8 = cfg->wgt == MOE_FP8_E4M3;
+  const bool fp8 = cfg->wgt == MOE_FP8_E4M3, fp4 = cfg->wgt == MOE_MXFP4;
   const int64_t N = pairs(cfg);
   const int64_t nseg = dispatch_segments(cfg);
   const int E = cfg->E;
@@ -378,7 +420,10 @@ static moe_status dispatch_launch(const moe_cfg* cfg, const int32_t* topk_idx, c
   if ((st = launch_status()) != MOE_OK) return st;
   if (!x_perm) return MOE_OK;
   const unsigned tblocks = (unsigned)((cfg->T + 3) / 4);
-  if (fp8) {
+  if (fp4) {
+    hipLaunchKernelGGL((permute_rows_fp4_kernel<8>), dim3(tblocks), dim3(256), 0, s, (const uint4*)x, inv,
+                       cfg->T, cfg->k, cfg->H, (uint32_t*)x_perm, (uint32_t*)x_perm_scale);
+  } else if (fp8) {
     hipLaunchKernelGGL((permute_rows_fp8_kernel<8>), dim3(tblocks), dim3(256), 0, s, (const uint4*)x, inv,
                        cfg->T, cfg->k, cfg->H, (uint2*)x_perm, x_perm_scale);
   } else {
@@ -393,10 +438,12 @@ static moe_status dispatch_check(const moe_cfg* cfg, const int32_t* topk_idx, co
                                  int32_t* offsets, int32_t* perm, int32_t* inv, void* x_perm, float* x_perm_scale) {
   moe_status st = validate_cfg(cfg);
   if (st != MOE_OK) return st;
-  const bool fp8 = cfg->wgt == MOE_FP8_E4M3;
+  const bool fp4 = cfg->wgt == MOE_MXFP4, scaled = fp4 || cfg->wgt == MOE_FP8_E4M3;
   // x_perm == nullptr: indices only (the expert FFN gathers the rows itself)
   if (!topk_idx || !counts || !offsets || !perm || !inv) return MOE_ERR_NULL;
-  if (x_perm && (!x || (fp8 && !x_perm_scale))) return MOE_ERR_NULL;
+  if (x_perm && (!x || (scaled && !x_perm_scale))) return MOE_ERR_NULL;
+  if (fp4 && x_perm && (misaligned(x, 16) || misaligned(x_perm, 16) || misaligned(x_perm_scale, 4)))
+    return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 

@@ -227,6 +227,20 @@ using namespace moe;
 
 namespace {
 
+// The MXFP4 kernels load 16-byte chunks of rows and codes and 4-byte scale words.
+bool fp4_misaligned(const moe_cfg* c, const void* x_perm, const void* x_perm_scale, const moe_expert_weights* w,
+                    const void* x, const void* y_perm, const void* y_shared, const void* ws) {
+  const void* chunks[] = {x_perm, w->w_gate_up, w->w_down, c->S > 0 ? w->ws_gate_up : nullptr,
+                          c->S > 0 ? w->ws_down : nullptr, x, y_perm, c->S > 0 ? y_shared : nullptr, ws};
+  for (const void* q : chunks)
+    if (misaligned(q, 16)) return true;
+  const void* words[] = {x_perm_scale, w->w_gate_up_scale, w->w_down_scale,
+                         c->S > 0 ? w->ws_gate_up_scale : nullptr, c->S > 0 ? w->ws_down_scale : nullptr};
+  for (const void* q : words)
+    if (misaligned(q, 4)) return true;
+  return false;
+}
+
 // Both FFN entry points: routed gate/up rows from x_perm (perm == nullptr) or
 // gathered from x through perm.
 moe_status expert_ffn(const moe_cfg* cfg, const void* x_perm, const float* x_perm_scale,
@@ -242,9 +256,9 @@ moe_status expert_ffn(const moe_cfg* cfg, const void* x_perm, const float* x_per
   if (!perm && !x_perm) return MOE_ERR_NULL;
   if (perm && gate_up && !x) return MOE_ERR_NULL;
   if (cfg->S > 0 && (!x || !y_shared || !w->ws_gate_up || !w->ws_down)) return MOE_ERR_NULL;
-  const bool fp8 = cfg->wgt == MOE_FP8_E4M3;
-  if (fp8 && ((!perm && !x_perm_scale) || !w->w_gate_up_scale || !w->w_down_scale)) return MOE_ERR_NULL;
-  if (fp8 && cfg->S > 0 && (!w->ws_gate_up_scale || !w->ws_down_scale)) return MOE_ERR_NULL;
+  const bool fp8 = cfg->wgt == MOE_FP8_E4M3, fp4 = cfg->wgt == MOE_MXFP4, scaled = fp8 || fp4;
+  if (scaled && ((!perm && !x_perm_scale) || !w->w_gate_up_scale || !w->w_down_scale)) return MOE_ERR_NULL;
+  if (scaled && cfg->S > 0 && (!w->ws_gate_up_scale || !w->ws_down_scale)) return MOE_ERR_NULL;
   if (saved) {
     if (cfg->act != MOE_BF16 || cfg->wgt != MOE_BF16) return MOE_ERR_UNSUPPORTED;
     if (!saved->g || !saved->u || (cfg->S > 0 && (!saved->gs || !saved->us))) return MOE_ERR_NULL;
@@ -252,14 +266,18 @@ moe_status expert_ffn(const moe_cfg* cfg, const void* x_perm, const float* x_per
   // gathered rows are addressed by 32-bit byte offsets into x (one row past
   // the end marks a dropped row)
   if (perm && cfg->act != MOE_F32 &&
-      ((int64_t)cfg->T + 1) * cfg->H * (fp8 ? 1 : (int64_t)act_bytes(cfg)) > INT32_MAX)
+      ((int64_t)cfg->T + 1) * cfg->H * (fp4 ? 1 : fp8 ? 2 : 2 * (int64_t)act_bytes(cfg)) / 2 > INT32_MAX)
     return MOE_ERR_UNSUPPORTED;
+  if (fp4 && fp4_misaligned(cfg, x_perm, x_perm_scale, w, x, y_perm, y_shared, ws)) return MOE_ERR_UNSUPPORTED;
   if (ws_bytes < FfnLayout(cfg).total) return MOE_ERR_WORKSPACE;
   if (cfg->T == 0) return MOE_OK;
   hipStream_t s = as_stream(stream);
   if (cfg->act == MOE_F32)
     return launch_ffn_f32(cfg, (const float*)x_perm, perm, offsets, w, (const float*)x, (float*)y_perm,
                           (float*)y_shared, ws, phase, s);
+  if (fp4)
+    return launch_ffn_fp4(cfg, (const uint8_t*)x_perm, (const uint8_t*)x_perm_scale, perm, offsets, w, (const bf16_t*)x,
+                          (bf16_t*)y_perm, (bf16_t*)y_shared, ws, phase, s);
   if (!fp8)
     return launch_ffn_bf16(cfg, (const bf16_t*)x_perm, perm, offsets, w, (const bf16_t*)x,
                            (bf16_t*)y_perm, (bf16_t*)y_shared, phase == MOE_FFN_DOWN ? nullptr : saved, ws,

@@ -96,6 +96,11 @@ constexpr int kFp8BM = MOE_FP8_BM;
 constexpr int kFp8BNH = 128;
 constexpr int kFp8BN2 = 256;
 constexpr int kFp8MaxKC = 64;
+// MXFP4 GEMMs: 256 token rows, or 32 where the routed experts get at most 32
+// rows each on average (the GEMMs then only stream weights); 128 h columns per
+// gate/up tile, 256 output columns per down tile.
+constexpr int kFp4BM = 256, kFp4DecBM = 32;
+constexpr int kFp4BNH = 128, kFp4BN2 = 256;
 
 // Row tiles per group in the tile order of a segment (see build_tiles_kernel).
 #ifndef MOE_GROUP_ROW_TILES
@@ -123,6 +128,7 @@ struct TileDesc {
 constexpr int kStripeGateUp = 8;
 constexpr int kStripeDown = 0;
 constexpr int kStripeFp8 = 2;
+constexpr int kStripeFp4 = 2;
 
 // Position j of XCD xcd in runs of P consecutive entries dealt to the 8 XCDs in turn.
 __host__ __device__ inline int xcd_run_index(int j, int xcd, int P) {
@@ -179,38 +185,42 @@ struct FfnLayout {
   int64_t nt1, nt1s, nt2;        // column tiles: gate/up routed, gate/up shared, down
   int64_t max1, max2;            // tile-table capacities
   size_t off_hdr, off_t1, off_t2, off_hp, off_hps, off_hs, off_hss, off_xq, off_xqs, total;
-  int hbytes;                    // bytes per stored h element
 
   explicit FfnLayout(const moe_cfg* c) {
     const int64_t P = pairs(c);
-    const bool f8 = c->wgt == MOE_FP8_E4M3;
+    const bool f8 = c->wgt == MOE_FP8_E4M3, f4 = c->wgt == MOE_MXFP4;
+    const int bm4 = P <= (int64_t)kFp4DecBM * c->E ? kFp4DecBM : kFp4BM;
     dec = small_batch(c);
-    bm1 = f8 ? kFp8BM : dec ? kDecBM : kBM1;
-    bm1_alt = f8 || dec ? 0 : kBM1Alt;
+    bm1 = f4 ? bm4 : f8 ? kFp8BM : dec ? kDecBM : kBM1;
+    bm1_alt = f4 || f8 || dec ? 0 : kBM1Alt;
     bm2_alt = 0;   // down tiles keep one height (320/256-row tiles of 8 wavefronts measured 1-2% slower)
-    bm2 = f8 ? kFp8BM : dec ? kDecBM : kBM2;
+    bm2 = f4 ? bm4 : f8 ? kFp8BM : dec ? kDecBM : kBM2;
     R1 = P / bm1 + c->E;
     Rs1 = c->S > 0 ? (c->T + bm1 - 1) / bm1 : 0;
     R2 = P / bm2 + c->E;
     Rs2 = c->S > 0 ? (c->T + bm2 - 1) / bm2 : 0;
-    const int bnh = f8 ? kFp8BNH : dec ? kDecBNH : kBNH, bn2 = f8 ? kFp8BN2 : dec ? kDecBN2 : kBN2;
+    const int bnh = f4 ? kFp4BNH : f8 ? kFp8BNH : dec ? kDecBNH : kBNH;
+    const int bn2 = f4 ? kFp4BN2 : f8 ? kFp8BN2 : dec ? kDecBN2 : kBN2;
     nt1 = (c->I + bnh - 1) / bnh;
     nt1s = ((int64_t)c->S * c->I + bnh - 1) / bnh;
     nt2 = (c->H + bn2 - 1) / bn2;
     max1 = R1 * nt1 + Rs1 * nt1s;
     max2 = (R2 + Rs2) * nt2;
-    hbytes = c->wgt == MOE_FP8_E4M3 ? 1 : (int)act_bytes(c);
-    const bool fp8 = c->wgt == MOE_FP8_E4M3;
     size_t o = 0;
     off_hdr = o; o = align_up(o + 64, 256);
     off_t1 = o; o = align_up(o + (size_t)max1 * sizeof(TileDesc), 256);
     off_t2 = o; o = align_up(o + (size_t)max2 * sizeof(TileDesc), 256);
-    off_hp = o; o = align_up(o + (size_t)P * c->I * hbytes, 256);
-    off_hps = o; o = align_up(o + (fp8 ? (size_t)P * (c->I / 128) * 4 : 0), 256);
-    off_hs = o; o = align_up(o + (size_t)c->T * c->S * c->I * hbytes, 256);
-    off_hss = o; o = align_up(o + (fp8 ? (size_t)c->T * c->S * (c->I / 128) * 4 : 0), 256);
-    off_xq = o; o = align_up(o + (fp8 ? (size_t)c->T * c->H : 0), 256);
-    off_xqs = o; o = align_up(o + (fp8 ? (size_t)c->T * (c->H / 128) * 4 : 0), 256);
+    // h codes take 1 byte (FP8) or half a byte (MXFP4) an element; both formats keep
+    // 4 scale bytes per 128 elements (one fp32, four E8M0)
+    auto stored = [&](size_t n) { return f4 ? n / 2 : f8 ? n : n * act_bytes(c); };
+    auto scale = [&](size_t n) { return f4 || f8 ? n / 128 * 4 : 0; };
+    const size_t nh = (size_t)P * c->I, nhs = (size_t)c->T * c->S * c->I, nx = (size_t)c->T * c->H;
+    off_hp = o; o = align_up(o + stored(nh), 256);
+    off_hps = o; o = align_up(o + scale(nh), 256);
+    off_hs = o; o = align_up(o + stored(nhs), 256);
+    off_hss = o; o = align_up(o + scale(nhs), 256);
+    off_xq = o; o = align_up(o + (f4 || f8 ? stored(nx) : 0), 256);
+    off_xqs = o; o = align_up(o + scale(nx), 256);
     total = o;
   }
 };

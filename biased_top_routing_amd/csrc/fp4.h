@@ -1,0 +1,83 @@
+// MXFP4: 32 neighbouring elements of a row share a power of two X = 2^(e - 127)
+// held as one byte e (E8M0; 255 is NaN), and an element is a 4-bit E2M1 code
+// (sign, 2 exponent bits with bias 1, 1 mantissa bit: 0, .5, 1, 1.5, 2, 3, 4, 6)
+// standing for its value times X (OCP Microscaling Formats specification).
+//
+// X is 2^(E - 2), E the exponent of the block's largest magnitude rounded to one
+// mantissa bit: a largest magnitude of at least 1.75 * 2^n counts as 2^(n+1), so
+// |v / X| < 7 for every element and the rounding to the nearest code (ties to
+// the even one) is off by at most half a step everywhere; with the plain floor
+// of the exponent, magnitudes between 7 X and 8 X would be cut to 6 X.  X is at
+// least 2^-126 (an fp32 normal; an all-zero block has e = 1).  A block that
+// holds an infinity or a NaN gets e = 255 and codes 0: it reads back as NaN.
+//
+// Storage: two codes a byte, the even element in the low half; scale bytes in
+// planes of 128 columns: byte b of word (c, row) belongs to the columns
+// [128 c + 32 b, + 32) of that row, words of a plane in row order.  The GEMMs
+// load the words of a tile's rows for one 128-wide K step, which are then
+// neighbours in memory, and each lane of a 16x16x128 MFMA takes one byte.
+#pragma once
+
+#include "common.h"
+
+namespace moe {
+
+#if defined(__HIP_DEVICE_COMPILE__)
+// Scale byte of a block whose largest magnitude has the fp32 bits `top` (sign cleared).
+__device__ __forceinline__ uint32_t mx_scale_byte(uint32_t top) {
+  if (top >= 0x7F800000u) return 255u;
+  const int e = (int)((top + 0x200000u) >> 23) - 2;
+  return (uint32_t)(e < 1 ? 1 : e);
+}
+
+// 8 values as E2M1 codes of scale byte e (1..254, or 255: codes 0), element i in
+// bits 4i..4i+3, by the hardware conversion (nearest, ties to the even code).
+__device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8], uint32_t e) {
+  const float x = __uint_as_float(e << 23);
+  uint32_t w = 0;
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[0], v[1], x, 0);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[2], v[3], x, 1);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[4], v[5], x, 2);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[6], v[7], x, 3);
+  return e == 255u ? 0u : w;
+}
+
+// Largest magnitude (fp32 bits) of 8 packed bf16 values; a NaN ranks above infinity.
+__device__ __forceinline__ uint32_t abs_top_bf16x8(uint4 r) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    m = max(m, (w[i] << 16) & 0x7FFF0000u);
+    m = max(m, w[i] & 0x7FFF0000u);
+  }
+  return m;
+}
+
+// A lane's chunk of 8 bf16 values, 4 consecutive lanes (4-aligned) holding one
+// 32-element block: its 8 codes, and the block's scale byte in *e.  Every lane
+// of the 4 must be active.
+__device__ __forceinline__ uint32_t mx_quant_chunk(uint4 raw, uint32_t* e) {
+  uint32_t m = abs_top_bf16x8(raw);
+  m = max(m, (uint32_t)__shfl_xor((int)m, 1));
+  m = max(m, (uint32_t)__shfl_xor((int)m, 2));
+  *e = mx_scale_byte(m);
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+  return e2m1x8(v, *e);
+}
+
+// The scale word of 128 columns from the scale bytes e that 16 consecutive
+// lanes (16-aligned) hold, 4 lanes a block: valid in the first of the 16.
+__device__ __forceinline__ uint32_t mx_scale_word(uint32_t e) {
+  uint32_t w = e | ((uint32_t)__shfl_down((int)e, 4) << 8);    // lanes 0..3: blocks 0, 1; lanes 8..11: blocks 2, 3
+  return w | ((uint32_t)__shfl_down((int)w, 8) << 16);
+}
+#endif
+
+}  // namespace moe

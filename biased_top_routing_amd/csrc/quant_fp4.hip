@@ -1,0 +1,134 @@
+// moe_quantize_fp4 / moe_dequantize_fp4: MXFP4 codes and scale bytes of bf16
+// matrices (format: fp4.h), and back.  Used offline for the expert weights, and
+// inside moe_expert_ffn for the rows of x.
+//
+// Both directions only move bytes: 2 in and 17/32 out an element, or the
+// reverse.  A workgroup takes 64 rows of one 128-column group, 16 lanes a row:
+// its 64 scale words are one 256-byte line of the group's plane, and a row's
+// piece is 256 bytes of bf16 or 64 bytes of codes.
+#include "common.h"
+#include "fp4.h"
+#include "kernels.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kRowsPerBlock = 64;
+
+__global__ __launch_bounds__(256) void quantize_fp4_kernel(const uint4* __restrict__ src, int rows, int cols,
+                                                           uint32_t* __restrict__ dst,
+                                                           uint32_t* __restrict__ scales) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int ncol = cols / 128;
+  const int c = blockIdx.x % ncol, sub = lane & 15;
+  const int64_t mat = blockIdx.y;
+  const int64_t nchunk = cols / 8;                      // 16-byte chunks of a row; also its code words
+  const int r0 = blockIdx.x / ncol * kRowsPerBlock + wave * 16 + (lane >> 4);
+  uint4 raw[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = r0 + i * 4;
+    raw[i] = r < rows ? src[(mat * rows + r) * nchunk + (int64_t)c * 16 + sub] : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = r0 + i * 4;
+    uint32_t e;
+    const uint32_t w = mx_quant_chunk(raw[i], &e);
+    const uint32_t sw = mx_scale_word(e);
+    if (r < rows) {
+      dst[(mat * rows + r) * nchunk + (int64_t)c * 16 + sub] = w;
+      if (sub == 0) scales[(mat * ncol + c) * rows + r] = sw;
+    }
+  }
+#endif
+}
+
+__global__ __launch_bounds__(256) void dequantize_fp4_kernel(const uint32_t* __restrict__ codes,
+                                                             const uint8_t* __restrict__ scales, int rows, int cols,
+                                                             uint4* __restrict__ dst) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int ncol = cols / 128;
+  const int c = blockIdx.x % ncol, sub = lane & 15;
+  const int64_t mat = blockIdx.y;
+  const int64_t nchunk = cols / 8;
+  const int r0 = blockIdx.x / ncol * kRowsPerBlock + wave * 16 + (lane >> 4);
+  uint32_t w[4], e[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = min(r0 + i * 4, rows - 1);
+    w[i] = codes[(mat * rows + r) * nchunk + (int64_t)c * 16 + sub];
+    e[i] = scales[((mat * ncol + c) * rows + r) * 4 + (sub >> 2)];
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = r0 + i * 4;
+    // X as fp32: e = 0 is the subnormal 2^-127, e = 255 a NaN
+    const float x = __uint_as_float(e[i] == 0u ? 0x00400000u : e[i] == 255u ? 0x7FC00000u : e[i] << 23);
+    uint32_t o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t h[2];
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const uint32_t code = w[i] >> (8 * j + 4 * b);
+        const uint32_t ex = (code >> 1) & 3u, m = code & 1u;
+        // E2M1 magnitude: m / 2 for exponent 0, else (1 + m / 2) 2^(ex - 1)
+        const float mag = ex == 0u ? 0.5f * (float)m : __uint_as_float(((ex + 126u) << 23) | (m << 22));
+        // (a two-bit significand times a power of two: exact in bf16)
+        h[b] = __float_as_uint((code & 8u ? -mag : mag) * x) >> 16;
+      }
+      o[j] = h[0] | (h[1] << 16);
+    }
+    if (r < rows) dst[(mat * rows + r) * nchunk + (int64_t)c * 16 + sub] = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+#endif
+}
+
+// Workgroups of one matrix: row blocks, and in each its column groups.
+int64_t fp4_blocks(int32_t rows, int32_t cols) {
+  return ((int64_t)rows + kRowsPerBlock - 1) / kRowsPerBlock * (cols / 128);
+}
+
+moe_status check_fp4(const void* bf16, const uint8_t* codes, const uint8_t* scales, int32_t n_mat, int32_t rows,
+                     int32_t cols) {
+  if (!bf16 || !codes || !scales) return MOE_ERR_NULL;
+  if (n_mat < 0 || n_mat > 65535 || rows < 0 || cols <= 0 || cols % 128) return MOE_ERR_SHAPE;
+  if (fp4_blocks(rows, cols) >= ((int64_t)1 << 31)) return MOE_ERR_SHAPE;
+  if (misaligned(bf16, 16) || misaligned(codes, 4) || misaligned(scales, 4)) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+}  // namespace
+
+moe_status launch_quantize_fp4(const bf16_t* src, int n_mat, int rows, int cols, uint8_t* dst, uint8_t* scales,
+                               hipStream_t st) {
+  if (n_mat == 0 || rows == 0) return MOE_OK;
+  hipLaunchKernelGGL(quantize_fp4_kernel, dim3((unsigned)fp4_blocks(rows, cols), (unsigned)n_mat), dim3(256), 0, st, (const uint4*)src, rows,
+                     cols, (uint32_t*)dst, (uint32_t*)scales);
+  return launch_status();
+}
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" moe_status moe_quantize_fp4(const void* src_bf16, int32_t n_mat, int32_t rows, int32_t cols, uint8_t* dst,
+                                       uint8_t* scales, void* stream) {
+  const moe_status st = check_fp4(src_bf16, dst, scales, n_mat, rows, cols);
+  if (st != MOE_OK) return st;
+  return launch_quantize_fp4((const bf16_t*)src_bf16, n_mat, rows, cols, dst, scales, as_stream(stream));
+}
+
+extern "C" moe_status moe_dequantize_fp4(const uint8_t* codes, const uint8_t* scales, int32_t n_mat, int32_t rows,
+                                         int32_t cols, void* dst_bf16, void* stream) {
+  const moe_status st = check_fp4(dst_bf16, codes, scales, n_mat, rows, cols);
+  if (st != MOE_OK) return st;
+  if (n_mat == 0 || rows == 0) return MOE_OK;
+  hipLaunchKernelGGL(dequantize_fp4_kernel, dim3((unsigned)fp4_blocks(rows, cols), (unsigned)n_mat), dim3(256), 0,
+                     as_stream(stream), (const uint32_t*)codes, scales, rows, cols, (uint4*)dst_bf16);
+  return launch_status();
+}

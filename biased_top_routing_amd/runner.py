@@ -37,11 +37,12 @@ class MoeLayerGPU:
         self.save_gu = save_gu
         self.keep_scores = keep_scores
         self.fp8 = cfg.wgt == "fp8_e4m3"
+        self.fp4 = cfg.wgt == "mxfp4"
         self.act_dtype = torch.float32 if cfg.act == "f32" else torch.bfloat16
         dev = lambda a: to_device(a, device)
         self.w_router = dev(weights.w_router)
         self.logit_offset = dev(weights.logit_offset)
-        if self.fp8:
+        if self.fp8 or self.fp4:
             self.w_gate_up, self.w_gate_up_scale = self._quantize(weights.w_gate_up)
             self.w_down, self.w_down_scale = self._quantize(weights.w_down)
             self.ws_gate_up, self.ws_gate_up_scale = self._quantize(weights.ws_gate_up)
@@ -56,8 +57,18 @@ class MoeLayerGPU:
         self.alloc(cfg.T if T is None else T)
 
     def _quantize(self, w_np):
-        """bf16 weights [n, rows, cols] -> E4M3 codes + one fp32 scale per 128 x 128 block (on the GPU)."""
+        """bf16 weights [n, rows, cols] -> E4M3 codes + one fp32 scale per 128 x 128 block, or MXFP4 codes
+        [n, rows, cols/2] + scale bytes [n, cols/128, rows, 4] (on the GPU)."""
         n, rows, cols = w_np.shape
+        if self.fp4:
+            codes = torch.empty((n, rows, cols // 2), dtype=torch.uint8, device=self.device)
+            scales = torch.empty((n, cols // 128, rows, 4), dtype=torch.uint8, device=self.device)
+            if n:
+                src = to_device(w_np, self.device)
+                L.moe_quantize_fp4(src, n, rows, cols, codes, scales)
+                torch.cuda.current_stream().synchronize()
+                del src
+            return codes, scales
         codes = torch.empty((n, rows, cols), dtype=torch.uint8, device=self.device)
         scales = torch.empty((n, rows // 128, cols // 128), dtype=torch.float32, device=self.device)
         if n:
@@ -85,6 +96,9 @@ class MoeLayerGPU:
         self.inv = torch.empty((T, c.k), dtype=i32, device=d)
         if self.gather:
             self.x_perm = self.x_perm_scale = None
+        elif self.fp4:
+            self.x_perm = torch.empty((P, c.H // 2), dtype=torch.uint8, device=d)
+            self.x_perm_scale = torch.empty((c.H // 128, P, 4), dtype=torch.uint8, device=d)
         elif self.fp8:
             self.x_perm = torch.empty((P, c.H), dtype=torch.uint8, device=d)
             self.x_perm_scale = torch.empty((P, c.H // 128), dtype=f32, device=d)

@@ -13,6 +13,16 @@
  *    contiguous dimension of both GEMM operands).  Indices are int32.
  *  - bf16 tensors are raw 16-bit bfloat16 values; fp8 tensors are raw OCP E4M3FN
  *    bytes (bias 7, no infinities, largest finite 448).
+ *  - MXFP4 matrices (OCP Microscaling) [rows, cols], cols % 128 == 0, are two
+ *    tensors: codes [rows, cols/2], two 4-bit E2M1 codes a byte (sign, then the
+ *    magnitudes 0, .5, 1, 1.5, 2, 3, 4, 6 as 0..7), the even column in the low
+ *    half; and scale bytes [cols/128, rows, 4]: byte e at (c, r, b) means that
+ *    the columns [128c + 32b, 128c + 32b + 32) of row r stand for code * 2^(e-127)
+ *    (e = 255: NaN).  (The scales of one 128-wide step of K over neighbouring
+ *    rows are neighbours, as the GEMMs load them.)  Scale pointers of MXFP4
+ *    tensors pass through the `float*` scale arguments and members.  Codes,
+ *    rows and workspaces must be 16-byte aligned and scale bytes 4-byte aligned
+ *    (MOE_ERR_UNSUPPORTED otherwise).
  *  - Every call validates all sizes and pointers on the host BEFORE touching the
  *    device and returns a negative moe_status on error (nothing is launched).  A
  *    failed launch returns MOE_ERR_LAUNCH.  Work is asynchronous on `stream`
@@ -47,7 +57,7 @@ typedef enum {
   MOE_ERR_SCRATCH = -6      /* sizes exceed the fixed scratch of a no-allocation entry point */
 } moe_status;
 
-typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_FP8_E4M3 = 2 } moe_dtype;
+typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_FP8_E4M3 = 2, MOE_MXFP4 = 3 } moe_dtype;
 
 /*
  * Layer configuration.
@@ -57,9 +67,9 @@ typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_FP8_E4M3 = 2 } moe_dtype;
  *  group_topr: a group's score is the fp32 sum of its group_topr largest biased
  *              scores, added from the largest down (1 <= group_topr <= E/G, <= 8).
  *  route_scale: gates are route_scale * s_j / sum(s) over the selected experts.
- *  act / wgt (moe_dtype): (F32, F32) | (BF16, BF16) | (BF16, FP8_E4M3).  The
- *              router always runs in `act` precision; FP8_E4M3 applies to the
- *              expert GEMMs only.
+ *  act / wgt (moe_dtype): (F32, F32) | (BF16, BF16) | (BF16, FP8_E4M3) |
+ *              (BF16, MXFP4).  The router always runs in `act` precision;
+ *              FP8_E4M3 and MXFP4 apply to the expert GEMMs only.
  *  bias_eq_mode: 0 - an expert whose load equals T*k/E counts as underloaded
  *              (+gamma), so every bias moves each step; 1 - it is left unchanged.
  * Supported ranges (every call checks them first and returns MOE_ERR_SHAPE
@@ -71,7 +81,8 @@ typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_FP8_E4M3 = 2 } moe_dtype;
  *  E*H*2 < 2^31, and (T*(k+S)/32 + E + 2) * (max(H, S*I)/64 + 2) < 2^30 (the
  *  grouped GEMMs count their tiles in 32 bits).  F32: H % 4 == 0, I % 4 == 0;
  *  BF16 experts: H % 64 == 0, I % 128 == 0; FP8 experts: H % 128 == 0,
- *  I % 128 == 0, H <= 8192 and max(S, 1)*I <= 8192 (64 scale blocks of K).
+ *  I % 128 == 0, H <= 8192 and max(S, 1)*I <= 8192 (64 scale blocks of K); MXFP4
+ *  experts: H % 128 == 0, I % 128 == 0, T*k*max(H, I) and T*max(H, S*I) under 2^36.
  */
 typedef struct {
   int32_t T, H, E, G, M, k, S, I;
@@ -147,10 +158,12 @@ moe_status moe_route(const moe_cfg* cfg, const void* x, const void* w_router,
  *  perm      [T*k] int32 out: flat pair ids f = t*k + j, stably sorted by expert
  *  inv       [T, k] int32 out: row of pair (t, j) in the permuted order
  *  x_perm    [T*k, H] out: row p = x[perm[p] / k]; act dtype, or E4M3 bytes when
- *            wgt == FP8_E4M3 (quantised per 1x128 tile: sc = amax/448, q = e4m3(v/sc)).
+ *            wgt == FP8_E4M3 (quantised per 1x128 tile: sc = amax/448, q = e4m3(v/sc)),
+ *            or MXFP4 codes [T*k, H/2] (quantised as by moe_quantize_fp4).
  *            NULL: only counts, offsets, perm and inv are written (x and
  *            x_perm_scale may then be NULL too), for moe_expert_ffn_gather.
- *  x_perm_scale [T*k, H/128] fp32 out (FP8 only, else NULL)
+ *  x_perm_scale [T*k, H/128] fp32 out (FP8), scale bytes [H/128, T*k, 4] out
+ *            (MXFP4), else NULL
  *  ws, ws_bytes  workspace of at least moe_workspace_bytes(cfg, MOE_WS_DISPATCH)
  */
 moe_status moe_dispatch(const moe_cfg* cfg, const int32_t* topk_idx, const void* x,
@@ -180,7 +193,10 @@ moe_status moe_dispatch_noalloc(const moe_cfg* cfg, const int32_t* topk_idx, con
                                 void* x_perm, float* x_perm_scale, void* stream);
 
 /* Expert weights.  Scales are only read when wgt == FP8_E4M3 (then the weight
- * tensors hold E4M3 bytes, one fp32 scale per 128 x 128 block). */
+ * tensors hold E4M3 bytes, one fp32 scale per 128 x 128 block) or MXFP4 (each
+ * expert's matrix as codes and scale bytes: w_gate_up [E, 2I, H/2] with
+ * [E, H/128, 2I, 4], w_down [E, H, I/2] with [E, I/128, H, 4], alike for the
+ * shared ones). */
 typedef struct {
   const void* w_gate_up;         /* [E, 2I, H]: gate rows [0, I), up rows [I, 2I) */
   const void* w_down;            /* [E, H, I] */
@@ -217,7 +233,9 @@ typedef struct {
  *               SwiGLU intermediates between the two phases
  *  phase        MOE_FFN_ALL | MOE_FFN_GATE_UP | MOE_FFN_DOWN
  * Intermediates are rounded to the activation dtype (bf16) or, for FP8, to E4M3
- * per 1x128 tile of each row; accumulation is fp32.
+ * per 1x128 tile of each row, or, for MXFP4, to E2M1 per 32 columns of each row
+ * (as by moe_quantize_fp4, from the fp32 values); accumulation is fp32.  MXFP4
+ * quantises x for the shared experts in the same way.
  */
 moe_status moe_expert_ffn(const moe_cfg* cfg, const void* x_perm, const float* x_perm_scale,
                           const int32_t* offsets, const moe_expert_weights* w, const void* x,
@@ -230,16 +248,17 @@ moe_status moe_expert_ffn(const moe_cfg* cfg, const void* x_perm, const float* x
  * x[perm[p] / k] (same arithmetic, same order: y_perm and y_shared equal
  * moe_expert_ffn's bit for bit).  For FP8 the kernel quantises x once per
  * 1x128 tile into the workspace and gathers codes and scales from there (the
- * same codes moe_dispatch would write into x_perm).
+ * same codes moe_dispatch would write into x_perm).  For MXFP4 it quantises x
+ * likewise, per 32 columns.
  *
  * Follows: the per-expert token rows of dispatch (DeepSeek-V3 Technical
  * Report：中英对照解读, §2.2) read in place instead of copied.
  *
- *  x         [T, H] act dtype in (bf16 for FP8 weights)
+ *  x         [T, H] act dtype in (bf16 for FP8 and MXFP4 weights)
  *  perm, offsets  as written by moe_dispatch (which may then skip x_perm)
  *  w, y_perm, y_shared, ws, ws_bytes, phase  as for moe_expert_ffn
  * MOE_ERR_UNSUPPORTED when (T+1) * H * (bytes per element) exceeds 2^31 - 1
- * (the gathered rows are addressed by 32-bit byte offsets; bf16/FP8 only).
+ * (the gathered rows are addressed by 32-bit byte offsets; bf16, FP8 and MXFP4).
  */
 moe_status moe_expert_ffn_gather(const moe_cfg* cfg, const void* x, const int32_t* perm,
                                  const int32_t* offsets, const moe_expert_weights* w,
@@ -314,6 +333,31 @@ moe_status moe_update_bias(const moe_cfg* cfg, const int32_t* counts, float* bia
  */
 moe_status moe_quantize_fp8(const void* src_bf16, int32_t n_mat, int32_t rows, int32_t cols,
                             int32_t block_rows, uint8_t* dst, float* scales, void* stream);
+
+/*
+ * moe_quantize_fp4 - MXFP4 codes and scale bytes of bf16 matrices
+ * [n_mat, rows, cols]: the weight preparation of the MXFP4 experts, and what
+ * moe_dispatch does to the rows of x.
+ *  dst     [n_mat, rows, cols/2] codes out
+ *  scales  [n_mat, cols/128, rows, 4] bytes out
+ * A block of 32 columns of a row gets the scale 2^(n-2), n the exponent of its
+ * largest magnitude rounded to one mantissa bit (1.75 * 2^n and above count as
+ * 2^(n+1)), and at least 2^-126; a code is the nearest E2M1 value of v / scale,
+ * ties to the even code: off by at most half a step.  A block that holds an
+ * infinity or a NaN gets scale byte 255 and codes 0 and reads back as NaN.
+ * cols must be a multiple of 128 (any rows), n_mat at most 65535 and
+ * ceil(rows/64) * cols/128 below 2^31 (MOE_ERR_SHAPE).
+ */
+moe_status moe_quantize_fp4(const void* src_bf16, int32_t n_mat, int32_t rows, int32_t cols, uint8_t* dst,
+                            uint8_t* scales, void* stream);
+
+/*
+ * moe_dequantize_fp4 - the bf16 values [n_mat, rows, cols] that MXFP4 codes and
+ * scale bytes stand for (exact; magnitudes of 2^128 and more become infinite,
+ * scale byte 255 NaN).  Same sizes and errors as moe_quantize_fp4.
+ */
+moe_status moe_dequantize_fp4(const uint8_t* codes, const uint8_t* scales, int32_t n_mat, int32_t rows,
+                              int32_t cols, void* dst_bf16, void* stream);
 
 /* ------------------------------------------------------------------ backward
  * The gradient of one layer pass (the training step the bias rule lives in),

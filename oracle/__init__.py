@@ -24,5 +24,6 @@ from .ffn import swiglu, routed_ffn, shared_ffn  # noqa: F401
 from .combine import combine  # noqa: F401
 from .balance import update_bias  # noqa: F401
 from .fp8 import e4m3_decode, e4m3_encode, quantize_rows_1x128, quantize_blocks_128x128, fp8_matmul  # noqa: F401
+from .mxfp4 import dequantize_mxfp4, e2m1_decode, e2m1_encode, quantize_mxfp4  # noqa: F401
 from .layer import decode_act, forward_from_routing, layer_forward, sampled_forward  # noqa: F401
 from .backward import backward_from_routing, gate_backward, seq_balance_loss, swiglu_backward  # noqa: F401

@@ -9,7 +9,8 @@ reading notes, Method §1).  With wgt == "fp8_e4m3" the expert GEMMs follow the
 fine-grained FP8 recipe of oracle.fp8 (qwbw.cn essay, FP8 part of the
 infrastructure section): x and h per 1x128 tile, weights per 128x128 block,
 while routing stays in higher precision (the same section keeps MoE gating in
-BF16/FP32).
+BF16/FP32).  With wgt == "mxfp4" x, h and the weights are MXFP4 values
+(oracle.mxfp4), summed exactly.
 
 `cfg` is any object with the attributes T H E G M k S I group_topr route_scale
 act wgt gamma bias_eq_mode.  Stored tensors are either float32 values or bf16
@@ -24,6 +25,7 @@ from .combine import combine
 from .dispatch import dispatch, permute_rows
 from .ffn import swiglu
 from .fp8 import fp8_matmul, quantize_blocks_128x128, quantize_rows_1x128
+from .mxfp4 import dequantize_mxfp4, quantize_mxfp4
 from .route import affinity, route
 
 F64 = np.float64
@@ -65,19 +67,41 @@ class _Fp8Expert:
         return self.down(qh, sh)
 
 
+class _Mxfp4Expert:
+    """One expert's weights in MXFP4, as the fp64 values they stand for."""
+
+    def __init__(self, w_gate_up, w_down):
+        self.wgu = dequantize_mxfp4(*quantize_mxfp4(decode_act(w_gate_up)))
+        self.wd = dequantize_mxfp4(*quantize_mxfp4(decode_act(w_down)))
+        self.I = self.wgu.shape[0] // 2
+
+    def hidden(self, xq):
+        """SwiGLU intermediate h (fp64) of rows xq (MXFP4 values)."""
+        ab = xq @ self.wgu.T
+        return _silu_mul(ab[:, :self.I], ab[:, self.I:])
+
+    def __call__(self, xq):
+        return dequantize_mxfp4(*quantize_mxfp4(self.hidden(xq))) @ self.wd.T
+
+
 def _expert_fn(cfg, w_gate_up, w_down):
     if cfg.wgt == "fp8_e4m3":
         ex = _Fp8Expert(w_gate_up, w_down)
         return lambda rows_q: ex(*rows_q)
+    if cfg.wgt == "mxfp4":
+        return _Mxfp4Expert(w_gate_up, w_down)
     wgu = decode_act(w_gate_up)
     wd = decode_act(w_down)
     return lambda rows: swiglu(rows, wgu, wd)
 
 
 def _rows_view(cfg, x32):
-    """What an expert consumes: fp64 rows, or (codes, scales) of 1x128 tiles for fp8."""
+    """What an expert consumes: fp64 rows (for mxfp4 the quantised values), or (codes, scales) of 1x128
+    tiles for fp8."""
     if cfg.wgt == "fp8_e4m3":
         return quantize_rows_1x128(x32)
+    if cfg.wgt == "mxfp4":
+        return dequantize_mxfp4(*quantize_mxfp4(x32))
     return x32.astype(F64)
 
 

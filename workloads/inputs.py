@@ -60,7 +60,7 @@ def _normal(g: np.random.Generator, shape, sigma: float) -> np.ndarray:
 def _encode(z: np.ndarray, dtype: str) -> np.ndarray:
     if dtype == "f32":
         return z
-    if dtype in ("bf16", "fp8_e4m3"):  # fp8 weights start as bf16; each side quantises them
+    if dtype in ("bf16", "fp8_e4m3", "mxfp4"):  # fp8 and mxfp4 weights start as bf16; each side quantises them
         return f32_to_bf16_bits(z)
     raise ValueError(dtype)
 
