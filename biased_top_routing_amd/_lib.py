@@ -84,6 +84,10 @@ def lib() -> ctypes.CDLL:
             "moe_dispatch_backward": [cfgp, vp, vp, vp, vp, vp, vp],
             "moe_update_bias": [cfgp, vp, vp, f32, vp],
             "moe_quantize_fp8": [vp, i32, i32, i32, i32, vp, vp, vp],
+            "moe_dispatch_local": [cfgp, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp],
+            "moe_combine_local": [cfgp, vp, vp, vp, vp, vp, vp],
+            "moe_combine_local_backward": [cfgp, vp, vp, vp, vp, vp, vp, vp],
+            "moe_dispatch_local_backward": [cfgp, vp, vp, vp, vp, vp, vp],
             "moe_quantize_fp4": [vp, i32, i32, i32, vp, vp, vp],
             "moe_dequantize_fp4": [vp, vp, i32, i32, i32, vp, vp],
             "moe_ffn_workspace_part": [cfgp, ctypes.c_int, ctypes.POINTER(sz), ctypes.POINTER(sz)],
@@ -262,6 +266,28 @@ def moe_update_bias(cfg, counts, bias, gamma, stream=None):
 def moe_quantize_fp8(src, n_mat, rows, cols, block_rows, dst, scales, stream=None):
     _check("moe_quantize_fp8", lib().moe_quantize_fp8(_p(src), n_mat, rows, cols, block_rows, _p(dst),
                                                       _p(scales), _s(stream)))
+
+
+def moe_dispatch_local(cfg, first_expert, n_tokens, topk_idx, x, counts, offsets, perm, inv, x_perm, x_perm_scale, ws,
+                       stream=None):
+    _check("moe_dispatch_local", lib().moe_dispatch_local(
+        ctypes.byref(cfg), int(first_expert), _c(n_tokens), _c(topk_idx), _c(x), _c(counts), _c(offsets), _c(perm),
+        _c(inv), _c(x_perm), _c(x_perm_scale), _c(ws), _nbytes(ws), _s(stream)))
+
+
+def moe_combine_local(cfg, y_perm, y_shared, inv, topk_w, y, stream=None):
+    _check("moe_combine_local", lib().moe_combine_local(ctypes.byref(cfg), _c(y_perm), _c(y_shared), _c(inv),
+                                                        _c(topk_w), _c(y), _s(stream)))
+
+
+def moe_combine_local_backward(cfg, dy, y_perm, inv, topk_w, dy_perm, d_topk_w, stream=None):
+    _check("moe_combine_local_backward", lib().moe_combine_local_backward(
+        ctypes.byref(cfg), _c(dy), _c(y_perm), _c(inv), _c(topk_w), _c(dy_perm), _c(d_topk_w), _s(stream)))
+
+
+def moe_dispatch_local_backward(cfg, dx_perm, dx_shared, dx_router, inv, dx, stream=None):
+    _check("moe_dispatch_local_backward", lib().moe_dispatch_local_backward(
+        ctypes.byref(cfg), _c(dx_perm), _c(dx_shared), _c(dx_router), _c(inv), _c(dx), _s(stream)))
 
 
 def moe_quantize_fp4(src, n_mat, rows, cols, dst, scales, stream=None):

@@ -114,6 +114,131 @@ __global__ __launch_bounds__(1024) void dispatch_bwd_kernel(const uint4* __restr
   }
 }
 
+// ---- the same two steps over a share of the batch: absent slots have inv = -1
+
+// The present slots of token t in slot order: their rows and slot numbers in LDS;
+// returns how many.  Called by the whole workgroup (k <= 32).
+__device__ __forceinline__ int present_slots(const int32_t* __restrict__ inv, int64_t t, int k, int32_t* row,
+                                             int32_t* slot) {
+  __shared__ int n_present;
+  if (threadIdx.x < kWave) {
+    const int j = threadIdx.x;
+    const int32_t p = j < k ? inv[t * k + j] : -1;
+    const uint64_t here = __ballot(p >= 0);
+    if (p >= 0) {
+      const int at = __popcll(here & ~(~0ull << j));
+      row[at] = p;
+      slot[at] = j;
+    }
+    if (j == 0) n_present = __popcll(here);
+  }
+  __syncthreads();
+  return n_present;
+}
+
+#if defined(__HIP_DEVICE_COMPILE__)
+__device__ __forceinline__ uint4 cvt_bf16x8(const float* f) {
+  return make_uint4(cvt_bf16x2(f[0], f[1]), cvt_bf16x2(f[2], f[3]), cvt_bf16x2(f[4], f[5]), cvt_bf16x2(f[6], f[7]));
+}
+#endif
+
+// One workgroup per token, one lane per 16-byte chunk of the row.  The present
+// slots are taken in batches whose rows are all requested before any is used;
+// per slot the lanes' products are summed by wavefront, then over the wavefronts
+// in order.
+constexpr int kLocalBatch = 4;
+__global__ __launch_bounds__(1024) void combine_local_bwd_kernel(const uint4* __restrict__ dy,
+                                                                const uint4* __restrict__ y_perm,
+                                                                const int32_t* __restrict__ inv,
+                                                                const float* __restrict__ topk_w, int k,
+                                                                int64_t nchunk, uint4* __restrict__ dy_perm,
+                                                                float* __restrict__ d_w) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __shared__ float red[kMaxWaves][kMaxTopK];
+  __shared__ int32_t row[kMaxTopK], slot[kMaxTopK];
+  const int64_t t = blockIdx.x;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int n = present_slots(inv, t, k, row, slot);
+  if ((int)threadIdx.x < k && inv[t * k + threadIdx.x] < 0) d_w[t * k + threadIdx.x] = 0.f;
+  for (int b = 0; b < n; b += kLocalBatch) {
+    float s[kLocalBatch];
+#pragma unroll
+    for (int i = 0; i < kLocalBatch; ++i) s[i] = 0.f;
+    for (int64_t c = threadIdx.x; c < nchunk; c += blockDim.x) {
+      float d[8];
+      uint4 r[kLocalBatch];
+#pragma unroll
+      for (int i = 0; i < kLocalBatch; ++i) r[i] = y_perm[row[min(b + i, n - 1)] * nchunk + c];
+      bf16x8_to_f32(dy[t * nchunk + c], d);
+#pragma unroll
+      for (int i = 0; i < kLocalBatch; ++i) {
+        if (b + i >= n) continue;
+        float y[8], o[8];
+        bf16x8_to_f32(r[i], y);
+        const float w = topk_w[t * k + slot[b + i]];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          s[i] = fmaf(d[q], y[q], s[i]);
+          o[q] = w * d[q];
+        }
+        dy_perm[row[b + i] * nchunk + c] = cvt_bf16x8(o);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kLocalBatch; ++i) {
+      if (b + i >= n) continue;
+      const float v = wave_sum(s[i]);
+      if (lane == 0) red[wave][b + i] = v;
+    }
+  }
+  __syncthreads();
+  if ((int)threadIdx.x < n) {
+    const int nw = (int)(blockDim.x / kWave);
+    float v = red[0][threadIdx.x];
+    for (int w = 1; w < nw; ++w) v += red[w][threadIdx.x];
+    d_w[t * k + slot[threadIdx.x]] = v;
+  }
+#endif
+}
+
+__global__ __launch_bounds__(1024) void dispatch_local_bwd_kernel(const uint4* __restrict__ dx_perm,
+                                                                 const uint4* __restrict__ dx_shared,
+                                                                 const float4* __restrict__ dx_router,
+                                                                 const int32_t* __restrict__ inv, int k,
+                                                                 int64_t nchunk, uint4* __restrict__ dx) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __shared__ int32_t row[kMaxTopK], slot[kMaxTopK];
+  const int64_t t = blockIdx.x;
+  const int n = present_slots(inv, t, k, row, slot);
+  for (int64_t c = threadIdx.x; c < nchunk; c += blockDim.x) {
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, v[8];
+    for (int b = 0; b < n; b += kLocalBatch) {
+      uint4 r[kLocalBatch];
+#pragma unroll
+      for (int i = 0; i < kLocalBatch; ++i) r[i] = dx_perm[row[min(b + i, n - 1)] * nchunk + c];
+#pragma unroll
+      for (int i = 0; i < kLocalBatch; ++i) {
+        if (b + i >= n) continue;
+        bf16x8_to_f32(r[i], v);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) acc[q] += v[q];
+      }
+    }
+    if (dx_shared) {
+      bf16x8_to_f32(dx_shared[t * nchunk + c], v);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) acc[q] += v[q];
+    }
+    if (dx_router) {
+      const float4 a = dx_router[(t * nchunk + c) * 2], e = dx_router[(t * nchunk + c) * 2 + 1];
+      acc[0] += a.x; acc[1] += a.y; acc[2] += a.z; acc[3] += a.w;
+      acc[4] += e.x; acc[5] += e.y; acc[6] += e.z; acc[7] += e.w;
+    }
+    dx[t * nchunk + c] = cvt_bf16x8(acc);
+  }
+#endif
+}
+
 constexpr int kMaxEPL = 8;   // experts per lane: E <= 512
 
 // Statistics of one chunk of kSeqChunk tokens of one sequence: per expert, how
@@ -260,6 +385,23 @@ extern "C" moe_status moe_combine_backward(const moe_cfg* cfg, const void* dy, c
   return launch_status();
 }
 
+extern "C" moe_status moe_combine_local_backward(const moe_cfg* cfg, const void* dy, const void* y_perm,
+                                                 const int32_t* inv, const float* topk_w, void* dy_perm,
+                                                 float* d_topk_w, void* stream) {
+  moe_status st = validate_cfg(cfg);
+  if (st != MOE_OK) return st;
+  if (!bwd_dtypes_ok(cfg)) return MOE_ERR_UNSUPPORTED;
+  if (cfg->T == 0) return MOE_OK;
+  if (!dy || !y_perm || !inv || !topk_w || !dy_perm || !d_topk_w) return MOE_ERR_NULL;
+  if (misaligned(dy, 16) || misaligned(y_perm, 16) || misaligned(dy_perm, 16) || misaligned(inv, 4) ||
+      misaligned(topk_w, 4) || misaligned(d_topk_w, 4))
+    return MOE_ERR_UNSUPPORTED;
+  const int64_t nchunk = (int64_t)cfg->H * 2 / 16;
+  hipLaunchKernelGGL(combine_local_bwd_kernel, dim3((unsigned)cfg->T), row_block(nchunk), 0, as_stream(stream),
+                     (const uint4*)dy, (const uint4*)y_perm, inv, topk_w, cfg->k, nchunk, (uint4*)dy_perm, d_topk_w);
+  return launch_status();
+}
+
 namespace {
 
 // Both expert backward entry points; saved == nullptr: recompute g, u.
@@ -355,6 +497,24 @@ extern "C" moe_status moe_dispatch_backward(const moe_cfg* cfg, const void* dx_p
   if (cfg->T == 0) return MOE_OK;
   const int64_t nchunk = (int64_t)cfg->H * 2 / 16;
   hipLaunchKernelGGL(dispatch_bwd_kernel, dim3((unsigned)cfg->T), row_block(nchunk), 0, as_stream(stream),
+                     (const uint4*)dx_perm, cfg->S > 0 ? (const uint4*)dx_shared : nullptr,
+                     (const float4*)dx_router, inv, cfg->k, nchunk, (uint4*)dx);
+  return launch_status();
+}
+
+extern "C" moe_status moe_dispatch_local_backward(const moe_cfg* cfg, const void* dx_perm, const void* dx_shared,
+                                                  const float* dx_router, const int32_t* inv, void* dx,
+                                                  void* stream) {
+  moe_status st = validate_cfg(cfg);
+  if (st != MOE_OK) return st;
+  if (!bwd_dtypes_ok(cfg)) return MOE_ERR_UNSUPPORTED;
+  if (cfg->T == 0) return MOE_OK;
+  if (!dx_perm || !inv || !dx || (cfg->S > 0 && !dx_shared)) return MOE_ERR_NULL;
+  if (misaligned(dx_perm, 16) || (cfg->S > 0 && misaligned(dx_shared, 16)) || misaligned(dx_router, 16) ||
+      misaligned(dx, 16) || misaligned(inv, 4))
+    return MOE_ERR_UNSUPPORTED;
+  const int64_t nchunk = (int64_t)cfg->H * 2 / 16;
+  hipLaunchKernelGGL(dispatch_local_bwd_kernel, dim3((unsigned)cfg->T), row_block(nchunk), 0, as_stream(stream),
                      (const uint4*)dx_perm, cfg->S > 0 ? (const uint4*)dx_shared : nullptr,
                      (const float4*)dx_router, inv, cfg->k, nchunk, (uint4*)dx);
   return launch_status();

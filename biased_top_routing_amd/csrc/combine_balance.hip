@@ -58,7 +58,9 @@ __device__ __forceinline__ void accum_chunk(float* acc, uint4 r, float g) {
 
 constexpr int kMaxCombineK = 32;   // validate_cfg bounds k
 
-template <bool BF16>
+// LOCAL: absent slots (inv = -1) take no part; the present ones are gathered in
+// slot order first, so a token costs the rows it has.
+template <bool BF16, bool LOCAL>
 __global__ __launch_bounds__(1024) void combine_kernel(const uint4* __restrict__ y_perm,
                                                       const uint4* __restrict__ y_shared,
                                                       const int32_t* __restrict__ inv,
@@ -75,11 +77,28 @@ __global__ __launch_bounds__(1024) void combine_kernel(const uint4* __restrict__
   const int64_t t = blockIdx.x;          // the whole workgroup on one token
   const int c0 = threadIdx.x, cstep = blockDim.x;
   if (t >= T) return;
-  if ((int)threadIdx.x < k) {
-    slot_row[threadIdx.x] = inv[t * k + threadIdx.x];
-    slot_w[threadIdx.x] = topk_w[t * k + threadIdx.x];
+  if constexpr (LOCAL) {
+    __shared__ int n_present;
+    if (threadIdx.x < kWave) {               // the first wavefront (k <= 32 of its lanes hold a slot)
+      const int j = threadIdx.x;
+      const int32_t p = j < k ? inv[t * k + j] : -1;
+      const uint64_t here = __ballot(p >= 0);
+      if (p >= 0) {
+        const int at = __popcll(here & ~(~0ull << j));
+        slot_row[at] = p;
+        slot_w[at] = topk_w[t * k + j];
+      }
+      if (j == 0) n_present = __popcll(here);
+    }
+    __syncthreads();
+    k = n_present;
+  } else {
+    if ((int)threadIdx.x < k) {
+      slot_row[threadIdx.x] = inv[t * k + threadIdx.x];
+      slot_w[threadIdx.x] = topk_w[t * k + threadIdx.x];
+    }
+    __syncthreads();
   }
-  __syncthreads();
   constexpr int V = BF16 ? 8 : 4;
   for (int64_t c = c0; c < nchunk; c += cstep) {
     float acc[V];
@@ -101,7 +120,12 @@ __global__ __launch_bounds__(1024) void combine_kernel(const uint4* __restrict__
       }
     }
     uint4 o;
-    if (BF16) {
+    if (BF16 && LOCAL) {
+#if defined(__HIP_DEVICE_COMPILE__)
+      o = make_uint4(cvt_bf16x2(acc[0], acc[1]), cvt_bf16x2(acc[2], acc[3]), cvt_bf16x2(acc[4], acc[5]),
+                     cvt_bf16x2(acc[6], acc[7]));
+#endif
+    } else if (BF16) {
       o = make_uint4(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]),
                      pack_bf16x2(acc[4], acc[5]), pack_bf16x2(acc[6], acc[7]));
     } else {
@@ -128,24 +152,52 @@ __global__ __launch_bounds__(256) void bias_update_kernel(const int32_t* __restr
 
 using namespace moe;
 
-extern "C" moe_status moe_combine(const moe_cfg* cfg, const void* y_perm, const void* y_shared,
-                                  const int32_t* inv, const float* topk_w, void* y, void* stream) {
+namespace {
+
+moe_status combine_check(const moe_cfg* cfg, const void* y_perm, const void* y_shared, const int32_t* inv,
+                         const float* topk_w, const void* y) {
   moe_status st = validate_cfg(cfg);
   if (st != MOE_OK) return st;
   if (!y_perm || !inv || !topk_w || !y) return MOE_ERR_NULL;
   if (cfg->S > 0 && !y_shared) return MOE_ERR_NULL;
+  return MOE_OK;
+}
+
+template <bool LOCAL>
+moe_status combine_launch(const moe_cfg* cfg, const void* y_perm, const void* y_shared, const int32_t* inv,
+                          const float* topk_w, void* y, void* stream) {
   if (cfg->T == 0) return MOE_OK;
   const int64_t nchunk = (int64_t)cfg->H * act_bytes(cfg) / 16;
   const dim3 grid((unsigned)cfg->T);
   const dim3 block((unsigned)std::min<int64_t>(align_up((size_t)nchunk, kWave), 1024));
   const uint4* ysh = cfg->S > 0 ? (const uint4*)y_shared : nullptr;
   if (cfg->act == MOE_F32)
-    hipLaunchKernelGGL((combine_kernel<false>), grid, block, 0, as_stream(stream), (const uint4*)y_perm,
+    hipLaunchKernelGGL((combine_kernel<false, LOCAL>), grid, block, 0, as_stream(stream), (const uint4*)y_perm,
                        ysh, inv, topk_w, cfg->T, cfg->k, nchunk, (uint4*)y);
   else
-    hipLaunchKernelGGL((combine_kernel<true>), grid, block, 0, as_stream(stream), (const uint4*)y_perm,
+    hipLaunchKernelGGL((combine_kernel<true, LOCAL>), grid, block, 0, as_stream(stream), (const uint4*)y_perm,
                        ysh, inv, topk_w, cfg->T, cfg->k, nchunk, (uint4*)y);
   return launch_status();
+}
+
+}  // namespace
+
+extern "C" moe_status moe_combine(const moe_cfg* cfg, const void* y_perm, const void* y_shared,
+                                  const int32_t* inv, const float* topk_w, void* y, void* stream) {
+  const moe_status st = combine_check(cfg, y_perm, y_shared, inv, topk_w, y);
+  return st != MOE_OK ? st : combine_launch<false>(cfg, y_perm, y_shared, inv, topk_w, y, stream);
+}
+
+extern "C" moe_status moe_combine_local(const moe_cfg* cfg, const void* y_perm, const void* y_shared,
+                                        const int32_t* inv, const float* topk_w, void* y, void* stream) {
+  moe_status st = validate_cfg(cfg);
+  if (st != MOE_OK || cfg->T == 0) return st;
+  st = combine_check(cfg, y_perm, y_shared, inv, topk_w, y);
+  if (st != MOE_OK) return st;
+  if (misaligned(y_perm, 16) || (cfg->S > 0 && misaligned(y_shared, 16)) || misaligned(y, 16) || misaligned(inv, 4) ||
+      misaligned(topk_w, 4))
+    return MOE_ERR_UNSUPPORTED;
+  return combine_launch<true>(cfg, y_perm, y_shared, inv, topk_w, y, stream);
 }
 
 extern "C" moe_status moe_update_bias(const moe_cfg* cfg, const int32_t* counts, float* bias, float gamma,

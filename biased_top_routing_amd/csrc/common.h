@@ -58,6 +58,16 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return (uint32_t)f32_to_bf16(lo) | ((uint32_t)f32_to_bf16(hi) << 16);
 }
 
+#if defined(__HIP_DEVICE_COMPILE__)
+// Two floats as packed bf16 by the hardware conversion (v_cvt_pk_bf16_f32: nearest,
+// ties to even; the bits of pack_bf16x2 for numbers, and NaN for every NaN).
+__device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
+  typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+  const bf16x2_t v = {(__bf16)lo, (__bf16)hi};
+  return __builtin_bit_cast(uint32_t, v);
+}
+#endif
+
 // fl32(v / sc) for a scale sc with y = fl32(1 / sc): the product q0 = v * y is
 // within one ulp of the quotient, its remainder v - q0 * sc is exact by FMA, and
 // one correction step q0 + remainder * y then rounds to the correctly rounded

@@ -37,21 +37,39 @@ __device__ __forceinline__ uint64_t same_expert_lanes(int e, bool valid, int nbi
   return m;
 }
 
+// Which pairs of a batch are dispatched.  LOCAL: those of the first *n_tokens
+// tokens (nullptr: all T) whose expert id less `first` lies in [0, E); every
+// other pair is absent.
+struct Window {
+  const int32_t* n_tokens;
+  int first, T, k;
+};
+
+// Pairs [0, limit) belong to live tokens.
+template <bool LOCAL>
+__device__ __forceinline__ int64_t live_pairs(const Window& w, int64_t N) {
+  if (!LOCAL || !w.n_tokens) return N;
+  return (int64_t)min(max(*w.n_tokens, 0), w.T) * w.k;
+}
+
 // The expert ids of segment `seg` held by this lane (pair lo + 64 it + lane),
 // all loaded before any is used; -1 past the last pair.
+template <bool LOCAL>
 __device__ __forceinline__ void load_segment(const int32_t* __restrict__ idx, int64_t seg, int64_t N,
-                                             int (&ev)[kSegPairs / kWave]) {
+                                             const Window& w, int (&ev)[kSegPairs / kWave]) {
   const int lane = threadIdx.x & (kWave - 1);
   const int64_t lo = seg * kSegPairs;
+  const int64_t limit = live_pairs<LOCAL>(w, N);
 #pragma unroll
   for (int it = 0; it < kSegPairs / kWave; ++it) {
     const int64_t f = lo + it * kWave + lane;
-    ev[it] = f < N ? idx[f] : -1;
+    ev[it] = f < limit ? (LOCAL ? (int)((unsigned)idx[f] - (unsigned)w.first) : idx[f]) : -1;
   }
 }
 
+template <bool LOCAL>
 __global__ __launch_bounds__(256) void count_kernel(const int32_t* __restrict__ idx, int64_t N,
-                                                    int E, int nbits, int64_t nseg,
+                                                    int E, int nbits, int64_t nseg, Window win,
                                                     int32_t* __restrict__ segcounts) {
   extern __shared__ int32_t cnt_all[];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
@@ -60,7 +78,7 @@ __global__ __launch_bounds__(256) void count_kernel(const int32_t* __restrict__ 
   for (int e = lane; e < E; e += kWave) cnt[e] = 0;
   __syncthreads();
   int ev[kSegPairs / kWave];
-  load_segment(idx, seg, N, ev);
+  load_segment<LOCAL>(idx, seg, N, win, ev);
 #pragma unroll
   for (int it = 0; it < kSegPairs / kWave; ++it) {
     const bool valid = (unsigned)ev[it] < (unsigned)E;   // (an id outside [0, E) is not counted)
@@ -134,8 +152,9 @@ __global__ __launch_bounds__(1024) void scan_kernel(int32_t* __restrict__ segcou
   if (tid == 0) offsets[0] = 0;
 }
 
+template <bool LOCAL>
 __global__ __launch_bounds__(256) void rank_kernel(const int32_t* __restrict__ idx, int64_t N, int E,
-                                                   int nbits, int64_t nseg,
+                                                   int nbits, int64_t nseg, Window win,
                                                    const int32_t* __restrict__ segprefix,
                                                    const int32_t* __restrict__ offsets,
                                                    int32_t* __restrict__ perm,
@@ -149,7 +168,7 @@ __global__ __launch_bounds__(256) void rank_kernel(const int32_t* __restrict__ i
   __syncthreads();
   const int64_t lo = seg * kSegPairs;
   int ev[kSegPairs / kWave];
-  load_segment(idx, seg, N, ev);
+  load_segment<LOCAL>(idx, seg, N, win, ev);
 #pragma unroll
   for (int it = 0; it < kSegPairs / kWave; ++it) {
     const int64_t f = lo + it * kWave + lane;
@@ -162,6 +181,8 @@ __global__ __launch_bounds__(256) void rank_kernel(const int32_t* __restrict__ i
     if (valid) {
       perm[pos] = (int32_t)f;
       inv[f] = pos;
+    } else if (LOCAL && f < N) {
+      inv[f] = -1;
     }
   }
 }
@@ -170,7 +191,9 @@ __global__ __launch_bounds__(256) void rank_kernel(const int32_t* __restrict__ i
 // k destination rows.  16-byte chunks; CPL chunks per lane per pass.  Plain
 // stores: with x read from HBM (the Infinity Cache flushed before the launch)
 // non-temporal ones were 11% slower, and a training step, which reads the
-// permuted rows back, ran at the same speed with either.
+// permuted rows back, ran at the same speed with either.  LOCAL (here and in the
+// quantising copies below): absent pairs (inv = -1) are skipped, and a token
+// without any present one is not read.
 #ifndef MOE_PERMUTE_NT
 #define MOE_PERMUTE_NT 0
 #endif
@@ -183,7 +206,7 @@ __device__ __forceinline__ void st_stream(uint4* p, uint4 v) {
   *p = v;
 #endif
 }
-template <int CPL>
+template <int CPL, bool LOCAL>
 __global__ __launch_bounds__(256) void permute_rows_kernel(const uint4* __restrict__ src,
                                                            const int32_t* __restrict__ inv, int T,
                                                            int k, int64_t nchunk,
@@ -191,7 +214,8 @@ __global__ __launch_bounds__(256) void permute_rows_kernel(const uint4* __restri
   const int lane = threadIdx.x & 63;
   const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (t >= T) return;
-  const int32_t myp = lane < k ? inv[t * k + lane] : 0;
+  const int32_t myp = lane < k ? inv[t * k + lane] : LOCAL ? -1 : 0;
+  if (LOCAL && !__any(myp >= 0)) return;
   for (int64_t c0 = 0; c0 < nchunk; c0 += (int64_t)CPL * kWave) {
     uint4 v[CPL];
 #pragma unroll
@@ -201,6 +225,7 @@ __global__ __launch_bounds__(256) void permute_rows_kernel(const uint4* __restri
     }
     for (int j = 0; j < k; ++j) {
       const int64_t p = __shfl(myp, j);
+      if (LOCAL && p < 0) continue;
 #pragma unroll
       for (int i = 0; i < CPL; ++i) {
         const int64_t c = c0 + i * kWave + lane;
@@ -237,7 +262,7 @@ __device__ __forceinline__ uint2 quant_chunk_1x128(uint4 raw, float* sc_out) {
 
 // fp8 dispatch: quantise the token's bf16 row per 1x128 tile once, then store
 // the codes and scales to each of its k destination rows.
-template <int CPL>
+template <int CPL, bool LOCAL>
 __global__ __launch_bounds__(256) void permute_rows_fp8_kernel(const uint4* __restrict__ src,
                                                                const int32_t* __restrict__ inv,
                                                                int T, int k, int H,
@@ -247,7 +272,8 @@ __global__ __launch_bounds__(256) void permute_rows_fp8_kernel(const uint4* __re
   const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (t >= T) return;      // whole wavefront exits together
   const int64_t nchunk = H / 8, ntile = H / 128;
-  const int32_t myp = lane < k ? inv[t * k + lane] : 0;
+  const int32_t myp = lane < k ? inv[t * k + lane] : LOCAL ? -1 : 0;
+  if (LOCAL && !__any(myp >= 0)) return;
   for (int64_t c0 = 0; c0 < nchunk; c0 += (int64_t)CPL * kWave) {
     uint2 q[CPL];
     float sc[CPL];
@@ -260,6 +286,7 @@ __global__ __launch_bounds__(256) void permute_rows_fp8_kernel(const uint4* __re
     }
     for (int j = 0; j < k; ++j) {
       const int64_t p = __shfl(myp, j);
+      if (LOCAL && p < 0) continue;
 #pragma unroll
       for (int i = 0; i < CPL; ++i) {
         const int64_t c = c0 + i * kWave + lane;
@@ -275,7 +302,7 @@ __global__ __launch_bounds__(256) void permute_rows_fp8_kernel(const uint4* __re
 // MXFP4 dispatch (format: fp4.h): quantise the token's bf16 row once, then store
 // the codes and the scale words of its 128-column groups to each of its k
 // destination rows (a row's scale words lie ntile planes of T*k words apart).
-template <int CPL>
+template <int CPL, bool LOCAL>
 __global__ __launch_bounds__(256) void permute_rows_fp4_kernel(const uint4* __restrict__ src,
                                                                const int32_t* __restrict__ inv,
                                                                int T, int k, int H,
@@ -286,7 +313,8 @@ __global__ __launch_bounds__(256) void permute_rows_fp4_kernel(const uint4* __re
   const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (t >= T) return;      // whole wavefront exits together
   const int64_t nchunk = H / 8, P = (int64_t)T * k;
-  const int32_t myp = lane < k ? inv[t * k + lane] : 0;
+  const int32_t myp = lane < k ? inv[t * k + lane] : LOCAL ? -1 : 0;
+  if (LOCAL && !__any(myp >= 0)) return;
   for (int64_t c0 = 0; c0 < nchunk; c0 += (int64_t)CPL * kWave) {
     uint32_t q[CPL], sw[CPL];
 #pragma unroll
@@ -300,6 +328,7 @@ __global__ __launch_bounds__(256) void permute_rows_fp4_kernel(const uint4* __re
     }
     for (int j = 0; j < k; ++j) {
       const int64_t p = __shfl(myp, j);
+      if (LOCAL && p < 0) continue;
 #pragma unroll
       for (int i = 0; i < CPL; ++i) {
         const int64_t c = c0 + i * kWave + lane;
@@ -392,9 +421,10 @@ __global__ __launch_bounds__(256) void quantize_blocks_kernel(const bf16_t* __re
 
 // The kernels of moe_dispatch, with the per-segment counts in `segc`
 // (dispatch_segments(cfg) * E int32, no contents required).  Arguments checked.
-static moe_status dispatch_launch(const moe_cfg* cfg, const int32_t* topk_idx, const void* x, int32_t* counts,
-                                  int32_t* offsets, int32_t* perm, int32_t* inv, void* x_perm, float* x_perm_scale,
-                                  int32_t* segc, hipStream_t s) {
+template <bool LOCAL>
+static moe_status dispatch_launch(const moe_cfg* cfg, const Window& win, const int32_t* topk_idx, const void* x,
+                                  int32_t* counts, int32_t* offsets, int32_t* perm, int32_t* inv, void* x_perm,
+                                  float* x_perm_scale, int32_t* segc, hipStream_t s) {
   moe_status st;
   const bool fp8 = cfg->wgt == MOE_FP8_E4M3, fp4 = cfg->wgt == MOE_MXFP4;
   const int64_t N = pairs(cfg);
@@ -406,8 +436,8 @@ static moe_status dispatch_launch(const moe_cfg* cfg, const int32_t* topk_idx, c
   while (Ep2 < E) Ep2 <<= 1;
   const unsigned blocks = (unsigned)((nseg + 3) / 4);
   if (nseg > 0) {
-    hipLaunchKernelGGL(count_kernel, dim3(blocks), dim3(256), 4 * E * sizeof(int32_t), s, topk_idx, N,
-                       E, nbits, nseg, segc);
+    hipLaunchKernelGGL(count_kernel<LOCAL>, dim3(blocks), dim3(256), 4 * E * sizeof(int32_t), s, topk_idx, N,
+                       E, nbits, nseg, win, segc);
     if ((st = launch_status()) != MOE_OK) return st;
   }
   const int P = 1024 / Ep2;
@@ -415,20 +445,20 @@ static moe_status dispatch_launch(const moe_cfg* cfg, const int32_t* topk_idx, c
                      nseg, E, Ep2, counts, offsets);
   if ((st = launch_status()) != MOE_OK) return st;
   if (nseg == 0) return MOE_OK;
-  hipLaunchKernelGGL(rank_kernel, dim3(blocks), dim3(256), 4 * E * sizeof(int32_t), s, topk_idx, N, E,
-                     nbits, nseg, segc, offsets, perm, inv);
+  hipLaunchKernelGGL(rank_kernel<LOCAL>, dim3(blocks), dim3(256), 4 * E * sizeof(int32_t), s, topk_idx, N, E,
+                     nbits, nseg, win, segc, offsets, perm, inv);
   if ((st = launch_status()) != MOE_OK) return st;
   if (!x_perm) return MOE_OK;
   const unsigned tblocks = (unsigned)((cfg->T + 3) / 4);
   if (fp4) {
-    hipLaunchKernelGGL((permute_rows_fp4_kernel<8>), dim3(tblocks), dim3(256), 0, s, (const uint4*)x, inv,
+    hipLaunchKernelGGL((permute_rows_fp4_kernel<8, LOCAL>), dim3(tblocks), dim3(256), 0, s, (const uint4*)x, inv,
                        cfg->T, cfg->k, cfg->H, (uint32_t*)x_perm, (uint32_t*)x_perm_scale);
   } else if (fp8) {
-    hipLaunchKernelGGL((permute_rows_fp8_kernel<8>), dim3(tblocks), dim3(256), 0, s, (const uint4*)x, inv,
+    hipLaunchKernelGGL((permute_rows_fp8_kernel<8, LOCAL>), dim3(tblocks), dim3(256), 0, s, (const uint4*)x, inv,
                        cfg->T, cfg->k, cfg->H, (uint2*)x_perm, x_perm_scale);
   } else {
     const int64_t nchunk = (int64_t)cfg->H * act_bytes(cfg) / 16;
-    hipLaunchKernelGGL((permute_rows_kernel<16>), dim3(tblocks), dim3(256), 0, s, (const uint4*)x, inv,
+    hipLaunchKernelGGL((permute_rows_kernel<16, LOCAL>), dim3(tblocks), dim3(256), 0, s, (const uint4*)x, inv,
                        cfg->T, cfg->k, nchunk, (uint4*)x_perm);
   }
   return launch_status();
@@ -459,8 +489,31 @@ extern "C" moe_status moe_dispatch(const moe_cfg* cfg, const int32_t* topk_idx, 
   if (st != MOE_OK) return st;
   if (!ws) return MOE_ERR_NULL;
   if (ws_bytes < dispatch_ws_bytes(cfg)) return MOE_ERR_WORKSPACE;
-  return dispatch_launch(cfg, topk_idx, x, counts, offsets, perm, inv, x_perm, x_perm_scale,
-                         static_cast<int32_t*>(ws), as_stream(stream));
+  return dispatch_launch<false>(cfg, Window{}, topk_idx, x, counts, offsets, perm, inv, x_perm, x_perm_scale,
+                                static_cast<int32_t*>(ws), as_stream(stream));
+}
+
+extern "C" moe_status moe_dispatch_local(const moe_cfg* cfg, int32_t first_expert, const int32_t* n_tokens,
+                                         const int32_t* topk_idx, const void* x, int32_t* counts, int32_t* offsets,
+                                         int32_t* perm, int32_t* inv, void* x_perm, float* x_perm_scale, void* ws,
+                                         size_t ws_bytes, void* stream) {
+  moe_status st = validate_cfg(cfg);
+  if (st != MOE_OK) return st;
+  if (cfg->T > 0) {   // (an empty batch's tensors may have no address)
+    st = dispatch_check(cfg, topk_idx, x, counts, offsets, perm, inv, x_perm, x_perm_scale);
+    if (st != MOE_OK) return st;
+  } else if (!counts || !offsets) {
+    return MOE_ERR_NULL;
+  }
+  if (first_expert < 0) return MOE_ERR_SHAPE;
+  if (!ws) return MOE_ERR_NULL;
+  if (ws_bytes < dispatch_ws_bytes(cfg)) return MOE_ERR_WORKSPACE;
+  for (const void* q : {(const void*)n_tokens, (const void*)topk_idx, (const void*)counts, (const void*)offsets,
+                        (const void*)perm, (const void*)inv, (const void*)x_perm_scale, (const void*)ws})
+    if (misaligned(q, 4)) return MOE_ERR_UNSUPPORTED;
+  if (x_perm && (misaligned(x, 16) || misaligned(x_perm, 16))) return MOE_ERR_UNSUPPORTED;
+  return dispatch_launch<true>(cfg, Window{n_tokens, first_expert, cfg->T, cfg->k}, topk_idx, x, counts, offsets, perm,
+                               inv, x_perm, x_perm_scale, static_cast<int32_t*>(ws), as_stream(stream));
 }
 
 // ------------------------------------------------ dispatch without a workspace
@@ -500,8 +553,8 @@ extern "C" moe_status moe_dispatch_noalloc(const moe_cfg* cfg, const int32_t* to
   if ((size_t)dispatch_segments(cfg) * cfg->E * sizeof(int32_t) > kDispatchScratchBytes) return MOE_ERR_SCRATCH;
   int32_t* segc = nullptr;
   if ((st = scratch_on_current_device(&segc)) != MOE_OK) return st;
-  return dispatch_launch(cfg, topk_idx, x, counts, offsets, perm, inv, x_perm, x_perm_scale, segc,
-                         as_stream(stream));
+  return dispatch_launch<false>(cfg, Window{}, topk_idx, x, counts, offsets, perm, inv, x_perm, x_perm_scale, segc,
+                                as_stream(stream));
 }
 
 extern "C" moe_status moe_quantize_fp8(const void* src_bf16, int32_t n_mat, int32_t rows, int32_t cols,

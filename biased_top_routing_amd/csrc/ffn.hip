@@ -151,6 +151,7 @@ __global__ __launch_bounds__(256) void gateup_f32_kernel(const float* __restrict
   const int64_t id = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (id >= nrows * hw) return;
   const int64_t row = id / hw;
+  if (offsets && row >= offsets[E]) return;   // behind the last present pair of a share
   const int c = (int)(id % hw);
   const int ex = offsets ? expert_of_row(offsets, E, row) : c / I;
   const int cc = c % I;
@@ -177,6 +178,7 @@ __global__ __launch_bounds__(256) void down_f32_kernel(const float* __restrict__
   const int64_t id = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (id >= nrows * H) return;
   const int64_t row = id / H;
+  if (offsets && row >= offsets[E]) return;   // behind the last present pair of a share
   const int n = (int)(id % H);
   const float* Wb = offsets ? W + (int64_t)expert_of_row(offsets, E, row) * H * I : W;
   const float* hr = h + row * kw;

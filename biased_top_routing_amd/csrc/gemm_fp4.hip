@@ -320,7 +320,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void gemm_fp4_kernel(Fp4Params p) 
 #pragma unroll
       for (int ni = 0; ni < NI; ++ni)
         *reinterpret_cast<uint2*>(stg + (mi * 16 + l16) * STG_PITCH + (ni * 16 + 4 * g) * 2) =
-            uint2{pack_bf16x2(acc[mi][ni][0], acc[mi][ni][1]), pack_bf16x2(acc[mi][ni][2], acc[mi][ni][3])};
+            uint2{cvt_bf16x2(acc[mi][ni][0], acc[mi][ni][1]), cvt_bf16x2(acc[mi][ni][2], acc[mi][ni][3])};
     // (the wavefront reads back only what it wrote; its LDS operations complete in order)
     __builtin_amdgcn_s_waitcnt(kLgkmWaitZero);
     __builtin_amdgcn_wave_barrier();

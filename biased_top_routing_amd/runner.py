@@ -10,6 +10,14 @@ the forward pass keeps the gate and up outputs (moe_expert_ffn_save) and the
 backward pass starts from them (moe_expert_ffn_backward_saved) instead of
 recomputing the gate/up GEMM.  With keep_scores=False, moe_route writes no
 [T, E] affinities (a forward pass that needs no router gradient).
+
+With share=(first, count) the layer holds the routed experts [first, first +
+count) only, as one of several ranks does: the router still ranks all E, and
+dispatch, combine and their gradients take the pairs that fall on its experts
+(moe_dispatch_local and the calls beside it).  forward(n_tokens=...) takes an
+int32 device tensor with the number of live tokens of a padded batch.  Either
+way y (and dx) is this share's sum; the bias update needs the loads of the whole
+batch, so gamma is refused.
 """
 from __future__ import annotations
 
@@ -30,8 +38,16 @@ def to_device(arr, device="cuda"):
 
 
 class MoeLayerGPU:
-    def __init__(self, cfg, weights, T=None, device="cuda", gather=False, save_gu=False, keep_scores=True):
+    def __init__(self, cfg, weights, T=None, device="cuda", gather=False, save_gu=False, keep_scores=True, share=None):
         self.c = cfg
+        self.share = share
+        first, self.n_exp = (0, cfg.E) if share is None else (int(share[0]), int(share[1]))
+        if first < 0 or self.n_exp < cfg.k or first + self.n_exp > cfg.E:
+            raise ValueError(f"share {share} of {cfg.E} experts: needs at least k = {cfg.k} experts inside the layer's")
+        if share is not None and len(weights.w_gate_up) not in (cfg.E, self.n_exp):
+            raise ValueError(f"{len(weights.w_gate_up)} experts' weights for a share of {self.n_exp} of {cfg.E}")
+        held = slice(first, first + self.n_exp) if share is not None and len(weights.w_gate_up) == cfg.E else slice(None)
+        self.n_tokens = None
         self.device = device
         self.gather = gather
         self.save_gu = save_gu
@@ -43,12 +59,12 @@ class MoeLayerGPU:
         self.w_router = dev(weights.w_router)
         self.logit_offset = dev(weights.logit_offset)
         if self.fp8 or self.fp4:
-            self.w_gate_up, self.w_gate_up_scale = self._quantize(weights.w_gate_up)
-            self.w_down, self.w_down_scale = self._quantize(weights.w_down)
+            self.w_gate_up, self.w_gate_up_scale = self._quantize(weights.w_gate_up[held])
+            self.w_down, self.w_down_scale = self._quantize(weights.w_down[held])
             self.ws_gate_up, self.ws_gate_up_scale = self._quantize(weights.ws_gate_up)
             self.ws_down, self.ws_down_scale = self._quantize(weights.ws_down)
         else:
-            self.w_gate_up, self.w_down = dev(weights.w_gate_up), dev(weights.w_down)
+            self.w_gate_up, self.w_down = dev(weights.w_gate_up[held]), dev(weights.w_down[held])
             self.ws_gate_up, self.ws_down = dev(weights.ws_gate_up), dev(weights.ws_down)
             self.w_gate_up_scale = self.w_down_scale = self.ws_gate_up_scale = self.ws_down_scale = None
         self.weights = L.expert_weights(self.w_gate_up, self.w_down, self.ws_gate_up, self.ws_down,
@@ -82,6 +98,8 @@ class MoeLayerGPU:
         c = self.c
         self.T = T
         self.cfg = L.cfg_from(c, T=T)
+        # the experts' configuration: the share's, whose experts form one group
+        self.cfg_x = self.cfg if self.share is None else L.cfg_from(c, T=T, E=self.n_exp, G=1, M=1, group_topr=1)
         d, P = self.device, T * c.k
         f32, i32 = torch.float32, torch.int32
         # the [T, E] affinities (the backward pass reads them); without them moe_route
@@ -90,8 +108,8 @@ class MoeLayerGPU:
         self.ws_route = torch.empty(L.moe_workspace_bytes(self.cfg, L.MOE_WS_ROUTE), dtype=torch.uint8, device=d)
         self.topk_idx = torch.empty((T, c.k), dtype=i32, device=d)
         self.topk_w = torch.empty((T, c.k), dtype=f32, device=d)
-        self.counts = torch.empty(c.E, dtype=i32, device=d)
-        self.offsets = torch.empty(c.E + 1, dtype=i32, device=d)
+        self.counts = torch.empty(self.n_exp, dtype=i32, device=d)
+        self.offsets = torch.empty(self.n_exp + 1, dtype=i32, device=d)
         self.perm = torch.empty(P, dtype=i32, device=d)
         self.inv = torch.empty((T, c.k), dtype=i32, device=d)
         if self.gather:
@@ -108,9 +126,9 @@ class MoeLayerGPU:
         self.y_perm = torch.empty((P, c.H), dtype=self.act_dtype, device=d)
         self.y_shared = torch.empty((T, c.H), dtype=self.act_dtype, device=d) if c.S > 0 else None
         self.y = torch.empty((T, c.H), dtype=self.act_dtype, device=d)
-        self.ws_dispatch = torch.empty(L.moe_workspace_bytes(self.cfg, L.MOE_WS_DISPATCH), dtype=torch.uint8,
+        self.ws_dispatch = torch.empty(L.moe_workspace_bytes(self.cfg_x, L.MOE_WS_DISPATCH), dtype=torch.uint8,
                                        device=d)
-        self.ws_ffn = torch.empty(L.moe_workspace_bytes(self.cfg, L.MOE_WS_FFN), dtype=torch.uint8, device=d)
+        self.ws_ffn = torch.empty(L.moe_workspace_bytes(self.cfg_x, L.MOE_WS_FFN), dtype=torch.uint8, device=d)
         if self.save_gu:
             bf = torch.bfloat16
             self.g = torch.empty((P, c.I), dtype=bf, device=d)
@@ -126,25 +144,38 @@ class MoeLayerGPU:
                     L.MOE_SCORES_IN if scores_in else 0, self.topk_idx, self.topk_w,
                     None if keep else self.ws_route)
 
+    @property
+    def partial(self):
+        """Whether some pairs of the batch may be absent (a share, or a padded batch)."""
+        return self.share is not None or self.n_tokens is not None
+
     def dispatch(self, x):
+        if self.partial:
+            L.moe_dispatch_local(self.cfg_x, 0 if self.share is None else self.share[0], self.n_tokens, self.topk_idx, x,
+                                 self.counts, self.offsets, self.perm, self.inv, self.x_perm, self.x_perm_scale,
+                                 self.ws_dispatch)
+            return
         L.moe_dispatch(self.cfg, self.topk_idx, x, self.counts, self.offsets, self.perm, self.inv, self.x_perm,
                        self.x_perm_scale, self.ws_dispatch)
 
     def expert_ffn(self, x, phase=L.MOE_FFN_ALL):
         if self.save_gu:
-            L.moe_expert_ffn_save(self.cfg, self.x_perm, self.perm, self.offsets, self.weights, x, self.y_perm,
+            L.moe_expert_ffn_save(self.cfg_x, self.x_perm, self.perm, self.offsets, self.weights, x, self.y_perm,
                                   self.y_shared, self.saved, self.ws_ffn, phase)
         elif self.gather:
-            L.moe_expert_ffn_gather(self.cfg, x, self.perm, self.offsets, self.weights, self.y_perm,
+            L.moe_expert_ffn_gather(self.cfg_x, x, self.perm, self.offsets, self.weights, self.y_perm,
                                     self.y_shared, self.ws_ffn, phase)
         else:
-            L.moe_expert_ffn(self.cfg, self.x_perm, self.x_perm_scale, self.offsets, self.weights, x,
+            L.moe_expert_ffn(self.cfg_x, self.x_perm, self.x_perm_scale, self.offsets, self.weights, x,
                              self.y_perm, self.y_shared, self.ws_ffn, phase)
 
     def combine(self):
-        L.moe_combine(self.cfg, self.y_perm, self.y_shared, self.inv, self.topk_w, self.y)
+        combine = L.moe_combine_local if self.partial else L.moe_combine
+        combine(self.cfg_x, self.y_perm, self.y_shared, self.inv, self.topk_w, self.y)
 
     def update_bias(self, bias, gamma):
+        if self.partial:
+            raise ValueError("the bias update needs the loads of a whole batch over every expert")
         L.moe_update_bias(self.cfg, self.counts, bias, gamma)
 
     # ---------------------------------------------------------------- backward
@@ -159,14 +190,14 @@ class MoeLayerGPU:
         self.dx_shared = torch.empty((T, c.H), dtype=bf, device=d) if c.S > 0 else None
         self.dx_router = torch.empty((T, c.H), dtype=f32, device=d)
         self.dx = torch.empty((T, c.H), dtype=bf, device=d)
-        self.g_w_gate_up = torch.empty((c.E, 2 * c.I, c.H), dtype=f32, device=d)
-        self.g_w_down = torch.empty((c.E, c.H, c.I), dtype=f32, device=d)
+        self.g_w_gate_up = torch.empty((self.n_exp, 2 * c.I, c.H), dtype=f32, device=d)
+        self.g_w_down = torch.empty((self.n_exp, c.H, c.I), dtype=f32, device=d)
         self.g_ws_gate_up = torch.empty((c.S, 2 * c.I, c.H), dtype=f32, device=d) if c.S > 0 else None
         self.g_ws_down = torch.empty((c.S, c.H, c.I), dtype=f32, device=d) if c.S > 0 else None
         self.g_w_router = torch.empty((c.E, c.H), dtype=f32, device=d)
         self.loss_bal = torch.empty(1, dtype=f32, device=d)
         self.grads = L.expert_grads(self.g_w_gate_up, self.g_w_down, self.g_ws_gate_up, self.g_ws_down)
-        self.ws_ffn_bwd = torch.empty(L.moe_workspace_bytes(self.cfg, L.MOE_WS_FFN_BWD), dtype=torch.uint8, device=d)
+        self.ws_ffn_bwd = torch.empty(L.moe_workspace_bytes(self.cfg_x, L.MOE_WS_FFN_BWD), dtype=torch.uint8, device=d)
         self.ws_route_bwd = torch.empty(L.moe_workspace_bytes(self.cfg, L.MOE_WS_ROUTE_BWD), dtype=torch.uint8,
                                         device=d)
         self._bwd_T = T
@@ -178,21 +209,29 @@ class MoeLayerGPU:
             raise ValueError("backward reads the permuted rows x_perm: build the layer with gather=False")
         if getattr(self, "_bwd_T", None) != self.T:
             self.alloc_backward()
-        cfg = self.cfg
-        L.moe_combine_backward(cfg, dy, self.y_perm, self.inv, self.topk_w, self.dy_perm, self.d_topk_w)
+        if self.n_tokens is not None and alpha:
+            raise ValueError("the balance loss counts every token of the batch: alpha has to be 0 for a padded one")
+        cfg = self.cfg_x
+        combine_backward = L.moe_combine_local_backward if self.partial else L.moe_combine_backward
+        dispatch_backward = L.moe_dispatch_local_backward if self.partial else L.moe_dispatch_backward
+        combine_backward(cfg, dy, self.y_perm, self.inv, self.topk_w, self.dy_perm, self.d_topk_w)
         if self.save_gu:
             L.moe_expert_ffn_backward_saved(cfg, self.x_perm, x, self.offsets, self.weights, self.saved, self.dy_perm,
                                             dy, self.dx_perm, self.dx_shared, self.grads, self.ws_ffn_bwd)
         else:
             L.moe_expert_ffn_backward(cfg, self.x_perm, x, self.offsets, self.weights, self.dy_perm, dy,
                                       self.dx_perm, self.dx_shared, self.grads, self.ws_ffn_bwd)
-        L.moe_route_backward(cfg, x, self.w_router, self.scores, self.topk_idx, self.d_topk_w, alpha, seq_len,
+        L.moe_route_backward(self.cfg, x, self.w_router, self.scores, self.topk_idx, self.d_topk_w, alpha, seq_len,
                              self.dx_router, self.g_w_router, self.loss_bal, self.ws_route_bwd)
-        L.moe_dispatch_backward(cfg, self.dx_perm, self.dx_shared, self.dx_router, self.inv, self.dx)
+        dispatch_backward(cfg, self.dx_perm, self.dx_shared, self.dx_router, self.inv, self.dx)
         return self.dx
 
-    def forward(self, x, bias, gamma=None, scores_in=False):
-        """One batch through the layer; with gamma set, bias is updated in place afterwards."""
+    def forward(self, x, bias, gamma=None, scores_in=False, n_tokens=None):
+        """One batch through the layer; with gamma set, bias is updated in place afterwards.
+        n_tokens: int32 device tensor of one element, the live tokens of a padded batch."""
+        if gamma is not None and (self.share is not None or n_tokens is not None):
+            raise ValueError("the bias update needs the loads of a whole batch over every expert")
+        self.n_tokens = n_tokens
         self.route(x, bias, scores_in)
         self.dispatch(x)
         self.expert_ffn(x)
@@ -202,9 +241,9 @@ class MoeLayerGPU:
         return self.y
 
     # ---------------------------------------------------------------- HIP graph
-    def capture(self, x, bias, gamma=None):
+    def capture(self, x, bias, gamma=None, n_tokens=None):
         """Record one forward() over the tensors x and bias (and the bias update when
-        gamma is set) into a HIP graph; replay() reruns it on whatever they then hold.
+        gamma is set) into a HIP graph; replay() reruns it on whatever they (and n_tokens) then hold.
         One graph serves every batch of this T: each launch is sized by capacity (the
         grouped GEMMs' tile tables are built on the device from the batch's routing)
         and no call allocates, copies or synchronises, so the recorded work is the
@@ -213,12 +252,12 @@ class MoeLayerGPU:
         side = torch.cuda.Stream()
         side.wait_stream(torch.cuda.current_stream())
         with torch.cuda.stream(side):
-            self.forward(x, bias, None)
+            self.forward(x, bias, None, n_tokens=n_tokens)
         torch.cuda.current_stream().wait_stream(side)
         self.graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(self.graph):
-            self.forward(x, bias, gamma)
-        self.graph_inputs = (x, bias)
+            self.forward(x, bias, gamma, n_tokens=n_tokens)
+        self.graph_inputs = (x, bias, n_tokens)
         return self.graph
 
     def replay(self):

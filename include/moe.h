@@ -359,6 +359,74 @@ moe_status moe_quantize_fp4(const void* src_bf16, int32_t n_mat, int32_t rows, i
 moe_status moe_dequantize_fp4(const uint8_t* codes, const uint8_t* scales, int32_t n_mat, int32_t rows,
                               int32_t cols, void* dst_bf16, void* stream);
 
+/* -------------------------------------------------------------- share of a batch
+ * The dispatch and combine of a rank that holds some of the experts, and of a
+ * batch padded to a fixed size (a HIP graph's): some (token, slot) pairs are
+ * absent.  cfg describes the share: E the experts held (G, M, group_topr such
+ * that the configuration is valid, e.g. 1, 1, 1; k <= E), T and k the batch's.
+ *   moe_dispatch_local -> moe_expert_ffn* (cfg of the share) -> moe_combine_local
+ * and, for a training step,
+ *   moe_combine_local_backward -> moe_expert_ffn_backward* ->
+ *   moe_route_backward (cfg of the router) -> moe_dispatch_local_backward
+ * The outputs of all ranks' shares (y, and dx and d_topk_w) sum to the whole
+ * layer's when the shared experts and the router term are given to one of them.
+ * With T == 0 tensors without elements may be NULL in these four calls.
+ * moe_update_bias compares with T*k pairs over cfg's E experts: it is for whole
+ * batches, with the counts of every share together.
+ *
+ * Follows: experts spread over the GPUs, every GPU running the tokens routed to
+ * its own (DeepSeek-V3 Technical Report：中英对照解读, §2.2; qwbw.cn essay,
+ * deployment section).
+ */
+
+/*
+ * moe_dispatch_local - moe_dispatch of the present pairs: pair (t, j) is present
+ * when t < *n_tokens and first_expert <= topk_idx[t, j] < first_expert + E (its
+ * expert in the share is topk_idx[t, j] - first_expert).  Any other value of
+ * topk_idx, negative ones included, makes the pair absent.
+ *
+ *  first_expert  >= 0 (MOE_ERR_SHAPE otherwise)
+ *  n_tokens  device pointer to one int32, the live tokens of the batch (taken as
+ *            0 when negative and as T when larger), or NULL: all T
+ *  counts, offsets  over the present pairs (offsets[E] of them)
+ *  perm      flat pair ids t*k + j of the present pairs, stably sorted by expert
+ *  inv       [T, k]: row of a present pair, -1 for an absent one
+ *  x_perm, x_perm_scale  the rows of the present pairs; may be NULL as for
+ *            moe_dispatch
+ *  perm, x_perm and x_perm_scale behind the last present pair stay as they were.
+ * The other arguments and errors are moe_dispatch's; results with every pair
+ * present are equal to its, bit for bit.  Rows must be 16-byte aligned, the rest
+ * 4-byte (MOE_ERR_UNSUPPORTED; so for the three calls below).
+ */
+moe_status moe_dispatch_local(const moe_cfg* cfg, int32_t first_expert, const int32_t* n_tokens,
+                              const int32_t* topk_idx, const void* x, int32_t* counts, int32_t* offsets,
+                              int32_t* perm, int32_t* inv, void* x_perm, float* x_perm_scale, void* ws,
+                              size_t ws_bytes, void* stream);
+
+/*
+ * moe_combine_local - moe_combine over the present slots (inv >= 0): a token
+ * without any gets y_shared[t] alone, or zero when S == 0.  Gates and rows of
+ * absent slots are not read.
+ */
+moe_status moe_combine_local(const moe_cfg* cfg, const void* y_perm, const void* y_shared,
+                             const int32_t* inv, const float* topk_w, void* y, void* stream);
+
+/*
+ * moe_combine_local_backward - moe_combine_backward over the present slots:
+ * dy_perm of the present pairs (rows behind the last stay as they were), and
+ * d_topk_w with 0 for absent slots.  bf16 only.
+ */
+moe_status moe_combine_local_backward(const moe_cfg* cfg, const void* dy, const void* y_perm,
+                                      const int32_t* inv, const float* topk_w, void* dy_perm,
+                                      float* d_topk_w, void* stream);
+
+/*
+ * moe_dispatch_local_backward - moe_dispatch_backward over the present slots:
+ * dx[t] = sum of dx_perm over them + dx_shared[t] + dx_router[t].  bf16 only.
+ */
+moe_status moe_dispatch_local_backward(const moe_cfg* cfg, const void* dx_perm, const void* dx_shared,
+                                       const float* dx_router, const int32_t* inv, void* dx, void* stream);
+
 /* ------------------------------------------------------------------ backward
  * The gradient of one layer pass (the training step the bias rule lives in),
  * for act = wgt = BF16 (other dtypes: MOE_ERR_UNSUPPORTED).  With the expert
