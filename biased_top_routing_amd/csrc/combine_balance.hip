@@ -58,9 +58,7 @@ __device__ __forceinline__ void accum_chunk(float* acc, uint4 r, float g) {
 
 constexpr int kMaxCombineK = 32;   // validate_cfg bounds k
 
-// LOCAL: absent slots (inv = -1) take no part; the present ones are gathered in
-// slot order first, so a token costs the rows it has.
-template <bool BF16, bool LOCAL>
+template <bool BF16>
 __global__ __launch_bounds__(1024) void combine_kernel(const uint4* __restrict__ y_perm,
                                                       const uint4* __restrict__ y_shared,
                                                       const int32_t* __restrict__ inv,
@@ -77,28 +75,11 @@ __global__ __launch_bounds__(1024) void combine_kernel(const uint4* __restrict__
   const int64_t t = blockIdx.x;          // the whole workgroup on one token
   const int c0 = threadIdx.x, cstep = blockDim.x;
   if (t >= T) return;
-  if constexpr (LOCAL) {
-    __shared__ int n_present;
-    if (threadIdx.x < kWave) {               // the first wavefront (k <= 32 of its lanes hold a slot)
-      const int j = threadIdx.x;
-      const int32_t p = j < k ? inv[t * k + j] : -1;
-      const uint64_t here = __ballot(p >= 0);
-      if (p >= 0) {
-        const int at = __popcll(here & ~(~0ull << j));
-        slot_row[at] = p;
-        slot_w[at] = topk_w[t * k + j];
-      }
-      if (j == 0) n_present = __popcll(here);
-    }
-    __syncthreads();
-    k = n_present;
-  } else {
-    if ((int)threadIdx.x < k) {
-      slot_row[threadIdx.x] = inv[t * k + threadIdx.x];
-      slot_w[threadIdx.x] = topk_w[t * k + threadIdx.x];
-    }
-    __syncthreads();
+  if ((int)threadIdx.x < k) {
+    slot_row[threadIdx.x] = inv[t * k + threadIdx.x];
+    slot_w[threadIdx.x] = topk_w[t * k + threadIdx.x];
   }
+  __syncthreads();
   constexpr int V = BF16 ? 8 : 4;
   for (int64_t c = c0; c < nchunk; c += cstep) {
     float acc[V];
@@ -120,12 +101,7 @@ __global__ __launch_bounds__(1024) void combine_kernel(const uint4* __restrict__
       }
     }
     uint4 o;
-    if (BF16 && LOCAL) {
-#if defined(__HIP_DEVICE_COMPILE__)
-      o = make_uint4(cvt_bf16x2(acc[0], acc[1]), cvt_bf16x2(acc[2], acc[3]), cvt_bf16x2(acc[4], acc[5]),
-                     cvt_bf16x2(acc[6], acc[7]));
-#endif
-    } else if (BF16) {
+    if (BF16) {
       o = make_uint4(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]),
                      pack_bf16x2(acc[4], acc[5]), pack_bf16x2(acc[6], acc[7]));
     } else {
@@ -134,6 +110,66 @@ __global__ __launch_bounds__(1024) void combine_kernel(const uint4* __restrict__
     }
     st_stream(&y[t * nchunk + c], o);
   }
+}
+
+// The combine of a share: absent slots (inv = -1) take no part, and a token costs
+// the rows it has, often none or one.  With so little to read per token the
+// kernel is bound by how many tokens are in flight: up to 512 lanes a token, each
+// with the loads of 2 chunks out at once (T = 16384, H = 7168, an eighth of the
+// experts: 81 us, 5.7 TB/s, against 162 us with the whole batch's 896 lanes a
+// token; 128 or 256 lanes with 2 to 7 chunks 84-88 us).
+constexpr int kCombineLocalLanes = 512, kCombineLocalU = 2;
+template <bool BF16>
+__global__ __launch_bounds__(kCombineLocalLanes) void combine_local_kernel(
+    const uint4* __restrict__ y_perm, const uint4* __restrict__ y_shared, const int32_t* __restrict__ inv,
+    const float* __restrict__ topk_w, int k, int64_t nchunk, uint4* __restrict__ y) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  constexpr int U = kCombineLocalU, V = BF16 ? 8 : 4;
+  const int TH = blockDim.x;
+  const int64_t t = blockIdx.x;
+  // every wavefront finds the present slots for itself: lane j holds slot j (k <= 32)
+  const int j = threadIdx.x & 63;
+  const int32_t p = j < k ? inv[t * k + j] : -1;
+  const float w = p >= 0 ? topk_w[t * k + j] : 0.f;
+  const uint64_t here = __ballot(p >= 0);
+  for (int64_t c0 = threadIdx.x & ~63; c0 < nchunk; c0 += U * TH) {   // (whole wavefronts)
+    float acc[U][V];
+    uint4 r[U];
+    int64_t c[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      c[u] = min(c0 + u * TH + j, nchunk - 1);          // past the end: the last chunk again, not stored
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[u][i] = 0.f;
+    }
+    if (y_shared) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) r[u] = ld_stream(&y_shared[t * nchunk + c[u]]);
+#pragma unroll
+      for (int u = 0; u < U; ++u) accum_chunk<BF16>(acc[u], r[u], 1.0f);
+    }
+    for (uint64_t left = here; left; left &= left - 1) {
+      const int s = __builtin_ctzll(left);
+      const int64_t row = __builtin_amdgcn_readlane(p, s);
+      const float g = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), s));
+#pragma unroll
+      for (int u = 0; u < U; ++u) r[u] = ld_stream(&y_perm[row * nchunk + c[u]]);
+#pragma unroll
+      for (int u = 0; u < U; ++u) accum_chunk<BF16>(acc[u], r[u], g);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (c0 + u * TH + j >= nchunk) continue;
+      const float* a = acc[u];
+      uint4 o;
+      if constexpr (BF16)
+        o = make_uint4(cvt_bf16x2(a[0], a[1]), cvt_bf16x2(a[2], a[3]), cvt_bf16x2(a[4], a[5]), cvt_bf16x2(a[6], a[7]));
+      else
+        o = make_uint4(__float_as_uint(a[0]), __float_as_uint(a[1]), __float_as_uint(a[2]), __float_as_uint(a[3]));
+      st_stream(&y[t * nchunk + c[u]], o);
+    }
+  }
+#endif
 }
 
 // One thread per expert; fp32 adds with round-to-nearest-even.
@@ -163,29 +199,24 @@ moe_status combine_check(const moe_cfg* cfg, const void* y_perm, const void* y_s
   return MOE_OK;
 }
 
-template <bool LOCAL>
-moe_status combine_launch(const moe_cfg* cfg, const void* y_perm, const void* y_shared, const int32_t* inv,
-                          const float* topk_w, void* y, void* stream) {
+}  // namespace
+
+extern "C" moe_status moe_combine(const moe_cfg* cfg, const void* y_perm, const void* y_shared,
+                                  const int32_t* inv, const float* topk_w, void* y, void* stream) {
+  const moe_status st = combine_check(cfg, y_perm, y_shared, inv, topk_w, y);
+  if (st != MOE_OK) return st;
   if (cfg->T == 0) return MOE_OK;
   const int64_t nchunk = (int64_t)cfg->H * act_bytes(cfg) / 16;
   const dim3 grid((unsigned)cfg->T);
   const dim3 block((unsigned)std::min<int64_t>(align_up((size_t)nchunk, kWave), 1024));
   const uint4* ysh = cfg->S > 0 ? (const uint4*)y_shared : nullptr;
   if (cfg->act == MOE_F32)
-    hipLaunchKernelGGL((combine_kernel<false, LOCAL>), grid, block, 0, as_stream(stream), (const uint4*)y_perm,
+    hipLaunchKernelGGL((combine_kernel<false>), grid, block, 0, as_stream(stream), (const uint4*)y_perm,
                        ysh, inv, topk_w, cfg->T, cfg->k, nchunk, (uint4*)y);
   else
-    hipLaunchKernelGGL((combine_kernel<true, LOCAL>), grid, block, 0, as_stream(stream), (const uint4*)y_perm,
+    hipLaunchKernelGGL((combine_kernel<true>), grid, block, 0, as_stream(stream), (const uint4*)y_perm,
                        ysh, inv, topk_w, cfg->T, cfg->k, nchunk, (uint4*)y);
   return launch_status();
-}
-
-}  // namespace
-
-extern "C" moe_status moe_combine(const moe_cfg* cfg, const void* y_perm, const void* y_shared,
-                                  const int32_t* inv, const float* topk_w, void* y, void* stream) {
-  const moe_status st = combine_check(cfg, y_perm, y_shared, inv, topk_w, y);
-  return st != MOE_OK ? st : combine_launch<false>(cfg, y_perm, y_shared, inv, topk_w, y, stream);
 }
 
 extern "C" moe_status moe_combine_local(const moe_cfg* cfg, const void* y_perm, const void* y_shared,
@@ -197,7 +228,16 @@ extern "C" moe_status moe_combine_local(const moe_cfg* cfg, const void* y_perm, 
   if (misaligned(y_perm, 16) || (cfg->S > 0 && misaligned(y_shared, 16)) || misaligned(y, 16) || misaligned(inv, 4) ||
       misaligned(topk_w, 4))
     return MOE_ERR_UNSUPPORTED;
-  return combine_launch<true>(cfg, y_perm, y_shared, inv, topk_w, y, stream);
+  const int64_t nchunk = (int64_t)cfg->H * act_bytes(cfg) / 16;
+  const uint4* ysh = cfg->S > 0 ? (const uint4*)y_shared : nullptr;
+  const int64_t lanes = std::min<int64_t>(align_up((size_t)nchunk, kWave), kCombineLocalLanes);
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)cfg->T), dim3((unsigned)lanes), 0, as_stream(stream),
+                       (const uint4*)y_perm, ysh, inv, topk_w, cfg->k, nchunk, (uint4*)y);
+  };
+  if (cfg->act == MOE_F32) go(combine_local_kernel<false>);
+  else go(combine_local_kernel<true>);
+  return launch_status();
 }
 
 extern "C" moe_status moe_update_bias(const moe_cfg* cfg, const int32_t* counts, float* bias, float gamma,

@@ -419,6 +419,132 @@ __global__ __launch_bounds__(256) void quantize_blocks_kernel(const bf16_t* __re
   if (threadIdx.x == 0) scales[(mat * nbr + br) * nbc + bc] = sc;
 }
 
+// ---- a small share in one launch
+// Row formats of the copy.
+enum { kRowsCopy = 0, kRowsFp8 = 1, kRowsFp4 = 2, kRowsNone = 3 };
+
+// Workgroup t < T does token t, workgroup T the counts.  A pair's row is the
+// number of pairs that come before it, ordered by (expert, pair id): with the
+// key expert * N + f of every pair, absent ones last, the keys below its own.
+// Every workgroup holds all N <= kSmallPairs keys in its registers, kSmallPer a
+// lane, and counts by ballot: k * kSmallPer compares a wavefront (8 slots: 128).
+// That repeats the counting T times, and saves the three launches that compute
+// it once (T = 128, k = 8, H = 7168: see the launcher).
+constexpr int kSmallThreads = 256, kSmallPer = 16, kSmallPairs = kSmallThreads * kSmallPer;
+
+template <int ROWS>
+__global__ __launch_bounds__(kSmallThreads) void dispatch_small_kernel(
+    const int32_t* __restrict__ idx, const uint4* __restrict__ x, int N, int E, int64_t nchunk, Window win,
+    int32_t* __restrict__ counts, int32_t* __restrict__ offsets, int32_t* __restrict__ perm, int32_t* __restrict__ inv,
+    void* __restrict__ x_perm, void* __restrict__ x_scale) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int k = win.k, limit = (int)live_pairs<true>(win, N);
+  const uint32_t absent = (uint32_t)E * (uint32_t)N;   // E <= 512, N <= 4096: below 2^31
+  auto key = [&](int f) {
+    const uint32_t e = f < limit ? (uint32_t)idx[f] - (uint32_t)win.first : ~0u;
+    return e < (uint32_t)E ? e * (uint32_t)N + (uint32_t)f : absent;
+  };
+  if ((int)blockIdx.x == win.T) {                       // counts and offsets
+    __shared__ int32_t cnt[512];
+    for (int e = tid; e < 512; e += kSmallThreads) cnt[e] = 0;
+    __syncthreads();
+    for (int f = tid; f < N; f += kSmallThreads) {
+      const uint32_t q = key(f);
+      if (q < absent) atomicAdd(&cnt[q / (uint32_t)N], 1);   // (integer counts: the order does not matter)
+    }
+    __syncthreads();
+    const int c0 = cnt[tid], c1 = cnt[tid + 256];
+    for (int d = 1; d < 512; d <<= 1) {                 // inclusive scan, two entries a thread
+      const int v0 = tid >= d ? cnt[tid - d] : 0, v1 = tid + 256 >= d ? cnt[tid + 256 - d] : 0;
+      __syncthreads();
+      cnt[tid] += v0;
+      cnt[tid + 256] += v1;
+      __syncthreads();
+    }
+    if (tid == 0) offsets[0] = 0;
+    if (tid < E) counts[tid] = c0, offsets[tid + 1] = cnt[tid];
+    if (tid + 256 < E) counts[tid + 256] = c1, offsets[tid + 257] = cnt[tid + 256];
+    return;
+  }
+  const int64_t t = blockIdx.x;
+  __shared__ int32_t below[4][32];
+  __shared__ int32_t dest[32];
+  uint32_t q[kSmallPer];
+#pragma unroll
+  for (int i = 0; i < kSmallPer; ++i) {
+    const int f = tid + i * kSmallThreads;
+    q[i] = f < N ? key(f) : absent;
+  }
+  for (int j = 0; j < k; ++j) {
+    const uint32_t mine = key((int)t * k + j);
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < kSmallPer; ++i) n += __popcll(__ballot(q[i] < mine));
+    if (lane == 0) below[wave][j] = mine < absent ? n : -1;
+  }
+  __syncthreads();
+  if (tid < k) {
+    const int f = (int)t * k + tid;
+    int32_t p = -1;
+    if (below[0][tid] >= 0) {
+      p = below[0][tid] + below[1][tid] + below[2][tid] + below[3][tid];
+      perm[p] = f;
+    }
+    inv[f] = p;
+    dest[tid] = p;
+  }
+  if constexpr (ROWS == kRowsNone) return;
+  __syncthreads();
+  bool any = false;
+  for (int j = 0; j < k; ++j) any |= dest[j] >= 0;
+  if (!any) return;
+  for (int64_t c0 = 0; c0 < nchunk; c0 += kSmallThreads) {
+    const int64_t c = c0 + tid;
+    // (quantised rows: a 16-lane group of 128 columns is wholly inside or outside the row)
+    const uint4 v = c < nchunk ? x[t * nchunk + c] : make_uint4(0, 0, 0, 0);
+    uint2 w8;
+    float sc;
+    uint32_t w4, sw;
+    if constexpr (ROWS == kRowsFp8) w8 = quant_chunk_1x128(v, &sc);
+    if constexpr (ROWS == kRowsFp4) {
+      uint32_t e;
+      w4 = mx_quant_chunk(v, &e);
+      sw = mx_scale_word(e);
+    }
+    for (int j = 0; j < k; ++j) {
+      const int64_t p = dest[j];
+      if (p < 0 || c >= nchunk) continue;
+      if constexpr (ROWS == kRowsCopy) static_cast<uint4*>(x_perm)[p * nchunk + c] = v;
+      if constexpr (ROWS == kRowsFp8) {
+        static_cast<uint2*>(x_perm)[p * nchunk + c] = w8;
+        if ((lane & 15) == 0) static_cast<float*>(x_scale)[p * (nchunk / 16) + c / 16] = sc;
+      }
+      if constexpr (ROWS == kRowsFp4) {
+        static_cast<uint32_t*>(x_perm)[p * nchunk + c] = w4;
+        if ((lane & 15) == 0) static_cast<uint32_t*>(x_scale)[c / 16 * N + p] = sw;
+      }
+    }
+  }
+#endif
+}
+
+static moe_status dispatch_small(const moe_cfg* cfg, const Window& win, const int32_t* topk_idx, const void* x,
+                                 int32_t* counts, int32_t* offsets, int32_t* perm, int32_t* inv, void* x_perm,
+                                 float* x_perm_scale, hipStream_t s) {
+  const int64_t nchunk = (int64_t)cfg->H * act_bytes(cfg) / 16;
+  const int N = (int)pairs(cfg);
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)cfg->T + 1), dim3(kSmallThreads), 0, s, topk_idx, (const uint4*)x, N,
+                       cfg->E, nchunk, win, counts, offsets, perm, inv, x_perm, (void*)x_perm_scale);
+  };
+  if (!x_perm) go(dispatch_small_kernel<kRowsNone>);
+  else if (cfg->wgt == MOE_MXFP4) go(dispatch_small_kernel<kRowsFp4>);
+  else if (cfg->wgt == MOE_FP8_E4M3) go(dispatch_small_kernel<kRowsFp8>);
+  else go(dispatch_small_kernel<kRowsCopy>);
+  return launch_status();
+}
+
 // The kernels of moe_dispatch, with the per-segment counts in `segc`
 // (dispatch_segments(cfg) * E int32, no contents required).  Arguments checked.
 template <bool LOCAL>
@@ -512,7 +638,10 @@ extern "C" moe_status moe_dispatch_local(const moe_cfg* cfg, int32_t first_exper
                         (const void*)perm, (const void*)inv, (const void*)x_perm_scale, (const void*)ws})
     if (misaligned(q, 4)) return MOE_ERR_UNSUPPORTED;
   if (x_perm && (misaligned(x, 16) || misaligned(x_perm, 16))) return MOE_ERR_UNSUPPORTED;
-  return dispatch_launch<true>(cfg, Window{n_tokens, first_expert, cfg->T, cfg->k}, topk_idx, x, counts, offsets, perm,
+  const Window win{n_tokens, first_expert, cfg->T, cfg->k};
+  if (pairs(cfg) <= kSmallPairs)
+    return dispatch_small(cfg, win, topk_idx, x, counts, offsets, perm, inv, x_perm, x_perm_scale, as_stream(stream));
+  return dispatch_launch<true>(cfg, win, topk_idx, x, counts, offsets, perm,
                                inv, x_perm, x_perm_scale, static_cast<int32_t*>(ws), as_stream(stream));
 }
 

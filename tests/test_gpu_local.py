@@ -72,6 +72,8 @@ CASES = [
     (700, 320, 40, 13, 27, 6, 699),
     (1100, 128, 64, 0, 64, 2, -3),
     (5000, 64, 256, 0, 256, 8, 4001),
+    (512, 128, 512, 0, 512, 8, 512),       # 4096 pairs: the last that one launch sorts
+    (513, 128, 512, 5, 300, 8, 500),
     (130, 8320, 512, 100, 300, 32, 77),
 ]
 
