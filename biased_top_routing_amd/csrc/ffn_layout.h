@@ -128,7 +128,10 @@ struct TileDesc {
 constexpr int kStripeGateUp = 8;
 constexpr int kStripeDown = 0;
 constexpr int kStripeFp8 = 2;
-constexpr int kStripeFp4 = 2;
+#ifndef SFP4
+#define SFP4 2
+#endif
+constexpr int kStripeFp4 = SFP4;
 
 // Position j of XCD xcd in runs of P consecutive entries dealt to the 8 XCDs in turn.
 __host__ __device__ inline int xcd_run_index(int j, int xcd, int P) {

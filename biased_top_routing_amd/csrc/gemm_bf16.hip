@@ -550,7 +550,7 @@ __global__ __launch_bounds__(64 * WM * WN) void router_topk_kernel(GemmParams p)
 }
 
 // CUs of the device current at the first call (a thread-safe one-time query).
-static int cu_count() {
+int cu_count() {
   static const int n_cu = [] {
     int dev = 0, n = 0;
     if (hipGetDevice(&dev) != hipSuccess || hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) !=

@@ -11,18 +11,33 @@
 //            the epilogue from the fp32 accumulators (one rounding, to E2M1)
 //   down     Y = h W_d^T, stored as bf16
 //
-// Tiling: a workgroup of WM x WN wavefronts computes a (WM*MI*16) x (WN*64)
-// tile; each wavefront owns MI x 4 MFMA blocks.  K advances 256 elements (128
-// bytes of codes) per slice through a ring of LDS stages filled by direct-to-LDS
-// buffer loads (16-byte chunks, XOR swizzle per row), the rows' scale words of
-// the slice's two 128-wide steps beside them.  K is a multiple of 128: the last
-// slice of an odd number of steps runs its first step only (its second half
-// holds bytes of the next row or nothing, and is not read).  The shared experts'
-// down GEMM walks the experts one after the other, each with its own slices.
-// The gate/up tile's 256 weight rows are the 128 gate rows and the 128 up rows
-// of 128 h columns; a wavefront holds gate and up of 32 of them, one scale block.
+//
+// Large batches: 256 x 256 tiles, one workgroup of 2 x 4 wavefronts a CU, each
+// wavefront 8 x 4 MFMA blocks, and the workgroups stay: each takes every 32nd tile
+// of its XCD's contiguous share of the table (one expert's tiles run on one XCD
+// at the same time and meet in its L2), and the loads run through the tiles
+// without a break.  K advances one 128-wide step (64 bytes of codes a row) per
+// slice through a ring of 4 LDS stages filled by direct-to-LDS buffer loads
+// (16-byte chunks, XOR swizzle per row), the rows' scale words of the step beside
+// them; when a tile's last slices are multiplied, the next tile's first ones are
+// on their way, and its epilogue runs over them.  A 4-bit MFMA takes half the time
+// of an 8-bit one on the same operand bytes, so the fragment reads are kept ahead
+// of it: a wavefront reads the token rows' fragments 3 blocks before their MFMAs
+// and the next slice's first ones under the current slice's last (each barrier
+// therefore covers the slice after the one it opens).
+//
+// Few rows per expert: 32 x 256 tiles that stream the weights, one workgroup of
+// 4 wavefronts per tile, two K steps (128 bytes a row: whole cache lines) per
+// slice and 4 stages.
+//
+// The shared experts' down GEMM walks the experts one after the other.  The
+// gate/up tile's 256 weight rows are the 128 gate rows and the 128 up rows of 128
+// h columns; a wavefront holds gate and up of 32 of them, one scale block.
 // All LDS is one array: with several LDS objects the compiler makes every LDS
 // read wait for the direct-to-LDS loads in flight.
+#include <algorithm>
+#include <type_traits>
+
 #include "common.h"
 #include "ffn_layout.h"
 #include "fp4.h"
@@ -58,7 +73,14 @@ struct Fp4Params {
   int T, H, E, S, I, k;
 };
 
+constexpr int kHPitch = 64 + 16;         // a tile row's 64 bytes of h codes in LDS
+constexpr int kYPitch = 64 * 2 + 16;     // 64 bf16 columns of a row in LDS
+
 #if defined(__HIP_DEVICE_COMPILE__)
+constexpr int NI4 = 4;          // MFMA column blocks of a wavefront
+constexpr int kDrop = 0x7FFFFFFF;   // a byte offset past every descriptor: the range check drops the load
+typedef __attribute__((address_space(3))) void lds_void_t;
+
 // 16 code bytes (32 elements of K) of an LDS row; a 4-bit operand fills the first half of the MFMA's registers.
 __device__ __forceinline__ i32x8_t frag4(const uint8_t* p) {
   const i32x4v_t a = *reinterpret_cast<const i32x4v_t*>(p);
@@ -69,284 +91,560 @@ __device__ __forceinline__ f32x4_t mfma_fp4(i32x8_t w, i32x8_t a, f32x4_t c, int
   constexpr int kE2M1 = 4;   // operand format selector
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, c, kE2M1, kE2M1, 0, sw, 0, sa);
 }
+
+// Waits until at most min(n, MAX) slices' loads (PER instructions each) of this wavefront are outstanding.
+template <int PER, int MAX>
+__device__ __forceinline__ void wait_loads(int n) {
+  static_assert(PER * MAX < 64, "vmcnt range");
+  if constexpr (MAX == 0) wait_vm<0>();
+  else if (n >= MAX) wait_vm<PER * MAX>();
+  else wait_loads<PER, MAX - 1>(n);
+}
+
+// Entry L of the tile table, read through the scalar cache.
+__device__ __forceinline__ TileDesc tile_at(const Fp4Params& p, int L) {
+  typedef const __attribute__((address_space(4))) int32_t* cptr;
+  const cptr t = (cptr)(uintptr_t)(p.tiles + L);
+  return TileDesc{t[0], t[1], t[2], t[3]};
+}
+
+// One tile's operands (all wavefront-uniform).
+template <int MODE>
+struct Operands4 {
+  const uint8_t *A, *SA, *W, *SW;
+  int lda, ldw;                 // bytes between rows
+  int a_rows;                   // rows the A descriptor covers
+  int a_bytes, w_bytes, sa_bytes, sw_bytes;
+  int sa_stride, sw_stride;     // bytes between the scale planes of K steps
+  int64_t w_one;                // one expert's weights and scale words, bytes
+  int sw_one;
+  int nk1, nexp;                // 128-wide K steps of one expert; experts whose K ranges follow each other
+  int ncols;                    // output columns of the segment
+  int ex, c0;                   // the tile's expert among the shared ones, and its first weight row there
+  bool shared, gather;
+
+  __device__ __forceinline__ Operands4(const Fp4Params& p, const TileDesc& d) {
+    shared = d.seg == p.E;
+    // routed gate/up rows gathered from the quantised x: row row0 + r of the
+    // expert-sorted order is token perm[row0 + r] / k (codes and scales)
+    gather = MODE == kGateUp4 && !shared && p.perm != nullptr;
+    const int K1 = MODE == kDown4 ? p.I : p.H;
+    nk1 = K1 / 128;
+    nexp = MODE == kDown4 && shared ? p.S : 1;
+    lda = nexp * K1 / 2;
+    ldw = K1 / 2;
+    const int a_total = shared || gather ? p.T : p.T * p.k;   // rows of the A tensor (scale plane length)
+    const int a_base = gather ? 0 : d.row0;
+    a_rows = gather ? p.T : d.rows;
+    A = (shared || gather ? p.a_shared : p.a_routed) + (int64_t)a_base * lda;
+    SA = (shared || gather ? p.sa_shared : p.sa_routed) + (int64_t)a_base * 4;
+    const int nrow_w = MODE == kGateUp4 ? 2 * p.I : p.H;      // weight rows of one expert
+    w_one = (int64_t)nrow_w * ldw;
+    sw_one = nrow_w * (K1 / 32);
+    W = shared ? p.w_shared : p.w_routed + d.seg * w_one;
+    SW = shared ? p.sw_shared : p.sw_routed + d.seg * (int64_t)sw_one;
+    a_bytes = a_rows * lda;
+    w_bytes = (int)((shared ? p.S : 1) * w_one);
+    sw_bytes = (shared ? p.S : 1) * sw_one;
+    sa_stride = a_total * 4;
+    sw_stride = nrow_w * 4;
+    sa_bytes = nexp * nk1 * sa_stride - a_base * 4;
+    ncols = MODE == kGateUp4 ? (shared ? p.S * p.I : p.I) : p.H;
+    // (a gate/up tile's 128 columns lie in one expert: I is a multiple of 128)
+    ex = MODE == kGateUp4 && shared ? d.nt * 128 / p.I : 0;
+    c0 = MODE == kGateUp4 ? d.nt * 128 - ex * p.I : d.nt * 256;
+  }
+
+  // weight row (in its expert) of tile column row r
+  __device__ __forceinline__ int wrow(const Fp4Params& p, int r) const {
+    if constexpr (MODE == kGateUp4) return c0 + (r < 128 ? r : r - 128 + p.I);
+    else return min(c0 + r, ncols - 1);
+  }
+};
+
+// Tile column of a wavefront's block ni, less its first: gate/up blocks 0, 1 are
+// gate rows of its 32 h columns, 2, 3 the matching up rows.
+template <int MODE>
+__device__ __forceinline__ constexpr int col_block(int ni) {
+  return MODE == kGateUp4 ? (ni / 2) * 128 + (ni % 2) * 16 : ni * 16;
+}
+
+// SwiGLU of one row block: acc[b] gate, acc[b + 2] up; the 8 h values of this lane
+// (block 0's four columns, then block 1's), their codes, and the scale byte of the
+// row's 32 columns, which the 4 lanes l16, + 16, + 32, + 48 hold together.
+__device__ __forceinline__ uint32_t swiglu_codes(const f32x4_t (&acc)[NI4], uint32_t* e) {
+  float v[8];
+  uint32_t m = 0;
+#pragma unroll
+  for (int b = 0; b < 2; ++b)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float gv = acc[b][r], uv = acc[b + 2][r];
+      const float h = gv * gate_sigmoid(gv) * uv;
+      v[b * 4 + r] = h;
+      m = max(m, __float_as_uint(h) & 0x7FFFFFFFu);
+    }
+  m = max(m, (uint32_t)__shfl_xor((int)m, 16));
+  m = max(m, (uint32_t)__shfl_xor((int)m, 32));
+  *e = mx_scale_byte(m);
+  return e2m1x8(v, *e);
+}
+
+// Workgroup barrier for LDS: this wavefront's LDS operations are done; loads and
+// stores in flight stay in flight (__syncthreads would wait for them).
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_s_waitcnt(kLgkmWaitZero);
+  asm volatile("s_barrier" ::: "memory");
+}
+
+// A wavefront's gate/up row block in LDS: codes [row][kHPitch] and scale bytes [row][4].
+__device__ __forceinline__ void stage_h(uint8_t* hc, uint8_t* hsc, int row, int wn, int g, uint32_t w, uint32_t e) {
+  uint8_t* dst = hc + row * kHPitch + wn * 16 + g * 2;
+  *reinterpret_cast<uint16_t*>(dst) = (uint16_t)w;
+  *reinterpret_cast<uint16_t*>(dst + 8) = (uint16_t)(w >> 16);
+  if (g == 0) hsc[row * 4 + wn] = (uint8_t)e;
+}
+
+// The staged gate/up tile to memory: 16 bytes a lane, 4 lanes a row, and the rows' scale words.
+template <int NT>
+__device__ __forceinline__ void store_h(const Fp4Params& p, const TileDesc& d, bool shared, const uint8_t* hc,
+                                        const uint8_t* hsc, int tid) {
+  const int hw = shared ? p.S * p.I / 2 : p.I / 2;      // bytes of an h row
+  uint8_t* out = shared ? p.out_shared : p.out_routed;
+  uint32_t* out_s = reinterpret_cast<uint32_t*>(shared ? p.out_shared_scale : p.out_routed_scale);
+  const int64_t plane = shared ? p.T : (int64_t)p.T * p.k;
+  for (int q = tid; q < d.rows * 4; q += NT) {
+    const int i = q >> 2, c = q & 3;
+    *reinterpret_cast<uint4*>(out + (d.row0 + i) * (int64_t)hw + d.nt * 64 + c * 16) =
+        *reinterpret_cast<const uint4*>(hc + i * kHPitch + c * 16);
+  }
+  for (int i = tid; i < d.rows; i += NT)
+    out_s[d.nt * plane + d.row0 + i] = *reinterpret_cast<const uint32_t*>(hsc + i * 4);
+}
+
+// 16 rows x 64 columns of a wavefront's down tile as bf16, through its own LDS
+// piece so that whole 128-byte row segments are stored, 16 bytes a lane.  (A
+// wavefront reads back only what it wrote; its LDS operations complete in order.)
+__device__ __forceinline__ void store_y(uint8_t* stg, const f32x4_t (&acc)[NI4], bf16_t* out, int64_t row0, int i0,
+                                        int rows, int col0, int ncols, int lane) {
+  const int l16 = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int ni = 0; ni < NI4; ++ni)
+    *reinterpret_cast<uint2*>(stg + l16 * kYPitch + (ni * 16 + 4 * g) * 2) =
+        uint2{cvt_bf16x2(acc[ni][0], acc[ni][1]), cvt_bf16x2(acc[ni][2], acc[ni][3])};
+  __builtin_amdgcn_s_waitcnt(kLgkmWaitZero);
+  __builtin_amdgcn_wave_barrier();
+  const int col = col0 + (lane & 7) * 8;   // (ncols is a multiple of 128: the segment is whole or absent)
+#pragma unroll
+  for (int it = 0; it < 2; ++it) {
+    const int lr = it * 8 + (lane >> 3), i = i0 + lr;
+    const uint4 v = *reinterpret_cast<const uint4*>(stg + lr * kYPitch + (lane & 7) * 16);
+    if (i < rows && col < ncols) *reinterpret_cast<uint4*>(out + (row0 + i) * ncols + col) = v;
+  }
+  __builtin_amdgcn_s_waitcnt(kLgkmWaitZero);
+  __builtin_amdgcn_wave_barrier();
+}
 #endif
 
-template <int MODE, int WM, int WN, int MI, int STAGES>
-__global__ __launch_bounds__(64 * WM * WN, 1) void gemm_fp4_kernel(Fp4Params p) {
-  constexpr int NI = 4;
-  constexpr int NW = WM * WN, NT = 64 * NW;
-  constexpr int BM = WM * MI * 16, BN = WN * NI * 16;
-  constexpr int BK = 128, CPR = BK / 16;               // bytes and 16-byte chunks of a row per slice
+// ------------------------------------------------------------------ large batches
+constexpr int kFp4Threads = 512;
+
+template <int MODE>
+__global__ __launch_bounds__(kFp4Threads, 1) void gemm_fp4_kernel(Fp4Params p) {
+  constexpr int WM = 2, WN = 4, MI = 8, STAGES = 4;
+  constexpr int NT = kFp4Threads, NW = NT / 64, BM = WM * MI * 16, BN = 256;
+  static_assert(WM * WN == NW && BM == kFp4BM && BN == kFp4BN2, "tile shape");
+  constexpr int BK = 64, CPR = BK / 16;                // bytes and 16-byte chunks of a row per slice
   constexpr int A_CH = BM * CPR / NT, B_CH = BN * CPR / NT;
-  static_assert(BM * CPR % NT == 0 && BN * CPR % NT == 0, "whole loads per thread");
-  constexpr int SC_W = 2 * (BM + BN);                  // scale words of a slice: A steps 0, 1, then B steps 0, 1
-  static_assert(2 * BM % 64 == 0 && 2 * BN % 64 == 0, "a wavefront's scale load is all A or all B");
-  constexpr int SC_CH = (SC_W + NT - 1) / NT;
-  constexpr int PER = A_CH + B_CH + SC_CH;             // loads per thread per slice
-  static_assert(MODE != kGateUp4 || BN == 256, "a gate/up tile is 128 columns of h");
-  constexpr int SC_OFF = (BM + BN) * BK;
-  constexpr int STAGE = SC_OFF + SC_CH * NT * 4;
-  // epilogue staging over the finished ring: down, (MI*16) x 64 bf16 per wavefront; gate/up, 64 code bytes
-  // and 4 scale bytes per tile row
-  constexpr int STG_PITCH = NI * 16 * 2 + 16;
-  constexpr int H_PITCH = 64 + 16;
-  constexpr int STG_BYTES = MODE == kDown4 ? NW * MI * 16 * STG_PITCH : BM * (H_PITCH + 4);
-  constexpr int LDS_BYTES = STAGES * STAGE > STG_BYTES ? STAGES * STAGE : STG_BYTES;
+  static_assert(BM + BN == NT && BM == NT / 2, "one scale word a thread: wavefronts 0-3 A's, 4-7 B's");
+  constexpr int PER = A_CH + B_CH + 1;                 // loads per thread per slice
+  constexpr int B_OFF = BM * BK, SC_OFF = B_OFF + BN * BK, STAGE = SC_OFF + NT * 4;
+  constexpr int STG_OFF = STAGES * STAGE;              // epilogue staging
+  constexpr int STG = BM * (kHPitch + 4) > NW * 16 * kYPitch ? BM * (kHPitch + 4) : NW * 16 * kYPitch;
+  constexpr int PERM_OFF = STG_OFF + STG;              // the next tile's perm entries (gathered rows)
+  constexpr int LDS_BYTES = PERM_OFF + BM * 4;
   static_assert(LDS_BYTES <= 163840, "LDS of a CU");
 #if defined(__HIP_DEVICE_COMPILE__)
   __shared__ __attribute__((aligned(16))) uint8_t lds[LDS_BYTES];
-
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
   const int l16 = lane & 15, g = lane >> 4;
 
-  // ------------------------------------------------------------ which tile
-  const int L = grouped_tile<kStripeFp4>(p.ntiles);
-  if (L < 0) return;
-  const TileDesc d = p.tiles[L];
-  const int seg = __builtin_amdgcn_readfirstlane(d.seg);
-  const int row0 = __builtin_amdgcn_readfirstlane(d.row0);
-  const int rows = __builtin_amdgcn_readfirstlane(d.rows);
-  const int nt = __builtin_amdgcn_readfirstlane(d.nt);
-  const bool shared = seg == p.E;
-  // Routed gate/up rows gathered from the quantised x: row row0 + r of the
-  // expert-sorted order is token perm[row0 + r] / k (codes and scales).
-  const bool gather = MODE == kGateUp4 && !shared && p.perm != nullptr;
+  // ------------------------------------------------------------ this workgroup's tiles
+  // XCD x = b mod 8 takes an equal contiguous share of the shared tiles and then
+  // one of the routed tiles; its workgroups take them in turn.
+  const int n_real = __builtin_amdgcn_readfirstlane(p.ntiles[0]), n_rt = __builtin_amdgcn_readfirstlane(p.ntiles[4]);
+  const int xcd = blockIdx.x & 7, per_s = (n_real - n_rt + 7) >> 3, per_r = (n_rt + 7) >> 3;
+  const int s_cnt = min(max(n_real - n_rt - xcd * per_s, 0), per_s);
+  const int r_cnt = min(max(n_rt - xcd * per_r, 0), per_r);
+  const int step = gridDim.x >> 3;
+  auto entry = [&](int q) { return q < s_cnt ? n_rt + xcd * per_s + q : xcd * per_r + q - s_cnt; };
+  int q = blockIdx.x >> 3;                             // position in the XCD's share
+  const int q_end = s_cnt + r_cnt;
+  if (q >= q_end) return;
 
-  // ------------------------------------------------------------ operands
-  const int K1 = MODE == kDown4 ? p.I : p.H;            // K of one expert
-  const int nexp = MODE == kDown4 && shared ? p.S : 1;  // experts whose K ranges follow each other
-  const int lda = nexp * K1 / 2, ldw = K1 / 2;          // bytes
-  const int a_total = shared || gather ? p.T : p.T * p.k;   // rows of the A tensor (scale plane length)
-  const int a_base = gather ? 0 : row0;
-  const int a_rows = gather ? p.T : rows;               // rows the A descriptor covers
-  const uint8_t* A = (shared || gather ? p.a_shared : p.a_routed) + (int64_t)a_base * lda;
-  const uint8_t* SA = (shared || gather ? p.sa_shared : p.sa_routed) + (int64_t)a_base * 4;
-  const int nrow_w = MODE == kGateUp4 ? 2 * p.I : p.H;  // weight rows of one expert
-  const int64_t w_one = (int64_t)nrow_w * ldw, sw_one = (int64_t)nrow_w * (K1 / 32);
-  const uint8_t* W = shared ? p.w_shared : p.w_routed + seg * w_one;
-  const uint8_t* SW = shared ? p.sw_shared : p.sw_routed + seg * sw_one;
-  const int w_bytes = (int)((shared ? p.S : 1) * w_one), sw_bytes = (int)((shared ? p.S : 1) * sw_one);
-  const int ncols = MODE == kGateUp4 ? (shared ? p.S * p.I : p.I) : p.H;
-  const int sa_stride = a_total * 4, sw_stride = nrow_w * 4;   // bytes between the scale planes of K steps
-  const int sa_bytes = (nexp * K1 / 128) * sa_stride - a_base * 4;
-
-  // weight row (within the descriptor: all shared experts together) of tile column row r
-  auto weight_row = [&](int r) {
-    if constexpr (MODE == kGateUp4) {
-      const bool up = r >= BN / 2;
-      const int c = min(nt * (BN / 2) + (up ? r - BN / 2 : r), ncols - 1);
-      return (c / p.I) * 2 * p.I + (up ? p.I : 0) + c % p.I;
-    } else {
-      return min(nt * BN + r, ncols - 1);
-    }
+  // ------------------------------------------------------------ the loads
+  // The stream of slices runs 3 slices ahead of the products, through the tiles.
+  TileDesc ld = tile_at(p, entry(q)), nd = ld;         // the tile being loaded, the one after it
+  bool more = false;                                   // nd is one
+  int left_l = 0, in_l = 0;                            // slices of ld to load yet, of its current expert
+  int ls = 0;                                          // stage the next slice goes to
+  int ak = 0, wk = 0, sk = 0;                          // scalar offsets of the next slice: A, W, scale words
+  int a_off[A_CH], b_off[B_CH], s_off = 0;
+  int w_next = 0, s_step = 0, s_next = 0, nk1 = 1;     // steps to the next expert's weights, between scale planes
+  const uint8_t *baseA = nullptr, *baseW = nullptr, *baseS = nullptr;
+  int bytesA = 0, bytesW = 0, bytesS = 0;              // 0 when the stream has ended: its loads are dropped
+  // the perm entries of a gathered tile's rows into LDS (wavefronts 0-3)
+  auto load_perm = [&](const TileDesc& d) {
+    if (MODE == kGateUp4 && p.perm != nullptr && d.seg != p.E && wave < BM / 64)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(p.perm + d.row0, d.rows * 4),
+                                               (lds_void_t*)(lds + PERM_OFF + wave * 256), 4, tid * 4, 0, 0, 0);
   };
-  // row of A for tile row r, or one past the descriptor (the range check drops the load)
-  auto a_row = [&](int r) {
-    int src = r < rows ? r : a_rows + 1;
-    if (MODE == kGateUp4 && gather && r < rows) src = p.perm[row0 + r] / p.k;
-    return src;
-  };
-
-  // ------------------------------------------------------------ load offsets
-  int a_off[A_CH], b_off[B_CH], s_off[SC_CH];
+  // start loading ld: its perm entries, if any, are in LDS
+  auto begin = [&]() {
+    const Operands4<MODE> o(p, ld);
+    const int32_t* rows = reinterpret_cast<const int32_t*>(lds + PERM_OFF);
+    // row of A for tile row r, or one past the descriptor (the range check drops the load)
+    auto a_row = [&](int r) { return r >= ld.rows ? o.a_rows + 1 : o.gather ? rows[r] / p.k : r; };
 #pragma unroll
-  for (int i = 0; i < A_CH; ++i) {
-    const int q = (i * NW + wave) * 64 + lane, r = q / CPR, pc = q % CPR;
-    a_off[i] = a_row(r) * lda + swz<CPR>(r, pc) * 16;
-  }
-#pragma unroll
-  for (int i = 0; i < B_CH; ++i) {
-    const int q = (i * NW + wave) * 64 + lane, r = q / CPR, pc = q % CPR;
-    b_off[i] = weight_row(r) * ldw + swz<CPR>(r, pc) * 16;
-  }
-  constexpr int kDrop = 0x7FFFFFFF;                     // past every descriptor
-#pragma unroll
-  for (int i = 0; i < SC_CH; ++i) {
-    const int q = (i * NW + wave) * 64 + lane;
-    if (q < 2 * BM) {
-      const int r = q % BM;
-      s_off[i] = r < rows ? (q / BM) * sa_stride + a_row(r) * 4 : kDrop;
-    } else if (q < SC_W) {
-      const int r = (q - 2 * BM) % BN;
-      int wr = weight_row(r);
-      int eoff = 0;
-      if constexpr (MODE == kGateUp4) {                 // scale words are kept per expert
-        eoff = (wr / nrow_w) * (int)sw_one;
-        wr %= nrow_w;
-      }
-      s_off[i] = eoff + (q - 2 * BM) / BN * sw_stride + wr * 4;
-    } else {
-      s_off[i] = kDrop;
+    for (int i = 0; i < A_CH; ++i) {
+      const int c = (i * NW + wave) * 64 + lane, r = c / CPR;
+      a_off[i] = a_row(r) * o.lda + swz<CPR>(r, c % CPR) * 16;
     }
-  }
-  const __amdgpu_buffer_rsrc_t rsrc_a = make_rsrc(A, a_rows * lda);
-  const __amdgpu_buffer_rsrc_t rsrc_w = make_rsrc(W, w_bytes);
-  const __amdgpu_buffer_rsrc_t rsrc_sa = make_rsrc(SA, sa_bytes);
-  const __amdgpu_buffer_rsrc_t rsrc_sw = make_rsrc(SW, sw_bytes);
-  typedef __attribute__((address_space(3))) void lds_void_t;
-  const int nk1 = (K1 + 255) / 256, nk = nexp * nk1;    // slices of one expert, of all
-  auto issue = [&](int stage, int kt) {
-    const int ex = MODE == kDown4 ? kt / nk1 : 0, j = MODE == kDown4 ? kt - ex * nk1 : kt;
-    const int ak = ex * ldw + j * BK, wk = ex * (int)w_one + j * BK;
-    const int as = (ex * (K1 / 128) + 2 * j) * sa_stride, ws = ex * (int)sw_one + 2 * j * sw_stride;
-    uint8_t* sb = lds + stage * STAGE;
 #pragma unroll
-    for (int i = 0; i < A_CH; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc_a, (lds_void_t*)(sb + (i * NW + wave) * 1024), 16, a_off[i], ak, 0,
-                                               0);
-#pragma unroll
-    for (int i = 0; i < B_CH; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc_w, (lds_void_t*)(sb + BM * BK + (i * NW + wave) * 1024), 16,
-                                               b_off[i], wk, 0, 0);
-#pragma unroll
-    for (int i = 0; i < SC_CH; ++i) {
-      lds_void_t* dst = (lds_void_t*)(sb + SC_OFF + (i * NW + wave) * 256);
-      if ((i * NW + wave) * 64 < 2 * BM)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc_sa, dst, 4, s_off[i], as, 0, 0);
-      else
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc_sw, dst, 4, s_off[i], ws, 0, 0);
+    for (int i = 0; i < B_CH; ++i) {
+      const int c = (i * NW + wave) * 64 + lane, r = c / CPR;
+      b_off[i] = (int)(o.ex * o.w_one) + o.wrow(p, r) * o.ldw + swz<CPR>(r, c % CPR) * 16;
     }
+    const bool sa = wave < NW / 2;                     // this wavefront loads A's scale words, else B's
+    if (sa) s_off = tid < ld.rows ? a_row(tid) * 4 : kDrop;
+    else s_off = o.ex * o.sw_one + o.wrow(p, tid - BM) * 4;
+    baseA = o.A; bytesA = o.a_bytes;
+    baseW = o.W; bytesW = o.w_bytes;
+    baseS = sa ? o.SA : o.SW;
+    bytesS = sa ? o.sa_bytes : o.sw_bytes;
+    s_step = sa ? o.sa_stride : o.sw_stride;
+    w_next = (int)o.w_one - o.nk1 * BK;
+    s_next = sa ? 0 : o.sw_one - o.nk1 * o.sw_stride;
+    ak = wk = sk = 0;
+    in_l = nk1 = o.nk1;
+    left_l = o.nk1 * o.nexp;
+    q += step;
+    more = q < q_end;
+    if (more) nd = tile_at(p, entry(q));
   };
-
-#pragma unroll
-  for (int s = 0; s < STAGES - 1; ++s)
-    if (s < nk) issue(s, s);
-
-  f32x4_t acc[MI][NI];
-#pragma unroll
-  for (int mi = 0; mi < MI; ++mi)
-#pragma unroll
-    for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-
-  // LDS rows of this lane's operands; lane group g supplies the elements [32g, 32g + 32) of a step
-  const int arow0 = wm * MI * 16 + l16;
-  int b_rd[NI];
-#pragma unroll
-  for (int ni = 0; ni < NI; ++ni) {
-    int brow;
-    if constexpr (MODE == kGateUp4)   // blocks 0, 1: gate rows of h columns wn*32 + ...; 2, 3: the matching up rows
-      brow = (ni < 2 ? 0 : BN / 2) + wn * 32 + (ni % 2) * 16;
+  // Load i of PER of the stream's next slice.
+  auto issue_part = [&](int i) {
+    uint8_t* sb = lds + ls * STAGE + wave * 1024;
+    if (i < A_CH)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(baseA, bytesA), (lds_void_t*)(sb + i * NW * 1024), 16, a_off[i],
+                                               ak, 0, 0);
+    else if (i < A_CH + B_CH)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(baseW, bytesW),
+                                               (lds_void_t*)(sb + B_OFF + (i - A_CH) * NW * 1024), 16, b_off[i - A_CH],
+                                               wk, 0, 0);
     else
-      brow = wn * NI * 16 + ni * 16;
-    b_rd[ni] = brow + l16;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(baseS, bytesS),
+                                               (lds_void_t*)(lds + ls * STAGE + SC_OFF + wave * 256), 4, s_off, sk, 0, 0);
+  };
+  // After a slice's loads.
+  auto advance = [&]() {
+    --left_l;
+    ak += BK;
+    wk += BK;
+    sk += s_step;
+    if (MODE == kDown4 && --in_l == 0) {               // the next shared expert's weights
+      in_l = nk1;
+      wk += w_next;
+      sk += s_next;
+    }
+    ls = ls == STAGES - 1 ? 0 : ls + 1;
+  };
+  // Before a slice's loads: the next tile is begun where the last one has ended.
+  auto prepare = [&]() {
+    if (left_l > 0) return;
+    if (!more) {
+      bytesA = bytesW = bytesS = 0;
+      return;
+    }
+    ld = nd;
+    if (MODE == kGateUp4 && p.perm != nullptr && p.H < 4 * 128) {
+      // tiles of fewer than 4 slices: the perm entries asked for below may not have arrived
+      wait_vm<0>();
+      lds_barrier();
+    }
+    begin();
+    if (MODE == kGateUp4 && p.perm != nullptr) {
+      lds_barrier();                                   // all have read this tile's entries: on to the next one's
+      if (more) load_perm(nd);
+    }
+  };
+  load_perm(ld);
+  wait_vm<0>();
+  lds_barrier();
+  begin();
+  lds_barrier();
+  if (more) load_perm(nd);
+#pragma unroll 1
+  for (int s = 0; s < STAGES - 1; ++s) {
+    prepare();
+#pragma unroll
+    for (int i = 0; i < PER; ++i) issue_part(i);
+    advance();
   }
-  const bool has_rows = wm * MI * 16 < rows;
 
-  int cur = 0, left = K1 / 128;                         // K steps left of the current expert
-  for (int kt = 0; kt < nk; ++kt) {
-    wait_slices<PER>(min(nk - 1, kt + STAGES - 2) - kt);
-    __builtin_amdgcn_s_waitcnt(kLgkmWaitZero);          // this wavefront's reads of the stage issued into next
-    asm volatile("s_barrier" ::: "memory");
-    if (kt + STAGES - 1 < nk) issue(cur == 0 ? STAGES - 1 : cur - 1, kt + STAGES - 1);
-    if (has_rows) {
-      const uint8_t* base = lds + cur * STAGE;
-#pragma unroll
-      for (int kk = 0; kk < 2; ++kk) {
-        if (kk == 1 && left < 2) break;
-        const int ch = swz<CPR>(l16, kk * 4 + g) * 16;
-        const uint8_t* sca = base + SC_OFF + kk * BM * 4 + g;
-        const uint8_t* scb = base + SC_OFF + (2 * BM + kk * BN) * 4 + g;
-        i32x8_t fb[NI];
-        int sb[NI];
-#pragma unroll
-        for (int ni = 0; ni < NI; ++ni) {
-          fb[ni] = frag4(base + BM * BK + b_rd[ni] * BK + ch);
-          sb[ni] = scb[b_rd[ni] * 4];
-        }
-#pragma unroll
-        for (int mi = 0; mi < MI; ++mi) {
-          const i32x8_t fa = frag4(base + (arow0 + mi * 16) * BK + ch);
-          const int sa = sca[(arow0 + mi * 16) * 4];
-#pragma unroll
-          for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = mfma_fp4(fb[ni], fa, acc[mi][ni], sb[ni], sa);
-        }
-      }
-    }
-    left -= 2;
-    if (left <= 0) left = K1 / 128;
-    cur = cur == STAGES - 1 ? 0 : cur + 1;
-  }
-
-  // ------------------------------------------------------------ epilogue
-  // acc[mi][ni][r] holds C[i][j] with i = arow0 + 16 mi (token row), j = 16 ni + 4 (lane / 16) + r
-  __syncthreads();   // every wavefront is done with the ring
-  if constexpr (MODE == kGateUp4) {
-    uint8_t* hc = lds;                                  // [BM][H_PITCH] codes
-    uint8_t* hsc = lds + BM * H_PITCH;                  // [BM][4] scale bytes
-#pragma unroll
-    for (int mi = 0; mi < MI; ++mi) {
-      float v[8];
-      uint32_t m = 0;
-#pragma unroll
-      for (int b = 0; b < 2; ++b)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float gv = acc[mi][b][r], uv = acc[mi][b + 2][r];
-          const float h = gv * gate_sigmoid(gv) * uv;
-          v[b * 4 + r] = h;
-          m = max(m, __float_as_uint(h) & 0x7FFFFFFFu);
-        }
-      m = max(m, (uint32_t)__shfl_xor((int)m, 16));
-      m = max(m, (uint32_t)__shfl_xor((int)m, 32));
-      const uint32_t e = mx_scale_byte(m);
-      const uint32_t w = e2m1x8(v, e);                  // block 0's four codes, then block 1's
-      const int i = arow0 + mi * 16;
-      uint8_t* dst = hc + i * H_PITCH + wn * 16 + g * 2;
-      *reinterpret_cast<uint16_t*>(dst) = (uint16_t)w;
-      *reinterpret_cast<uint16_t*>(dst + 8) = (uint16_t)(w >> 16);
-      if (g == 0) hsc[i * 4 + wn] = (uint8_t)e;
-    }
-    __syncthreads();
-    uint8_t* out = shared ? p.out_shared : p.out_routed;
-    uint32_t* out_s = reinterpret_cast<uint32_t*>(shared ? p.out_shared_scale : p.out_routed_scale);
-    const int64_t plane = shared ? p.T : (int64_t)p.T * p.k;
-    for (int q = tid; q < BM * 4; q += NT) {            // 4 lanes a row, 16 bytes each
-      const int i = q >> 2, c = q & 3;
-      if (i < rows)
-        *reinterpret_cast<uint4*>(out + (row0 + i) * (int64_t)(ncols / 2) + nt * 64 + c * 16) =
-            *reinterpret_cast<const uint4*>(hc + i * H_PITCH + c * 16);
-    }
-    for (int i = tid; i < rows; i += NT)
-      out_s[nt * plane + row0 + i] = *reinterpret_cast<const uint32_t*>(hsc + i * 4);
-  } else {
-    // a lane holds 4 adjacent columns of a row; through LDS the wavefront stores
-    // whole 128-byte row segments, 16 bytes a lane
-    uint8_t* stg = lds + wave * (MI * 16 * STG_PITCH);
-    bf16_t* out = reinterpret_cast<bf16_t*>(shared ? p.out_shared : p.out_routed);
-    const int col = nt * BN + wn * 64 + (lane & 7) * 8;   // ncols is a multiple of 128: the segment is whole or absent
+  // ------------------------------------------------------------ the products
+  // this lane's fragments in a stage: tile rows arow0 + 16 mi and brow + col_block(ni);
+  // lane group g supplies the elements [32g, 32g + 32) of the step
+  const int arow0 = wm * MI * 16 + l16;
+  const int ch = swz<CPR>(l16, g) * 16;                // (the same for every 16th row)
+  const int brow = wn * (MODE == kGateUp4 ? 32 : 64) + l16;
+  const int a_lane = arow0 * BK + ch, b_lane = B_OFF + brow * BK + ch;
+  const int sa_lane = SC_OFF + arow0 * 4 + g, sb_lane = SC_OFF + (BM + brow) * 4 + g;
+  constexpr int NB = 4, D = 3;                         // A fragments held, and read ahead
+  static_assert(MI % NB == 0 && D < NB && PER < MI, "the buffers rotate within a slice");
+  f32x4_t acc[MI][NI4];
+  i32x8_t fa[NB], fb[NI4], fbn[NI4];
+  int ra[NB], rb[NI4], rbn[NI4];
+  auto clear = [&]() {
 #pragma unroll
     for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
-      for (int ni = 0; ni < NI; ++ni)
-        *reinterpret_cast<uint2*>(stg + (mi * 16 + l16) * STG_PITCH + (ni * 16 + 4 * g) * 2) =
-            uint2{cvt_bf16x2(acc[mi][ni][0], acc[mi][ni][1]), cvt_bf16x2(acc[mi][ni][2], acc[mi][ni][3])};
-    // (the wavefront reads back only what it wrote; its LDS operations complete in order)
-    __builtin_amdgcn_s_waitcnt(kLgkmWaitZero);
-    __builtin_amdgcn_wave_barrier();
+      for (int ni = 0; ni < NI4; ++ni) acc[mi][ni] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  };
+  auto read_a = [&](int buf, const uint8_t* stage, int mi) {
+    fa[buf] = frag4(stage + a_lane + mi * 16 * BK);
+    ra[buf] = stage[sa_lane + mi * 64];
+  };
+  auto read_b = [&](const uint8_t* stage, int ni) {
+    fbn[ni] = frag4(stage + b_lane + col_block<MODE>(ni) * BK);
+    rbn[ni] = stage[sb_lane + col_block<MODE>(ni) * 4];
+  };
+  auto next_b = [&]() {
 #pragma unroll
-    for (int it = 0; it < MI * 2; ++it) {
-      const int lr = it * 8 + (lane >> 3);
-      const int i = wm * MI * 16 + lr;
-      const uint4 v = *reinterpret_cast<const uint4*>(stg + lr * STG_PITCH + (lane & 7) * 16);
-      if (i < rows && col < ncols) *reinterpret_cast<uint4*>(out + (row0 + i) * (int64_t)ncols + col) = v;
+    for (int ni = 0; ni < NI4; ++ni) {
+      fb[ni] = fbn[ni];
+      rb[ni] = rbn[ni];
     }
+  };
+  auto slices_of = [&](const TileDesc& d) {
+    return (MODE == kDown4 ? (d.seg == p.E ? p.S * p.I : p.I) : p.H) / 128;
+  };
+  wait_vm<PER*(STAGES - 2)>();                         // the first slice
+  lds_barrier();
+#pragma unroll
+  for (int ni = 0; ni < NI4; ++ni) read_b(lds, ni);
+#pragma unroll
+  for (int i = 0; i < D; ++i) read_a(i, lds, i);
+  next_b();
+  clear();
+
+  int qc = blockIdx.x >> 3;
+  TileDesc cd = tile_at(p, entry(qc)), after = cd;     // the tile being computed, the one after it
+  if (qc + step < q_end) after = tile_at(p, entry(qc + step));
+  int left = slices_of(cd), cs = 0;                    // slices of cd to compute, the stage of the next one
+  while (true) {
+    // One slice: its B fragments and its first D A fragments are in registers; it
+    // leaves the next slice's there.  (After the last slice: read, not used.)
+    prepare();
+    wait_vm<PER*(STAGES - 3)>();                       // this slice and the next one have landed
+    lds_barrier();                                     // ... everywhere, and the stage loaded into is free
+    const uint8_t* here = lds + cs * STAGE;
+    cs = cs == STAGES - 1 ? 0 : cs + 1;
+    const uint8_t* next = lds + cs * STAGE;
+    if (wm * MI * 16 < cd.rows) {
+#pragma unroll
+      for (int mi = 0; mi < MI; ++mi) {
+        read_a((mi + D) % NB, mi + D < MI ? here : next, (mi + D) % MI);
+        if (mi >= MI - NI4) read_b(next, mi - (MI - NI4));
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int ni = 0; ni < NI4; ++ni)
+          acc[mi][ni] = mfma_fp4(fb[ni], fa[mi % NB], acc[mi][ni], rb[ni], ra[mi % NB]);
+        // the loads of the slice to come, one after each of the first row blocks: a
+        // wavefront whose load waits for room in the memory pipeline has MFMAs running
+        if (mi < PER) issue_part(mi);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    } else {                                           // no rows here, perhaps some in the next tile
+#pragma unroll
+      for (int i = 0; i < PER; ++i) issue_part(i);
+#pragma unroll
+      for (int i = 0; i < D; ++i) read_a(i, next, i);
+#pragma unroll
+      for (int ni = 0; ni < NI4; ++ni) read_b(next, ni);
+    }
+    next_b();
+    advance();
+    if (--left > 0) continue;
+
+    // acc[mi][ni][r] holds C[i][j] with i = arow0 + 16 mi (token row), j = block column + 4 (lane / 16) + r
+    const bool shared = cd.seg == p.E;
+    if constexpr (MODE == kGateUp4) {
+      uint8_t* hc = lds + STG_OFF;
+      uint8_t* hsc = hc + BM * kHPitch;
+#pragma unroll
+      for (int mi = 0; mi < MI; ++mi) {
+        uint32_t e;
+        const uint32_t w = swiglu_codes(acc[mi], &e);
+        stage_h(hc, hsc, arow0 + mi * 16, wn, g, w, e);
+      }
+      lds_barrier();
+      store_h<NT>(p, cd, shared, hc, hsc, tid);
+      // (the staging is written again only after the next tile's barriers)
+    } else {
+      bf16_t* out = reinterpret_cast<bf16_t*>(shared ? p.out_shared : p.out_routed);
+#pragma unroll
+      for (int mi = 0; mi < MI; ++mi)
+        store_y(lds + STG_OFF + wave * 16 * kYPitch, acc[mi], out, cd.row0, (wm * MI + mi) * 16, cd.rows,
+                cd.nt * BN + wn * 64, p.H, lane);
+    }
+    qc += step;
+    if (qc >= q_end) break;
+    cd = after;
+    if (qc + step < q_end) after = tile_at(p, entry(qc + step));
+    left = slices_of(cd);
+    clear();
   }
 #endif
 }
 
-// Tile shapes <WM, WN, MI, STAGES>: large batches, and few rows per expert.
-#define MOE_FP4_TILE 2, 4, 8, 2
-#define MOE_FP4_DEC_TILE 1, 4, 2, 4
+// ------------------------------------------------------------------ few rows per expert
+template <int MODE>
+__global__ __launch_bounds__(256, 1) void gemm_fp4_rows_kernel(Fp4Params p) {
+  constexpr int WN = 4, MI = kFp4DecBM / 16, STAGES = 4, NT = 256, NW = 4, BM = kFp4DecBM, BN = 256;
+  constexpr int BK = 128, CPR = BK / 16;               // bytes (two K steps) and 16-byte chunks of a row per slice
+  constexpr int A_CH = BM * CPR / NT, B_CH = BN * CPR / NT;
+  static_assert(BM * CPR % NT == 0 && BN * CPR % NT == 0, "whole loads per thread");
+  // scale words of a slice: A's of step 0, of step 1, then B's likewise
+  constexpr int SC_CH = (2 * (BM + BN) + NT - 1) / NT;
+  static_assert(2 * BM % 64 == 0, "a wavefront's scale load is all A or all B");
+  constexpr int PER = A_CH + B_CH + SC_CH;             // loads per thread per slice
+  constexpr int SC_OFF = (BM + BN) * BK, STAGE = SC_OFF + SC_CH * NT * 4;
+  constexpr int LDS_BYTES = STAGES * STAGE;
+  static_assert(LDS_BYTES <= 163840 && BM * (kHPitch + 4) <= LDS_BYTES && NW * 16 * kYPitch <= LDS_BYTES, "LDS of a CU");
+#if defined(__HIP_DEVICE_COMPILE__)
+  __shared__ __attribute__((aligned(16))) uint8_t lds[LDS_BYTES];
+  const int tid = threadIdx.x, lane = tid & 63, wn = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int l16 = lane & 15, g = lane >> 4;
+  const int L = grouped_tile<kStripeFp4>(p.ntiles);
+  if (L < 0) return;
+  const TileDesc d = tile_at(p, L);
+  const Operands4<MODE> o(p, d);
+  auto a_row = [&](int r) { return r >= d.rows ? o.a_rows + 1 : o.gather ? p.perm[d.row0 + r] / p.k : r; };
+  int a_off[A_CH], b_off[B_CH], s_off[SC_CH];
+#pragma unroll
+  for (int i = 0; i < A_CH; ++i) {
+    const int c = i * NT + tid, r = c / CPR;
+    a_off[i] = a_row(r) * o.lda + swz<CPR>(r, c % CPR) * 16;
+  }
+#pragma unroll
+  for (int i = 0; i < B_CH; ++i) {
+    const int c = i * NT + tid, r = c / CPR;
+    b_off[i] = (int)(o.ex * o.w_one) + o.wrow(p, r) * o.ldw + swz<CPR>(r, c % CPR) * 16;
+  }
+#pragma unroll
+  for (int i = 0; i < SC_CH; ++i) {
+    const int c = i * NT + tid, cb = c - 2 * BM;
+    if (c < 2 * BM) s_off[i] = c % BM < d.rows ? c / BM * o.sa_stride + a_row(c % BM) * 4 : kDrop;
+    else s_off[i] = cb < 2 * BN ? o.ex * o.sw_one + cb / BN * o.sw_stride + o.wrow(p, cb % BN) * 4 : kDrop;
+  }
+  const __amdgpu_buffer_rsrc_t ra = make_rsrc(o.A, o.a_bytes), rw = make_rsrc(o.W, o.w_bytes),
+                               rsa = make_rsrc(o.SA, o.sa_bytes), rsw = make_rsrc(o.SW, o.sw_bytes);
+  // slices of one expert (the last one of an odd number of steps holds one step: its
+  // second half is bytes of the next row or nothing, and is not read), of all
+  const int ns1 = (o.nk1 + 1) / 2, ns = o.nexp * ns1;
+  auto issue = [&](int stage, int kt) {
+    const int ex = MODE == kDown4 ? kt / ns1 : 0, j = MODE == kDown4 ? kt - ex * ns1 : kt;
+    const int ak = ex * o.ldw + j * BK, wk = ex * (int)o.w_one + j * BK;
+    const int as = (ex * o.nk1 + 2 * j) * o.sa_stride, ws = ex * o.sw_one + 2 * j * o.sw_stride;
+    uint8_t* sb = lds + stage * STAGE;
+#pragma unroll
+    for (int i = 0; i < A_CH; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void_t*)(sb + (i * NW + wn) * 1024), 16, a_off[i], ak, 0, 0);
+#pragma unroll
+    for (int i = 0; i < B_CH; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void_t*)(sb + BM * BK + (i * NW + wn) * 1024), 16, b_off[i], wk,
+                                               0, 0);
+#pragma unroll
+    for (int i = 0; i < SC_CH; ++i) {
+      lds_void_t* dst = (lds_void_t*)(sb + SC_OFF + (i * NW + wn) * 256);
+      if ((i * NW + wn) * 64 < 2 * BM) __builtin_amdgcn_raw_ptr_buffer_load_lds(rsa, dst, 4, s_off[i], as, 0, 0);
+      else __builtin_amdgcn_raw_ptr_buffer_load_lds(rsw, dst, 4, s_off[i], ws, 0, 0);
+    }
+  };
+#pragma unroll
+  for (int s = 0; s < STAGES - 1; ++s)
+    if (s < ns) issue(s, s);
+  f32x4_t acc[MI][NI4];
+#pragma unroll
+  for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+    for (int ni = 0; ni < NI4; ++ni) acc[mi][ni] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  const int brow = wn * (MODE == kGateUp4 ? 32 : 64) + l16;
+  int cur = 0, left = o.nk1;                           // K steps left of the current expert
+  for (int kt = 0; kt < ns; ++kt) {
+    wait_loads<PER, STAGES - 2>(min(ns - 1, kt + STAGES - 2) - kt);
+    lds_barrier();
+    if (kt + STAGES - 1 < ns) issue(cur == 0 ? STAGES - 1 : cur - 1, kt + STAGES - 1);
+    const uint8_t* base = lds + cur * STAGE;
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      if (kk == 1 && left < 2) break;
+      const int ch = swz<CPR>(l16, kk * 4 + g) * 16;
+      const uint8_t* sca = base + SC_OFF + kk * BM * 4 + g;
+      const uint8_t* scb = base + SC_OFF + (2 * BM + kk * BN) * 4 + g;
+      i32x8_t fb[NI4];
+      int sb[NI4];
+#pragma unroll
+      for (int ni = 0; ni < NI4; ++ni) {
+        const int r = brow + col_block<MODE>(ni);
+        fb[ni] = frag4(base + BM * BK + r * BK + ch);
+        sb[ni] = scb[r * 4];
+      }
+#pragma unroll
+      for (int mi = 0; mi < MI; ++mi) {
+        const i32x8_t fa = frag4(base + (l16 + mi * 16) * BK + ch);
+        const int sa = sca[(l16 + mi * 16) * 4];
+#pragma unroll
+        for (int ni = 0; ni < NI4; ++ni) acc[mi][ni] = mfma_fp4(fb[ni], fa, acc[mi][ni], sb[ni], sa);
+      }
+    }
+    left -= 2;
+    if (left <= 0) left = o.nk1;
+    cur = cur == STAGES - 1 ? 0 : cur + 1;
+  }
+  lds_barrier();                                       // every wavefront is done with the ring
+  if constexpr (MODE == kGateUp4) {
+    uint8_t* hsc = lds + BM * kHPitch;
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi) {
+      uint32_t e;
+      const uint32_t w = swiglu_codes(acc[mi], &e);
+      stage_h(lds, hsc, l16 + mi * 16, wn, g, w, e);
+    }
+    lds_barrier();
+    store_h<NT>(p, d, o.shared, lds, hsc, tid);
+  } else {
+    bf16_t* out = reinterpret_cast<bf16_t*>(o.shared ? p.out_shared : p.out_routed);
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi)
+      store_y(lds + wn * 16 * kYPitch, acc[mi], out, d.row0, mi * 16, d.rows, d.nt * BN + wn * 64, p.H, lane);
+  }
+#endif
+}
 
 template <int MODE>
 moe_status launch_gemm_fp4(const FfnLayout& L, int64_t max_tiles, const Fp4Params& p, hipStream_t st) {
-  const int64_t grid = grouped_grid(max_tiles, kStripeFp4);
-  if (grid == 0) return MOE_OK;
-  if (L.bm1 == kFp4DecBM)
-    hipLaunchKernelGGL((gemm_fp4_kernel<MODE, MOE_FP4_DEC_TILE>), dim3((unsigned)grid), dim3(256), 0, st, p);
-  else
-    hipLaunchKernelGGL((gemm_fp4_kernel<MODE, MOE_FP4_TILE>), dim3((unsigned)grid), dim3(512), 0, st, p);
+  if (max_tiles == 0) return MOE_OK;
+  if (L.bm1 == kFp4DecBM) {
+    hipLaunchKernelGGL(gemm_fp4_rows_kernel<MODE>, dim3((unsigned)grouped_grid(max_tiles, kStripeFp4)), dim3(256), 0,
+                       st, p);
+  } else {
+    // one workgroup a CU (its LDS leaves no room for two), whole rounds of the 8 XCDs
+    const int64_t grid = std::min<int64_t>(std::max(cu_count() / 8 * 8, 8), (int64_t)align_up((size_t)max_tiles, 8));
+    hipLaunchKernelGGL(gemm_fp4_kernel<MODE>, dim3((unsigned)grid), dim3(kFp4Threads), 0, st, p);
+  }
   return launch_status();
 }
 

@@ -5,6 +5,9 @@
 
 namespace moe {
 
+// Compute units of the current device, asked for once per device.
+int cu_count();
+
 moe_status launch_route_topk(const moe_cfg* c, const float* scores, const float* bias, int32_t* idx,
                              float* w, hipStream_t st);
 
