@@ -37,39 +37,21 @@ __device__ __forceinline__ uint64_t same_expert_lanes(int e, bool valid, int nbi
   return m;
 }
 
-// Which pairs of a batch are dispatched.  LOCAL: those of the first *n_tokens
-// tokens (nullptr: all T) whose expert id less `first` lies in [0, E); every
-// other pair is absent.
-struct Window {
-  const int32_t* n_tokens;
-  int first, T, k;
-};
-
-// Pairs [0, limit) belong to live tokens.
-template <bool LOCAL>
-__device__ __forceinline__ int64_t live_pairs(const Window& w, int64_t N) {
-  if (!LOCAL || !w.n_tokens) return N;
-  return (int64_t)min(max(*w.n_tokens, 0), w.T) * w.k;
-}
-
 // The expert ids of segment `seg` held by this lane (pair lo + 64 it + lane),
 // all loaded before any is used; -1 past the last pair.
-template <bool LOCAL>
 __device__ __forceinline__ void load_segment(const int32_t* __restrict__ idx, int64_t seg, int64_t N,
-                                             const Window& w, int (&ev)[kSegPairs / kWave]) {
+                                             int (&ev)[kSegPairs / kWave]) {
   const int lane = threadIdx.x & (kWave - 1);
   const int64_t lo = seg * kSegPairs;
-  const int64_t limit = live_pairs<LOCAL>(w, N);
 #pragma unroll
   for (int it = 0; it < kSegPairs / kWave; ++it) {
     const int64_t f = lo + it * kWave + lane;
-    ev[it] = f < limit ? (LOCAL ? (int)((unsigned)idx[f] - (unsigned)w.first) : idx[f]) : -1;
+    ev[it] = f < N ? idx[f] : -1;
   }
 }
 
-template <bool LOCAL>
 __global__ __launch_bounds__(256) void count_kernel(const int32_t* __restrict__ idx, int64_t N,
-                                                    int E, int nbits, int64_t nseg, Window win,
+                                                    int E, int nbits, int64_t nseg,
                                                     int32_t* __restrict__ segcounts) {
   extern __shared__ int32_t cnt_all[];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
@@ -78,7 +60,7 @@ __global__ __launch_bounds__(256) void count_kernel(const int32_t* __restrict__ 
   for (int e = lane; e < E; e += kWave) cnt[e] = 0;
   __syncthreads();
   int ev[kSegPairs / kWave];
-  load_segment<LOCAL>(idx, seg, N, win, ev);
+  load_segment(idx, seg, N, ev);
 #pragma unroll
   for (int it = 0; it < kSegPairs / kWave; ++it) {
     const bool valid = (unsigned)ev[it] < (unsigned)E;   // (an id outside [0, E) is not counted)
@@ -152,9 +134,8 @@ __global__ __launch_bounds__(1024) void scan_kernel(int32_t* __restrict__ segcou
   if (tid == 0) offsets[0] = 0;
 }
 
-template <bool LOCAL>
 __global__ __launch_bounds__(256) void rank_kernel(const int32_t* __restrict__ idx, int64_t N, int E,
-                                                   int nbits, int64_t nseg, Window win,
+                                                   int nbits, int64_t nseg,
                                                    const int32_t* __restrict__ segprefix,
                                                    const int32_t* __restrict__ offsets,
                                                    int32_t* __restrict__ perm,
@@ -168,7 +149,7 @@ __global__ __launch_bounds__(256) void rank_kernel(const int32_t* __restrict__ i
   __syncthreads();
   const int64_t lo = seg * kSegPairs;
   int ev[kSegPairs / kWave];
-  load_segment<LOCAL>(idx, seg, N, win, ev);
+  load_segment(idx, seg, N, ev);
 #pragma unroll
   for (int it = 0; it < kSegPairs / kWave; ++it) {
     const int64_t f = lo + it * kWave + lane;
@@ -181,9 +162,109 @@ __global__ __launch_bounds__(256) void rank_kernel(const int32_t* __restrict__ i
     if (valid) {
       perm[pos] = (int32_t)f;
       inv[f] = pos;
-    } else if (LOCAL && f < N) {
-      inv[f] = -1;
     }
+  }
+}
+
+// ---- the same over a share: some pairs are absent
+// Present are the pairs of the first *n_tokens tokens (nullptr: all T) whose
+// expert id less `first` lies in [0, E).
+struct Window {
+  const int32_t* n_tokens;
+  int first, T, k;
+};
+
+// Pairs [0, limit) belong to live tokens.
+__device__ __forceinline__ int64_t live_pairs(const Window& w, int64_t N) {
+  return w.n_tokens ? (int64_t)min(max(*w.n_tokens, 0), w.T) * w.k : N;
+}
+
+// One workgroup per segment, a quarter of its pairs per wavefront (a wavefront
+// alone walks its 16 rounds of ballots one after the other: at 131072 pairs the
+// whole dispatch takes 18 us longer with one).
+constexpr int kQuarter = kSegPairs / 4;
+
+// The share's experts of this lane's pairs (lo + 64 it + lane), -1 for absent ones;
+// every id is asked for before the live count is looked at.
+__device__ __forceinline__ void load_quarter(const int32_t* __restrict__ idx, int64_t lo, int64_t N, const Window& w,
+                                             int E, int (&ev)[kQuarter / kWave]) {
+  const int lane = threadIdx.x & (kWave - 1);
+  uint32_t id[kQuarter / kWave];
+#pragma unroll
+  for (int it = 0; it < kQuarter / kWave; ++it) {
+    const int64_t f = lo + it * kWave + lane;
+    id[it] = f < N ? (uint32_t)idx[f] : ~0u;
+  }
+  const int64_t limit = live_pairs(w, N);
+#pragma unroll
+  for (int it = 0; it < kQuarter / kWave; ++it) {
+    const uint32_t e = id[it] - (uint32_t)w.first;
+    ev[it] = lo + it * kWave + lane < limit && e < (uint32_t)E ? (int)e : -1;
+  }
+}
+
+// Counts the wavefront's pairs by expert in cnt (zeroed), and gives each present
+// one the number of earlier ones of its expert.
+__device__ __forceinline__ void count_quarter(const int (&ev)[kQuarter / kWave], int nbits, int32_t* cnt,
+                                              int (&before)[kQuarter / kWave]) {
+#pragma unroll
+  for (int it = 0; it < kQuarter / kWave; ++it) {
+    const bool here = ev[it] >= 0;
+    const int e = here ? ev[it] : 0;
+    const uint64_t m = same_expert_lanes(e, here, nbits);
+    const int32_t base = here ? cnt[e] : 0;
+    before[it] = base + __popcll(m & lanes_below());
+    if (here && (m & lanes_below()) == 0) cnt[e] = base + __popcll(m);
+  }
+}
+
+__global__ __launch_bounds__(256) void count_local_kernel(const int32_t* __restrict__ idx, int64_t N, int E, int nbits,
+                                                          Window win, int32_t* __restrict__ segcounts) {
+  extern __shared__ int32_t cnt_all[];                  // [4][E]
+  const int wave = threadIdx.x >> 6;
+  const int64_t seg = blockIdx.x;
+  for (int e = threadIdx.x; e < 4 * E; e += 256) cnt_all[e] = 0;
+  int ev[kQuarter / kWave], before[kQuarter / kWave];
+  load_quarter(idx, seg * kSegPairs + wave * kQuarter, N, win, E, ev);
+  __syncthreads();
+  count_quarter(ev, nbits, cnt_all + wave * E, before);
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += 256)
+    segcounts[seg * E + e] = cnt_all[e] + cnt_all[E + e] + cnt_all[2 * E + e] + cnt_all[3 * E + e];
+}
+
+__global__ __launch_bounds__(256) void rank_local_kernel(const int32_t* __restrict__ idx, int64_t N, int E, int nbits,
+                                                         Window win, const int32_t* __restrict__ segprefix,
+                                                         const int32_t* __restrict__ offsets,
+                                                         int32_t* __restrict__ perm, int32_t* __restrict__ inv) {
+  extern __shared__ int32_t cnt_all[];                  // [4][E] counts, then [4][E] first rows
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int64_t seg = blockIdx.x, lo = seg * kSegPairs + wave * kQuarter;
+  for (int e = threadIdx.x; e < 4 * E; e += 256) cnt_all[e] = 0;
+  int ev[kQuarter / kWave], before[kQuarter / kWave];
+  load_quarter(idx, lo, N, win, E, ev);
+  __syncthreads();
+  count_quarter(ev, nbits, cnt_all + wave * E, before);
+  __syncthreads();
+  int32_t* first = cnt_all + 4 * E;
+  for (int e = threadIdx.x; e < E; e += 256) {
+    int32_t at = offsets[e] + segprefix[seg * E + e];
+    for (int w = 0; w < 4; ++w) {
+      first[w * E + e] = at;
+      at += cnt_all[w * E + e];
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int it = 0; it < kQuarter / kWave; ++it) {
+    const int64_t f = lo + it * kWave + lane;
+    if (f >= N) continue;
+    int32_t pos = -1;
+    if (ev[it] >= 0) {
+      pos = first[wave * E + ev[it]] + before[it];
+      perm[pos] = (int32_t)f;
+    }
+    inv[f] = pos;
   }
 }
 
@@ -229,7 +310,14 @@ __global__ __launch_bounds__(256) void permute_rows_kernel(const uint4* __restri
 #pragma unroll
       for (int i = 0; i < CPL; ++i) {
         const int64_t c = c0 + i * kWave + lane;
-        if (c < nchunk) st_stream(&dst[p * nchunk + c], v[i]);
+        if (c >= nchunk) continue;
+        // (a share's rows: non-temporal, T = 16384, H = 7168, an eighth of the experts
+        // 92 -> 83 us the whole dispatch, every expert of T = 8192 230 -> 201 us)
+        if constexpr (LOCAL)
+          __builtin_nontemporal_store(u32x4_t{v[i].x, v[i].y, v[i].z, v[i].w},
+                                      reinterpret_cast<u32x4_t*>(&dst[p * nchunk + c]));
+        else
+          st_stream(&dst[p * nchunk + c], v[i]);
       }
     }
   }
@@ -439,7 +527,7 @@ __global__ __launch_bounds__(kSmallThreads) void dispatch_small_kernel(
     void* __restrict__ x_perm, void* __restrict__ x_scale) {
 #if defined(__HIP_DEVICE_COMPILE__)
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int k = win.k, limit = (int)live_pairs<true>(win, N);
+  const int k = win.k, limit = (int)live_pairs(win, N);
   const uint32_t absent = (uint32_t)E * (uint32_t)N;   // E <= 512, N <= 4096: below 2^31
   auto key = [&](int f) {
     const uint32_t e = f < limit ? (uint32_t)idx[f] - (uint32_t)win.first : ~0u;
@@ -562,8 +650,12 @@ static moe_status dispatch_launch(const moe_cfg* cfg, const Window& win, const i
   while (Ep2 < E) Ep2 <<= 1;
   const unsigned blocks = (unsigned)((nseg + 3) / 4);
   if (nseg > 0) {
-    hipLaunchKernelGGL(count_kernel<LOCAL>, dim3(blocks), dim3(256), 4 * E * sizeof(int32_t), s, topk_idx, N,
-                       E, nbits, nseg, win, segc);
+    if constexpr (LOCAL)
+      hipLaunchKernelGGL(count_local_kernel, dim3((unsigned)nseg), dim3(256), 4 * E * sizeof(int32_t), s, topk_idx, N,
+                         E, nbits, win, segc);
+    else
+      hipLaunchKernelGGL(count_kernel, dim3(blocks), dim3(256), 4 * E * sizeof(int32_t), s, topk_idx, N,
+                         E, nbits, nseg, segc);
     if ((st = launch_status()) != MOE_OK) return st;
   }
   const int P = 1024 / Ep2;
@@ -571,8 +663,12 @@ static moe_status dispatch_launch(const moe_cfg* cfg, const Window& win, const i
                      nseg, E, Ep2, counts, offsets);
   if ((st = launch_status()) != MOE_OK) return st;
   if (nseg == 0) return MOE_OK;
-  hipLaunchKernelGGL(rank_kernel<LOCAL>, dim3(blocks), dim3(256), 4 * E * sizeof(int32_t), s, topk_idx, N, E,
-                     nbits, nseg, win, segc, offsets, perm, inv);
+  if constexpr (LOCAL)
+    hipLaunchKernelGGL(rank_local_kernel, dim3((unsigned)nseg), dim3(256), 8 * E * sizeof(int32_t), s, topk_idx, N, E,
+                       nbits, win, segc, offsets, perm, inv);
+  else
+    hipLaunchKernelGGL(rank_kernel, dim3(blocks), dim3(256), 4 * E * sizeof(int32_t), s, topk_idx, N, E,
+                       nbits, nseg, segc, offsets, perm, inv);
   if ((st = launch_status()) != MOE_OK) return st;
   if (!x_perm) return MOE_OK;
   const unsigned tblocks = (unsigned)((cfg->T + 3) / 4);

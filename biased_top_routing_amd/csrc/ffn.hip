@@ -9,6 +9,7 @@
 
 #include "common.h"
 #include "ffn_layout.h"
+#include "fp4.h"
 #include "kernels.h"
 
 namespace moe {
@@ -25,25 +26,30 @@ namespace moe {
 // their weight rows are shared in that XCD's L2, also for segments far larger
 // than the number of tiles in flight.  Every workgroup computes the prefix sums over segments in LDS
 // (at most 513 segments) and writes its own share of the entries.
-__global__ __launch_bounds__(1024) void build_tiles_kernel(const int32_t* __restrict__ offsets, int E,
-                                                           int S, int T, int bm1, int bm1_alt, int bm2,
-                                                           int bm2_alt, int nt1, int nt1s,
-                                                           int nt2,
-                                                           TileDesc* __restrict__ t1,
-                                                           TileDesc* __restrict__ t2,
-                                                           int32_t* __restrict__ hdr) {
+struct TileTables {
+  int E, S, T, bm1, bm1_alt, bm2, bm2_alt, nt1, nt1s, nt2;
+  TileDesc *t1, *t2;     // t2 == nullptr: the first table only
+  int32_t* hdr;
+};
+
+// Block b of nb blocks of 1024 threads.
+__device__ void build_tiles_block(const int32_t* __restrict__ offsets, const TileTables& p, int b, int nb) {
   __shared__ int32_t pre1[1024], pre2[1024], mt1_s[1024], mt2_s[1024], row0_s[1024], rows_s[1024], hb1_s[1024],
       hb2_s[1024];
-  const int tid = threadIdx.x;
-  const int nseg = E + (S > 0 ? 1 : 0);
+  __shared__ int32_t wave1[16], wave2[16];
+  const int E = p.E, nt1 = p.nt1, nt1s = p.nt1s, nt2 = p.nt2, bm1 = p.bm1, bm2 = p.bm2;
+  TileDesc *t1 = p.t1, *t2 = p.t2;
+  int32_t* hdr = p.hdr;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int nseg = E + (p.S > 0 ? 1 : 0);
   int c1 = 0, c2 = 0;
   if (tid < nseg) {
-    const int rows = tid < E ? offsets[tid + 1] - offsets[tid] : T;
+    const int rows = tid < E ? offsets[tid + 1] - offsets[tid] : p.T;
     const int row0 = tid < E ? offsets[tid] : 0;
     const int mt1 = (rows + bm1 - 1) / bm1, mt2 = (rows + bm2 - 1) / bm2;
     // as many tiles of bm1_alt rows cover the segment: use that height
-    hb1_s[tid] = bm1_alt > 0 && (int64_t)mt1 * bm1_alt >= rows ? bm1_alt : bm1;
-    hb2_s[tid] = bm2_alt > 0 && (int64_t)mt2 * bm2_alt >= rows ? bm2_alt : bm2;
+    hb1_s[tid] = p.bm1_alt > 0 && (int64_t)mt1 * p.bm1_alt >= rows ? p.bm1_alt : bm1;
+    hb2_s[tid] = p.bm2_alt > 0 && (int64_t)mt2 * p.bm2_alt >= rows ? p.bm2_alt : bm2;
     c1 = mt1 * (tid < E ? nt1 : nt1s);
     c2 = mt2 * nt2;
     mt1_s[tid] = mt1;
@@ -51,36 +57,37 @@ __global__ __launch_bounds__(1024) void build_tiles_kernel(const int32_t* __rest
     row0_s[tid] = row0;
     rows_s[tid] = rows;
   }
-  pre1[tid] = c1;
-  pre2[tid] = c2;
-  __syncthreads();
-  for (int d = 1; d < 1024; d <<= 1) {   // inclusive scans
-    const int v1 = tid >= d ? pre1[tid - d] : 0;
-    const int v2 = tid >= d ? pre2[tid - d] : 0;
-    __syncthreads();
-    pre1[tid] += v1;
-    pre2[tid] += v2;
-    __syncthreads();
+  // exclusive prefixes over the segments: within each wavefront, then over the wavefronts
+  int v1 = c1, v2 = c2;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int u1 = __shfl_up(v1, d), u2 = __shfl_up(v2, d);
+    if (lane >= d) v1 += u1, v2 += u2;
   }
-  // turn into exclusive prefixes: ex[g] = inc[g] - c[g]
-  const int inc1 = pre1[tid], inc2 = pre2[tid];
-  const int total1 = pre1[nseg - 1], total2 = pre2[nseg - 1];
+  if (lane == 63) wave1[wave] = v1, wave2[wave] = v2;
   __syncthreads();
-  pre1[tid] = inc1 - c1;
-  pre2[tid] = inc2 - c2;
+  int total1 = 0, total2 = 0, base1 = 0, base2 = 0;
+#pragma unroll
+  for (int w = 0; w < 16; ++w) {
+    if (w == wave) base1 = total1, base2 = total2;
+    total1 += wave1[w];
+    total2 += wave2[w];
+  }
+  pre1[tid] = base1 + v1 - c1;
+  pre2[tid] = base2 + v2 - c2;
   __syncthreads();
-  if (tid == 0 && blockIdx.x == 0) {
+  if (tid == 0 && b == 0) {
     hdr[0] = total1;
     hdr[1] = t2 ? total2 : 0;
     // tiles of the routed segments (they come first; the shared ones follow)
-    hdr[4] = S > 0 ? pre1[E] : total1;
-    hdr[5] = t2 ? (S > 0 ? pre2[E] : total2) : 0;
+    hdr[4] = p.S > 0 ? pre1[E] : total1;
+    hdr[5] = t2 ? (p.S > 0 ? pre2[E] : total2) : 0;
   }
   for (int pass = 0; pass < (t2 ? 2 : 1); ++pass) {   // t2 == nullptr: the first table only
     const int* pre = pass == 0 ? pre1 : pre2;
     const int total = pass == 0 ? total1 : total2;
     TileDesc* out = pass == 0 ? t1 : t2;
-    for (int L = blockIdx.x * 1024 + tid; L < total; L += gridDim.x * 1024) {
+    for (int L = b * 1024 + tid; L < total; L += nb * 1024) {
       int lo = 0, hi = nseg;           // last g with pre[g] <= L and a non-empty segment
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -108,23 +115,66 @@ __global__ __launch_bounds__(1024) void build_tiles_kernel(const int32_t* __rest
   }
 }
 
+__global__ __launch_bounds__(1024) void build_tiles_kernel(const int32_t* __restrict__ offsets, TileTables p) {
+  build_tiles_block(offsets, p, blockIdx.x, gridDim.x);
+}
+
+// The tables of an MXFP4 call and x in MXFP4 (fp4.h) in one launch: blocks [0, nb)
+// build, the others quantise, 4 groups of 256 lanes each.  (Two launches of a few
+// microseconds each stood before the GEMMs: T = 1, H = 7168, 8 experts and a shared
+// one 59.0 -> 56.5 us the whole call.)
+__global__ __launch_bounds__(1024) void build_tiles_quantize_fp4_kernel(const int32_t* __restrict__ offsets,
+                                                                       TileTables p, int nb,
+                                                                       const uint4* __restrict__ x, int rows,
+                                                                       int cols, int64_t blocks,
+                                                                       uint32_t* __restrict__ dst,
+                                                                       uint32_t* __restrict__ scales) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  if ((int)blockIdx.x < nb) {
+    build_tiles_block(offsets, p, blockIdx.x, nb);
+    return;
+  }
+  const int64_t b = ((int64_t)blockIdx.x - nb) * 4 + (threadIdx.x >> 8);
+  if (b < blocks) quantize_fp4_block(x, rows, cols, b, 0, threadIdx.x & 255, dst, scales);
+#endif
+}
+
+// Blocks that fill the larger of two tables of at most max1 and max2 entries.
+static unsigned table_blocks(int64_t max1, int64_t max2) {
+  return (unsigned)std::min<int64_t>(std::max<int64_t>((std::max(max1, max2) + 1023) / 1024, 1), 64);
+}
+
 moe_status launch_build_tile_tables(const moe_cfg* c, const int32_t* offsets, int bm1, int bm1_alt, int nt1,
                                     int nt1s, TileDesc* t1, int64_t max1, int bm2, int bm2_alt, int nt2, TileDesc* t2,
                                     int64_t max2, int32_t* hdr, hipStream_t st) {
-  const int64_t most = max1 > max2 ? max1 : max2;
-  const unsigned blocks = (unsigned)std::min<int64_t>(std::max<int64_t>((most + 1023) / 1024, 1), 64);
-  hipLaunchKernelGGL(build_tiles_kernel, dim3(blocks), dim3(1024), 0, st, offsets, c->E, c->S, c->T, bm1, bm1_alt,
-                     bm2, bm2_alt, nt1, nt1s, nt2, t1, t2, hdr);
+  const TileTables p{c->E, c->S, c->T, bm1, bm1_alt, bm2, bm2_alt, nt1, nt1s, nt2, t1, t2, hdr};
+  hipLaunchKernelGGL(build_tiles_kernel, dim3(table_blocks(max1, max2)), dim3(1024), 0, st, offsets, p);
   return launch_status();
+}
+
+static TileTables ffn_tables(const moe_cfg* c, const FfnLayout& L, char* base) {
+  return TileTables{c->E, c->S, c->T, L.bm1, L.bm1_alt, L.bm2, L.bm2_alt, (int)L.nt1, (int)L.nt1s, (int)L.nt2,
+                    reinterpret_cast<TileDesc*>(base + L.off_t1), reinterpret_cast<TileDesc*>(base + L.off_t2),
+                    reinterpret_cast<int32_t*>(base + L.off_hdr)};
 }
 
 moe_status launch_build_tiles(const moe_cfg* c, const int32_t* offsets, void* ws, hipStream_t st) {
   const FfnLayout L(c);
+  hipLaunchKernelGGL(build_tiles_kernel, dim3(table_blocks(L.max1, L.max2)), dim3(1024), 0, st, offsets,
+                     ffn_tables(c, L, static_cast<char*>(ws)));
+  return launch_status();
+}
+
+moe_status launch_build_tiles_quantize_fp4(const moe_cfg* c, const int32_t* offsets, const bf16_t* x, void* ws,
+                                           hipStream_t st) {
+  const FfnLayout L(c);
   char* base = static_cast<char*>(ws);
-  return launch_build_tile_tables(c, offsets, L.bm1, L.bm1_alt, (int)L.nt1, (int)L.nt1s,
-                                  reinterpret_cast<TileDesc*>(base + L.off_t1), L.max1, L.bm2, L.bm2_alt, (int)L.nt2,
-                                  reinterpret_cast<TileDesc*>(base + L.off_t2), L.max2,
-                                  reinterpret_cast<int32_t*>(base + L.off_hdr), st);
+  const unsigned nb = table_blocks(L.max1, L.max2);
+  const int64_t blocks = quantize_fp4_blocks(c->T, c->H);
+  hipLaunchKernelGGL(build_tiles_quantize_fp4_kernel, dim3(nb + (unsigned)((blocks + 3) / 4)), dim3(1024), 0, st,
+                     offsets, ffn_tables(c, L, base), (int)nb, (const uint4*)x, c->T, c->H, blocks,
+                     (uint32_t*)(base + L.off_xq), (uint32_t*)(base + L.off_xqs));
+  return launch_status();
 }
 
 // ------------------------------------------------------------ fp32 experts

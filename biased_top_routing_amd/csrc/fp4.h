@@ -22,6 +22,13 @@
 
 namespace moe {
 
+// A quantising workgroup of 256 lanes takes kFp4Rows rows of one 128-column group
+// of a matrix; workgroups of one matrix: row blocks, and in each its column groups.
+constexpr int kFp4Rows = 64;
+inline int64_t quantize_fp4_blocks(int64_t rows, int64_t cols) {
+  return (rows + kFp4Rows - 1) / kFp4Rows * (cols / 128);
+}
+
 #if defined(__HIP_DEVICE_COMPILE__)
 // Scale byte of a block whose largest magnitude has the fp32 bits `top` (sign cleared).
 __device__ __forceinline__ uint32_t mx_scale_byte(uint32_t top) {
@@ -77,6 +84,33 @@ __device__ __forceinline__ uint32_t mx_quant_chunk(uint4 raw, uint32_t* e) {
 __device__ __forceinline__ uint32_t mx_scale_word(uint32_t e) {
   uint32_t w = e | ((uint32_t)__shfl_down((int)e, 4) << 8);    // lanes 0..3: blocks 0, 1; lanes 8..11: blocks 2, 3
   return w | ((uint32_t)__shfl_down((int)w, 8) << 16);
+}
+
+// Workgroup b of matrix mat [rows, cols] (lane tid of 256): its codes and scale words.
+__device__ __forceinline__ void quantize_fp4_block(const uint4* __restrict__ src, int rows, int cols, int64_t b,
+                                                   int64_t mat, int tid, uint32_t* __restrict__ dst,
+                                                   uint32_t* __restrict__ scales) {
+  const int ncol = cols / 128, lane = tid & 63, sub = lane & 15;
+  const int c = (int)(b % ncol);
+  const int64_t nchunk = cols / 8;                      // 16-byte chunks of a row; also its code words
+  const int r0 = (int)(b / ncol) * kFp4Rows + (tid >> 6) * 16 + (lane >> 4);
+  uint4 raw[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = r0 + i * 4;
+    raw[i] = r < rows ? src[(mat * rows + r) * nchunk + (int64_t)c * 16 + sub] : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = r0 + i * 4;
+    uint32_t e;
+    const uint32_t w = mx_quant_chunk(raw[i], &e);
+    const uint32_t sw = mx_scale_word(e);
+    if (r < rows) {
+      dst[(mat * rows + r) * nchunk + (int64_t)c * 16 + sub] = w;
+      if (sub == 0) scales[(mat * ncol + c) * rows + r] = sw;
+    }
+  }
 }
 #endif
 

@@ -661,11 +661,9 @@ moe_status launch_ffn_fp4(const moe_cfg* c, const uint8_t* x_perm, const uint8_t
   Fp4Params p{};
   p.T = c->T; p.H = c->H; p.E = c->E; p.S = c->S; p.I = c->I; p.k = c->k;
   if (phase == MOE_FFN_ALL || phase == MOE_FFN_GATE_UP) {
-    if ((s = launch_build_tiles(c, offsets, ws, st)) != MOE_OK) return s;
-    // x once in MXFP4: the shared experts' operand, and the routed one when its rows are gathered
-    if ((c->S > 0 || perm) &&
-        (s = launch_quantize_fp4(x, 1, c->T, c->H, base + L.off_xq, base + L.off_xqs, st)) != MOE_OK)
-      return s;
+    // the tile tables, and x once in MXFP4: the shared experts' operand, and the routed one when its rows are gathered
+    s = c->S > 0 || perm ? launch_build_tiles_quantize_fp4(c, offsets, x, ws, st) : launch_build_tiles(c, offsets, ws, st);
+    if (s != MOE_OK) return s;
     p.perm = perm;
     p.a_routed = x_perm; p.sa_routed = x_perm_scale;
     p.a_shared = base + L.off_xq; p.sa_shared = base + L.off_xqs;

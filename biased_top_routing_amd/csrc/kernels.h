@@ -43,12 +43,11 @@ moe_status launch_ffn_fp4(const moe_cfg* c, const uint8_t* x_perm, const uint8_t
                           const bf16_t* x, bf16_t* y_perm, bf16_t* y_shared, void* ws, int phase,
                           hipStream_t st);
 
-// MXFP4 codes and scale words (fp4.h) of n_mat bf16 matrices [rows, cols].
-moe_status launch_quantize_fp4(const bf16_t* src, int n_mat, int rows, int cols, uint8_t* dst, uint8_t* scales,
-                               hipStream_t st);
-
 // Builds the tile tables of the grouped GEMMs from the per-expert offsets.
 moe_status launch_build_tiles(const moe_cfg* c, const int32_t* offsets, void* ws, hipStream_t st);
+// The same, and x [T, H] quantised to MXFP4 into the workspace.
+moe_status launch_build_tiles_quantize_fp4(const moe_cfg* c, const int32_t* offsets, const bf16_t* x, void* ws,
+                                           hipStream_t st);
 
 struct TileDesc;
 // Two tables (t1: row height bm1, or bm1_alt for a segment that needs no more

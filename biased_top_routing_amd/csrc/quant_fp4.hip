@@ -14,35 +14,11 @@ namespace moe {
 
 namespace {
 
-constexpr int kRowsPerBlock = 64;
-
 __global__ __launch_bounds__(256) void quantize_fp4_kernel(const uint4* __restrict__ src, int rows, int cols,
                                                            uint32_t* __restrict__ dst,
                                                            uint32_t* __restrict__ scales) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int ncol = cols / 128;
-  const int c = blockIdx.x % ncol, sub = lane & 15;
-  const int64_t mat = blockIdx.y;
-  const int64_t nchunk = cols / 8;                      // 16-byte chunks of a row; also its code words
-  const int r0 = blockIdx.x / ncol * kRowsPerBlock + wave * 16 + (lane >> 4);
-  uint4 raw[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = r0 + i * 4;
-    raw[i] = r < rows ? src[(mat * rows + r) * nchunk + (int64_t)c * 16 + sub] : make_uint4(0, 0, 0, 0);
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = r0 + i * 4;
-    uint32_t e;
-    const uint32_t w = mx_quant_chunk(raw[i], &e);
-    const uint32_t sw = mx_scale_word(e);
-    if (r < rows) {
-      dst[(mat * rows + r) * nchunk + (int64_t)c * 16 + sub] = w;
-      if (sub == 0) scales[(mat * ncol + c) * rows + r] = sw;
-    }
-  }
+  quantize_fp4_block(src, rows, cols, blockIdx.x, blockIdx.y, threadIdx.x, dst, scales);
 #endif
 }
 
@@ -55,7 +31,7 @@ __global__ __launch_bounds__(256) void dequantize_fp4_kernel(const uint32_t* __r
   const int c = blockIdx.x % ncol, sub = lane & 15;
   const int64_t mat = blockIdx.y;
   const int64_t nchunk = cols / 8;
-  const int r0 = blockIdx.x / ncol * kRowsPerBlock + wave * 16 + (lane >> 4);
+  const int r0 = blockIdx.x / ncol * kFp4Rows + wave * 16 + (lane >> 4);
   uint32_t w[4], e[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -88,29 +64,16 @@ __global__ __launch_bounds__(256) void dequantize_fp4_kernel(const uint32_t* __r
 #endif
 }
 
-// Workgroups of one matrix: row blocks, and in each its column groups.
-int64_t fp4_blocks(int32_t rows, int32_t cols) {
-  return ((int64_t)rows + kRowsPerBlock - 1) / kRowsPerBlock * (cols / 128);
-}
-
 moe_status check_fp4(const void* bf16, const uint8_t* codes, const uint8_t* scales, int32_t n_mat, int32_t rows,
                      int32_t cols) {
   if (!bf16 || !codes || !scales) return MOE_ERR_NULL;
   if (n_mat < 0 || n_mat > 65535 || rows < 0 || cols <= 0 || cols % 128) return MOE_ERR_SHAPE;
-  if (fp4_blocks(rows, cols) >= ((int64_t)1 << 31)) return MOE_ERR_SHAPE;
+  if (quantize_fp4_blocks(rows, cols) >= ((int64_t)1 << 31)) return MOE_ERR_SHAPE;
   if (misaligned(bf16, 16) || misaligned(codes, 4) || misaligned(scales, 4)) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
 }  // namespace
-
-moe_status launch_quantize_fp4(const bf16_t* src, int n_mat, int rows, int cols, uint8_t* dst, uint8_t* scales,
-                               hipStream_t st) {
-  if (n_mat == 0 || rows == 0) return MOE_OK;
-  hipLaunchKernelGGL(quantize_fp4_kernel, dim3((unsigned)fp4_blocks(rows, cols), (unsigned)n_mat), dim3(256), 0, st, (const uint4*)src, rows,
-                     cols, (uint32_t*)dst, (uint32_t*)scales);
-  return launch_status();
-}
 
 }  // namespace moe
 
@@ -120,7 +83,10 @@ extern "C" moe_status moe_quantize_fp4(const void* src_bf16, int32_t n_mat, int3
                                        uint8_t* scales, void* stream) {
   const moe_status st = check_fp4(src_bf16, dst, scales, n_mat, rows, cols);
   if (st != MOE_OK) return st;
-  return launch_quantize_fp4((const bf16_t*)src_bf16, n_mat, rows, cols, dst, scales, as_stream(stream));
+  if (n_mat == 0 || rows == 0) return MOE_OK;
+  hipLaunchKernelGGL(quantize_fp4_kernel, dim3((unsigned)quantize_fp4_blocks(rows, cols), (unsigned)n_mat), dim3(256),
+                     0, as_stream(stream), (const uint4*)src_bf16, rows, cols, (uint32_t*)dst, (uint32_t*)scales);
+  return launch_status();
 }
 
 extern "C" moe_status moe_dequantize_fp4(const uint8_t* codes, const uint8_t* scales, int32_t n_mat, int32_t rows,
@@ -128,7 +94,7 @@ extern "C" moe_status moe_dequantize_fp4(const uint8_t* codes, const uint8_t* sc
   const moe_status st = check_fp4(dst_bf16, codes, scales, n_mat, rows, cols);
   if (st != MOE_OK) return st;
   if (n_mat == 0 || rows == 0) return MOE_OK;
-  hipLaunchKernelGGL(dequantize_fp4_kernel, dim3((unsigned)fp4_blocks(rows, cols), (unsigned)n_mat), dim3(256), 0,
+  hipLaunchKernelGGL(dequantize_fp4_kernel, dim3((unsigned)quantize_fp4_blocks(rows, cols), (unsigned)n_mat), dim3(256), 0,
                      as_stream(stream), (const uint32_t*)codes, scales, rows, cols, (uint4*)dst_bf16);
   return launch_status();
 }
