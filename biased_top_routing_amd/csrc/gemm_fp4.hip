@@ -162,15 +162,26 @@ struct Operands4 {
   }
 };
 
-// Tile column of a wavefront's block ni, less its first: gate/up blocks 0, 1 are
-// gate rows of its 32 h columns, 2, 3 the matching up rows.
+// The order of a wavefront's columns: block ni, MFMA row 4 g + r is column
+// 8 g + 4 (ni mod 2) + r of its 32 gate columns (ni < 2) or of the up columns 128
+// further on, or of its first or second 32 output columns, so that a lane holds 8
+// neighbouring columns of a row in two blocks: 4 bytes of codes, 16 of bf16.  The
+// tile column whose LDS row lane l16 reads is col_lane + col_off.
+__device__ __forceinline__ int col_lane(int l16) { return 8 * (l16 >> 2) + (l16 & 3); }
 template <int MODE>
-__device__ __forceinline__ constexpr int col_block(int ni) {
-  return MODE == kGateUp4 ? (ni / 2) * 128 + (ni % 2) * 16 : ni * 16;
+__device__ __forceinline__ constexpr int col_off(int ni) {
+  return (ni / 2) * (MODE == kGateUp4 ? 128 : 32) + (ni % 2) * 4;
+}
+// Physical chunk of logical chunk c in LDS row r of the weights (CPR chunks a
+// row): 8 lanes' rows (4, and 4 that lie 8 further on) meet no bank twice.
+template <int CPR>
+__device__ __forceinline__ int swz_w(int r, int c) {
+  if constexpr (CPR == 8) return c ^ ((r & 3) | (((r >> 3) & 1) << 2));
+  else return c ^ (((r >> 1) & 1) | (((r >> 3) & 1) << 1));
 }
 
-// SwiGLU of one row block: acc[b] gate, acc[b + 2] up; the 8 h values of this lane
-// (block 0's four columns, then block 1's), their codes, and the scale byte of the
+// SwiGLU of one row block: acc[b] gate, acc[b + 2] up; the codes of this lane's 8 h
+// values (neighbouring columns), and the scale byte of the
 // row's 32 columns, which the 4 lanes l16, + 16, + 32, + 48 hold together.
 __device__ __forceinline__ uint32_t swiglu_codes(const f32x4_t (&acc)[NI4], uint32_t* e) {
   float v[8];
@@ -199,9 +210,7 @@ __device__ __forceinline__ void lds_barrier() {
 
 // A wavefront's gate/up row block in LDS: codes [row][kHPitch] and scale bytes [row][4].
 __device__ __forceinline__ void stage_h(uint8_t* hc, uint8_t* hsc, int row, int wn, int g, uint32_t w, uint32_t e) {
-  uint8_t* dst = hc + row * kHPitch + wn * 16 + g * 2;
-  *reinterpret_cast<uint16_t*>(dst) = (uint16_t)w;
-  *reinterpret_cast<uint16_t*>(dst + 8) = (uint16_t)(w >> 16);
+  *reinterpret_cast<uint32_t*>(hc + row * kHPitch + wn * 16 + g * 4) = w;
   if (g == 0) hsc[row * 4 + wn] = (uint8_t)e;
 }
 
@@ -229,9 +238,10 @@ __device__ __forceinline__ void store_y(uint8_t* stg, const f32x4_t (&acc)[NI4],
                                         int rows, int col0, int ncols, int lane) {
   const int l16 = lane & 15, g = lane >> 4;
 #pragma unroll
-  for (int ni = 0; ni < NI4; ++ni)
-    *reinterpret_cast<uint2*>(stg + l16 * kYPitch + (ni * 16 + 4 * g) * 2) =
-        uint2{cvt_bf16x2(acc[ni][0], acc[ni][1]), cvt_bf16x2(acc[ni][2], acc[ni][3])};
+  for (int b = 0; b < NI4; b += 2)
+    *reinterpret_cast<uint4*>(stg + l16 * kYPitch + (b * 16 + 8 * g) * 2) =
+        make_uint4(cvt_bf16x2(acc[b][0], acc[b][1]), cvt_bf16x2(acc[b][2], acc[b][3]),
+                   cvt_bf16x2(acc[b + 1][0], acc[b + 1][1]), cvt_bf16x2(acc[b + 1][2], acc[b + 1][3]));
   __builtin_amdgcn_s_waitcnt(kLgkmWaitZero);
   __builtin_amdgcn_wave_barrier();
   const int col = col0 + (lane & 7) * 8;   // (ncols is a multiple of 128: the segment is whole or absent)
@@ -260,7 +270,7 @@ __global__ __launch_bounds__(kFp4Threads, 1) void gemm_fp4_kernel(Fp4Params p) {
   constexpr int PER = A_CH + B_CH + 1;                 // loads per thread per slice
   constexpr int B_OFF = BM * BK, SC_OFF = B_OFF + BN * BK, STAGE = SC_OFF + NT * 4;
   constexpr int STG_OFF = STAGES * STAGE;              // epilogue staging
-  constexpr int STG = BM * (kHPitch + 4) > NW * 16 * kYPitch ? BM * (kHPitch + 4) : NW * 16 * kYPitch;
+  constexpr int STG = MODE == kGateUp4 ? BM * (kHPitch + 4) : NW * 16 * kYPitch;
   constexpr int PERM_OFF = STG_OFF + STG;              // the next tile's perm entries (gathered rows)
   constexpr int LDS_BYTES = PERM_OFF + BM * 4;
   static_assert(LDS_BYTES <= 163840, "LDS of a CU");
@@ -314,7 +324,7 @@ __global__ __launch_bounds__(kFp4Threads, 1) void gemm_fp4_kernel(Fp4Params p) {
 #pragma unroll
     for (int i = 0; i < B_CH; ++i) {
       const int c = (i * NW + wave) * 64 + lane, r = c / CPR;
-      b_off[i] = (int)(o.ex * o.w_one) + o.wrow(p, r) * o.ldw + swz<CPR>(r, c % CPR) * 16;
+      b_off[i] = (int)(o.ex * o.w_one) + o.wrow(p, r) * o.ldw + swz_w<CPR>(r, c % CPR) * 16;
     }
     const bool sa = wave < NW / 2;                     // this wavefront loads A's scale words, else B's
     if (sa) s_off = tid < ld.rows ? a_row(tid) * 4 : kDrop;
@@ -394,12 +404,12 @@ __global__ __launch_bounds__(kFp4Threads, 1) void gemm_fp4_kernel(Fp4Params p) {
   }
 
   // ------------------------------------------------------------ the products
-  // this lane's fragments in a stage: tile rows arow0 + 16 mi and brow + col_block(ni);
+  // this lane's fragments in a stage: tile rows arow0 + 16 mi and brow + col_off(ni);
   // lane group g supplies the elements [32g, 32g + 32) of the step
   const int arow0 = wm * MI * 16 + l16;
-  const int ch = swz<CPR>(l16, g) * 16;                // (the same for every 16th row)
-  const int brow = wn * (MODE == kGateUp4 ? 32 : 64) + l16;
-  const int a_lane = arow0 * BK + ch, b_lane = B_OFF + brow * BK + ch;
+  const int brow = wn * (MODE == kGateUp4 ? 32 : 64) + col_lane(l16);
+  const int a_lane = arow0 * BK + swz<CPR>(l16, g) * 16;   // (the swizzles are the same for every block)
+  const int b_lane = B_OFF + brow * BK + swz_w<CPR>(col_lane(l16), g) * 16;
   const int sa_lane = SC_OFF + arow0 * 4 + g, sb_lane = SC_OFF + (BM + brow) * 4 + g;
   constexpr int NB = 4, D = 3;                         // A fragments held, and read ahead
   static_assert(MI % NB == 0 && D < NB && PER < MI, "the buffers rotate within a slice");
@@ -417,8 +427,8 @@ __global__ __launch_bounds__(kFp4Threads, 1) void gemm_fp4_kernel(Fp4Params p) {
     ra[buf] = stage[sa_lane + mi * 64];
   };
   auto read_b = [&](const uint8_t* stage, int ni) {
-    fbn[ni] = frag4(stage + b_lane + col_block<MODE>(ni) * BK);
-    rbn[ni] = stage[sb_lane + col_block<MODE>(ni) * 4];
+    fbn[ni] = frag4(stage + b_lane + col_off<MODE>(ni) * BK);
+    rbn[ni] = stage[sb_lane + col_off<MODE>(ni) * 4];
   };
   auto next_b = [&]() {
 #pragma unroll
@@ -478,7 +488,7 @@ __global__ __launch_bounds__(kFp4Threads, 1) void gemm_fp4_kernel(Fp4Params p) {
     advance();
     if (--left > 0) continue;
 
-    // acc[mi][ni][r] holds C[i][j] with i = arow0 + 16 mi (token row), j = block column + 4 (lane / 16) + r
+    // acc[mi][ni][r] holds C[i][j] with i = arow0 + 16 mi (token row), j in the order of col_off
     const bool shared = cd.seg == p.E;
     if constexpr (MODE == kGateUp4) {
       uint8_t* hc = lds + STG_OFF;
@@ -494,6 +504,8 @@ __global__ __launch_bounds__(kFp4Threads, 1) void gemm_fp4_kernel(Fp4Params p) {
       // (the staging is written again only after the next tile's barriers)
     } else {
       bf16_t* out = reinterpret_cast<bf16_t*>(shared ? p.out_shared : p.out_routed);
+      // (stored straight from the registers, in halves or by exchange in whole row
+      // segments, the stores come in one burst in front of the next loads: 3% slower)
 #pragma unroll
       for (int mi = 0; mi < MI; ++mi)
         store_y(lds + STG_OFF + wave * 16 * kYPitch, acc[mi], out, cd.row0, (wm * MI + mi) * 16, cd.rows,
@@ -541,7 +553,7 @@ __global__ __launch_bounds__(256, 1) void gemm_fp4_rows_kernel(Fp4Params p) {
 #pragma unroll
   for (int i = 0; i < B_CH; ++i) {
     const int c = i * NT + tid, r = c / CPR;
-    b_off[i] = (int)(o.ex * o.w_one) + o.wrow(p, r) * o.ldw + swz<CPR>(r, c % CPR) * 16;
+    b_off[i] = (int)(o.ex * o.w_one) + o.wrow(p, r) * o.ldw + swz_w<CPR>(r, c % CPR) * 16;
   }
 #pragma unroll
   for (int i = 0; i < SC_CH; ++i) {
@@ -581,7 +593,7 @@ __global__ __launch_bounds__(256, 1) void gemm_fp4_rows_kernel(Fp4Params p) {
   for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
     for (int ni = 0; ni < NI4; ++ni) acc[mi][ni] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  const int brow = wn * (MODE == kGateUp4 ? 32 : 64) + l16;
+  const int brow = wn * (MODE == kGateUp4 ? 32 : 64) + col_lane(l16);
   int cur = 0, left = o.nk1;                           // K steps left of the current expert
   for (int kt = 0; kt < ns; ++kt) {
     wait_loads<PER, STAGES - 2>(min(ns - 1, kt + STAGES - 2) - kt);
@@ -591,15 +603,15 @@ __global__ __launch_bounds__(256, 1) void gemm_fp4_rows_kernel(Fp4Params p) {
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk) {
       if (kk == 1 && left < 2) break;
-      const int ch = swz<CPR>(l16, kk * 4 + g) * 16;
+      const int ch = swz<CPR>(l16, kk * 4 + g) * 16, chw = swz_w<CPR>(col_lane(l16), kk * 4 + g) * 16;
       const uint8_t* sca = base + SC_OFF + kk * BM * 4 + g;
       const uint8_t* scb = base + SC_OFF + (2 * BM + kk * BN) * 4 + g;
       i32x8_t fb[NI4];
       int sb[NI4];
 #pragma unroll
       for (int ni = 0; ni < NI4; ++ni) {
-        const int r = brow + col_block<MODE>(ni);
-        fb[ni] = frag4(base + BM * BK + r * BK + ch);
+        const int r = brow + col_off<MODE>(ni);
+        fb[ni] = frag4(base + BM * BK + r * BK + chw);
         sb[ni] = scb[r * 4];
       }
 #pragma unroll
