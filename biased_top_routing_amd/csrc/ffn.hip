@@ -135,7 +135,7 @@ __global__ __launch_bounds__(1024) void build_tiles_quantize_fp4_kernel(const in
     return;
   }
   const int64_t b = ((int64_t)blockIdx.x - nb) * 4 + (threadIdx.x >> 8);
-  if (b < blocks) quantize_fp4_block(x, rows, cols, b, 0, threadIdx.x & 255, dst, scales);
+  if (b < blocks) quantize_fp4_block<false>(x, rows, cols, b, 0, threadIdx.x & 255, dst, scales);
 #endif
 }
 

