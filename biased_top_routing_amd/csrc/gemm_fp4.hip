@@ -16,15 +16,17 @@
 // wavefront 8 x 4 MFMA blocks, and the workgroups stay: each takes every 32nd tile
 // of its XCD's contiguous share of the table (one expert's tiles run on one XCD
 // at the same time and meet in its L2), and the loads run through the tiles
-// without a break.  K advances one 128-wide step (64 bytes of codes a row) per
-// slice through a ring of 4 LDS stages filled by direct-to-LDS buffer loads
-// (16-byte chunks, XOR swizzle per row), the rows' scale words of the step beside
-// them; when a tile's last slices are multiplied, the next tile's first ones are
-// on their way, and its epilogue runs over them.  A 4-bit MFMA takes half the time
-// of an 8-bit one on the same operand bytes, so the fragment reads are kept ahead
-// of it: a wavefront reads the token rows' fragments 3 blocks before their MFMAs
-// and the next slice's first ones under the current slice's last (each barrier
-// therefore covers the slice after the one it opens).
+// without a break.  K advances two 128-wide steps (128 bytes of codes a row: whole
+// cache lines; single steps, in half lines, loaded 20% slower) per slice through two
+// LDS stages filled by direct-to-LDS buffer loads (16-byte chunks, XOR swizzle per
+// row), the rows' scale words of both steps beside them.  There is one barrier a
+// slice, two row blocks before its end: the next slice has landed by then, this
+// one's last fragments have been read, and the loads of the slice after next go
+// out into its stage, one after each row block's MFMAs.  A 4-bit MFMA takes half the
+// time of an 8-bit one on the same operand bytes, so the fragment reads are kept
+// ahead of it: the token rows' 3 blocks, the weights' a K step.  When a tile's last
+// slices are multiplied the next tile's first ones are on their way, and its
+// epilogue runs over them.
 //
 // Few rows per expert: 32 x 256 tiles that stream the weights, one workgroup of
 // 4 wavefronts per tile, two K steps (128 bytes a row: whole cache lines) per
@@ -101,6 +103,14 @@ __device__ __forceinline__ void wait_loads(int n) {
   else wait_loads<PER, MAX - 1>(n);
 }
 
+// v as a value that the compiler cannot compute ahead of this point (what a tile's
+// begin and epilogue derive from the lane would otherwise be computed before the
+// loops and held, or spilled, through them).
+__device__ __forceinline__ int opaque(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
 // Entry L of the tile table, read through the scalar cache.
 __device__ __forceinline__ TileDesc tile_at(const Fp4Params& p, int L) {
   typedef const __attribute__((address_space(4))) int32_t* cptr;
@@ -155,7 +165,7 @@ struct Operands4 {
     c0 = MODE == kGateUp4 ? d.nt * 128 - ex * p.I : d.nt * 256;
   }
 
-  // weight row (in its expert) of tile column row r
+  // weight row (in its expert) of tile column row r, the last one for rows past the columns
   __device__ __forceinline__ int wrow(const Fp4Params& p, int r) const {
     if constexpr (MODE == kGateUp4) return c0 + (r < 128 ? r : r - 128 + p.I);
     else return min(c0 + r, ncols - 1);
@@ -261,15 +271,15 @@ constexpr int kFp4Threads = 512;
 
 template <int MODE>
 __global__ __launch_bounds__(kFp4Threads, 1) void gemm_fp4_kernel(Fp4Params p) {
-  constexpr int WM = 2, WN = 4, MI = 8, STAGES = 4;
+  constexpr int WM = 2, WN = 4, MI = 8;
   constexpr int NT = kFp4Threads, NW = NT / 64, BM = WM * MI * 16, BN = 256;
   static_assert(WM * WN == NW && BM == kFp4BM && BN == kFp4BN2, "tile shape");
-  constexpr int BK = 64, CPR = BK / 16;                // bytes and 16-byte chunks of a row per slice
-  constexpr int A_CH = BM * CPR / NT, B_CH = BN * CPR / NT;
-  static_assert(BM + BN == NT && BM == NT / 2, "one scale word a thread: wavefronts 0-3 A's, 4-7 B's");
-  constexpr int PER = A_CH + B_CH + 1;                 // loads per thread per slice
-  constexpr int B_OFF = BM * BK, SC_OFF = B_OFF + BN * BK, STAGE = SC_OFF + NT * 4;
-  constexpr int STG_OFF = STAGES * STAGE;              // epilogue staging
+  constexpr int BK = 128, CPR = BK / 16;               // bytes (two K steps) and 16-byte chunks of a row per slice
+  constexpr int A_CH = BM * CPR / NT, B_CH = BN * CPR / NT, RPL = NT / CPR;   // loads per thread, rows between them
+  static_assert(BM + BN == NT && BM == NT / 2, "one scale word a thread and step: wavefronts 0-3 A's, 4-7 B's");
+  constexpr int PER = A_CH + B_CH + 2;                 // loads per thread per slice
+  constexpr int B_OFF = BM * BK, SC_OFF = B_OFF + BN * BK, STAGE = SC_OFF + 2 * NT * 4;
+  constexpr int STG_OFF = 2 * STAGE;                   // epilogue staging
   constexpr int STG = MODE == kGateUp4 ? BM * (kHPitch + 4) : NW * 16 * kYPitch;
   constexpr int PERM_OFF = STG_OFF + STG;              // the next tile's perm entries (gathered rows)
   constexpr int LDS_BYTES = PERM_OFF + BM * 4;
@@ -294,14 +304,17 @@ __global__ __launch_bounds__(kFp4Threads, 1) void gemm_fp4_kernel(Fp4Params p) {
   if (q >= q_end) return;
 
   // ------------------------------------------------------------ the loads
-  // The stream of slices runs 3 slices ahead of the products, through the tiles.
+  // The stream of slices runs a slice ahead of the products, through the tiles.
   TileDesc ld = tile_at(p, entry(q)), nd = ld;         // the tile being loaded, the one after it
   bool more = false;                                   // nd is one
-  int left_l = 0, in_l = 0;                            // slices of ld to load yet, of its current expert
+  int left_l = 0, in_l = 0;                            // experts of ld to load yet, K steps of the current one
   int ls = 0;                                          // stage the next slice goes to
   int ak = 0, wk = 0, sk = 0;                          // scalar offsets of the next slice: A, W, scale words
-  int a_off[A_CH], b_off[B_CH], s_off = 0;
-  int w_next = 0, s_step = 0, s_next = 0, nk1 = 1;     // steps to the next expert's weights, between scale planes
+  // A: an offset a load where rows are gathered, else one and the rows' distance; W: one,
+  // the rows' distance, and what lies between gate and up rows
+  constexpr int A_OFF = MODE == kGateUp4 ? A_CH : 1;
+  int a_off[A_OFF], b_off = 0, s_off = 0, a_dist = 0, w_dist = 0, w_gap = 0;
+  int s_step = 0, a_skip = 0, w_skip = 0, s_skip = 0, nk1 = 1;   // scale plane distance; extra steps to the next expert
   const uint8_t *baseA = nullptr, *baseW = nullptr, *baseS = nullptr;
   int bytesA = 0, bytesW = 0, bytesS = 0;              // 0 when the stream has ended: its loads are dropped
   // the perm entries of a gathered tile's rows into LDS (wavefronts 0-3)
@@ -314,105 +327,103 @@ __global__ __launch_bounds__(kFp4Threads, 1) void gemm_fp4_kernel(Fp4Params p) {
   auto begin = [&]() {
     const Operands4<MODE> o(p, ld);
     const int32_t* rows = reinterpret_cast<const int32_t*>(lds + PERM_OFF);
-    // row of A for tile row r, or one past the descriptor (the range check drops the load)
-    auto a_row = [&](int r) { return r >= ld.rows ? o.a_rows + 1 : o.gather ? rows[r] / p.k : r; };
+    const int tid = opaque(threadIdx.x), lr = tid / CPR, ca = swz<CPR>(lr, tid % CPR) * 16, cw = swz_w<CPR>(lr, tid % CPR) * 16;
+    static_assert(RPL % 16 == 0, "a thread's rows have one swizzle");
+    // (rows past the tile's lie past the descriptor: the range check drops their loads)
+    if constexpr (MODE == kGateUp4) {
 #pragma unroll
-    for (int i = 0; i < A_CH; ++i) {
-      const int c = (i * NW + wave) * 64 + lane, r = c / CPR;
-      a_off[i] = a_row(r) * o.lda + swz<CPR>(r, c % CPR) * 16;
+      for (int i = 0; i < A_CH; ++i) {
+        const int r = lr + i * RPL;
+        a_off[i] = (r >= ld.rows ? o.a_rows + 1 : o.gather ? rows[r] / p.k : r) * o.lda + ca;
+      }
+    } else {
+      a_off[0] = lr * o.lda + ca;
+      a_dist = RPL * o.lda;
     }
-#pragma unroll
-    for (int i = 0; i < B_CH; ++i) {
-      const int c = (i * NW + wave) * 64 + lane, r = c / CPR;
-      b_off[i] = (int)(o.ex * o.w_one) + o.wrow(p, r) * o.ldw + swz_w<CPR>(r, c % CPR) * 16;
-    }
+    b_off = (int)(o.ex * o.w_one) + (o.c0 + lr) * o.ldw + cw;
+    w_dist = RPL * o.ldw;
+    w_gap = MODE == kGateUp4 ? (p.I - 128) * o.ldw : 0;
     const bool sa = wave < NW / 2;                     // this wavefront loads A's scale words, else B's
-    if (sa) s_off = tid < ld.rows ? a_row(tid) * 4 : kDrop;
-    else s_off = o.ex * o.sw_one + o.wrow(p, tid - BM) * 4;
+    if (sa) s_off = tid < ld.rows ? (o.gather ? rows[tid] / p.k : tid) * 4 : kDrop;
+    else s_off = o.ex * o.sw_one + (o.c0 + tid - BM + (MODE == kGateUp4 && tid - BM >= 128 ? p.I - 128 : 0)) * 4;
     baseA = o.A; bytesA = o.a_bytes;
     baseW = o.W; bytesW = o.w_bytes;
     baseS = sa ? o.SA : o.SW;
     bytesS = sa ? o.sa_bytes : o.sw_bytes;
     s_step = sa ? o.sa_stride : o.sw_stride;
-    w_next = (int)o.w_one - o.nk1 * BK;
-    s_next = sa ? 0 : o.sw_one - o.nk1 * o.sw_stride;
+    // from the slice after an expert's last one (which may hold one step only) to the next expert's first
+    const int over = (o.nk1 + 1) / 2 * 2 - o.nk1;
+    a_skip = -over * 64;
+    w_skip = (int)o.w_one - o.nk1 * 64 - over * 64;
+    s_skip = sa ? -over * s_step : o.sw_one - (o.nk1 + over) * s_step;
     ak = wk = sk = 0;
     in_l = nk1 = o.nk1;
-    left_l = o.nk1 * o.nexp;
+    left_l = o.nexp;
     q += step;
     more = q < q_end;
     if (more) nd = tile_at(p, entry(q));
   };
-  // Load i of PER of the stream's next slice.
+  // Load i of PER of the stream's next slice.  (Only offsets that lie inside the
+  // descriptor whatever the lane go through the scalar offset: the range check
+  // compares the lane's offset with what the scalar one leaves of it.)
   auto issue_part = [&](int i) {
     uint8_t* sb = lds + ls * STAGE + wave * 1024;
     if (i < A_CH)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(baseA, bytesA), (lds_void_t*)(sb + i * NW * 1024), 16, a_off[i],
-                                               ak, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(baseA, bytesA), (lds_void_t*)(sb + i * NW * 1024), 16,
+                                               MODE == kGateUp4 ? a_off[i % A_OFF] : a_off[0] + i * a_dist, ak, 0, 0);
     else if (i < A_CH + B_CH)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(baseW, bytesW),
-                                               (lds_void_t*)(sb + B_OFF + (i - A_CH) * NW * 1024), 16, b_off[i - A_CH],
-                                               wk, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          make_rsrc(baseW, bytesW), (lds_void_t*)(sb + B_OFF + (i - A_CH) * NW * 1024), 16,
+          b_off + (i - A_CH) * w_dist + ((i - A_CH) * RPL >= 128 ? w_gap : 0), wk, 0, 0);
     else
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(baseS, bytesS),
-                                               (lds_void_t*)(lds + ls * STAGE + SC_OFF + wave * 256), 4, s_off, sk, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          make_rsrc(baseS, bytesS), (lds_void_t*)(lds + ls * STAGE + SC_OFF + (i - A_CH - B_CH) * NT * 4 + wave * 256),
+          4, (int)((unsigned)s_off + (unsigned)((i - A_CH - B_CH) * s_step)), sk, 0, 0);
   };
   // After a slice's loads.
   auto advance = [&]() {
-    --left_l;
     ak += BK;
     wk += BK;
-    sk += s_step;
-    if (MODE == kDown4 && --in_l == 0) {               // the next shared expert's weights
+    sk += 2 * s_step;
+    in_l -= 2;
+    if (in_l <= 0) {
+      --left_l;
       in_l = nk1;
-      wk += w_next;
-      sk += s_next;
+      if (MODE == kDown4) {                            // the next shared expert's K range
+        ak += a_skip;
+        wk += w_skip;
+        sk += s_skip;
+      }
     }
-    ls = ls == STAGES - 1 ? 0 : ls + 1;
+    ls ^= 1;
   };
   // Before a slice's loads: the next tile is begun where the last one has ended.
   auto prepare = [&]() {
     if (left_l > 0) return;
     if (!more) {
       bytesA = bytesW = bytesS = 0;
+      ak = wk = sk = 0;
       return;
     }
     ld = nd;
-    if (MODE == kGateUp4 && p.perm != nullptr && p.H < 4 * 128) {
-      // tiles of fewer than 4 slices: the perm entries asked for below may not have arrived
-      wait_vm<0>();
-      lds_barrier();
-    }
     begin();
     if (MODE == kGateUp4 && p.perm != nullptr) {
       lds_barrier();                                   // all have read this tile's entries: on to the next one's
       if (more) load_perm(nd);
     }
   };
-  load_perm(ld);
-  wait_vm<0>();
-  lds_barrier();
-  begin();
-  lds_barrier();
-  if (more) load_perm(nd);
-#pragma unroll 1
-  for (int s = 0; s < STAGES - 1; ++s) {
-    prepare();
-#pragma unroll
-    for (int i = 0; i < PER; ++i) issue_part(i);
-    advance();
-  }
 
   // ------------------------------------------------------------ the products
   // this lane's fragments in a stage: tile rows arow0 + 16 mi and brow + col_off(ni);
-  // lane group g supplies the elements [32g, 32g + 32) of the step
+  // lane group g supplies the elements [32g, 32g + 32) of a step (the swizzles are the
+  // same for every block, and a row's second step is 64 bytes away by exclusive or)
   const int arow0 = wm * MI * 16 + l16;
   const int brow = wn * (MODE == kGateUp4 ? 32 : 64) + col_lane(l16);
-  const int a_lane = arow0 * BK + swz<CPR>(l16, g) * 16;   // (the swizzles are the same for every block)
+  const int a_lane = arow0 * BK + swz<CPR>(l16, g) * 16;
   const int b_lane = B_OFF + brow * BK + swz_w<CPR>(col_lane(l16), g) * 16;
   const int sa_lane = SC_OFF + arow0 * 4 + g, sb_lane = SC_OFF + (BM + brow) * 4 + g;
-  constexpr int NB = 4, D = 3;                         // A fragments held, and read ahead
-  static_assert(MI % NB == 0 && D < NB && PER < MI, "the buffers rotate within a slice");
+  constexpr int NB = 4, D = 2;                         // A fragments held, and read ahead
+  static_assert(MI % NB == 0 && D < NB && PER == MI + 2, "the buffers rotate within a step; the issue schedule");
   f32x4_t acc[MI][NI4];
   i32x8_t fa[NB], fb[NI4], fbn[NI4];
   int ra[NB], rb[NI4], rbn[NI4];
@@ -422,13 +433,13 @@ __global__ __launch_bounds__(kFp4Threads, 1) void gemm_fp4_kernel(Fp4Params p) {
 #pragma unroll
       for (int ni = 0; ni < NI4; ++ni) acc[mi][ni] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   };
-  auto read_a = [&](int buf, const uint8_t* stage, int mi) {
-    fa[buf] = frag4(stage + a_lane + mi * 16 * BK);
-    ra[buf] = stage[sa_lane + mi * 64];
+  auto read_a = [&](const uint8_t* stage, int kk, int mi) {
+    fa[mi % NB] = frag4(stage + (a_lane ^ (kk * 64)) + mi * 16 * BK);
+    ra[mi % NB] = stage[sa_lane + kk * NT * 4 + mi * 64];
   };
-  auto read_b = [&](const uint8_t* stage, int ni) {
-    fbn[ni] = frag4(stage + b_lane + col_off<MODE>(ni) * BK);
-    rbn[ni] = stage[sb_lane + col_off<MODE>(ni) * 4];
+  auto read_b = [&](const uint8_t* stage, int kk, int ni) {
+    fbn[ni] = frag4(stage + (b_lane ^ (kk * 64)) + col_off<MODE>(ni) * BK);
+    rbn[ni] = stage[sb_lane + kk * NT * 4 + col_off<MODE>(ni) * 4];
   };
   auto next_b = [&]() {
 #pragma unroll
@@ -437,86 +448,118 @@ __global__ __launch_bounds__(kFp4Threads, 1) void gemm_fp4_kernel(Fp4Params p) {
       rb[ni] = rbn[ni];
     }
   };
-  auto slices_of = [&](const TileDesc& d) {
-    return (MODE == kDown4 ? (d.seg == p.E ? p.S * p.I : p.I) : p.H) / 128;
+  auto read_first = [&](const uint8_t* stage) {        // a slice's first fragments
+#pragma unroll
+    for (int ni = 0; ni < NI4; ++ni) read_b(stage, 0, ni);
+#pragma unroll
+    for (int i = 0; i < D; ++i) read_a(stage, 0, i);
   };
-  wait_vm<PER*(STAGES - 2)>();                         // the first slice
+  auto multiply = [&](int mi) {
+#pragma unroll
+    for (int ni = 0; ni < NI4; ++ni)
+      acc[mi][ni] = mfma_fp4(fb[ni], fa[mi % NB], acc[mi][ni], rb[ni], ra[mi % NB]);
+  };
+  // K step KK of the slice in stage `here`; of the second one all but the last row
+  // block, which is multiplied over the barrier.  The loads of the slice to come go
+  // out one after each row block of the first step.
+  auto products = [&](auto kkc, const uint8_t* here) {
+    constexpr int KK = decltype(kkc)::value;
+#pragma unroll
+    for (int mi = 0; mi < MI - KK; ++mi) {
+      if (mi + D < MI) read_a(here, KK, mi + D);
+      else if (KK == 0) read_a(here, 1, mi + D - MI);
+      if (KK == 0 && mi < NI4) read_b(here, 1, mi);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(mi);
+      if (KK == 0) issue_part(2 + mi);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (KK == 0) {
+      next_b();
+      advance();
+    }
+  };
+  load_perm(ld);
+  wait_vm<0>();
   lds_barrier();
+  begin();
+  lds_barrier();
+  if (more) load_perm(nd);
 #pragma unroll
-  for (int ni = 0; ni < NI4; ++ni) read_b(lds, ni);
-#pragma unroll
-  for (int i = 0; i < D; ++i) read_a(i, lds, i);
-  next_b();
+  for (int i = 0; i < PER; ++i) issue_part(i);
+  advance();
   clear();
 
   int qc = blockIdx.x >> 3;
   TileDesc cd = tile_at(p, entry(qc)), after = cd;     // the tile being computed, the one after it
   if (qc + step < q_end) after = tile_at(p, entry(qc + step));
-  int left = slices_of(cd), cs = 0;                    // slices of cd to compute, the stage of the next one
+  const int steps1 = (MODE == kDown4 ? p.I : p.H) / 128;   // K steps of an expert
+  auto experts = [&]() { return MODE == kDown4 && cd.seg == p.E ? p.S : 1; };
+  int cs = 0, left = steps1, exps = experts();         // stage of the next slice; K steps left of the expert, experts
+  bool half = false;                                   // a slice's last row block is to be multiplied
+  bool done = false;                                   // ... and it is the tile's last slice
   while (true) {
-    // One slice: its B fragments and its first D A fragments are in registers; it
-    // leaves the next slice's there.  (After the last slice: read, not used.)
+    // The slice's one barrier: the next slice has landed, everywhere (it was asked for a
+    // slice ago), and this one's stage is free; loading into it begins.
+    wait_vm<0>();
+    lds_barrier();
     prepare();
-    wait_vm<PER*(STAGES - 3)>();                       // this slice and the next one have landed
-    lds_barrier();                                     // ... everywhere, and the stage loaded into is free
     const uint8_t* here = lds + cs * STAGE;
-    cs = cs == STAGES - 1 ? 0 : cs + 1;
-    const uint8_t* next = lds + cs * STAGE;
-    if (wm * MI * 16 < cd.rows) {
-#pragma unroll
-      for (int mi = 0; mi < MI; ++mi) {
-        read_a((mi + D) % NB, mi + D < MI ? here : next, (mi + D) % MI);
-        if (mi >= MI - NI4) read_b(next, mi - (MI - NI4));
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int ni = 0; ni < NI4; ++ni)
-          acc[mi][ni] = mfma_fp4(fb[ni], fa[mi % NB], acc[mi][ni], rb[ni], ra[mi % NB]);
-        // the loads of the slice to come, one after each of the first row blocks: a
-        // wavefront whose load waits for room in the memory pipeline has MFMAs running
-        if (mi < PER) issue_part(mi);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    } else {                                           // no rows here, perhaps some in the next tile
-#pragma unroll
-      for (int i = 0; i < PER; ++i) issue_part(i);
-#pragma unroll
-      for (int i = 0; i < D; ++i) read_a(i, next, i);
-#pragma unroll
-      for (int ni = 0; ni < NI4; ++ni) read_b(next, ni);
-    }
+    cs ^= 1;
+    read_first(here);                                  // (D < NB: not the buffer in use; after the last slice: not used)
+    __builtin_amdgcn_sched_barrier(0);
+    if (half) multiply(MI - 1);
+    issue_part(0);
+    issue_part(1);
     next_b();
-    advance();
-    if (--left > 0) continue;
-
-    // acc[mi][ni][r] holds C[i][j] with i = arow0 + 16 mi (token row), j in the order of col_off
-    const bool shared = cd.seg == p.E;
-    if constexpr (MODE == kGateUp4) {
-      uint8_t* hc = lds + STG_OFF;
-      uint8_t* hsc = hc + BM * kHPitch;
+    if (done) {
+      // acc[mi][ni][r] holds C[i][j] with i = arow0 + 16 mi (token row), j in the order of col_off
+      const bool shared = cd.seg == p.E;
+      const int tid = opaque(threadIdx.x), lane = tid & 63, l16 = lane & 15, g = lane >> 4;
+      if constexpr (MODE == kGateUp4) {
+        uint8_t* hc = lds + STG_OFF;
+        uint8_t* hsc = hc + BM * kHPitch;
 #pragma unroll
-      for (int mi = 0; mi < MI; ++mi) {
-        uint32_t e;
-        const uint32_t w = swiglu_codes(acc[mi], &e);
-        stage_h(hc, hsc, arow0 + mi * 16, wn, g, w, e);
+        for (int mi = 0; mi < MI; ++mi) {
+          uint32_t e;
+          const uint32_t w = swiglu_codes(acc[mi], &e);
+          stage_h(hc, hsc, wm * MI * 16 + l16 + mi * 16, wn, g, w, e);
+        }
+        lds_barrier();
+        store_h<NT>(p, cd, shared, hc, hsc, tid);
+        // (the staging is written again only after the next slice's barrier)
+      } else {
+        bf16_t* out = reinterpret_cast<bf16_t*>(shared ? p.out_shared : p.out_routed);
+        // (stored straight from the registers, in halves or by exchange in whole row
+        // segments, the stores come in one burst in front of the next loads: 3% slower)
+#pragma unroll
+        for (int mi = 0; mi < MI; ++mi)
+          store_y(lds + STG_OFF + wave * 16 * kYPitch, acc[mi], out, cd.row0, (wm * MI + mi) * 16, cd.rows,
+                  cd.nt * BN + wn * 64, p.H, lane);
       }
-      lds_barrier();
-      store_h<NT>(p, cd, shared, hc, hsc, tid);
-      // (the staging is written again only after the next tile's barriers)
-    } else {
-      bf16_t* out = reinterpret_cast<bf16_t*>(shared ? p.out_shared : p.out_routed);
-      // (stored straight from the registers, in halves or by exchange in whole row
-      // segments, the stores come in one burst in front of the next loads: 3% slower)
-#pragma unroll
-      for (int mi = 0; mi < MI; ++mi)
-        store_y(lds + STG_OFF + wave * 16 * kYPitch, acc[mi], out, cd.row0, (wm * MI + mi) * 16, cd.rows,
-                cd.nt * BN + wn * 64, p.H, lane);
+      qc += step;
+      if (qc >= q_end) break;
+      cd = after;
+      if (qc + step < q_end) after = tile_at(p, entry(qc + step));
+      exps = experts();
+      clear();
     }
-    qc += step;
-    if (qc >= q_end) break;
-    cd = after;
-    if (qc + step < q_end) after = tile_at(p, entry(qc + step));
-    left = slices_of(cd);
-    clear();
+    half = wm * MI * 16 < cd.rows;
+    if (!half) {                                       // no rows here, perhaps some in the next tile
+#pragma unroll
+      for (int i = 2; i < PER; ++i) issue_part(i);
+      advance();
+    } else {
+      products(std::integral_constant<int, 0>{}, here);
+      if (left >= 2) products(std::integral_constant<int, 1>{}, here);
+      else half = false;                               // a slice of one step: what was read ahead is not used
+    }
+    left -= 2;
+    done = false;
+    if (left <= 0) {
+      left = steps1;
+      done = --exps == 0;
+    }
   }
 #endif
 }
