@@ -96,10 +96,15 @@ constexpr int kFp8BM = MOE_FP8_BM;
 constexpr int kFp8BNH = 128;
 constexpr int kFp8BN2 = 256;
 constexpr int kFp8MaxKC = 64;
-// MXFP4 GEMMs: 256 token rows, or 32 where the routed experts get at most 32
-// rows each on average (the GEMMs then only stream weights); 128 h columns per
-// gate/up tile, 256 output columns per down tile.
-constexpr int kFp4BM = 256, kFp4DecBM = 32;
+// MXFP4 GEMMs: tiles of 256 token rows, or of 32 or 64 where the routed experts get
+// at most 24 or 56 rows each on average: the GEMMs then stream weights, and a tile's
+// height decides how often (H = 7168, I = 2048, 256 experts, the whole call in us
+// with 32 / 64 / 256 rows a tile: 24 rows an expert 1069 / 1093 / 1326, 32 rows
+// 1277 / 1133 / 1358, 48 rows 1648 / 1205 / 1367, 64 rows 1998 / 1605 / 1413; 128
+// rows a tile are nowhere best); 128 h columns per gate/up tile, 256 output columns
+// per down tile.
+constexpr int kFp4BM = 256, kFp4RowsBM = 32, kFp4MidBM = 64;
+constexpr int kFp4RowsAvg = 24, kFp4MidAvg = 56;
 constexpr int kFp4BNH = 128, kFp4BN2 = 256;
 
 // Row tiles per group in the tile order of a segment (see build_tiles_kernel).
@@ -128,10 +133,7 @@ struct TileDesc {
 constexpr int kStripeGateUp = 8;
 constexpr int kStripeDown = 0;
 constexpr int kStripeFp8 = 2;
-#ifndef SFP4
-#define SFP4 2
-#endif
-constexpr int kStripeFp4 = SFP4;
+constexpr int kStripeFp4 = 2;
 
 // Position j of XCD xcd in runs of P consecutive entries dealt to the 8 XCDs in turn.
 __host__ __device__ inline int xcd_run_index(int j, int xcd, int P) {
@@ -192,7 +194,7 @@ struct FfnLayout {
   explicit FfnLayout(const moe_cfg* c) {
     const int64_t P = pairs(c);
     const bool f8 = c->wgt == MOE_FP8_E4M3, f4 = c->wgt == MOE_MXFP4;
-    const int bm4 = P <= (int64_t)kFp4DecBM * c->E ? kFp4DecBM : kFp4BM;
+    const int bm4 = P <= (int64_t)kFp4RowsAvg * c->E ? kFp4RowsBM : P <= (int64_t)kFp4MidAvg * c->E ? kFp4MidBM : kFp4BM;
     dec = small_batch(c);
     bm1 = f4 ? bm4 : f8 ? kFp8BM : dec ? kDecBM : kBM1;
     bm1_alt = f4 || f8 || dec ? 0 : kBM1Alt;

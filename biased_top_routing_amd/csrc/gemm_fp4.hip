@@ -28,9 +28,8 @@
 // slices are multiplied the next tile's first ones are on their way, and its
 // epilogue runs over them.
 //
-// Few rows per expert: 32 x 256 tiles that stream the weights, one workgroup of
-// 4 wavefronts per tile, two K steps (128 bytes a row: whole cache lines) per
-// slice and 4 stages.
+// Few rows per expert: 32 x 256 or 64 x 256 tiles that stream the weights, one
+// workgroup of 4 wavefronts per tile, two K steps per slice and 4 or 3 stages.
 //
 // The shared experts' down GEMM walks the experts one after the other.  The
 // gate/up tile's 256 weight rows are the 128 gate rows and the 128 up rows of 128
@@ -565,9 +564,9 @@ __global__ __launch_bounds__(kFp4Threads, 1) void gemm_fp4_kernel(Fp4Params p) {
 }
 
 // ------------------------------------------------------------------ few rows per expert
-template <int MODE>
+template <int MODE, int BM, int STAGES>
 __global__ __launch_bounds__(256, 1) void gemm_fp4_rows_kernel(Fp4Params p) {
-  constexpr int WN = 4, MI = kFp4DecBM / 16, STAGES = 4, NT = 256, NW = 4, BM = kFp4DecBM, BN = 256;
+  constexpr int WN = 4, MI = BM / 16, NT = 256, NW = 4, BN = 256;
   constexpr int BK = 128, CPR = BK / 16;               // bytes (two K steps) and 16-byte chunks of a row per slice
   constexpr int A_CH = BM * CPR / NT, B_CH = BN * CPR / NT;
   static_assert(BM * CPR % NT == 0 && BN * CPR % NT == 0, "whole loads per thread");
@@ -692,9 +691,11 @@ __global__ __launch_bounds__(256, 1) void gemm_fp4_rows_kernel(Fp4Params p) {
 template <int MODE>
 moe_status launch_gemm_fp4(const FfnLayout& L, int64_t max_tiles, const Fp4Params& p, hipStream_t st) {
   if (max_tiles == 0) return MOE_OK;
-  if (L.bm1 == kFp4DecBM) {
-    hipLaunchKernelGGL(gemm_fp4_rows_kernel<MODE>, dim3((unsigned)grouped_grid(max_tiles, kStripeFp4)), dim3(256), 0,
-                       st, p);
+  const dim3 rows_grid((unsigned)grouped_grid(max_tiles, kStripeFp4));
+  if (L.bm1 == kFp4RowsBM) {
+    hipLaunchKernelGGL((gemm_fp4_rows_kernel<MODE, kFp4RowsBM, 4>), rows_grid, dim3(256), 0, st, p);
+  } else if (L.bm1 == kFp4MidBM) {
+    hipLaunchKernelGGL((gemm_fp4_rows_kernel<MODE, kFp4MidBM, 3>), rows_grid, dim3(256), 0, st, p);
   } else {
     // one workgroup a CU (its LDS leaves no room for two), whole rounds of the 8 XCDs
     const int64_t grid = std::min<int64_t>(std::max(cu_count() / 8 * 8, 8), (int64_t)align_up((size_t)max_tiles, 8));

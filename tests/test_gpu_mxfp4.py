@@ -200,8 +200,8 @@ def _spread(bits, g):
 
 
 CASES = [
-    # (T, H, E, G, M, k, S, I): small tiles (up to 32 rows an expert on average) and large ones, odd numbers
-    # of 128-wide K steps in either GEMM, one step only, several shared experts, ragged tiles, one token,
+    # (T, H, E, G, M, k, S, I): tiles of 32 rows (up to 24 rows an expert on average), 64 (56) and 256, odd
+    # numbers of 128-wide K steps in either GEMM, one step only, several shared experts, ragged tiles, one token,
     # more experts than pairs, column tiles past the end
     (1, 256, 8, 2, 1, 2, 1, 128),
     (1, 128, 4, 1, 1, 1, 0, 128),
@@ -213,6 +213,8 @@ CASES = [
     (1000, 1152, 8, 8, 3, 2, 2, 256),
     (130, 7168, 4, 2, 1, 2, 1, 128),
     (90, 256, 4, 1, 1, 2, 1, 2048),
+    (100, 1152, 8, 2, 2, 3, 2, 384),
+    (400, 256, 16, 4, 2, 2, 3, 128),
 ]
 
 
@@ -261,7 +263,7 @@ def test_expert_ffn_mxfp4(T, H, E, G, M, k, S, I):
     assert np.isfinite(host(y)).all()
 
 
-@pytest.mark.parametrize("T,H,E,G,M,k,S,I", [CASES[0], CASES[3], CASES[5]])
+@pytest.mark.parametrize("T,H,E,G,M,k,S,I", [CASES[0], CASES[3], CASES[5], CASES[10]])
 def test_gather_and_phases_equal_sorted(T, H, E, G, M, k, S, I):
     """Rows gathered from x, and the two phases called apart, give the same bits as the whole call on sorted
     rows; rows that no pair has stay as they were."""
