@@ -422,7 +422,7 @@ extern "C" moe_status moe_combine_backward(const moe_cfg* cfg, const void* dy, c
 extern "C" moe_status moe_combine_local_backward(const moe_cfg* cfg, const void* dy, const void* y_perm,
                                                  const int32_t* inv, const float* topk_w, void* dy_perm,
                                                  float* d_topk_w, void* stream) {
-  moe_status st = validate_cfg(cfg);
+  moe_status st = validate_share(cfg);
   if (st != MOE_OK) return st;
   if (!bwd_dtypes_ok(cfg)) return MOE_ERR_UNSUPPORTED;
   if (cfg->T == 0) return MOE_OK;
@@ -539,7 +539,7 @@ extern "C" moe_status moe_dispatch_backward(const moe_cfg* cfg, const void* dx_p
 extern "C" moe_status moe_dispatch_local_backward(const moe_cfg* cfg, const void* dx_perm, const void* dx_shared,
                                                   const float* dx_router, const int32_t* inv, void* dx,
                                                   void* stream) {
-  moe_status st = validate_cfg(cfg);
+  moe_status st = validate_share(cfg);
   if (st != MOE_OK) return st;
   if (!bwd_dtypes_ok(cfg)) return MOE_ERR_UNSUPPORTED;
   if (cfg->T == 0) return MOE_OK;

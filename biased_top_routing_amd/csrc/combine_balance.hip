@@ -221,7 +221,7 @@ extern "C" moe_status moe_combine(const moe_cfg* cfg, const void* y_perm, const 
 
 extern "C" moe_status moe_combine_local(const moe_cfg* cfg, const void* y_perm, const void* y_shared,
                                         const int32_t* inv, const float* topk_w, void* y, void* stream) {
-  moe_status st = validate_cfg(cfg);
+  moe_status st = validate_share(cfg);
   if (st != MOE_OK || cfg->T == 0) return st;
   st = combine_check(cfg, y_perm, y_shared, inv, topk_w, y);
   if (st != MOE_OK) return st;

@@ -25,6 +25,12 @@ __device__ __forceinline__ float gate_sigmoid(float g) {
 
 // ----------------------------------------------------------------- host side
 moe_status validate_cfg(const moe_cfg* c);
+// ... and for the calls of a share of a batch: a workgroup of up to 512 lanes a
+// token, in a grid of fewer than 2^32 lanes.
+inline moe_status validate_share(const moe_cfg* c) {
+  const moe_status st = validate_cfg(c);
+  return st == MOE_OK && c->T >= 1 << 23 ? MOE_ERR_SHAPE : st;
+}
 bool gemm_dtype_ok(const moe_cfg* c);
 inline hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
 inline int64_t pairs(const moe_cfg* c) { return (int64_t)c->T * c->k; }

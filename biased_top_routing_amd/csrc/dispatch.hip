@@ -516,8 +516,11 @@ enum { kRowsCopy = 0, kRowsFp8 = 1, kRowsFp4 = 2, kRowsNone = 3 };
 // key expert * N + f of every pair, absent ones last, the keys below its own.
 // Every workgroup holds all N <= kSmallPairs keys in its registers, kSmallPer a
 // lane, and counts by ballot: k * kSmallPer compares a wavefront (8 slots: 128).
-// That repeats the counting T times, and saves the three launches that compute
-// it once (T = 128, k = 8, H = 7168: see the launcher).
+// That repeats the counting T times, and saves the three launches that compute it
+// once.  Measured, one launch against four (bf16, every expert held): T = 128, k =
+// 8, H = 7168: 9.5 and 19.5 us; at 4096 pairs, T = 512, k = 8, H = 7168: 18.2 and
+// 26.6 us (an eighth of the experts held: 10.6 and 15.2), T = 4096, k = 1, H = 1024:
+// 13.7 and 16.9 us.  More pairs would need more than 16 keys a lane.
 constexpr int kSmallThreads = 256, kSmallPer = 16, kSmallPairs = kSmallThreads * kSmallPer;
 
 template <int ROWS>
@@ -719,7 +722,7 @@ extern "C" moe_status moe_dispatch_local(const moe_cfg* cfg, int32_t first_exper
                                          const int32_t* topk_idx, const void* x, int32_t* counts, int32_t* offsets,
                                          int32_t* perm, int32_t* inv, void* x_perm, float* x_perm_scale, void* ws,
                                          size_t ws_bytes, void* stream) {
-  moe_status st = validate_cfg(cfg);
+  moe_status st = validate_share(cfg);
   if (st != MOE_OK) return st;
   if (cfg->T > 0) {   // (an empty batch's tensors may have no address)
     st = dispatch_check(cfg, topk_idx, x, counts, offsets, perm, inv, x_perm, x_perm_scale);

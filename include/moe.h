@@ -346,7 +346,7 @@ moe_status moe_quantize_fp8(const void* src_bf16, int32_t n_mat, int32_t rows, i
  * ties to the even code: off by at most half a step.  A block that holds an
  * infinity or a NaN gets scale byte 255 and codes 0 and reads back as NaN.
  * cols must be a multiple of 128 (any rows), n_mat at most 65535 and
- * ceil(rows/16) * ceil(cols/512) below 2^31 (MOE_ERR_SHAPE).
+ * ceil(rows/16) * ceil(cols/512) below 2^24 (MOE_ERR_SHAPE).
  */
 moe_status moe_quantize_fp4(const void* src_bf16, int32_t n_mat, int32_t rows, int32_t cols, uint8_t* dst,
                             uint8_t* scales, void* stream);
@@ -370,7 +370,8 @@ moe_status moe_dequantize_fp4(const uint8_t* codes, const uint8_t* scales, int32
  *   moe_route_backward (cfg of the router) -> moe_dispatch_local_backward
  * The outputs of all ranks' shares (y, and dx and d_topk_w) sum to the whole
  * layer's when the shared experts and the router term are given to one of them.
- * With T == 0 tensors without elements may be NULL in these four calls.
+ * With T == 0 tensors without elements may be NULL in these four calls; they take
+ * T below 2^23 (MOE_ERR_SHAPE).
  * moe_update_bias compares with T*k pairs over cfg's E experts: it is for whole
  * batches, with the counts of every share together.
  *

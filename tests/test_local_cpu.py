@@ -78,6 +78,16 @@ def test_backward_local_refusals():
     assert db(ctypes.byref(_cfg(E=8, T=0)), *[A] * 5, None) == L.MOE_OK
 
 
+def test_batches_past_a_grid_are_refused():
+    lib, ws = L.lib(), 1 << 40
+    for T, status in ((1 << 23, L.MOE_ERR_SHAPE), ((1 << 23) - 1, L.MOE_ERR_NULL)):
+        c = ctypes.byref(_cfg(E=8, T=T))
+        assert lib.moe_dispatch_local(c, 0, None, *[A] * 5, None, A, None, A, ws, None) == status
+        assert lib.moe_combine_local(c, A, A, A, None, A, None) == status
+        assert lib.moe_combine_local_backward(c, A, A, A, None, A, A, None) == status
+        assert lib.moe_dispatch_local_backward(c, A, A, None, None, A, None) == status
+
+
 def test_binding_refuses_strided_tensors():
     cfg = _cfg(E=8, T=4, H=64)
     y = torch.zeros((24, 128), dtype=torch.bfloat16)

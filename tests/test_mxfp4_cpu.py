@@ -78,6 +78,7 @@ def test_pack_round_trips():
     ((16, 1, 4, 96, 16, 16), L.MOE_ERR_SHAPE),
     ((16, 65536, 4, 128, 16, 16), L.MOE_ERR_SHAPE),
     ((16, 1, 2147483647, 128 * 64, 16, 16), L.MOE_ERR_SHAPE),
+    ((16, 1, 1 << 28, 128, 16, 16), L.MOE_ERR_SHAPE),      # a grid of 2^32 lanes
     ((8, 1, 4, 128, 16, 16), L.MOE_ERR_UNSUPPORTED),       # misaligned
     ((16, 1, 4, 128, 18, 16), L.MOE_ERR_UNSUPPORTED),
     ((16, 1, 4, 128, 16, 17), L.MOE_ERR_UNSUPPORTED),
