@@ -194,7 +194,9 @@ struct FfnLayout {
   explicit FfnLayout(const moe_cfg* c) {
     const int64_t P = pairs(c);
     const bool f8 = c->wgt == MOE_FP8_E4M3, f4 = c->wgt == MOE_MXFP4;
-    const int bm4 = P <= (int64_t)kFp4RowsAvg * c->E ? kFp4RowsBM : P <= (int64_t)kFp4MidAvg * c->E ? kFp4MidBM : kFp4BM;
+    const int bm4 = P <= (int64_t)kFp4RowsAvg * c->E  ? kFp4RowsBM
+                    : P <= (int64_t)kFp4MidAvg * c->E ? kFp4MidBM
+                                                      : kFp4BM;
     dec = small_batch(c);
     bm1 = f4 ? bm4 : f8 ? kFp8BM : dec ? kDecBM : kBM1;
     bm1_alt = f4 || f8 || dec ? 0 : kBM1Alt;

@@ -11,25 +11,34 @@
 //            the epilogue from the fp32 accumulators (one rounding, to E2M1)
 //   down     Y = h W_d^T, stored as bf16
 //
-//
 // Large batches: 256 x 256 tiles, one workgroup of 2 x 4 wavefronts a CU, each
 // wavefront 8 x 4 MFMA blocks, and the workgroups stay: each takes every 32nd tile
 // of its XCD's contiguous share of the table (one expert's tiles run on one XCD
 // at the same time and meet in its L2), and the loads run through the tiles
 // without a break.  K advances two 128-wide steps (128 bytes of codes a row: whole
-// cache lines; single steps, in half lines, loaded 20% slower) per slice through two
-// LDS stages filled by direct-to-LDS buffer loads (16-byte chunks, XOR swizzle per
+// cache lines; by single steps, in half lines, the layer below takes 2.83 and 1.52
+// ms) per slice through two LDS stages filled by direct-to-LDS buffer loads (16-byte chunks, XOR swizzle per
 // row), the rows' scale words of both steps beside them.  There is one barrier a
-// slice, two row blocks before its end: the next slice has landed by then, this
-// one's last fragments have been read, and the loads of the slice after next go
+// slice, before the MFMAs of its last row block: the next slice has landed by then,
+// this one's last fragments have been read, and the loads of the slice after next go
 // out into its stage, one after each row block's MFMAs.  A 4-bit MFMA takes half the
 // time of an 8-bit one on the same operand bytes, so the fragment reads are kept
-// ahead of it: the token rows' 3 blocks, the weights' a K step.  When a tile's last
-// slices are multiplied the next tile's first ones are on their way, and its
-// epilogue runs over them.
+// ahead of it: the token rows' 2 blocks, the weights' a K step.  When a tile's last
+// slice is multiplied the next tile's first one is on its way, and its epilogue runs
+// over it.
+//   T = 16384, H = 7168, I = 2048, 256 experts, 8 + 1 a token: gate/up 2.58 ms (3.36
+// PFLOP/s), down 1.41 ms (3.06 PFLOP/s, 2.1 GB of y among it).  The MFMAs alone, from
+// registers, reach 7.0 PFLOP/s on such operands (the chip's power limit; 9.8 on
+// zeros).  Of gate/up's time they are 1.2 ms; the LDS reads, the barriers and the
+// epilogue add 0.2 ms each, and the rest is operand loads that do not hide: without
+// them the kernel takes 1.8 ms, without the MFMAs 2.2 ms.  Measured without gain:
+// 3 or 4 stages of single steps (deeper, but half lines), runs of tiles dealt to the
+// XCDs instead of shares, a K walk that starts elsewhere in each tile, cache hints on
+// the weights (slower), wave priorities, waits that leave the stores out.
 //
 // Few rows per expert: 32 x 256 or 64 x 256 tiles that stream the weights, one
-// workgroup of 4 wavefronts per tile, two K steps per slice and 4 or 3 stages.
+// workgroup of 4 wavefronts per tile, two K steps per slice and 4 or 3 stages (T =
+// 128 on the layer above: the whole call 0.99 ms, 6.0 GB of weights at 6.1 TB/s).
 //
 // The shared experts' down GEMM walks the experts one after the other.  The
 // gate/up tile's 256 weight rows are the 128 gate rows and the 128 up rows of 128
@@ -181,17 +190,13 @@ template <int MODE>
 __device__ __forceinline__ constexpr int col_off(int ni) {
   return (ni / 2) * (MODE == kGateUp4 ? 128 : 32) + (ni % 2) * 4;
 }
-// Physical chunk of logical chunk c in LDS row r of the weights (CPR chunks a
-// row): 8 lanes' rows (4, and 4 that lie 8 further on) meet no bank twice.
-template <int CPR>
-__device__ __forceinline__ int swz_w(int r, int c) {
-  if constexpr (CPR == 8) return c ^ ((r & 3) | (((r >> 3) & 1) << 2));
-  else return c ^ (((r >> 1) & 1) | (((r >> 3) & 1) << 1));
-}
+// Physical 16-byte chunk of logical chunk c of 8 in LDS row r of the weights: 8
+// lanes' rows (4, and 4 that lie 8 further on) meet no bank twice.
+__device__ __forceinline__ int swz_w(int r, int c) { return c ^ ((r & 3) | (((r >> 3) & 1) << 2)); }
 
 // SwiGLU of one row block: acc[b] gate, acc[b + 2] up; the codes of this lane's 8 h
-// values (neighbouring columns), and the scale byte of the
-// row's 32 columns, which the 4 lanes l16, + 16, + 32, + 48 hold together.
+// values (neighbouring columns), and the scale byte of the row's 32 columns, which
+// the 4 lanes l16, + 16, + 32, + 48 hold together.
 __device__ __forceinline__ uint32_t swiglu_codes(const f32x4_t (&acc)[NI4], uint32_t* e) {
   float v[8];
   uint32_t m = 0;
@@ -326,7 +331,8 @@ __global__ __launch_bounds__(kFp4Threads, 1) void gemm_fp4_kernel(Fp4Params p) {
   auto begin = [&]() {
     const Operands4<MODE> o(p, ld);
     const int32_t* rows = reinterpret_cast<const int32_t*>(lds + PERM_OFF);
-    const int tid = opaque(threadIdx.x), lr = tid / CPR, ca = swz<CPR>(lr, tid % CPR) * 16, cw = swz_w<CPR>(lr, tid % CPR) * 16;
+    const int tid = opaque(threadIdx.x), lr = tid / CPR;
+    const int ca = swz<CPR>(lr, tid % CPR) * 16, cw = swz_w(lr, tid % CPR) * 16;
     static_assert(RPL % 16 == 0, "a thread's rows have one swizzle");
     // (rows past the tile's lie past the descriptor: the range check drops their loads)
     if constexpr (MODE == kGateUp4) {
@@ -419,7 +425,7 @@ __global__ __launch_bounds__(kFp4Threads, 1) void gemm_fp4_kernel(Fp4Params p) {
   const int arow0 = wm * MI * 16 + l16;
   const int brow = wn * (MODE == kGateUp4 ? 32 : 64) + col_lane(l16);
   const int a_lane = arow0 * BK + swz<CPR>(l16, g) * 16;
-  const int b_lane = B_OFF + brow * BK + swz_w<CPR>(col_lane(l16), g) * 16;
+  const int b_lane = B_OFF + brow * BK + swz_w(col_lane(l16), g) * 16;
   const int sa_lane = SC_OFF + arow0 * 4 + g, sb_lane = SC_OFF + (BM + brow) * 4 + g;
   constexpr int NB = 4, D = 2;                         // A fragments held, and read ahead
   static_assert(MI % NB == 0 && D < NB && PER == MI + 2, "the buffers rotate within a step; the issue schedule");
@@ -505,7 +511,7 @@ __global__ __launch_bounds__(kFp4Threads, 1) void gemm_fp4_kernel(Fp4Params p) {
     prepare();
     const uint8_t* here = lds + cs * STAGE;
     cs ^= 1;
-    read_first(here);                                  // (D < NB: not the buffer in use; after the last slice: not used)
+    read_first(here);                                  // (not into the buffer in use; after the last slice unused)
     __builtin_amdgcn_sched_barrier(0);
     if (half) multiply(MI - 1);
     issue_part(0);
@@ -576,7 +582,8 @@ __global__ __launch_bounds__(256, 1) void gemm_fp4_rows_kernel(Fp4Params p) {
   constexpr int PER = A_CH + B_CH + SC_CH;             // loads per thread per slice
   constexpr int SC_OFF = (BM + BN) * BK, STAGE = SC_OFF + SC_CH * NT * 4;
   constexpr int LDS_BYTES = STAGES * STAGE;
-  static_assert(LDS_BYTES <= 163840 && BM * (kHPitch + 4) <= LDS_BYTES && NW * 16 * kYPitch <= LDS_BYTES, "LDS of a CU");
+  static_assert(LDS_BYTES <= 163840, "LDS of a CU");
+  static_assert(BM * (kHPitch + 4) <= LDS_BYTES && NW * 16 * kYPitch <= LDS_BYTES, "the epilogue's staging");
 #if defined(__HIP_DEVICE_COMPILE__)
   __shared__ __attribute__((aligned(16))) uint8_t lds[LDS_BYTES];
   const int tid = threadIdx.x, lane = tid & 63, wn = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -595,7 +602,7 @@ __global__ __launch_bounds__(256, 1) void gemm_fp4_rows_kernel(Fp4Params p) {
 #pragma unroll
   for (int i = 0; i < B_CH; ++i) {
     const int c = i * NT + tid, r = c / CPR;
-    b_off[i] = (int)(o.ex * o.w_one) + o.wrow(p, r) * o.ldw + swz_w<CPR>(r, c % CPR) * 16;
+    b_off[i] = (int)(o.ex * o.w_one) + o.wrow(p, r) * o.ldw + swz_w(r, c % CPR) * 16;
   }
 #pragma unroll
   for (int i = 0; i < SC_CH; ++i) {
@@ -645,7 +652,7 @@ __global__ __launch_bounds__(256, 1) void gemm_fp4_rows_kernel(Fp4Params p) {
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk) {
       if (kk == 1 && left < 2) break;
-      const int ch = swz<CPR>(l16, kk * 4 + g) * 16, chw = swz_w<CPR>(col_lane(l16), kk * 4 + g) * 16;
+      const int ch = swz<CPR>(l16, kk * 4 + g) * 16, chw = swz_w(col_lane(l16), kk * 4 + g) * 16;
       const uint8_t* sca = base + SC_OFF + kk * BM * 4 + g;
       const uint8_t* scb = base + SC_OFF + (2 * BM + kk * BN) * 4 + g;
       i32x8_t fb[NI4];
@@ -718,7 +725,8 @@ moe_status launch_ffn_fp4(const moe_cfg* c, const uint8_t* x_perm, const uint8_t
   p.T = c->T; p.H = c->H; p.E = c->E; p.S = c->S; p.I = c->I; p.k = c->k;
   if (phase == MOE_FFN_ALL || phase == MOE_FFN_GATE_UP) {
     // the tile tables, and x once in MXFP4: the shared experts' operand, and the routed one when its rows are gathered
-    s = c->S > 0 || perm ? launch_build_tiles_quantize_fp4(c, offsets, x, ws, st) : launch_build_tiles(c, offsets, ws, st);
+    if (c->S > 0 || perm) s = launch_build_tiles_quantize_fp4(c, offsets, x, ws, st);
+    else s = launch_build_tiles(c, offsets, ws, st);
     if (s != MOE_OK) return s;
     p.perm = perm;
     p.a_routed = x_perm; p.sa_routed = x_perm_scale;
