@@ -96,16 +96,27 @@ constexpr int kFp8BM = MOE_FP8_BM;
 constexpr int kFp8BNH = 128;
 constexpr int kFp8BN2 = 256;
 constexpr int kFp8MaxKC = 64;
-// MXFP4 GEMMs: tiles of 256 token rows, or of 32 or 64 where the routed experts get
+// MXFP4 GEMMs: tiles of 256 or 288 token rows, or of 32 or 64 where the routed experts get
 // at most 24 or 56 rows each on average: the GEMMs then stream weights, and a tile's
 // height decides how often (H = 7168, I = 2048, 256 experts, the whole call in us
 // with 32 / 64 / 256 rows a tile: 24 rows an expert 1069 / 1093 / 1326, 32 rows
 // 1277 / 1133 / 1358, 48 rows 1648 / 1205 / 1367, 64 rows 1998 / 1605 / 1413; 128
 // rows a tile are nowhere best); 128 h columns per gate/up tile, 256 output columns
 // per down tile.
-constexpr int kFp4BM = 256, kFp4RowsBM = 32, kFp4MidBM = 64;
+constexpr int kFp4BM = 256, kFp4HighBM = 288, kFp4RowsBM = 32, kFp4MidBM = 64;
 constexpr int kFp4RowsAvg = 24, kFp4MidAvg = 56;
 constexpr int kFp4BNH = 128, kFp4BN2 = 256;
+// 288 rows take more time a tile and are right where they save one: a segment somewhat
+// longer than the mean (by twice the square root, the spread of an even routing) needs
+// fewer such tiles.  The layer above, 256 / 288 rows a tile: 256 rows an expert 2534 /
+// 2268 us, 512 rows 4260 / 4002, where it saves none (384 rows) 3307 / 3327, 64 rows
+// 1439 / 1476; H = 2048, I = 1408, 64 experts, 384 rows, skewed 238 / 247.
+inline int fp4_tile_rows(int64_t avg) {
+  int64_t dev = 1;
+  while ((dev + 1) * (dev + 1) <= avg) ++dev;
+  const int64_t most = avg + 2 * dev;
+  return (most + kFp4HighBM - 1) / kFp4HighBM < (most + kFp4BM - 1) / kFp4BM ? kFp4HighBM : kFp4BM;
+}
 
 // Row tiles per group in the tile order of a segment (see build_tiles_kernel).
 #ifndef MOE_GROUP_ROW_TILES
@@ -196,7 +207,7 @@ struct FfnLayout {
     const bool f8 = c->wgt == MOE_FP8_E4M3, f4 = c->wgt == MOE_MXFP4;
     const int bm4 = P <= (int64_t)kFp4RowsAvg * c->E  ? kFp4RowsBM
                     : P <= (int64_t)kFp4MidAvg * c->E ? kFp4MidBM
-                                                      : kFp4BM;
+                                                      : fp4_tile_rows(P / c->E);
     dec = small_batch(c);
     bm1 = f4 ? bm4 : f8 ? kFp8BM : dec ? kDecBM : kBM1;
     bm1_alt = f4 || f8 || dec ? 0 : kBM1Alt;

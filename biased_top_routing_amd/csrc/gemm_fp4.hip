@@ -11,30 +11,32 @@
 //            the epilogue from the fp32 accumulators (one rounding, to E2M1)
 //   down     Y = h W_d^T, stored as bf16
 //
-// Large batches: 256 x 256 tiles, one workgroup of 2 x 4 wavefronts a CU, each
-// wavefront 8 x 4 MFMA blocks, and the workgroups stay: each takes every 32nd tile
-// of its XCD's contiguous share of the table (one expert's tiles run on one XCD
-// at the same time and meet in its L2), and the loads run through the tiles
-// without a break.  K advances two 128-wide steps (128 bytes of codes a row: whole
-// cache lines; by single steps, in half lines, the layer below takes 2.83 and 1.52
-// ms) per slice through two LDS stages filled by direct-to-LDS buffer loads (16-byte chunks, XOR swizzle per
-// row), the rows' scale words of both steps beside them.  There is one barrier a
-// slice, before the MFMAs of its last row block: the next slice has landed by then,
+// Large batches: tiles of 256 or 288 token rows x 256 weight rows, one workgroup of
+// 2 x 4 wavefronts a CU, each wavefront 8 x 4 or 9 x 4 MFMA blocks, and the
+// workgroups stay: each takes a 32nd of its XCD's contiguous share of the table (one
+// expert's tiles run on one XCD at the same time and meet in its L2), and the loads
+// run through the tiles without a break.  K advances two 128-wide steps (128 bytes of
+// codes a row: whole cache lines; by single steps, in half lines, gate/up takes 7%
+// and down 8% longer) per slice through two LDS stages filled by direct-to-LDS buffer
+// loads (16-byte chunks, XOR swizzle per row), the rows' scale words of both steps
+// beside them.  There is one barrier a slice, before the MFMAs of its last row block: the next slice has landed by then,
 // this one's last fragments have been read, and the loads of the slice after next go
 // out into its stage, one after each row block's MFMAs.  A 4-bit MFMA takes half the
 // time of an 8-bit one on the same operand bytes, so the fragment reads are kept
 // ahead of it: the token rows' 2 blocks, the weights' a K step.  When a tile's last
 // slice is multiplied the next tile's first one is on its way, and its epilogue runs
 // over it.
-//   T = 16384, H = 7168, I = 2048, 256 experts, 8 + 1 a token: gate/up 2.58 ms (3.36
-// PFLOP/s), down 1.41 ms (3.06 PFLOP/s, 2.1 GB of y among it).  The MFMAs alone, from
+//   T = 16384, H = 7168, I = 2048, 256 experts, 8 + 1 a token: gate/up 2.51 ms (3.45
+// PFLOP/s), down 1.42 ms (3.05 PFLOP/s, 2.1 GB of y among it).  The MFMAs alone, from
 // registers, reach 7.0 PFLOP/s on such operands (the chip's power limit; 9.8 on
 // zeros).  Of gate/up's time they are 1.2 ms; the LDS reads, the barriers and the
-// epilogue add 0.2 ms each, and the rest is operand loads that do not hide: without
-// them the kernel takes 1.8 ms, without the MFMAs 2.2 ms.  Measured without gain:
-// 3 or 4 stages of single steps (deeper, but half lines), runs of tiles dealt to the
-// XCDs instead of shares, a K walk that starts elsewhere in each tile, cache hints on
-// the weights (slower), wave priorities, waits that leave the stores out.
+// epilogue add 0.2 ms each, and the rest is operand loads that do not hide: with
+// 256-row tiles the kernel takes 1.8 ms without them and 2.2 ms without the MFMAs.
+// Measured without gain: 3 or 4 stages of single steps (deeper, but half lines), runs
+// of tiles dealt to the XCDs instead of shares, a K walk that starts elsewhere in
+// each tile, cache hints on the weights (slower), wave priorities, waits that leave
+// the stores out, row blocks skipped where a tile is short (branches between the
+// MFMAs: 2% to 10% slower, with MFMA work saved).
 //
 // Few rows per expert: 32 x 256 or 64 x 256 tiles that stream the weights, one
 // workgroup of 4 wavefronts per tile, two K steps per slice and 4 or 3 stages (T =
@@ -84,7 +86,7 @@ struct Fp4Params {
 };
 
 constexpr int kHPitch = 64 + 16;         // a tile row's 64 bytes of h codes in LDS
-constexpr int kYPitch = 64 * 2 + 16;     // 64 bf16 columns of a row in LDS
+constexpr int align64(int n) { return (n + 63) / 64 * 64; }
 
 #if defined(__HIP_DEVICE_COMPILE__)
 constexpr int NI4 = 4;          // MFMA column blocks of a wavefront
@@ -245,15 +247,16 @@ __device__ __forceinline__ void store_h(const Fp4Params& p, const TileDesc& d, b
     out_s[d.nt * plane + d.row0 + i] = *reinterpret_cast<const uint32_t*>(hsc + i * 4);
 }
 
-// 16 rows x 64 columns of a wavefront's down tile as bf16, through its own LDS
-// piece so that whole 128-byte row segments are stored, 16 bytes a lane.  (A
-// wavefront reads back only what it wrote; its LDS operations complete in order.)
-__device__ __forceinline__ void store_y(uint8_t* stg, const f32x4_t (&acc)[NI4], bf16_t* out, int64_t row0, int i0,
-                                        int rows, int col0, int ncols, int lane) {
+// 16 rows x 64 columns of a wavefront's down tile as bf16, through its own two 1 KB
+// pieces of LDS (8 rows each, `dist` bytes apart, 16-byte chunks XOR swizzled), so
+// that whole 128-byte row segments are stored, 16 bytes a lane.  (A wavefront reads
+// back only what it wrote; its LDS operations complete in order.)
+__device__ __forceinline__ void store_y(uint8_t* stg, int dist, const f32x4_t (&acc)[NI4], bf16_t* out, int64_t row0,
+                                        int i0, int rows, int col0, int ncols, int lane) {
   const int l16 = lane & 15, g = lane >> 4;
 #pragma unroll
   for (int b = 0; b < NI4; b += 2)
-    *reinterpret_cast<uint4*>(stg + l16 * kYPitch + (b * 16 + 8 * g) * 2) =
+    *reinterpret_cast<uint4*>(stg + (l16 >> 3) * dist + (l16 & 7) * 128 + ((2 * b + g) ^ (l16 & 7)) * 16) =
         make_uint4(cvt_bf16x2(acc[b][0], acc[b][1]), cvt_bf16x2(acc[b][2], acc[b][3]),
                    cvt_bf16x2(acc[b + 1][0], acc[b + 1][1]), cvt_bf16x2(acc[b + 1][2], acc[b + 1][3]));
   __builtin_amdgcn_s_waitcnt(kLgkmWaitZero);
@@ -262,7 +265,8 @@ __device__ __forceinline__ void store_y(uint8_t* stg, const f32x4_t (&acc)[NI4],
 #pragma unroll
   for (int it = 0; it < 2; ++it) {
     const int lr = it * 8 + (lane >> 3), i = i0 + lr;
-    const uint4 v = *reinterpret_cast<const uint4*>(stg + lr * kYPitch + (lane & 7) * 16);
+    const uint4 v =
+        *reinterpret_cast<const uint4*>(stg + it * dist + (lane >> 3) * 128 + ((lane & 7) ^ (lane >> 3)) * 16);
     if (i < rows && col < ncols) *reinterpret_cast<uint4*>(out + (row0 + i) * ncols + col) = v;
   }
   __builtin_amdgcn_s_waitcnt(kLgkmWaitZero);
@@ -273,21 +277,26 @@ __device__ __forceinline__ void store_y(uint8_t* stg, const f32x4_t (&acc)[NI4],
 // ------------------------------------------------------------------ large batches
 constexpr int kFp4Threads = 512;
 
-template <int MODE>
+template <int MODE, int BM>
 __global__ __launch_bounds__(kFp4Threads, 1) void gemm_fp4_kernel(Fp4Params p) {
-  constexpr int WM = 2, WN = 4, MI = 8;
-  constexpr int NT = kFp4Threads, NW = NT / 64, BM = WM * MI * 16, BN = 256;
-  static_assert(WM * WN == NW && BM == kFp4BM && BN == kFp4BN2, "tile shape");
+  constexpr int WM = 2, WN = 4, MI = BM / (WM * 16);
+  constexpr int NT = kFp4Threads, NW = NT / 64, BN = 256;
+  static_assert(WM * WN == NW && WM * MI * 16 == BM && BN == kFp4BN2, "tile shape");
   constexpr int BK = 128, CPR = BK / 16;               // bytes (two K steps) and 16-byte chunks of a row per slice
-  constexpr int A_CH = BM * CPR / NT, B_CH = BN * CPR / NT, RPL = NT / CPR;   // loads per thread, rows between them
-  static_assert(BM + BN == NT && BM == NT / 2, "one scale word a thread and step: wavefronts 0-3 A's, 4-7 B's");
+  constexpr int RPL = NT / CPR;                        // rows a load of all threads covers
+  constexpr int A_CH = (BM + RPL - 1) / RPL, B_CH = BN / RPL;   // loads per thread; A's last one covers AX rows
+  // of a step's scale words wavefronts 0-3 load A's first 256, wavefronts 4-7 B's; past 256 rows (32 of
+  // them) A's last load is wavefronts 0-3's alone
+  constexpr int AX = BM - 256;
+  static_assert(BN == 256 && NT == 512 && (AX == 0 || AX == RPL / 2), "the loads of a slice");
   constexpr int PER = A_CH + B_CH + 2;                 // loads per thread per slice
-  constexpr int B_OFF = BM * BK, SC_OFF = B_OFF + BN * BK, STAGE = SC_OFF + 2 * NT * 4;
-  constexpr int STG_OFF = 2 * STAGE;                   // epilogue staging
-  constexpr int STG = MODE == kGateUp4 ? BM * (kHPitch + 4) : NW * 16 * kYPitch;
-  constexpr int PERM_OFF = STG_OFF + STG;              // the next tile's perm entries (gathered rows)
-  constexpr int LDS_BYTES = PERM_OFF + BM * 4;
+  constexpr int SCP = (BM + BN) * 4;                   // a step's scale words: A's, B's
+  constexpr int B_OFF = BM * BK, SC_OFF = B_OFF + BN * BK, STAGE = SC_OFF + 2 * SCP;
+  constexpr int PERM_OFF = 2 * STAGE;                  // the next tile's perm entries (gathered rows)
+  constexpr int LDS_BYTES = PERM_OFF + align64(BM) * 4;
   static_assert(LDS_BYTES <= 163840, "LDS of a CU");
+  // the epilogue's staging: the weights' part of the stage that is filled next
+  static_assert(BM * (kHPitch + 4) <= BN * BK && B_CH >= 2, "the epilogue's staging");
 #if defined(__HIP_DEVICE_COMPILE__)
   __shared__ __attribute__((aligned(16))) uint8_t lds[LDS_BYTES];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -302,8 +311,12 @@ __global__ __launch_bounds__(kFp4Threads, 1) void gemm_fp4_kernel(Fp4Params p) {
   const int s_cnt = min(max(n_real - n_rt - xcd * per_s, 0), per_s);
   const int r_cnt = min(max(n_rt - xcd * per_r, 0), per_r);
   const int step = gridDim.x >> 3;
+  // the n-th of this workgroup: round n takes the next `step` positions of the share, turned by 5 n
+  // (an expert's row tiles of one column follow each other, the last one shorter: without the turn
+  // a workgroup might get only long ones; 32 + 5 shares no divisor with their number, at most 8)
+  auto place = [&](int n) { return n * step + ((int)(blockIdx.x >> 3) + 5 * n) % step; };
   auto entry = [&](int q) { return q < s_cnt ? n_rt + xcd * per_s + q : xcd * per_r + q - s_cnt; };
-  int q = blockIdx.x >> 3;                             // position in the XCD's share
+  int nq = 0, q = place(0);                            // position in the XCD's share
   const int q_end = s_cnt + r_cnt;
   if (q >= q_end) return;
 
@@ -319,11 +332,15 @@ __global__ __launch_bounds__(kFp4Threads, 1) void gemm_fp4_kernel(Fp4Params p) {
   constexpr int A_OFF = MODE == kGateUp4 ? A_CH : 1;
   int a_off[A_OFF], b_off = 0, s_off = 0, a_dist = 0, w_dist = 0, w_gap = 0;
   int s_step = 0, a_skip = 0, w_skip = 0, s_skip = 0, nk1 = 1;   // scale plane distance; extra steps to the next expert
-  const uint8_t *baseA = nullptr, *baseW = nullptr, *baseS = nullptr;
-  int bytesA = 0, bytesW = 0, bytesS = 0;              // 0 when the stream has ended: its loads are dropped
-  // the perm entries of a gathered tile's rows into LDS (wavefronts 0-3)
+  // the scale words of A's last AX rows: wavefront 4 loads those of a slice's first step, 5 the second's,
+  // 64 rows each (the rows before them twice)
+  int sx_off = 0, sa_step = 0;
+  int s_first = 0;                                     // down: first byte of this wavefront's scale words
+  const uint8_t *baseA = nullptr, *baseW = nullptr, *baseS = nullptr, *baseSA = nullptr;
+  int bytesA = 0, bytesW = 0, bytesS = 0, bytesSA = 0;   // 0 when the stream has ended: its loads are dropped
+  // the perm entries of a gathered tile's rows into LDS
   auto load_perm = [&](const TileDesc& d) {
-    if (MODE == kGateUp4 && p.perm != nullptr && d.seg != p.E && wave < BM / 64)
+    if (MODE == kGateUp4 && p.perm != nullptr && d.seg != p.E && wave < align64(BM) / 64)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(p.perm + d.row0, d.rows * 4),
                                                (lds_void_t*)(lds + PERM_OFF + wave * 256), 4, tid * 4, 0, 0, 0);
   };
@@ -349,8 +366,16 @@ __global__ __launch_bounds__(kFp4Threads, 1) void gemm_fp4_kernel(Fp4Params p) {
     w_dist = RPL * o.ldw;
     w_gap = MODE == kGateUp4 ? (p.I - 128) * o.ldw : 0;
     const bool sa = wave < NW / 2;                     // this wavefront loads A's scale words, else B's
-    if (sa) s_off = tid < ld.rows ? (o.gather ? rows[tid] / p.k : tid) * 4 : kDrop;
-    else s_off = o.ex * o.sw_one + (o.c0 + tid - BM + (MODE == kGateUp4 && tid - BM >= 128 ? p.I - 128 : 0)) * 4;
+    if constexpr (MODE == kGateUp4) {
+      const int xr = BM - 64 + (tid & 63);
+      if (sa) s_off = tid < ld.rows ? (o.gather ? rows[tid] / p.k : tid) * 4 : kDrop;
+      else s_off = o.ex * o.sw_one + (o.c0 + tid - BN + (tid - BN >= 128 ? p.I - 128 : 0)) * 4;
+      sx_off = xr < ld.rows ? (o.gather ? rows[xr] / p.k : xr) * 4 + (wave == NW / 2 + 1 ? o.sa_stride : 0) : kDrop;
+    } else {                                           // (what lies past the tile is read where it is there, not used)
+      s_first = sa ? wave * 256 : o.c0 * 4 + (wave - NW / 2) * 256;
+    }
+    sa_step = o.sa_stride;
+    baseSA = o.SA; bytesSA = o.sa_bytes;
     baseA = o.A; bytesA = o.a_bytes;
     baseW = o.W; bytesW = o.w_bytes;
     baseS = sa ? o.SA : o.SW;
@@ -364,7 +389,7 @@ __global__ __launch_bounds__(kFp4Threads, 1) void gemm_fp4_kernel(Fp4Params p) {
     ak = wk = sk = 0;
     in_l = nk1 = o.nk1;
     left_l = o.nexp;
-    q += step;
+    q = place(++nq);
     more = q < q_end;
     if (more) nd = tile_at(p, entry(q));
   };
@@ -373,7 +398,18 @@ __global__ __launch_bounds__(kFp4Threads, 1) void gemm_fp4_kernel(Fp4Params p) {
   // compares the lane's offset with what the scalar one leaves of it.)
   auto issue_part = [&](int i) {
     uint8_t* sb = lds + ls * STAGE + wave * 1024;
-    if (i < A_CH)
+    // (the down kernel has no registers to keep what the lane and scalars give at once)
+    const unsigned lane4 = (opaque(threadIdx.x) & 63) * 4;
+    const unsigned s_lane = MODE == kGateUp4 ? (unsigned)s_off : lane4 + (unsigned)s_first;
+    const unsigned sx_lane =
+        MODE == kGateUp4 ? (unsigned)sx_off : lane4 + (unsigned)((BM - 64) * 4 + (wave == NW / 2 + 1 ? sa_step : 0));
+    if (AX > 0 && i == A_CH - 1 && wave >= NW / 2) {   // (rows past the tile: the scale words of the last ones instead)
+      if (wave < NW / 2 + 2)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            make_rsrc(baseSA, bytesSA),
+            (lds_void_t*)(lds + ls * STAGE + SC_OFF + (wave - NW / 2) * SCP + (BM - 64) * 4), 4, (int)sx_lane,
+            ak / 64 * sa_step, 0, 0);
+    } else if (i < A_CH)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(baseA, bytesA), (lds_void_t*)(sb + i * NW * 1024), 16,
                                                MODE == kGateUp4 ? a_off[i % A_OFF] : a_off[0] + i * a_dist, ak, 0, 0);
     else if (i < A_CH + B_CH)
@@ -382,8 +418,9 @@ __global__ __launch_bounds__(kFp4Threads, 1) void gemm_fp4_kernel(Fp4Params p) {
           b_off + (i - A_CH) * w_dist + ((i - A_CH) * RPL >= 128 ? w_gap : 0), wk, 0, 0);
     else
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          make_rsrc(baseS, bytesS), (lds_void_t*)(lds + ls * STAGE + SC_OFF + (i - A_CH - B_CH) * NT * 4 + wave * 256),
-          4, (int)((unsigned)s_off + (unsigned)((i - A_CH - B_CH) * s_step)), sk, 0, 0);
+          make_rsrc(baseS, bytesS),
+          (lds_void_t*)(lds + ls * STAGE + SC_OFF + (i - A_CH - B_CH) * SCP + wave * 256 + (wave < NW / 2 ? 0 : AX * 4)),
+          4, (int)(s_lane + (unsigned)((i - A_CH - B_CH) * s_step)), sk, 0, 0);
   };
   // After a slice's loads.
   auto advance = [&]() {
@@ -406,7 +443,7 @@ __global__ __launch_bounds__(kFp4Threads, 1) void gemm_fp4_kernel(Fp4Params p) {
   auto prepare = [&]() {
     if (left_l > 0) return;
     if (!more) {
-      bytesA = bytesW = bytesS = 0;
+      bytesA = bytesW = bytesS = bytesSA = 0;
       ak = wk = sk = 0;
       return;
     }
@@ -427,7 +464,7 @@ __global__ __launch_bounds__(kFp4Threads, 1) void gemm_fp4_kernel(Fp4Params p) {
   const int a_lane = arow0 * BK + swz<CPR>(l16, g) * 16;
   const int b_lane = B_OFF + brow * BK + swz_w(col_lane(l16), g) * 16;
   const int sa_lane = SC_OFF + arow0 * 4 + g, sb_lane = SC_OFF + (BM + brow) * 4 + g;
-  constexpr int NB = 4, D = 2;                         // A fragments held, and read ahead
+  constexpr int NB = MI % 3 == 0 ? 3 : 4, D = 2;       // A fragments held, and read ahead
   static_assert(MI % NB == 0 && D < NB && PER == MI + 2, "the buffers rotate within a step; the issue schedule");
   f32x4_t acc[MI][NI4];
   i32x8_t fa[NB], fb[NI4], fbn[NI4];
@@ -440,11 +477,11 @@ __global__ __launch_bounds__(kFp4Threads, 1) void gemm_fp4_kernel(Fp4Params p) {
   };
   auto read_a = [&](const uint8_t* stage, int kk, int mi) {
     fa[mi % NB] = frag4(stage + (a_lane ^ (kk * 64)) + mi * 16 * BK);
-    ra[mi % NB] = stage[sa_lane + kk * NT * 4 + mi * 64];
+    ra[mi % NB] = stage[sa_lane + kk * SCP + mi * 64];
   };
   auto read_b = [&](const uint8_t* stage, int kk, int ni) {
     fbn[ni] = frag4(stage + (b_lane ^ (kk * 64)) + col_off<MODE>(ni) * BK);
-    rbn[ni] = stage[sb_lane + kk * NT * 4 + col_off<MODE>(ni) * 4];
+    rbn[ni] = stage[sb_lane + kk * SCP + col_off<MODE>(ni) * 4];
   };
   auto next_b = [&]() {
 #pragma unroll
@@ -495,9 +532,9 @@ __global__ __launch_bounds__(kFp4Threads, 1) void gemm_fp4_kernel(Fp4Params p) {
   advance();
   clear();
 
-  int qc = blockIdx.x >> 3;
-  TileDesc cd = tile_at(p, entry(qc)), after = cd;     // the tile being computed, the one after it
-  if (qc + step < q_end) after = tile_at(p, entry(qc + step));
+  int nc = 0, qc = place(1);                           // the tile after the one being computed
+  TileDesc cd = tile_at(p, entry(place(0))), after = cd;
+  if (qc < q_end) after = tile_at(p, entry(qc));
   const int steps1 = (MODE == kDown4 ? p.I : p.H) / 128;   // K steps of an expert
   auto experts = [&]() { return MODE == kDown4 && cd.seg == p.E ? p.S : 1; };
   int cs = 0, left = steps1, exps = experts();         // stage of the next slice; K steps left of the expert, experts
@@ -522,7 +559,7 @@ __global__ __launch_bounds__(kFp4Threads, 1) void gemm_fp4_kernel(Fp4Params p) {
       const bool shared = cd.seg == p.E;
       const int tid = opaque(threadIdx.x), lane = tid & 63, l16 = lane & 15, g = lane >> 4;
       if constexpr (MODE == kGateUp4) {
-        uint8_t* hc = lds + STG_OFF;
+        uint8_t* hc = lds + ls * STAGE + B_OFF;
         uint8_t* hsc = hc + BM * kHPitch;
 #pragma unroll
         for (int mi = 0; mi < MI; ++mi) {
@@ -532,20 +569,20 @@ __global__ __launch_bounds__(kFp4Threads, 1) void gemm_fp4_kernel(Fp4Params p) {
         }
         lds_barrier();
         store_h<NT>(p, cd, shared, hc, hsc, tid);
-        // (the staging is written again only after the next slice's barrier)
+        lds_barrier();                                 // the staging is read: its loads may go out
       } else {
         bf16_t* out = reinterpret_cast<bf16_t*>(shared ? p.out_shared : p.out_routed);
         // (stored straight from the registers, in halves or by exchange in whole row
         // segments, the stores come in one burst in front of the next loads: 3% slower)
 #pragma unroll
         for (int mi = 0; mi < MI; ++mi)
-          store_y(lds + STG_OFF + wave * 16 * kYPitch, acc[mi], out, cd.row0, (wm * MI + mi) * 16, cd.rows,
-                  cd.nt * BN + wn * 64, p.H, lane);
+          store_y(lds + ls * STAGE + B_OFF + wave * 1024, NW * 1024, acc[mi], out, cd.row0, (wm * MI + mi) * 16,
+                  cd.rows, cd.nt * BN + wn * 64, p.H, lane);
       }
-      qc += step;
       if (qc >= q_end) break;
       cd = after;
-      if (qc + step < q_end) after = tile_at(p, entry(qc + step));
+      qc = place(++nc + 1);
+      if (qc < q_end) after = tile_at(p, entry(qc));
       exps = experts();
       clear();
     }
@@ -583,7 +620,7 @@ __global__ __launch_bounds__(256, 1) void gemm_fp4_rows_kernel(Fp4Params p) {
   constexpr int SC_OFF = (BM + BN) * BK, STAGE = SC_OFF + SC_CH * NT * 4;
   constexpr int LDS_BYTES = STAGES * STAGE;
   static_assert(LDS_BYTES <= 163840, "LDS of a CU");
-  static_assert(BM * (kHPitch + 4) <= LDS_BYTES && NW * 16 * kYPitch <= LDS_BYTES, "the epilogue's staging");
+  static_assert(BM * (kHPitch + 4) <= LDS_BYTES && NW * 2048 <= LDS_BYTES, "the epilogue's staging");
 #if defined(__HIP_DEVICE_COMPILE__)
   __shared__ __attribute__((aligned(16))) uint8_t lds[LDS_BYTES];
   const int tid = threadIdx.x, lane = tid & 63, wn = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -690,7 +727,7 @@ __global__ __launch_bounds__(256, 1) void gemm_fp4_rows_kernel(Fp4Params p) {
     bf16_t* out = reinterpret_cast<bf16_t*>(o.shared ? p.out_shared : p.out_routed);
 #pragma unroll
     for (int mi = 0; mi < MI; ++mi)
-      store_y(lds + wn * 16 * kYPitch, acc[mi], out, d.row0, mi * 16, d.rows, d.nt * BN + wn * 64, p.H, lane);
+      store_y(lds + wn * 2048, 1024, acc[mi], out, d.row0, mi * 16, d.rows, d.nt * BN + wn * 64, p.H, lane);
   }
 #endif
 }
@@ -706,7 +743,10 @@ moe_status launch_gemm_fp4(const FfnLayout& L, int64_t max_tiles, const Fp4Param
   } else {
     // one workgroup a CU (its LDS leaves no room for two), whole rounds of the 8 XCDs
     const int64_t grid = std::min<int64_t>(std::max(cu_count() / 8 * 8, 8), (int64_t)align_up((size_t)max_tiles, 8));
-    hipLaunchKernelGGL(gemm_fp4_kernel<MODE>, dim3((unsigned)grid), dim3(kFp4Threads), 0, st, p);
+    if (L.bm1 == kFp4BM)
+      hipLaunchKernelGGL((gemm_fp4_kernel<MODE, kFp4BM>), dim3((unsigned)grid), dim3(kFp4Threads), 0, st, p);
+    else
+      hipLaunchKernelGGL((gemm_fp4_kernel<MODE, kFp4HighBM>), dim3((unsigned)grid), dim3(kFp4Threads), 0, st, p);
   }
   return launch_status();
 }

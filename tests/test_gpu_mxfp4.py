@@ -215,6 +215,12 @@ CASES = [
     (90, 256, 4, 1, 1, 2, 1, 2048),
     (100, 1152, 8, 2, 2, 3, 2, 384),
     (400, 256, 16, 4, 2, 2, 3, 128),
+    # every routed segment as long as the batch: 256-row tiles, 288-row ones
+    (288, 256, 2, 1, 1, 2, 1, 256),
+    (577, 128, 1, 1, 1, 1, 2, 384),
+    (250, 256, 2, 1, 1, 2, 1, 384),
+    (240, 128, 2, 1, 1, 2, 1, 128),
+    (500, 640, 2, 1, 1, 2, 3, 384),
 ]
 
 
