@@ -561,14 +561,29 @@ __global__ __launch_bounds__(kSmallThreads) void dispatch_small_kernel(
   const int64_t t = blockIdx.x;
   __shared__ int32_t below[4][32];
   __shared__ int32_t dest[32];
+  // the row's first chunks are on their way while the pairs are counted
+  constexpr int U = 4;
+  const uint4* row = x + t * nchunk;
+  uint4 v[U];
+  auto load = [&](int64_t c0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t c = c0 + u * kSmallThreads + tid;
+      v[u] = c < nchunk ? row[c] : make_uint4(0, 0, 0, 0);
+    }
+  };
   uint32_t q[kSmallPer];
 #pragma unroll
   for (int i = 0; i < kSmallPer; ++i) {
     const int f = tid + i * kSmallThreads;
     q[i] = f < N ? key(f) : absent;
   }
+  const uint32_t own = lane < k ? key((int)t * k + lane) : absent;   // the token's pairs, one a lane
+  if constexpr (ROWS != kRowsNone) {
+    if ((int)t * k < limit) load(0);
+  }
   for (int j = 0; j < k; ++j) {
-    const uint32_t mine = key((int)t * k + j);
+    const uint32_t mine = (uint32_t)__builtin_amdgcn_readlane((int)own, j);
     int n = 0;
 #pragma unroll
     for (int i = 0; i < kSmallPer; ++i) n += __popcll(__ballot(q[i] < mine));
@@ -590,30 +605,34 @@ __global__ __launch_bounds__(kSmallThreads) void dispatch_small_kernel(
   bool any = false;
   for (int j = 0; j < k; ++j) any |= dest[j] >= 0;
   if (!any) return;
-  for (int64_t c0 = 0; c0 < nchunk; c0 += kSmallThreads) {
-    const int64_t c = c0 + tid;
-    // (quantised rows: a 16-lane group of 128 columns is wholly inside or outside the row)
-    const uint4 v = c < nchunk ? x[t * nchunk + c] : make_uint4(0, 0, 0, 0);
-    uint2 w8;
-    float sc;
-    uint32_t w4, sw;
-    if constexpr (ROWS == kRowsFp8) w8 = quant_chunk_1x128(v, &sc);
-    if constexpr (ROWS == kRowsFp4) {
-      uint32_t e;
-      w4 = mx_quant_chunk(v, &e);
-      sw = mx_scale_word(e);
-    }
-    for (int j = 0; j < k; ++j) {
-      const int64_t p = dest[j];
-      if (p < 0 || c >= nchunk) continue;
-      if constexpr (ROWS == kRowsCopy) static_cast<uint4*>(x_perm)[p * nchunk + c] = v;
-      if constexpr (ROWS == kRowsFp8) {
-        static_cast<uint2*>(x_perm)[p * nchunk + c] = w8;
-        if ((lane & 15) == 0) static_cast<float*>(x_scale)[p * (nchunk / 16) + c / 16] = sc;
-      }
+  for (int64_t c0 = 0; c0 < nchunk; c0 += U * kSmallThreads) {
+    if (c0 > 0) load(c0);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t c = c0 + u * kSmallThreads + tid;
+      // (quantised rows: a 16-lane group of 128 columns is wholly inside or outside the row)
+      uint2 w8;
+      float sc;
+      uint32_t w4, sw;
+      if constexpr (ROWS == kRowsFp8) w8 = quant_chunk_1x128(v[u], &sc);
       if constexpr (ROWS == kRowsFp4) {
-        static_cast<uint32_t*>(x_perm)[p * nchunk + c] = w4;
-        if ((lane & 15) == 0) static_cast<uint32_t*>(x_scale)[c / 16 * N + p] = sw;
+        uint32_t e;
+        w4 = mx_quant_chunk(v[u], &e);
+        sw = mx_scale_word(e);
+      }
+      if (c >= nchunk) continue;
+      for (int j = 0; j < k; ++j) {
+        const int64_t p = dest[j];
+        if (p < 0) continue;
+        if constexpr (ROWS == kRowsCopy) static_cast<uint4*>(x_perm)[p * nchunk + c] = v[u];
+        if constexpr (ROWS == kRowsFp8) {
+          static_cast<uint2*>(x_perm)[p * nchunk + c] = w8;
+          if ((lane & 15) == 0) static_cast<float*>(x_scale)[p * (nchunk / 16) + c / 16] = sc;
+        }
+        if constexpr (ROWS == kRowsFp4) {
+          static_cast<uint32_t*>(x_perm)[p * nchunk + c] = w4;
+          if ((lane & 15) == 0) static_cast<uint32_t*>(x_scale)[c / 16 * N + p] = sw;
+        }
       }
     }
   }

@@ -19,13 +19,13 @@
 // codes a row: whole cache lines; by single steps, in half lines, gate/up takes 7%
 // and down 8% longer) per slice through two LDS stages filled by direct-to-LDS buffer
 // loads (16-byte chunks, XOR swizzle per row), the rows' scale words of both steps
-// beside them.  There is one barrier a slice, before the MFMAs of its last row block: the next slice has landed by then,
-// this one's last fragments have been read, and the loads of the slice after next go
-// out into its stage, one after each row block's MFMAs.  A 4-bit MFMA takes half the
-// time of an 8-bit one on the same operand bytes, so the fragment reads are kept
-// ahead of it: the token rows' 2 blocks, the weights' a K step.  When a tile's last
-// slice is multiplied the next tile's first one is on its way, and its epilogue runs
-// over it.
+// beside them.  There is one barrier a slice, before the MFMAs of its last row block:
+// the next slice has landed by then, this one's last fragments have been read, and
+// the loads of the slice after next go out into its stage, one after each row block's
+// MFMAs.  A 4-bit MFMA takes half the time of an 8-bit one on the same operand bytes,
+// so the fragment reads are kept ahead of it: the token rows' 2 blocks, the weights' a
+// K step.  When a tile's last slice is multiplied the next tile's first one is on its
+// way, and its epilogue runs over it.
 //   T = 16384, H = 7168, I = 2048, 256 experts, 8 + 1 a token: gate/up 2.51 ms (3.45
 // PFLOP/s), down 1.42 ms (3.05 PFLOP/s, 2.1 GB of y among it).  The MFMAs alone, from
 // registers, reach 7.0 PFLOP/s on such operands (the chip's power limit; 9.8 on
@@ -419,7 +419,8 @@ __global__ __launch_bounds__(kFp4Threads, 1) void gemm_fp4_kernel(Fp4Params p) {
     else
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
           make_rsrc(baseS, bytesS),
-          (lds_void_t*)(lds + ls * STAGE + SC_OFF + (i - A_CH - B_CH) * SCP + wave * 256 + (wave < NW / 2 ? 0 : AX * 4)),
+          (lds_void_t*)(lds + ls * STAGE + SC_OFF + (i - A_CH - B_CH) * SCP + wave * 256 +
+                        (wave < NW / 2 ? 0 : AX * 4)),
           4, (int)(s_lane + (unsigned)((i - A_CH - B_CH) * s_step)), sk, 0, 0);
   };
   // After a slice's loads.
