@@ -262,5 +262,6 @@ class MoeLayerGPU:
 
     def replay(self):
         """One replay of the captured step on the current stream; returns y."""
+        self.n_tokens = self.graph_inputs[2]     # backward() then takes the pairs that the graph's batch has
         self.graph.replay()
         return self.y

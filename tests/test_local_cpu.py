@@ -95,6 +95,17 @@ def test_binding_refuses_strided_tensors():
         L.moe_combine_local(cfg, y[:, ::2], A, A, A, A, stream=0)
 
 
+def test_replay_leaves_its_own_batch():
+    """A forward pass of a whole batch between a padded graph's replays: backward() after the replay has absent
+    pairs again."""
+    layer = MoeLayerGPU(TINY, make_weights(TINY), device="cpu")
+    n = torch.zeros(1, dtype=torch.int32)
+    layer.graph, layer.graph_inputs = type("Graph", (), {"replay": lambda self: None})(), (None, None, n)
+    assert not layer.partial
+    layer.replay()
+    assert layer.partial and layer.n_tokens is n
+
+
 def test_runner_refuses_bad_shares():
     """Shares outside the layer, smaller than k, or given other experts' weights (before any allocation)."""
     w = make_weights(TINY)
