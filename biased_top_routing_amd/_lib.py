@@ -139,14 +139,17 @@ def _p(t) -> int | None:
 
 
 def _c(t) -> int | None:
-    """_p for the entry points that check what they are given: a tensor has to be dense,
-    and on the current device when it is on a GPU (its stream and kernels are)."""
+    """_p for the entry points that check what they are given: a tensor has to be dense, and on the
+    current device (its stream and kernels are there) or in pinned host memory, unless it is empty."""
     if t is None or isinstance(t, int):
         return t
     if not t.is_contiguous():
         raise ValueError(f"tensor of shape {tuple(t.shape)} with strides {t.stride()} is not contiguous")
     d = t.get_device()                       # -1 on the host
-    if d >= 0 and d != _device():
+    if d < 0:
+        if t.numel() and not t.is_pinned():
+            raise ValueError(f"tensor of shape {tuple(t.shape)} on {t.device}: no GPU can read it")
+    elif d != _device():
         raise ValueError(f"tensor on {t.device}, but the current device is cuda:{_device()}")
     return t.data_ptr()
 

@@ -95,6 +95,14 @@ def test_binding_refuses_strided_tensors():
         L.moe_combine_local(cfg, y[:, ::2], A, A, A, A, stream=0)
 
 
+def test_binding_refuses_host_tensors():
+    cfg = _cfg(E=8)
+    for args in ([torch.zeros(4), A, A, A, A], [A, A, A, A, torch.zeros((2, 2))]):
+        with pytest.raises(ValueError):
+            L.moe_combine_local(cfg, *args, stream=0)
+    L.moe_combine_local(_cfg(E=8, T=0), torch.zeros(0), None, None, None, None, stream=0)
+
+
 def test_replay_leaves_its_own_batch():
     """A forward pass of a whole batch between a padded graph's replays: backward() after the replay has absent
     pairs again."""
