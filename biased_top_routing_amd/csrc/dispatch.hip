@@ -233,22 +233,66 @@ __global__ __launch_bounds__(256) void count_local_kernel(const int32_t* __restr
     segcounts[seg * E + e] = cnt_all[e] + cnt_all[E + e] + cnt_all[2 * E + e] + cnt_all[3 * E + e];
 }
 
+// SUM: segcounts are the segments' counts as they were taken, and every workgroup
+// adds up what it needs of them (at most kSumCounts, E <= 256) instead of waiting for
+// scan_kernel; workgroup 0 writes counts and offsets (bf16 rows, the whole dispatch
+// with scan_kernel and without: T = 16384, k = 8, H = 7168, 32 of 256 experts held 83.2
+// and 79.0 us; H = 1024, all 256 held, 32768 counts 72.5 and 70.4; T = 4096, k = 6, H =
+// 2048, 8 of 64 held 17.4 and 14.3).
+constexpr int kSumCounts = 32768;
+
+template <bool SUM>
 __global__ __launch_bounds__(256) void rank_local_kernel(const int32_t* __restrict__ idx, int64_t N, int E, int nbits,
-                                                         Window win, const int32_t* __restrict__ segprefix,
-                                                         const int32_t* __restrict__ offsets,
+                                                         Window win, const int32_t* __restrict__ segcounts, int nseg,
+                                                         int32_t* __restrict__ counts, int32_t* __restrict__ offsets,
                                                          int32_t* __restrict__ perm, int32_t* __restrict__ inv) {
   extern __shared__ int32_t cnt_all[];                  // [4][E] counts, then [4][E] first rows
+  __shared__ int32_t all_s[256], earlier_s[256], wave_s[4];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int64_t seg = blockIdx.x, lo = seg * kSegPairs + wave * kQuarter;
   for (int e = threadIdx.x; e < 4 * E; e += 256) cnt_all[e] = 0;
   int ev[kQuarter / kWave], before[kQuarter / kWave];
   load_quarter(idx, lo, N, win, E, ev);
+  if constexpr (SUM) {                                  // a power of two of threads an expert
+    const int e = threadIdx.x & ((1 << nbits) - 1), part = threadIdx.x >> nbits, parts = 256 >> nbits;
+    int32_t all = 0, earlier = 0;
+    if (e < E) {
+#pragma unroll 8
+      for (int b = part; b < nseg; b += parts) {
+        const int32_t c = segcounts[b * E + e];
+        all += c;
+        earlier += b < seg ? c : 0;
+      }
+    }
+    all_s[threadIdx.x] = all;
+    earlier_s[threadIdx.x] = earlier;
+  }
   __syncthreads();
   count_quarter(ev, nbits, cnt_all + wave * E, before);
+  if constexpr (SUM) {
+    const int e = threadIdx.x, step = 1 << nbits;
+    int32_t all = 0, earlier = 0;
+    if (e < E)
+      for (int i = e; i < 256; i += step) all += all_s[i], earlier += earlier_s[i];
+    int32_t upto = all;                                 // inclusive scan over the experts
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int32_t v = __shfl_up(upto, d);
+      if (lane >= d) upto += v;
+    }
+    if (lane == 63) wave_s[wave] = upto;
+    __syncthreads();
+    for (int w = 0; w < wave; ++w) upto += wave_s[w];
+    if (seg == 0) {
+      if (e < E) counts[e] = all, offsets[e + 1] = upto;
+      if (e == 0) offsets[0] = 0;
+    }
+    earlier_s[e] = upto - all + earlier;                // (all entries have been read: the barrier above)
+  }
   __syncthreads();
   int32_t* first = cnt_all + 4 * E;
   for (int e = threadIdx.x; e < E; e += 256) {
-    int32_t at = offsets[e] + segprefix[seg * E + e];
+    int32_t at = SUM ? earlier_s[e] : offsets[e] + segcounts[seg * E + e];
     for (int w = 0; w < 4; ++w) {
       first[w * E + e] = at;
       at += cnt_all[w * E + e];
@@ -516,11 +560,11 @@ enum { kRowsCopy = 0, kRowsFp8 = 1, kRowsFp4 = 2, kRowsNone = 3 };
 // key expert * N + f of every pair, absent ones last, the keys below its own.
 // Every workgroup holds all N <= kSmallPairs keys in its registers, kSmallPer a
 // lane, and counts by ballot: k * kSmallPer compares a wavefront (8 slots: 128).
-// That repeats the counting T times, and saves the three launches that compute it
-// once.  Measured, one launch against four (bf16, every expert held): T = 128, k =
-// 8, H = 7168: 9.5 and 19.5 us; at 4096 pairs, T = 512, k = 8, H = 7168: 18.2 and
-// 26.6 us (an eighth of the experts held: 10.6 and 15.2), T = 4096, k = 1, H = 1024:
-// 13.7 and 16.9 us.  More pairs would need more than 16 keys a lane.
+// That repeats the counting T times, and saves the two launches that compute it once.
+// Measured, one launch against three (bf16, every expert held): T = 128, k = 8, H =
+// 7168: 8.7 and 15.8 us; at 4096 pairs, T = 512, k = 8, H = 7168: 17.9 and 21.8 us (an
+// eighth of the experts held: 10.0 and 13.3), T = 4096, k = 1, H = 1024: 13.8 and 13.7
+// us.  More pairs would need more than 16 keys a lane.
 constexpr int kSmallThreads = 256, kSmallPer = 16, kSmallPairs = kSmallThreads * kSmallPer;
 
 template <int ROWS>
@@ -670,6 +714,22 @@ static moe_status dispatch_launch(const moe_cfg* cfg, const Window& win, const i
   while ((1 << nbits) < E) ++nbits;
   int Ep2 = 1;
   while (Ep2 < E) Ep2 <<= 1;
+  auto permute = [&]() -> moe_status {
+    if (!x_perm) return MOE_OK;
+    const unsigned tblocks = (unsigned)((cfg->T + 3) / 4);
+    if (fp4) {
+      hipLaunchKernelGGL((permute_rows_fp4_kernel<8, LOCAL>), dim3(tblocks), dim3(256), 0, s, (const uint4*)x, inv,
+                         cfg->T, cfg->k, cfg->H, (uint32_t*)x_perm, (uint32_t*)x_perm_scale);
+    } else if (fp8) {
+      hipLaunchKernelGGL((permute_rows_fp8_kernel<8, LOCAL>), dim3(tblocks), dim3(256), 0, s, (const uint4*)x, inv,
+                         cfg->T, cfg->k, cfg->H, (uint2*)x_perm, x_perm_scale);
+    } else {
+      const int64_t nchunk = (int64_t)cfg->H * act_bytes(cfg) / 16;
+      hipLaunchKernelGGL((permute_rows_kernel<16, LOCAL>), dim3(tblocks), dim3(256), 0, s, (const uint4*)x, inv,
+                         cfg->T, cfg->k, nchunk, (uint4*)x_perm);
+    }
+    return launch_status();
+  };
   const unsigned blocks = (unsigned)((nseg + 3) / 4);
   if (nseg > 0) {
     if constexpr (LOCAL)
@@ -680,32 +740,25 @@ static moe_status dispatch_launch(const moe_cfg* cfg, const Window& win, const i
                          E, nbits, nseg, segc);
     if ((st = launch_status()) != MOE_OK) return st;
   }
+  if (LOCAL && nseg > 0 && E <= 256 && nseg * E <= kSumCounts) {
+    hipLaunchKernelGGL(rank_local_kernel<true>, dim3((unsigned)nseg), dim3(256), 8 * E * sizeof(int32_t), s, topk_idx, N,
+                       E, nbits, win, segc, (int)nseg, counts, offsets, perm, inv);
+    if ((st = launch_status()) != MOE_OK) return st;
+    return permute();
+  }
   const int P = 1024 / Ep2;
   hipLaunchKernelGGL(scan_kernel, dim3(1), dim3(1024), (size_t)(P + 1) * Ep2 * sizeof(int32_t), s, segc,
                      nseg, E, Ep2, counts, offsets);
   if ((st = launch_status()) != MOE_OK) return st;
   if (nseg == 0) return MOE_OK;
   if constexpr (LOCAL)
-    hipLaunchKernelGGL(rank_local_kernel, dim3((unsigned)nseg), dim3(256), 8 * E * sizeof(int32_t), s, topk_idx, N, E,
-                       nbits, win, segc, offsets, perm, inv);
+    hipLaunchKernelGGL(rank_local_kernel<false>, dim3((unsigned)nseg), dim3(256), 8 * E * sizeof(int32_t), s, topk_idx,
+                       N, E, nbits, win, segc, (int)nseg, counts, offsets, perm, inv);
   else
     hipLaunchKernelGGL(rank_kernel, dim3(blocks), dim3(256), 4 * E * sizeof(int32_t), s, topk_idx, N, E,
                        nbits, nseg, segc, offsets, perm, inv);
   if ((st = launch_status()) != MOE_OK) return st;
-  if (!x_perm) return MOE_OK;
-  const unsigned tblocks = (unsigned)((cfg->T + 3) / 4);
-  if (fp4) {
-    hipLaunchKernelGGL((permute_rows_fp4_kernel<8, LOCAL>), dim3(tblocks), dim3(256), 0, s, (const uint4*)x, inv,
-                       cfg->T, cfg->k, cfg->H, (uint32_t*)x_perm, (uint32_t*)x_perm_scale);
-  } else if (fp8) {
-    hipLaunchKernelGGL((permute_rows_fp8_kernel<8, LOCAL>), dim3(tblocks), dim3(256), 0, s, (const uint4*)x, inv,
-                       cfg->T, cfg->k, cfg->H, (uint2*)x_perm, x_perm_scale);
-  } else {
-    const int64_t nchunk = (int64_t)cfg->H * act_bytes(cfg) / 16;
-    hipLaunchKernelGGL((permute_rows_kernel<16, LOCAL>), dim3(tblocks), dim3(256), 0, s, (const uint4*)x, inv,
-                       cfg->T, cfg->k, nchunk, (uint4*)x_perm);
-  }
-  return launch_status();
+  return permute();
 }
 
 static moe_status dispatch_check(const moe_cfg* cfg, const int32_t* topk_idx, const void* x, int32_t* counts,

@@ -75,6 +75,8 @@ CASES = [
     (512, 128, 512, 0, 512, 8, 512),       # 4096 pairs: the last that one launch sorts
     (513, 128, 512, 5, 300, 8, 500),
     (130, 8320, 512, 100, 300, 32, 77),
+    (4200, 64, 4, 1, 1, 1, None),
+    (20000, 64, 256, 0, 256, 8, 19000),    # more segment counts than a workgroup adds up
 ]
 
 
