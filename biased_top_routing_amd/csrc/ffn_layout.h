@@ -216,6 +216,7 @@ struct FfnLayout {
     R1 = P / bm1 + c->E;
     Rs1 = c->S > 0 ? (c->T + bm1 - 1) / bm1 : 0;
     R2 = P / bm2 + c->E;
+    if (f4) R1 = std::min(R1, P), R2 = std::min(R2, P);   // (few pairs: no more tiles than rows)
     Rs2 = c->S > 0 ? (c->T + bm2 - 1) / bm2 : 0;
     const int bnh = f4 ? kFp4BNH : f8 ? kFp8BNH : dec ? kDecBNH : kBNH;
     const int bn2 = f4 ? kFp4BN2 : f8 ? kFp8BN2 : dec ? kDecBN2 : kBN2;
