@@ -741,8 +741,8 @@ static moe_status dispatch_launch(const moe_cfg* cfg, const Window& win, const i
     if ((st = launch_status()) != MOE_OK) return st;
   }
   if (LOCAL && nseg > 0 && E <= 256 && nseg * E <= kSumCounts) {
-    hipLaunchKernelGGL(rank_local_kernel<true>, dim3((unsigned)nseg), dim3(256), 8 * E * sizeof(int32_t), s, topk_idx, N,
-                       E, nbits, win, segc, (int)nseg, counts, offsets, perm, inv);
+    hipLaunchKernelGGL(rank_local_kernel<true>, dim3((unsigned)nseg), dim3(256), 8 * E * sizeof(int32_t), s, topk_idx,
+                       N, E, nbits, win, segc, (int)nseg, counts, offsets, perm, inv);
     if ((st = launch_status()) != MOE_OK) return st;
     return permute();
   }

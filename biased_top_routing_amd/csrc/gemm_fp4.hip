@@ -38,9 +38,14 @@
 // the stores out, row blocks skipped where a tile is short (branches between the
 // MFMAs: 2% to 10% slower, with MFMA work saved).
 //
-// Few rows per expert: 32 x 256 or 64 x 256 tiles that stream the weights, one
-// workgroup of 4 wavefronts per tile, two K steps per slice and 4 or 3 stages (T =
-// 128 on the layer above: the whole call 0.99 ms, 6.0 GB of weights at 6.1 TB/s).
+// Few rows per expert: the GEMMs stream the weights.  Tiles of 64 x 256, one workgroup
+// of 4 wavefronts each, 3 stages of two K steps; or of 32 rows in 4 parts of 64 weight
+// rows, a workgroup of one wavefront each, 3 stages, 4 of them a CU, which nothing but
+// their own loads holds up (layer above, the whole call in us with 4 wavefronts a
+// workgroup and 4 stages / 2 and 3 / 1 and 3: T = 1 53.4 / 52.7 / 50.2, 16 419 / 406 /
+// 406, 128 996 / 983 / 983, 512 1066 / 1056 / 1064; H = 2048, I = 1408, T = 2, 6 + 2 a
+// token 29.7 / 25.5 / 25.4; 64-row tiles in parts: 32 rows an expert 1152 / 1130 /
+// 1271, 48 rows 1213 / 1237 / 1430).  T = 128 reads its 5.9 GB at 6.0 TB/s.
 //
 // The shared experts' down GEMM walks the experts one after the other.  The
 // gate/up tile's 256 weight rows are the 128 gate rows and the 128 up rows of 128
@@ -175,22 +180,24 @@ struct Operands4 {
     c0 = MODE == kGateUp4 ? d.nt * 128 - ex * p.I : d.nt * 256;
   }
 
-  // weight row (in its expert) of tile column row r, the last one for rows past the columns
-  __device__ __forceinline__ int wrow(const Fp4Params& p, int r) const {
-    if constexpr (MODE == kGateUp4) return c0 + (r < 128 ? r : r - 128 + p.I);
-    else return min(c0 + r, ncols - 1);
+  // weight row (in its expert) of row r of part `part` of the tile's columns (BN weight rows a part), the
+  // last one for rows past the columns
+  template <int BN>
+  __device__ __forceinline__ int wrow(const Fp4Params& p, int part, int r) const {
+    if constexpr (MODE == kGateUp4) return c0 + part * (BN / 2) + (r < BN / 2 ? r : r - BN / 2 + p.I);
+    else return min(c0 + part * BN + r, ncols - 1);
   }
 };
 
 // The order of a wavefront's columns: block ni, MFMA row 4 g + r is column
-// 8 g + 4 (ni mod 2) + r of its 32 gate columns (ni < 2) or of the up columns 128
+// 8 g + 4 (ni mod 2) + r of its 32 gate columns (ni < 2) or of the up columns BN / 2
 // further on, or of its first or second 32 output columns, so that a lane holds 8
 // neighbouring columns of a row in two blocks: 4 bytes of codes, 16 of bf16.  The
 // tile column whose LDS row lane l16 reads is col_lane + col_off.
 __device__ __forceinline__ int col_lane(int l16) { return 8 * (l16 >> 2) + (l16 & 3); }
-template <int MODE>
+template <int MODE, int BN>
 __device__ __forceinline__ constexpr int col_off(int ni) {
-  return (ni / 2) * (MODE == kGateUp4 ? 128 : 32) + (ni % 2) * 4;
+  return (ni / 2) * (MODE == kGateUp4 ? BN / 2 : 32) + (ni % 2) * 4;
 }
 // Physical 16-byte chunk of logical chunk c of 8 in LDS row r of the weights: 8
 // lanes' rows (4, and 4 that lie 8 further on) meet no bank twice.
@@ -230,21 +237,24 @@ __device__ __forceinline__ void stage_h(uint8_t* hc, uint8_t* hsc, int row, int 
   if (g == 0) hsc[row * 4 + wn] = (uint8_t)e;
 }
 
-// The staged gate/up tile to memory: 16 bytes a lane, 4 lanes a row, and the rows' scale words.
-template <int NT>
-__device__ __forceinline__ void store_h(const Fp4Params& p, const TileDesc& d, bool shared, const uint8_t* hc,
+// The staged gate/up tile, or its quarter `part` (WN = 1), to memory: 16 bytes a lane,
+// WN lanes a row, and the rows' scale words, or bytes of them.
+template <int NT, int WN>
+__device__ __forceinline__ void store_h(const Fp4Params& p, const TileDesc& d, int part, bool shared, const uint8_t* hc,
                                         const uint8_t* hsc, int tid) {
   const int hw = shared ? p.S * p.I / 2 : p.I / 2;      // bytes of an h row
   uint8_t* out = shared ? p.out_shared : p.out_routed;
-  uint32_t* out_s = reinterpret_cast<uint32_t*>(shared ? p.out_shared_scale : p.out_routed_scale);
+  uint8_t* out_s = shared ? p.out_shared_scale : p.out_routed_scale;
   const int64_t plane = shared ? p.T : (int64_t)p.T * p.k;
-  for (int q = tid; q < d.rows * 4; q += NT) {
-    const int i = q >> 2, c = q & 3;
-    *reinterpret_cast<uint4*>(out + (d.row0 + i) * (int64_t)hw + d.nt * 64 + c * 16) =
+  for (int q = tid; q < d.rows * WN; q += NT) {
+    const int i = q / WN, c = q % WN;
+    *reinterpret_cast<uint4*>(out + (d.row0 + i) * (int64_t)hw + d.nt * 64 + (part * WN + c) * 16) =
         *reinterpret_cast<const uint4*>(hc + i * kHPitch + c * 16);
   }
+  using scales_t = std::conditional_t<WN == 4, uint32_t, uint8_t>;
   for (int i = tid; i < d.rows; i += NT)
-    out_s[d.nt * plane + d.row0 + i] = *reinterpret_cast<const uint32_t*>(hsc + i * 4);
+    *reinterpret_cast<scales_t*>(out_s + (d.nt * plane + d.row0 + i) * 4 + part * WN) =
+        *reinterpret_cast<const scales_t*>(hsc + i * 4);
 }
 
 // 16 rows x 64 columns of a wavefront's down tile as bf16, through its own two 1 KB
@@ -481,8 +491,8 @@ __global__ __launch_bounds__(kFp4Threads, 1) void gemm_fp4_kernel(Fp4Params p) {
     ra[mi % NB] = stage[sa_lane + kk * SCP + mi * 64];
   };
   auto read_b = [&](const uint8_t* stage, int kk, int ni) {
-    fbn[ni] = frag4(stage + (b_lane ^ (kk * 64)) + col_off<MODE>(ni) * BK);
-    rbn[ni] = stage[sb_lane + kk * SCP + col_off<MODE>(ni) * 4];
+    fbn[ni] = frag4(stage + (b_lane ^ (kk * 64)) + col_off<MODE, BN>(ni) * BK);
+    rbn[ni] = stage[sb_lane + kk * SCP + col_off<MODE, BN>(ni) * 4];
   };
   auto next_b = [&]() {
 #pragma unroll
@@ -569,7 +579,7 @@ __global__ __launch_bounds__(kFp4Threads, 1) void gemm_fp4_kernel(Fp4Params p) {
           stage_h(hc, hsc, wm * MI * 16 + l16 + mi * 16, wn, g, w, e);
         }
         lds_barrier();
-        store_h<NT>(p, cd, shared, hc, hsc, tid);
+        store_h<NT, WN>(p, cd, 0, shared, hc, hsc, tid);
         lds_barrier();                                 // the staging is read: its loads may go out
       } else {
         bf16_t* out = reinterpret_cast<bf16_t*>(shared ? p.out_shared : p.out_routed);
@@ -608,9 +618,10 @@ __global__ __launch_bounds__(kFp4Threads, 1) void gemm_fp4_kernel(Fp4Params p) {
 }
 
 // ------------------------------------------------------------------ few rows per expert
-template <int MODE, int BM, int STAGES>
-__global__ __launch_bounds__(256, 1) void gemm_fp4_rows_kernel(Fp4Params p) {
-  constexpr int WN = 4, MI = BM / 16, NT = 256, NW = 4, BN = 256;
+template <int MODE, int BM, int STAGES, int WN>
+__global__ __launch_bounds__(WN * 64, 1) void gemm_fp4_rows_kernel(Fp4Params p) {
+  constexpr int MI = BM / 16, NW = WN, NT = NW * 64, BN = NW * 64, PARTS = 4 / WN;
+  static_assert(PARTS * BN == kFp4BN2 && (WN == 1 || WN == 4), "the tiles of the table, whole or in quarters");
   constexpr int BK = 128, CPR = BK / 16;               // bytes (two K steps) and 16-byte chunks of a row per slice
   constexpr int A_CH = BM * CPR / NT, B_CH = BN * CPR / NT;
   static_assert(BM * CPR % NT == 0 && BN * CPR % NT == 0, "whole loads per thread");
@@ -626,7 +637,10 @@ __global__ __launch_bounds__(256, 1) void gemm_fp4_rows_kernel(Fp4Params p) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[LDS_BYTES];
   const int tid = threadIdx.x, lane = tid & 63, wn = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, g = lane >> 4;
-  const int L = grouped_tile<kStripeFp4>(p.ntiles);
+  // (the parts of a tile go to one XCD)
+  const int part = (blockIdx.x >> 3) % PARTS, b = (blockIdx.x >> 3) / PARTS * 8 + (blockIdx.x & 7);
+  const int L = grouped_tile_at(b, __builtin_amdgcn_readfirstlane(p.ntiles[0]),
+                                __builtin_amdgcn_readfirstlane(p.ntiles[4]), kStripeFp4);
   if (L < 0) return;
   const TileDesc d = tile_at(p, L);
   const Operands4<MODE> o(p, d);
@@ -640,13 +654,15 @@ __global__ __launch_bounds__(256, 1) void gemm_fp4_rows_kernel(Fp4Params p) {
 #pragma unroll
   for (int i = 0; i < B_CH; ++i) {
     const int c = i * NT + tid, r = c / CPR;
-    b_off[i] = (int)(o.ex * o.w_one) + o.wrow(p, r) * o.ldw + swz_w(r, c % CPR) * 16;
+    b_off[i] = (int)(o.ex * o.w_one) + o.template wrow<BN>(p, part, r) * o.ldw + swz_w(r, c % CPR) * 16;
   }
 #pragma unroll
   for (int i = 0; i < SC_CH; ++i) {
     const int c = i * NT + tid, cb = c - 2 * BM;
     if (c < 2 * BM) s_off[i] = c % BM < d.rows ? c / BM * o.sa_stride + a_row(c % BM) * 4 : kDrop;
-    else s_off[i] = cb < 2 * BN ? o.ex * o.sw_one + cb / BN * o.sw_stride + o.wrow(p, cb % BN) * 4 : kDrop;
+    else if (cb < 2 * BN)
+      s_off[i] = o.ex * o.sw_one + cb / BN * o.sw_stride + o.template wrow<BN>(p, part, cb % BN) * 4;
+    else s_off[i] = kDrop;
   }
   const __amdgpu_buffer_rsrc_t ra = make_rsrc(o.A, o.a_bytes), rw = make_rsrc(o.W, o.w_bytes),
                                rsa = make_rsrc(o.SA, o.sa_bytes), rsw = make_rsrc(o.SW, o.sw_bytes);
@@ -697,7 +713,7 @@ __global__ __launch_bounds__(256, 1) void gemm_fp4_rows_kernel(Fp4Params p) {
       int sb[NI4];
 #pragma unroll
       for (int ni = 0; ni < NI4; ++ni) {
-        const int r = brow + col_off<MODE>(ni);
+        const int r = brow + col_off<MODE, BN>(ni);
         fb[ni] = frag4(base + BM * BK + r * BK + chw);
         sb[ni] = scb[r * 4];
       }
@@ -723,12 +739,13 @@ __global__ __launch_bounds__(256, 1) void gemm_fp4_rows_kernel(Fp4Params p) {
       stage_h(lds, hsc, l16 + mi * 16, wn, g, w, e);
     }
     lds_barrier();
-    store_h<NT>(p, d, o.shared, lds, hsc, tid);
+    store_h<NT, WN>(p, d, part, o.shared, lds, hsc, tid);
   } else {
     bf16_t* out = reinterpret_cast<bf16_t*>(o.shared ? p.out_shared : p.out_routed);
 #pragma unroll
     for (int mi = 0; mi < MI; ++mi)
-      store_y(lds + wn * 2048, 1024, acc[mi], out, d.row0, mi * 16, d.rows, d.nt * BN + wn * 64, p.H, lane);
+      store_y(lds + wn * 2048, 1024, acc[mi], out, d.row0, mi * 16, d.rows, d.nt * kFp4BN2 + part * BN + wn * 64, p.H,
+              lane);
   }
 #endif
 }
@@ -736,11 +753,11 @@ __global__ __launch_bounds__(256, 1) void gemm_fp4_rows_kernel(Fp4Params p) {
 template <int MODE>
 moe_status launch_gemm_fp4(const FfnLayout& L, int64_t max_tiles, const Fp4Params& p, hipStream_t st) {
   if (max_tiles == 0) return MOE_OK;
-  const dim3 rows_grid((unsigned)grouped_grid(max_tiles, kStripeFp4));
+  const unsigned rows_grid = (unsigned)grouped_grid(max_tiles, kStripeFp4);
   if (L.bm1 == kFp4RowsBM) {
-    hipLaunchKernelGGL((gemm_fp4_rows_kernel<MODE, kFp4RowsBM, 4>), rows_grid, dim3(256), 0, st, p);
+    hipLaunchKernelGGL((gemm_fp4_rows_kernel<MODE, kFp4RowsBM, 3, 1>), dim3(4 * rows_grid), dim3(64), 0, st, p);
   } else if (L.bm1 == kFp4MidBM) {
-    hipLaunchKernelGGL((gemm_fp4_rows_kernel<MODE, kFp4MidBM, 3>), rows_grid, dim3(256), 0, st, p);
+    hipLaunchKernelGGL((gemm_fp4_rows_kernel<MODE, kFp4MidBM, 3, 4>), dim3(rows_grid), dim3(256), 0, st, p);
   } else {
     // one workgroup a CU (its LDS leaves no room for two), whole rounds of the 8 XCDs
     const int64_t grid = std::min<int64_t>(std::max(cu_count() / 8 * 8, 8), (int64_t)align_up((size_t)max_tiles, 8));
