@@ -99,9 +99,10 @@ constexpr int kFp8MaxKC = 64;
 // MXFP4 GEMMs: tiles of 256 or 288 token rows, or of 32 or 64 where the routed experts get
 // at most 24 or 56 rows each on average: the GEMMs then stream weights, and a tile's
 // height decides how often (H = 7168, I = 2048, 256 experts, the whole call in us
-// with 32 / 64 / 256 rows a tile: 24 rows an expert 1069 / 1093 / 1326, 32 rows
-// 1277 / 1133 / 1358, 48 rows 1648 / 1205 / 1367, 64 rows 1998 / 1605 / 1413; 128
-// rows a tile are nowhere best); 128 h columns per gate/up tile, 256 output columns
+// with 32 / 64 / 256 rows a tile: 20 rows an expert 1101 / 1111 / -, 24 rows 1149 /
+// 1121 / 1326, 32 rows 1277 / 1133 / 1358, 48 rows 1648 / 1205 / 1367, 64 rows 1998 /
+// 1605 / 1413; 128 rows a tile are nowhere best; H = 2048, I = 1408, 64 experts, 24
+// rows 85 / 100 / -); 128 h columns per gate/up tile, 256 output columns
 // per down tile.
 constexpr int kFp4BM = 256, kFp4HighBM = 288, kFp4RowsBM = 32, kFp4MidBM = 64;
 constexpr int kFp4RowsAvg = 24, kFp4MidAvg = 56;
