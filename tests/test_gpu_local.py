@@ -444,3 +444,41 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for lay, want in zip(layers, alone):
         assert torch.equal(lay.y.view(torch.int16), want.view(torch.int16))
+
+
+def test_rows_past_32_bit_offsets():
+    """A batch that repeats 512 tokens 128 times: its permuted rows take 7.5 GB, and every repetition gives what
+    the 512 tokens give alone, bit for bit (a row's products and sums do not depend on where it lies)."""
+    n, R, H, E, k = 512, 128, 7168, 8, 8
+    g = rng(78, 1)
+    c = MID.with_(T=n, H=H, E=E, G=1, M=1, k=k, S=1, I=128, sigma=0.05, wgt="mxfp4")
+    wts = make_weights(c)
+    bits = lambda *s: to_device(f32_to_bf16_bits(g.standard_normal(s).astype(np.float32)))
+    x, dy = bits(n, H), bits(n, H)
+    idx = dev_i32(np.argsort(g.random((n, E)), axis=1).astype(np.int32))
+    w = dev_f32(g.random((n, k)).astype(np.float32))
+    held = MoeLayerGPU(c, wts, T=1)          # its quantised weights
+
+    def run(T):
+        cfg = L.make_cfg(T, H, E, 1, 1, k, 1, 128, 1, 1.0, "bf16", "mxfp4")
+        grad = L.make_cfg(T, H, E, 1, 1, k, 0, 128, 1, 1.0, "bf16", "bf16")
+        rep = lambda a: a.repeat(T // n, 1)
+        u8, bf = dict(dtype=torch.uint8, device="cuda"), dict(dtype=torch.bfloat16, device="cuda")
+        P = T * k
+        xp, xs = torch.empty((P, H // 2), **u8), torch.empty((H // 128, P, 4), **u8)
+        xt, wt, dyt = rep(x), rep(w), rep(dy)
+        _, offsets, _, inv = _dispatch(cfg, 0, None, rep(idx), xt, xp, xs)
+        assert (host(offsets) == np.arange(E + 1) * T).all()
+        yp, ysh, y, dx = torch.empty((P, H), **bf), *(torch.empty((T, H), **bf) for _ in range(3))
+        ws = torch.empty(L.moe_workspace_bytes(cfg, L.MOE_WS_FFN), **u8)
+        L.moe_expert_ffn(cfg, xp, xs, offsets, held.weights, xt, yp, ysh, ws)
+        L.moe_combine_local(cfg, yp, ysh, inv, wt, y)
+        dyp, dw = torch.empty((P, H), **bf), torch.empty((T, k), dtype=torch.float32, device="cuda")
+        L.moe_combine_local_backward(grad, dyt, yp, inv, wt, dyp, dw)
+        L.moe_dispatch_local_backward(grad, dyp, None, None, inv, dx)
+        torch.cuda.synchronize()
+        return [a.view(torch.int16 if a.dtype == torch.bfloat16 else torch.int32) for a in (y, dw, dx)]
+
+    say("rows past 32-bit offsets")
+    for name, one, many in zip(("y", "d_topk_w", "dx"), run(n), run(n * R)):
+        assert torch.equal(many.view(R, n, -1), one.view(1, n, -1).expand(R, -1, -1)), name
