@@ -96,22 +96,23 @@ constexpr int kFp8BM = MOE_FP8_BM;
 constexpr int kFp8BNH = 128;
 constexpr int kFp8BN2 = 256;
 constexpr int kFp8MaxKC = 64;
-// MXFP4 GEMMs: tiles of 256 or 288 token rows, or of 32 or 64 where the routed experts get
-// at most 24 or 56 rows each on average: the GEMMs then stream weights, and a tile's
-// height decides how often (H = 7168, I = 2048, 256 experts, the whole call in us
-// with 32 / 64 / 256 rows a tile: 20 rows an expert 1101 / 1111 / -, 24 rows 1149 /
-// 1121 / 1326, 32 rows 1277 / 1133 / 1358, 48 rows 1648 / 1205 / 1367, 64 rows 1998 /
-// 1605 / 1413; 128 rows a tile are nowhere best; H = 2048, I = 1408, 64 experts, 24
-// rows 85 / 100 / -); 128 h columns per gate/up tile, 256 output columns
-// per down tile.
-constexpr int kFp4BM = 256, kFp4HighBM = 288, kFp4RowsBM = 32, kFp4MidBM = 64;
-constexpr int kFp4RowsAvg = 24, kFp4MidAvg = 56;
+// MXFP4 GEMMs: token rows per tile by the mean rows of a routed expert: 32 up to 20
+// (the GEMMs stream weights, and the 32-row tiles' small workgroups do it best), 128
+// up to 120 (two slices of loads in flight instead of one), 256 or 288 (below) beyond;
+// 128 h columns per gate/up tile, 256 output columns per down tile.  The whole call in
+// us at H = 7168, I = 2048, 256 experts, 32 / 128 rows a tile: 8 rows an expert 1017 /
+// 1052, 16 rows 1068 / 1080, 20 rows 1102 / 1088, 24 rows 1152 / 1099; 128 / 256 rows a
+// tile: 64 rows an expert 1211 / 1440, 96 rows 1322 / 1514, 112 rows 1455 / 1563, 128
+// rows 1662 / 1651; at H = 2048, I = 1408, 64 experts, 32 / 128 rows a tile: 16 rows 81 /
+// 84, 24 rows 84 / 85, 128 / 256: 64 rows 100 / 126, 100 rows 113 / 137.
+constexpr int kFp4RowsBM = 32, kFp4LowBM = 128, kFp4BM = 256, kFp4HighBM = 288;
+constexpr int kFp4RowsAvg = 20, kFp4LowAvg = 120;
 constexpr int kFp4BNH = 128, kFp4BN2 = 256;
 // 288 rows take more time a tile and are right where they save one: a segment somewhat
 // longer than the mean (by twice the square root, the spread of an even routing) needs
-// fewer such tiles.  The layer above, 256 / 288 rows a tile: 256 rows an expert 2534 /
-// 2268 us, 512 rows 4260 / 4002, where it saves none (384 rows) 3307 / 3327, 64 rows
-// 1439 / 1476; H = 2048, I = 1408, 64 experts, 384 rows, skewed 238 / 247.
+// fewer such tiles.  The first layer above, 256 / 288 rows a tile: 256 rows an expert 2534 /
+// 2268 us, 512 rows 4260 / 4002, where it saves none (384 rows) 3307 / 3327; the
+// second, 384 rows, skewed 238 / 247.
 inline int fp4_tile_rows(int64_t avg) {
   int64_t dev = 1;
   while ((dev + 1) * (dev + 1) <= avg) ++dev;
@@ -207,7 +208,7 @@ struct FfnLayout {
     const int64_t P = pairs(c);
     const bool f8 = c->wgt == MOE_FP8_E4M3, f4 = c->wgt == MOE_MXFP4;
     const int bm4 = P <= (int64_t)kFp4RowsAvg * c->E  ? kFp4RowsBM
-                    : P <= (int64_t)kFp4MidAvg * c->E ? kFp4MidBM
+                    : P <= (int64_t)kFp4LowAvg * c->E ? kFp4LowBM
                                                       : fp4_tile_rows(P / c->E);
     dec = small_batch(c);
     bm1 = f4 ? bm4 : f8 ? kFp8BM : dec ? kDecBM : kBM1;

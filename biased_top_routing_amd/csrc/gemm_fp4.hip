@@ -11,8 +11,8 @@
 //            the epilogue from the fp32 accumulators (one rounding, to E2M1)
 //   down     Y = h W_d^T, stored as bf16
 //
-// Large batches: tiles of 256 or 288 token rows x 256 weight rows, one workgroup of
-// 2 x 4 wavefronts a CU, each wavefront 8 x 4 or 9 x 4 MFMA blocks, and the
+// Large batches: tiles of 128, 256 or 288 token rows x 256 weight rows, one workgroup
+// of 2 x 4 wavefronts a CU, each wavefront 4 x 4 to 9 x 4 MFMA blocks, and the
 // workgroups stay: each takes a 32nd of its XCD's contiguous share of the table (one
 // expert's tiles run on one XCD at the same time and meet in its L2), and the loads
 // run through the tiles without a break.  K advances two 128-wide steps (128 bytes of
@@ -38,14 +38,16 @@
 // the stores out, row blocks skipped where a tile is short (branches between the
 // MFMAs: 2% to 10% slower, with MFMA work saved).
 //
-// Few rows per expert: the GEMMs stream the weights.  Tiles of 64 x 256, one workgroup
-// of 4 wavefronts each, 3 stages of two K steps; or of 32 rows in 4 parts of 64 weight
-// rows, a workgroup of one wavefront each, 3 stages, 4 of them a CU, which nothing but
-// their own loads holds up (layer above, the whole call in us with 4 wavefronts a
-// workgroup and 4 stages / 2 and 3 / 1 and 3: T = 1 53.4 / 52.7 / 50.2, 16 419 / 406 /
-// 406, 128 996 / 983 / 983, 512 1066 / 1056 / 1064; H = 2048, I = 1408, T = 2, 6 + 2 a
-// token 29.7 / 25.5 / 25.4; 64-row tiles in parts: 32 rows an expert 1152 / 1130 /
-// 1271, 48 rows 1213 / 1237 / 1430).  T = 128 reads its 5.9 GB at 6.0 TB/s.
+// 128-row tiles leave room for 3 stages: two slices are on their way, and a slice takes
+// 1.3 us where the others take 2 whatever rows they hold (64 rows an expert on that
+// layer: the whole call 1.21 ms against 1.44 with 256-row tiles).
+//
+// Few rows per expert: the GEMMs stream the weights.  Tiles of 32 rows in 4 parts of 64
+// weight rows, a workgroup of one wavefront each, 3 stages of two K steps, 4 of them a
+// CU, which nothing but their own loads holds up (layer above, the whole call in us
+// with 4 wavefronts a workgroup and 4 stages / 2 and 3 / 1 and 3: T = 1 53.4 / 52.7 /
+// 50.2, 16 419 / 406 / 406, 128 996 / 983 / 983, 512 1066 / 1056 / 1064; H = 2048, I =
+// 1408, T = 2, 6 + 2 a token 29.7 / 25.5 / 25.4).  T = 128 reads its 5.9 GB at 6.0 TB/s.
 //
 // The shared experts' down GEMM walks the experts one after the other.  The
 // gate/up tile's 256 weight rows are the 128 gate rows and the 128 up rows of 128
@@ -287,7 +289,7 @@ __device__ __forceinline__ void store_y(uint8_t* stg, int dist, const f32x4_t (&
 // ------------------------------------------------------------------ large batches
 constexpr int kFp4Threads = 512;
 
-template <int MODE, int BM>
+template <int MODE, int BM, int STAGES>
 __global__ __launch_bounds__(kFp4Threads, 1) void gemm_fp4_kernel(Fp4Params p) {
   constexpr int WM = 2, WN = 4, MI = BM / (WM * 16);
   constexpr int NT = kFp4Threads, NW = NT / 64, BN = 256;
@@ -297,12 +299,12 @@ __global__ __launch_bounds__(kFp4Threads, 1) void gemm_fp4_kernel(Fp4Params p) {
   constexpr int A_CH = (BM + RPL - 1) / RPL, B_CH = BN / RPL;   // loads per thread; A's last one covers AX rows
   // of a step's scale words wavefronts 0-3 load A's first 256, wavefronts 4-7 B's; past 256 rows (32 of
   // them) A's last load is wavefronts 0-3's alone
-  constexpr int AX = BM - 256;
-  static_assert(BN == 256 && NT == 512 && (AX == 0 || AX == RPL / 2), "the loads of a slice");
-  constexpr int PER = A_CH + B_CH + 2;                 // loads per thread per slice
-  constexpr int SCP = (BM + BN) * 4;                   // a step's scale words: A's, B's
+  constexpr int ASC = BM > 256 ? BM : 256, AX = ASC - 256;
+  static_assert(BN == 256 && NT == 512 && (AX == 0 || (AX == RPL / 2 && STAGES == 2)), "the loads of a slice");
+  constexpr int PER = A_CH + B_CH + 2;                 // loads per thread per slice (every wavefront's, unless AX)
+  constexpr int SCP = (ASC + BN) * 4;                  // a step's scale words: A's, B's
   constexpr int B_OFF = BM * BK, SC_OFF = B_OFF + BN * BK, STAGE = SC_OFF + 2 * SCP;
-  constexpr int PERM_OFF = 2 * STAGE;                  // the next tile's perm entries (gathered rows)
+  constexpr int PERM_OFF = STAGES * STAGE;                  // the next tile's perm entries (gathered rows)
   constexpr int LDS_BYTES = PERM_OFF + align64(BM) * 4;
   static_assert(LDS_BYTES <= 163840, "LDS of a CU");
   // the epilogue's staging: the weights' part of the stage that is filled next
@@ -448,7 +450,7 @@ __global__ __launch_bounds__(kFp4Threads, 1) void gemm_fp4_kernel(Fp4Params p) {
         sk += s_skip;
       }
     }
-    ls ^= 1;
+    ls = ls == STAGES - 1 ? 0 : ls + 1;
   };
   // Before a slice's loads: the next tile is begun where the last one has ended.
   auto prepare = [&]() {
@@ -474,9 +476,9 @@ __global__ __launch_bounds__(kFp4Threads, 1) void gemm_fp4_kernel(Fp4Params p) {
   const int brow = wn * (MODE == kGateUp4 ? 32 : 64) + col_lane(l16);
   const int a_lane = arow0 * BK + swz<CPR>(l16, g) * 16;
   const int b_lane = B_OFF + brow * BK + swz_w(col_lane(l16), g) * 16;
-  const int sa_lane = SC_OFF + arow0 * 4 + g, sb_lane = SC_OFF + (BM + brow) * 4 + g;
+  const int sa_lane = SC_OFF + arow0 * 4 + g, sb_lane = SC_OFF + (ASC + brow) * 4 + g;
   constexpr int NB = MI % 3 == 0 ? 3 : 4, D = 2;       // A fragments held, and read ahead
-  static_assert(MI % NB == 0 && D < NB && PER == MI + 2, "the buffers rotate within a step; the issue schedule");
+  static_assert(MI % NB == 0 && D < NB && MI >= NI4, "the buffers rotate within a step; B's next step is read in one");
   f32x4_t acc[MI][NI4];
   i32x8_t fa[NB], fb[NI4], fbn[NI4];
   int ra[NB], rb[NI4], rbn[NI4];
@@ -524,7 +526,10 @@ __global__ __launch_bounds__(kFp4Threads, 1) void gemm_fp4_kernel(Fp4Params p) {
       if (KK == 0 && mi < NI4) read_b(here, 1, mi);
       __builtin_amdgcn_sched_barrier(0);
       multiply(mi);
-      if (KK == 0) issue_part(2 + mi);
+      if (KK == 0) {
+#pragma unroll
+        for (int i = 2 + (PER - 2) * mi / MI; i < 2 + (PER - 2) * (mi + 1) / MI; ++i) issue_part(i);
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
     if (KK == 0) {
@@ -541,6 +546,17 @@ __global__ __launch_bounds__(kFp4Threads, 1) void gemm_fp4_kernel(Fp4Params p) {
 #pragma unroll
   for (int i = 0; i < PER; ++i) issue_part(i);
   advance();
+#pragma unroll
+  for (int s = 2; s < STAGES; ++s) {
+    if (left_l <= 0) {                                 // (the next tile's perm entries)
+      wait_vm<0>();
+      lds_barrier();
+    }
+    prepare();
+#pragma unroll
+    for (int i = 0; i < PER; ++i) issue_part(i);
+    advance();
+  }
   clear();
 
   int nc = 0, qc = place(1);                           // the tile after the one being computed
@@ -554,11 +570,11 @@ __global__ __launch_bounds__(kFp4Threads, 1) void gemm_fp4_kernel(Fp4Params p) {
   while (true) {
     // The slice's one barrier: the next slice has landed, everywhere (it was asked for a
     // slice ago), and this one's stage is free; loading into it begins.
-    wait_vm<0>();
+    wait_vm<PER * (STAGES - 2)>();
     lds_barrier();
     prepare();
     const uint8_t* here = lds + cs * STAGE;
-    cs ^= 1;
+    cs = cs == STAGES - 1 ? 0 : cs + 1;
     read_first(here);                                  // (not into the buffer in use; after the last slice unused)
     __builtin_amdgcn_sched_barrier(0);
     if (half) multiply(MI - 1);
@@ -618,25 +634,25 @@ __global__ __launch_bounds__(kFp4Threads, 1) void gemm_fp4_kernel(Fp4Params p) {
 }
 
 // ------------------------------------------------------------------ few rows per expert
-template <int MODE, int BM, int STAGES, int WN>
-__global__ __launch_bounds__(WN * 64, 1) void gemm_fp4_rows_kernel(Fp4Params p) {
-  constexpr int MI = BM / 16, NW = WN, NT = NW * 64, BN = NW * 64, PARTS = 4 / WN;
-  static_assert(PARTS * BN == kFp4BN2 && (WN == 1 || WN == 4), "the tiles of the table, whole or in quarters");
+template <int MODE>
+__global__ __launch_bounds__(64, 1) void gemm_fp4_rows_kernel(Fp4Params p) {
+  constexpr int BM = kFp4RowsBM, STAGES = 3, PARTS = 4;
+  constexpr int MI = BM / 16, NT = 64, BN = 64;
+  static_assert(PARTS * BN == kFp4BN2, "the tiles of the table, in quarters");
   constexpr int BK = 128, CPR = BK / 16;               // bytes (two K steps) and 16-byte chunks of a row per slice
   constexpr int A_CH = BM * CPR / NT, B_CH = BN * CPR / NT;
   static_assert(BM * CPR % NT == 0 && BN * CPR % NT == 0, "whole loads per thread");
   // scale words of a slice: A's of step 0, of step 1, then B's likewise
   constexpr int SC_CH = (2 * (BM + BN) + NT - 1) / NT;
-  static_assert(2 * BM % 64 == 0, "a wavefront's scale load is all A or all B");
+  static_assert(2 * BM % 64 == 0, "a scale load is all A or all B");
   constexpr int PER = A_CH + B_CH + SC_CH;             // loads per thread per slice
   constexpr int SC_OFF = (BM + BN) * BK, STAGE = SC_OFF + SC_CH * NT * 4;
   constexpr int LDS_BYTES = STAGES * STAGE;
   static_assert(LDS_BYTES <= 163840, "LDS of a CU");
-  static_assert(BM * (kHPitch + 4) <= LDS_BYTES && NW * 2048 <= LDS_BYTES, "the epilogue's staging");
+  static_assert(BM * (kHPitch + 4) <= LDS_BYTES && 2048 <= LDS_BYTES, "the epilogue's staging");
 #if defined(__HIP_DEVICE_COMPILE__)
   __shared__ __attribute__((aligned(16))) uint8_t lds[LDS_BYTES];
-  const int tid = threadIdx.x, lane = tid & 63, wn = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int l16 = lane & 15, g = lane >> 4;
+  const int lane = threadIdx.x, l16 = lane & 15, g = lane >> 4;
   // (the parts of a tile go to one XCD)
   const int part = (blockIdx.x >> 3) % PARTS, b = (blockIdx.x >> 3) / PARTS * 8 + (blockIdx.x & 7);
   const int L = grouped_tile_at(b, __builtin_amdgcn_readfirstlane(p.ntiles[0]),
@@ -648,17 +664,17 @@ __global__ __launch_bounds__(WN * 64, 1) void gemm_fp4_rows_kernel(Fp4Params p) 
   int a_off[A_CH], b_off[B_CH], s_off[SC_CH];
 #pragma unroll
   for (int i = 0; i < A_CH; ++i) {
-    const int c = i * NT + tid, r = c / CPR;
+    const int c = i * NT + lane, r = c / CPR;
     a_off[i] = a_row(r) * o.lda + swz<CPR>(r, c % CPR) * 16;
   }
 #pragma unroll
   for (int i = 0; i < B_CH; ++i) {
-    const int c = i * NT + tid, r = c / CPR;
+    const int c = i * NT + lane, r = c / CPR;
     b_off[i] = (int)(o.ex * o.w_one) + o.template wrow<BN>(p, part, r) * o.ldw + swz_w(r, c % CPR) * 16;
   }
 #pragma unroll
   for (int i = 0; i < SC_CH; ++i) {
-    const int c = i * NT + tid, cb = c - 2 * BM;
+    const int c = i * NT + lane, cb = c - 2 * BM;
     if (c < 2 * BM) s_off[i] = c % BM < d.rows ? c / BM * o.sa_stride + a_row(c % BM) * 4 : kDrop;
     else if (cb < 2 * BN)
       s_off[i] = o.ex * o.sw_one + cb / BN * o.sw_stride + o.template wrow<BN>(p, part, cb % BN) * 4;
@@ -676,15 +692,14 @@ __global__ __launch_bounds__(WN * 64, 1) void gemm_fp4_rows_kernel(Fp4Params p) 
     uint8_t* sb = lds + stage * STAGE;
 #pragma unroll
     for (int i = 0; i < A_CH; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void_t*)(sb + (i * NW + wn) * 1024), 16, a_off[i], ak, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void_t*)(sb + i * 1024), 16, a_off[i], ak, 0, 0);
 #pragma unroll
     for (int i = 0; i < B_CH; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void_t*)(sb + BM * BK + (i * NW + wn) * 1024), 16, b_off[i], wk,
-                                               0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void_t*)(sb + BM * BK + i * 1024), 16, b_off[i], wk, 0, 0);
 #pragma unroll
     for (int i = 0; i < SC_CH; ++i) {
-      lds_void_t* dst = (lds_void_t*)(sb + SC_OFF + (i * NW + wn) * 256);
-      if ((i * NW + wn) * 64 < 2 * BM) __builtin_amdgcn_raw_ptr_buffer_load_lds(rsa, dst, 4, s_off[i], as, 0, 0);
+      lds_void_t* dst = (lds_void_t*)(sb + SC_OFF + i * 256);
+      if (i * 64 < 2 * BM) __builtin_amdgcn_raw_ptr_buffer_load_lds(rsa, dst, 4, s_off[i], as, 0, 0);
       else __builtin_amdgcn_raw_ptr_buffer_load_lds(rsw, dst, 4, s_off[i], ws, 0, 0);
     }
   };
@@ -696,7 +711,6 @@ __global__ __launch_bounds__(WN * 64, 1) void gemm_fp4_rows_kernel(Fp4Params p) 
   for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
     for (int ni = 0; ni < NI4; ++ni) acc[mi][ni] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  const int brow = wn * (MODE == kGateUp4 ? 32 : 64) + col_lane(l16);
   int cur = 0, left = o.nk1;                           // K steps left of the current expert
   for (int kt = 0; kt < ns; ++kt) {
     wait_loads<PER, STAGES - 2>(min(ns - 1, kt + STAGES - 2) - kt);
@@ -713,7 +727,7 @@ __global__ __launch_bounds__(WN * 64, 1) void gemm_fp4_rows_kernel(Fp4Params p) 
       int sb[NI4];
 #pragma unroll
       for (int ni = 0; ni < NI4; ++ni) {
-        const int r = brow + col_off<MODE, BN>(ni);
+        const int r = col_lane(l16) + col_off<MODE, BN>(ni);
         fb[ni] = frag4(base + BM * BK + r * BK + chw);
         sb[ni] = scb[r * 4];
       }
@@ -729,23 +743,22 @@ __global__ __launch_bounds__(WN * 64, 1) void gemm_fp4_rows_kernel(Fp4Params p) 
     if (left <= 0) left = o.nk1;
     cur = cur == STAGES - 1 ? 0 : cur + 1;
   }
-  lds_barrier();                                       // every wavefront is done with the ring
+  lds_barrier();                                       // the ring has been read
   if constexpr (MODE == kGateUp4) {
     uint8_t* hsc = lds + BM * kHPitch;
 #pragma unroll
     for (int mi = 0; mi < MI; ++mi) {
       uint32_t e;
       const uint32_t w = swiglu_codes(acc[mi], &e);
-      stage_h(lds, hsc, l16 + mi * 16, wn, g, w, e);
+      stage_h(lds, hsc, l16 + mi * 16, 0, g, w, e);
     }
     lds_barrier();
-    store_h<NT, WN>(p, d, part, o.shared, lds, hsc, tid);
+    store_h<NT, 1>(p, d, part, o.shared, lds, hsc, lane);
   } else {
     bf16_t* out = reinterpret_cast<bf16_t*>(o.shared ? p.out_shared : p.out_routed);
 #pragma unroll
     for (int mi = 0; mi < MI; ++mi)
-      store_y(lds + wn * 2048, 1024, acc[mi], out, d.row0, mi * 16, d.rows, d.nt * kFp4BN2 + part * BN + wn * 64, p.H,
-              lane);
+      store_y(lds, 1024, acc[mi], out, d.row0, mi * 16, d.rows, d.nt * kFp4BN2 + part * BN, p.H, lane);
   }
 #endif
 }
@@ -753,19 +766,19 @@ __global__ __launch_bounds__(WN * 64, 1) void gemm_fp4_rows_kernel(Fp4Params p) 
 template <int MODE>
 moe_status launch_gemm_fp4(const FfnLayout& L, int64_t max_tiles, const Fp4Params& p, hipStream_t st) {
   if (max_tiles == 0) return MOE_OK;
-  const unsigned rows_grid = (unsigned)grouped_grid(max_tiles, kStripeFp4);
   if (L.bm1 == kFp4RowsBM) {
-    hipLaunchKernelGGL((gemm_fp4_rows_kernel<MODE, kFp4RowsBM, 3, 1>), dim3(4 * rows_grid), dim3(64), 0, st, p);
-  } else if (L.bm1 == kFp4MidBM) {
-    hipLaunchKernelGGL((gemm_fp4_rows_kernel<MODE, kFp4MidBM, 3, 4>), dim3(rows_grid), dim3(256), 0, st, p);
-  } else {
-    // one workgroup a CU (its LDS leaves no room for two), whole rounds of the 8 XCDs
-    const int64_t grid = std::min<int64_t>(std::max(cu_count() / 8 * 8, 8), (int64_t)align_up((size_t)max_tiles, 8));
-    if (L.bm1 == kFp4BM)
-      hipLaunchKernelGGL((gemm_fp4_kernel<MODE, kFp4BM>), dim3((unsigned)grid), dim3(kFp4Threads), 0, st, p);
-    else
-      hipLaunchKernelGGL((gemm_fp4_kernel<MODE, kFp4HighBM>), dim3((unsigned)grid), dim3(kFp4Threads), 0, st, p);
+    const unsigned parts = 4 * (unsigned)grouped_grid(max_tiles, kStripeFp4);
+    hipLaunchKernelGGL(gemm_fp4_rows_kernel<MODE>, dim3(parts), dim3(64), 0, st, p);
+    return launch_status();
   }
+  // one workgroup a CU (its LDS leaves no room for two), whole rounds of the 8 XCDs
+  const int64_t grid = std::min<int64_t>(std::max(cu_count() / 8 * 8, 8), (int64_t)align_up((size_t)max_tiles, 8));
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(kFp4Threads), 0, st, p);
+  };
+  if (L.bm1 == kFp4LowBM) go(gemm_fp4_kernel<MODE, kFp4LowBM, 3>);
+  else if (L.bm1 == kFp4BM) go(gemm_fp4_kernel<MODE, kFp4BM, 2>);
+  else go(gemm_fp4_kernel<MODE, kFp4HighBM, 2>);
   return launch_status();
 }
 
