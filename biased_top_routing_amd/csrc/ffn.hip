@@ -30,6 +30,7 @@ struct TileTables {
   int E, S, T, bm1, bm1_alt, bm2, bm2_alt, nt1, nt1s, nt2;
   TileDesc *t1, *t2;     // t2 == nullptr: the first table only
   int32_t* hdr;
+  bool fp4_choose;       // MXFP4: bm1 and bm2 are the lowest of the heights, the rows that are there decide
 };
 
 // Block b of nb blocks of 1024 threads.
@@ -37,7 +38,8 @@ __device__ void build_tiles_block(const int32_t* __restrict__ offsets, const Til
   __shared__ int32_t pre1[1024], pre2[1024], mt1_s[1024], mt2_s[1024], row0_s[1024], rows_s[1024], hb1_s[1024],
       hb2_s[1024];
   __shared__ int32_t wave1[16], wave2[16];
-  const int E = p.E, nt1 = p.nt1, nt1s = p.nt1s, nt2 = p.nt2, bm1 = p.bm1, bm2 = p.bm2;
+  const int E = p.E, nt1 = p.nt1, nt1s = p.nt1s, nt2 = p.nt2;
+  const int bm1 = p.fp4_choose ? fp4_tile_rows(offsets[E] / E) : p.bm1, bm2 = p.fp4_choose ? bm1 : p.bm2;
   TileDesc *t1 = p.t1, *t2 = p.t2;
   int32_t* hdr = p.hdr;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -79,6 +81,7 @@ __device__ void build_tiles_block(const int32_t* __restrict__ offsets, const Til
   if (tid == 0 && b == 0) {
     hdr[0] = total1;
     hdr[1] = t2 ? total2 : 0;
+    if (p.fp4_choose) hdr[kFp4TileRows] = bm1;
     // tiles of the routed segments (they come first; the shared ones follow)
     hdr[4] = p.S > 0 ? pre1[E] : total1;
     hdr[5] = t2 ? (p.S > 0 ? pre2[E] : total2) : 0;
@@ -147,7 +150,7 @@ static unsigned table_blocks(int64_t max1, int64_t max2) {
 moe_status launch_build_tile_tables(const moe_cfg* c, const int32_t* offsets, int bm1, int bm1_alt, int nt1,
                                     int nt1s, TileDesc* t1, int64_t max1, int bm2, int bm2_alt, int nt2, TileDesc* t2,
                                     int64_t max2, int32_t* hdr, hipStream_t st) {
-  const TileTables p{c->E, c->S, c->T, bm1, bm1_alt, bm2, bm2_alt, nt1, nt1s, nt2, t1, t2, hdr};
+  const TileTables p{c->E, c->S, c->T, bm1, bm1_alt, bm2, bm2_alt, nt1, nt1s, nt2, t1, t2, hdr, false};
   hipLaunchKernelGGL(build_tiles_kernel, dim3(table_blocks(max1, max2)), dim3(1024), 0, st, offsets, p);
   return launch_status();
 }
@@ -155,7 +158,7 @@ moe_status launch_build_tile_tables(const moe_cfg* c, const int32_t* offsets, in
 static TileTables ffn_tables(const moe_cfg* c, const FfnLayout& L, char* base) {
   return TileTables{c->E, c->S, c->T, L.bm1, L.bm1_alt, L.bm2, L.bm2_alt, (int)L.nt1, (int)L.nt1s, (int)L.nt2,
                     reinterpret_cast<TileDesc*>(base + L.off_t1), reinterpret_cast<TileDesc*>(base + L.off_t2),
-                    reinterpret_cast<int32_t*>(base + L.off_hdr)};
+                    reinterpret_cast<int32_t*>(base + L.off_hdr), c->wgt == MOE_MXFP4 && L.bm1 != kFp4RowsBM};
 }
 
 moe_status launch_build_tiles(const moe_cfg* c, const int32_t* offsets, void* ws, hipStream_t st) {

@@ -113,12 +113,17 @@ constexpr int kFp4BNH = 128, kFp4BN2 = 256;
 // fewer such tiles.  The first layer above, 256 / 288 rows a tile: 256 rows an expert 2534 /
 // 2268 us, 512 rows 4260 / 4002, where it saves none (384 rows) 3307 / 3327; the
 // second, 384 rows, skewed 238 / 247.
-inline int fp4_tile_rows(int64_t avg) {
-  int64_t dev = 1;
-  while ((dev + 1) * (dev + 1) <= avg) ++dev;
-  const int64_t most = avg + 2 * dev;
+// The choice among the three is the table builder's, which knows the rows that are
+// there (a share of a batch, or a padded one, has fewer than T * k): header entry
+// kFp4TileRows.  The host sizes tables and grid for the lowest.  (32 of 256 experts held,
+// H = 7168, I = 2048, by the rows that are there and by T * k: T = 512 151 and 188 us, T =
+// 2048 174 and 206 us; whole batches, one kernel for three: up to 0.6% slower.)
+__host__ __device__ inline int fp4_tile_rows(int avg) {
+  if (avg <= kFp4LowAvg) return kFp4LowBM;
+  const int64_t most = avg + (int64_t)(2.f * sqrtf((float)avg));
   return (most + kFp4HighBM - 1) / kFp4HighBM < (most + kFp4BM - 1) / kFp4BM ? kFp4HighBM : kFp4BM;
 }
+constexpr int kFp4TileRows = 6;
 
 // Row tiles per group in the tile order of a segment (see build_tiles_kernel).
 #ifndef MOE_GROUP_ROW_TILES
@@ -208,8 +213,7 @@ struct FfnLayout {
     const int64_t P = pairs(c);
     const bool f8 = c->wgt == MOE_FP8_E4M3, f4 = c->wgt == MOE_MXFP4;
     const int bm4 = P <= (int64_t)kFp4RowsAvg * c->E  ? kFp4RowsBM
-                    : P <= (int64_t)kFp4LowAvg * c->E ? kFp4LowBM
-                                                      : fp4_tile_rows(P / c->E);
+                                                      : kFp4LowBM;
     dec = small_batch(c);
     bm1 = f4 ? bm4 : f8 ? kFp8BM : dec ? kDecBM : kBM1;
     bm1_alt = f4 || f8 || dec ? 0 : kBM1Alt;

@@ -88,6 +88,7 @@ struct Fp4Params {
   uint8_t* out_shared_scale;
   const TileDesc* tiles;
   const int32_t* ntiles;
+  const int32_t* tile_rows;   // rows per tile
   const int32_t* perm;        // gate/up: non-null -> routed rows gathered from a_shared / sa_shared
   int T, H, E, S, I, k;
 };
@@ -288,9 +289,12 @@ __device__ __forceinline__ void store_y(uint8_t* stg, int dist, const f32x4_t (&
 
 // ------------------------------------------------------------------ large batches
 constexpr int kFp4Threads = 512;
+constexpr int kFp4Lds = 160256;
 
+#if defined(__HIP_DEVICE_COMPILE__)
+// The GEMM over tiles of BM rows, in kFp4Lds bytes of LDS.
 template <int MODE, int BM, int STAGES>
-__global__ __launch_bounds__(kFp4Threads, 1) void gemm_fp4_kernel(Fp4Params p) {
+__device__ __forceinline__ void gemm_fp4_tiles(const Fp4Params& p, uint8_t* lds) {
   constexpr int WM = 2, WN = 4, MI = BM / (WM * 16);
   constexpr int NT = kFp4Threads, NW = NT / 64, BN = 256;
   static_assert(WM * WN == NW && WM * MI * 16 == BM && BN == kFp4BN2, "tile shape");
@@ -306,11 +310,9 @@ __global__ __launch_bounds__(kFp4Threads, 1) void gemm_fp4_kernel(Fp4Params p) {
   constexpr int B_OFF = BM * BK, SC_OFF = B_OFF + BN * BK, STAGE = SC_OFF + 2 * SCP;
   constexpr int PERM_OFF = STAGES * STAGE;                  // the next tile's perm entries (gathered rows)
   constexpr int LDS_BYTES = PERM_OFF + align64(BM) * 4;
-  static_assert(LDS_BYTES <= 163840, "LDS of a CU");
+  static_assert(LDS_BYTES <= kFp4Lds, "LDS");
   // the epilogue's staging: the weights' part of the stage that is filled next
   static_assert(BM * (kHPitch + 4) <= BN * BK && B_CH >= 2, "the epilogue's staging");
-#if defined(__HIP_DEVICE_COMPILE__)
-  __shared__ __attribute__((aligned(16))) uint8_t lds[LDS_BYTES];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
   const int l16 = lane & 15, g = lane >> 4;
@@ -630,6 +632,18 @@ __global__ __launch_bounds__(kFp4Threads, 1) void gemm_fp4_kernel(Fp4Params p) {
       done = --exps == 0;
     }
   }
+}
+#endif
+
+// The table's builder chose the tiles' height from the rows that are there.
+template <int MODE>
+__global__ __launch_bounds__(kFp4Threads, 1) void gemm_fp4_kernel(Fp4Params p) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kFp4Lds];
+  const int bm = __builtin_amdgcn_readfirstlane(*p.tile_rows);
+  if (bm == kFp4LowBM) gemm_fp4_tiles<MODE, kFp4LowBM, 3>(p, lds);
+  else if (bm == kFp4BM) gemm_fp4_tiles<MODE, kFp4BM, 2>(p, lds);
+  else gemm_fp4_tiles<MODE, kFp4HighBM, 2>(p, lds);
 #endif
 }
 
@@ -773,12 +787,7 @@ moe_status launch_gemm_fp4(const FfnLayout& L, int64_t max_tiles, const Fp4Param
   }
   // one workgroup a CU (its LDS leaves no room for two), whole rounds of the 8 XCDs
   const int64_t grid = std::min<int64_t>(std::max(cu_count() / 8 * 8, 8), (int64_t)align_up((size_t)max_tiles, 8));
-  auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(kFp4Threads), 0, st, p);
-  };
-  if (L.bm1 == kFp4LowBM) go(gemm_fp4_kernel<MODE, kFp4LowBM, 3>);
-  else if (L.bm1 == kFp4BM) go(gemm_fp4_kernel<MODE, kFp4BM, 2>);
-  else go(gemm_fp4_kernel<MODE, kFp4HighBM, 2>);
+  hipLaunchKernelGGL(gemm_fp4_kernel<MODE>, dim3((unsigned)grid), dim3(kFp4Threads), 0, st, p);
   return launch_status();
 }
 
@@ -793,6 +802,7 @@ moe_status launch_ffn_fp4(const moe_cfg* c, const uint8_t* x_perm, const uint8_t
   auto bytes = [](const void* q) { return static_cast<const uint8_t*>(q); };
   moe_status s;
   Fp4Params p{};
+  p.tile_rows = hdr + kFp4TileRows;
   p.T = c->T; p.H = c->H; p.E = c->E; p.S = c->S; p.I = c->I; p.k = c->k;
   if (phase == MOE_FFN_ALL || phase == MOE_FFN_GATE_UP) {
     // the tile tables, and x once in MXFP4: the shared experts' operand, and the routed one when its rows are gathered
