@@ -388,6 +388,30 @@ def test_padded_batch_replays(wgt):
         assert torch.equal(y[n:], eager.y_shared[n:]), step
 
 
+@pytest.mark.parametrize("gather", [True, False])
+def test_live_rows_choose_the_mxfp4_tiles(gather):
+    """One graph of a padded batch whose live rows an expert ask for 256-, 288- and 128-row tiles in turn: the same
+    bits for a live token whatever the tiles (its products and sums have one order)."""
+    c = MID.with_(T=1100, H=384, E=4, G=1, M=1, k=2, S=1, I=256, wgt="mxfp4")
+    wts = make_weights(c)
+    bias, x = dev_f32(wts.bias0), to_device(make_x(c))
+    whole = MoeLayerGPU(c, wts, gather=gather)
+    want = whole.forward(x, bias).clone()
+    layer, n = MoeLayerGPU(c, wts, gather=gather), torch.tensor([c.T], **I32)
+    say(f"tiles of live rows gather={gather}")
+    layer.capture(x, bias, n_tokens=n)
+    for live in (1100, 1000, 200, 5, 1000, 1100):
+        n.fill_(live)
+        layer.y.zero_()
+        layer.y_perm.fill_(float("nan"))
+        torch.cuda.synchronize()
+        y = layer.replay()
+        torch.cuda.synchronize()
+        assert int(layer.offsets[-1]) == 2 * live
+        assert torch.equal(y[:live].view(torch.int16), want[:live].view(torch.int16)), live
+        assert torch.equal(y[live:].view(torch.int16), layer.y_shared[live:].view(torch.int16)), live
+
+
 def test_training_step_of_a_share():
     """Forward and backward of two shares on buffers whose unused rows are NaN: the weight gradients are the
     whole layer's for the experts held, and dx and the router's gradient sum to the whole layer's."""
