@@ -39,15 +39,40 @@ __device__ void build_tiles_block(const int32_t* __restrict__ offsets, const Til
       hb2_s[1024];
   __shared__ int32_t wave1[16], wave2[16];
   const int E = p.E, nt1 = p.nt1, nt1s = p.nt1s, nt2 = p.nt2;
-  const int bm1 = p.fp4_choose ? fp4_tile_rows(offsets[E] / E) : p.bm1, bm2 = p.fp4_choose ? bm1 : p.bm2;
   TileDesc *t1 = p.t1, *t2 = p.t2;
   int32_t* hdr = p.hdr;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int nseg = E + (p.S > 0 ? 1 : 0);
+  int bm1 = p.bm1, bm2 = p.bm2;
+  int rows = p.T, row0 = 0;
+  if (tid < E) {
+    row0 = offsets[tid];
+    rows = offsets[tid + 1] - row0;
+  }
+  if (p.fp4_choose) {                                   // the tiles of the routed segments at each height
+    __shared__ int32_t tiles_s[3][16];
+    int n[3] = {0, 0, 0};
+    if (tid < E) {
+      n[0] = (rows + kFp4LowBM - 1) / kFp4LowBM;
+      n[1] = (rows + kFp4BM - 1) / kFp4BM;
+      n[2] = (rows + kFp4HighBM - 1) / kFp4HighBM;
+    }
+#pragma unroll
+    for (int h = 0; h < 3; ++h) {
+#pragma unroll
+      for (int d = 32; d > 0; d >>= 1) n[h] += __shfl_xor(n[h], d);
+      if (lane == 0) tiles_s[h][wave] = n[h];
+    }
+    __syncthreads();
+    int sum[3] = {0, 0, 0};
+#pragma unroll
+    for (int h = 0; h < 3; ++h)
+#pragma unroll
+      for (int w = 0; w < 16; ++w) sum[h] += tiles_s[h][w];
+    bm1 = bm2 = fp4_tile_rows(sum[0], sum[1], sum[2]);
+  }
   int c1 = 0, c2 = 0;
   if (tid < nseg) {
-    const int rows = tid < E ? offsets[tid + 1] - offsets[tid] : p.T;
-    const int row0 = tid < E ? offsets[tid] : 0;
     const int mt1 = (rows + bm1 - 1) / bm1, mt2 = (rows + bm2 - 1) / bm2;
     // as many tiles of bm1_alt rows cover the segment: use that height
     hb1_s[tid] = p.bm1_alt > 0 && (int64_t)mt1 * p.bm1_alt >= rows ? p.bm1_alt : bm1;

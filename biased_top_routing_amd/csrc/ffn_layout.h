@@ -96,32 +96,34 @@ constexpr int kFp8BM = MOE_FP8_BM;
 constexpr int kFp8BNH = 128;
 constexpr int kFp8BN2 = 256;
 constexpr int kFp8MaxKC = 64;
-// MXFP4 GEMMs: token rows per tile by the mean rows of a routed expert: 32 up to 20
-// (the GEMMs stream weights, and the 32-row tiles' small workgroups do it best), 128
-// up to 120 (two slices of loads in flight instead of one), 256 or 288 (below) beyond;
-// 128 h columns per gate/up tile, 256 output columns per down tile.  The whole call in
-// us at H = 7168, I = 2048, 256 experts, 32 / 128 rows a tile: 8 rows an expert 1017 /
-// 1052, 16 rows 1068 / 1080, 20 rows 1102 / 1088, 24 rows 1152 / 1099; 128 / 256 rows a
-// tile: 64 rows an expert 1211 / 1440, 96 rows 1322 / 1514, 112 rows 1455 / 1563, 128
-// rows 1662 / 1651; at H = 2048, I = 1408, 64 experts, 32 / 128 rows a tile: 16 rows 81 /
-// 84, 24 rows 84 / 85, 128 / 256: 64 rows 100 / 126, 100 rows 113 / 137.
+// MXFP4 GEMMs: 32 token rows per tile where the pairs make at most 20 an expert (the
+// GEMMs stream weights, and the 32-row tiles' small workgroups do it best), else 128,
+// 256 or 288 by the tiles that each height takes (below); 128 h columns per gate/up
+// tile, 256 output columns per down tile.  The whole call in us at H = 7168, I = 2048,
+// 256 experts, 32 / 128 rows a tile: 8 rows an expert 1017 / 1052, 16 rows 1068 / 1080,
+// 20 rows 1102 / 1088, 24 rows 1152 / 1099; at H = 2048, I = 1408, 64 experts: 16 rows 81 /
+// 84, 24 rows 84 / 85.
 constexpr int kFp4RowsBM = 32, kFp4LowBM = 128, kFp4BM = 256, kFp4HighBM = 288;
-constexpr int kFp4RowsAvg = 20, kFp4LowAvg = 120;
+constexpr int kFp4RowsAvg = 20;
 constexpr int kFp4BNH = 128, kFp4BN2 = 256;
-// 288 rows take more time a tile and are right where they save one: a segment somewhat
-// longer than the mean (by twice the square root, the spread of an even routing) needs
-// fewer such tiles.  The first layer above, 256 / 288 rows a tile: 256 rows an expert 2534 /
-// 2268 us, 512 rows 4260 / 4002, where it saves none (384 rows) 3307 / 3327; the
-// second, 384 rows, skewed 238 / 247.
-// The choice among the three is the table builder's, which knows the rows that are
-// there (a share of a batch, or a padded one, has fewer than T * k): header entry
-// kFp4TileRows.  The host sizes tables and grid for the lowest.  (32 of 256 experts held,
-// H = 7168, I = 2048, by the rows that are there and by T * k: T = 512 151 and 188 us, T =
-// 2048 174 and 206 us; whole batches, one kernel for three: up to 0.6% slower.)
-__host__ __device__ inline int fp4_tile_rows(int avg) {
-  if (avg <= kFp4LowAvg) return kFp4LowBM;
-  const int64_t most = avg + (int64_t)(2.f * sqrtf((float)avg));
-  return (most + kFp4HighBM - 1) / kFp4HighBM < (most + kFp4BM - 1) / kFp4BM ? kFp4HighBM : kFp4BM;
+// A tile of 128 rows has two slices of loads in flight instead of one and takes less
+// time than one of 256 however few rows that holds: it is right while it takes at most
+// 1.4 times as many.  128 / 256 rows a tile, us (first layer above: even routing, v, or
+// Zipf 1.1 over 64 experts, V; second: Zipf 1.1, s, even, e; mean rows an expert; tiles'
+// ratio): v64 1.00 1210 / 1440, v112 1.06 1455 / 1563, v128 1.49 1662 / 1651, V150 1.35
+// 596 / 625, V220 1.46 772 / 744, s80 1.18 110 / 127, s130 1.31 130 / 140, s160 1.38 145 /
+// 157, s220 1.48 163 / 165, e140 1.81 138 / 138, e220 2.00 165 / 152.
+//   288 rows take more time a tile and are right where they save a tenth of the tiles:
+// 256 / 288 rows a tile, v256 0.67 2534 / 2268, v512 0.81 4260 / 4002, v384 1.00 3307 / 3327,
+// s384 0.94 238 / 247.
+//   The table builder chooses: it knows the rows that are there (a share of a batch, or a
+// padded one, has fewer than T * k; 32 of 256 experts held, H = 7168, I = 2048, T = 512: 151
+// us, and 188 as T * k would have it).  It leaves the height in header entry kFp4TileRows;
+// the host sizes tables and grid for the lowest.  (One kernel for three heights is up to
+// 0.6% slower than one each.)
+__host__ __device__ inline int fp4_tile_rows(int n_low, int n, int n_high) {
+  if ((int64_t)5 * n_low <= (int64_t)7 * n) return kFp4LowBM;
+  return (int64_t)10 * n_high <= (int64_t)9 * n ? kFp4HighBM : kFp4BM;
 }
 constexpr int kFp4TileRows = 6;
 
