@@ -293,11 +293,24 @@ def moe_quantize_fp8(src, n_mat, rows, cols, block_rows, dst, scales, stream=Non
                                                       _p(scales), _s(stream)))
 
 
+def live_count(n_tokens) -> int | None:
+    """Address of the live count of a padded batch: None (every token), or an int32 tensor of one element, which the
+    kernels read on the device.  A Python number is refused, as it would be taken for an address."""
+    import torch
+    if n_tokens is None:
+        return None
+    if not isinstance(n_tokens, torch.Tensor):
+        raise TypeError(f"n_tokens is an int32 tensor of one element on the device, not {n_tokens!r}")
+    if n_tokens.dtype != torch.int32 or n_tokens.numel() != 1:
+        raise ValueError(f"n_tokens is an int32 tensor of one element, not {n_tokens.numel()} of {n_tokens.dtype}")
+    return _c(n_tokens)
+
+
 def moe_dispatch_local(cfg, first_expert, n_tokens, topk_idx, x, counts, offsets, perm, inv, x_perm, x_perm_scale, ws,
                        stream=None):
     _check("moe_dispatch_local", lib().moe_dispatch_local(
-        ctypes.byref(cfg), int(first_expert), _c(n_tokens), _c(topk_idx), _c(x), _c(counts), _c(offsets), _c(perm),
-        _c(inv), _c(x_perm), _c(x_perm_scale), _c(ws), _nbytes(ws), _s(stream)))
+        ctypes.byref(cfg), int(first_expert), live_count(n_tokens), _c(topk_idx), _c(x), _c(counts), _c(offsets),
+        _c(perm), _c(inv), _c(x_perm), _c(x_perm_scale), _c(ws), _nbytes(ws), _s(stream)))
 
 
 def moe_combine_local(cfg, y_perm, y_shared, inv, topk_w, y, stream=None):

@@ -229,8 +229,7 @@ class MoeLayerGPU:
     def forward(self, x, bias, gamma=None, scores_in=False, n_tokens=None):
         """One batch through the layer; with gamma set, bias is updated in place afterwards.
         n_tokens: int32 device tensor of one element, the live tokens of a padded batch."""
-        if gamma is not None and (self.share is not None or n_tokens is not None):
-            raise ValueError("the bias update needs the loads of a whole batch over every expert")
+        self._check_batch(gamma, n_tokens)
         self.n_tokens = n_tokens
         self.route(x, bias, scores_in)
         self.dispatch(x)
@@ -239,6 +238,12 @@ class MoeLayerGPU:
         if gamma is not None:
             self.update_bias(bias, gamma)
         return self.y
+
+    def _check_batch(self, gamma, n_tokens):
+        """Refuses what forward() cannot run, before anything is launched."""
+        L.live_count(n_tokens)
+        if gamma is not None and (self.share is not None or n_tokens is not None):
+            raise ValueError("the bias update needs the loads of a whole batch over every expert")
 
     # ---------------------------------------------------------------- HIP graph
     def capture(self, x, bias, gamma=None, n_tokens=None):
@@ -249,6 +254,7 @@ class MoeLayerGPU:
         and no call allocates, copies or synchronises, so the recorded work is the
         same kernels forward() launches.  A warm-up pass (no bias update) on a side
         stream precedes the capture."""
+        self._check_batch(gamma, n_tokens)
         side = torch.cuda.Stream()
         side.wait_stream(torch.cuda.current_stream())
         with torch.cuda.stream(side):
