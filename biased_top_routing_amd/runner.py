@@ -17,7 +17,9 @@ dispatch, combine and their gradients take the pairs that fall on its experts
 (moe_dispatch_local and the calls beside it).  forward(n_tokens=...) takes an
 int32 device tensor with the number of live tokens of a padded batch.  Either
 way y (and dx) is this share's sum; the bias update needs the loads of the whole
-batch, so gamma is refused.
+batch, so gamma is refused.  The shares of the ranks add up to the layer when what
+every rank could compute is given to one of them: the shared experts (the others'
+cfg has S = 0) and the balance loss (adds_balance=True; the others pass alpha = 0).
 """
 from __future__ import annotations
 
@@ -38,10 +40,12 @@ def to_device(arr, device="cuda"):
 
 
 class MoeLayerGPU:
-    def __init__(self, cfg, weights, T=None, device="cuda", gather=False, save_gu=False, keep_scores=True, share=None):
+    def __init__(self, cfg, weights, T=None, device="cuda", gather=False, save_gu=False, keep_scores=True, share=None,
+                 adds_balance=False):
         self.c = cfg
         self.share = share
         first, self.n_exp = (0, cfg.E) if share is None else (int(share[0]), int(share[1]))
+        self.adds_balance = adds_balance or self.n_exp == cfg.E
         if first < 0 or self.n_exp < cfg.k or first + self.n_exp > cfg.E:
             raise ValueError(f"share {share} of {cfg.E} experts: needs at least k = {cfg.k} experts inside the layer's")
         if share is not None and len(weights.w_gate_up) not in (cfg.E, self.n_exp):
@@ -207,10 +211,13 @@ class MoeLayerGPU:
         (same x, same routing).  Fills dx, the fp32 weight gradients and loss_bal; returns dx."""
         if self.gather:
             raise ValueError("backward reads the permuted rows x_perm: build the layer with gather=False")
-        if getattr(self, "_bwd_T", None) != self.T:
-            self.alloc_backward()
         if self.n_tokens is not None and alpha:
             raise ValueError("the balance loss counts every token of the batch: alpha has to be 0 for a padded one")
+        if alpha and not self.adds_balance:
+            raise ValueError("every share's gradients would hold the whole balance term: build one of them with "
+                             "adds_balance=True, and pass alpha = 0 to the others")
+        if getattr(self, "_bwd_T", None) != self.T:
+            self.alloc_backward()
         cfg = self.cfg_x
         combine_backward = L.moe_combine_local_backward if self.partial else L.moe_combine_backward
         dispatch_backward = L.moe_dispatch_local_backward if self.partial else L.moe_dispatch_backward

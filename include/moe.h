@@ -369,7 +369,10 @@ moe_status moe_dequantize_fp4(const uint8_t* codes, const uint8_t* scales, int32
  *   moe_combine_local_backward -> moe_expert_ffn_backward* ->
  *   moe_route_backward (cfg of the router) -> moe_dispatch_local_backward
  * The outputs of all ranks' shares (y, and dx and d_topk_w) sum to the whole
- * layer's when the shared experts and the router term are given to one of them.
+ * layer's when the shared experts are given to one of them.  moe_route_backward is
+ * called once with the sum of the ranks' d_topk_w, or by each rank with its own:
+ * dx_router and dw_router are linear in d_topk_w and add up too, but the balance
+ * term does not depend on it, so alpha is 0 on all ranks but one.
  * With T == 0 tensors without elements may be NULL in these four calls; they take
  * T below 2^23 (MOE_ERR_SHAPE).
  * moe_update_bias compares with T*k pairs over cfg's E experts: it is for whole
