@@ -208,7 +208,9 @@ class MoeLayerGPU:
 
     def backward(self, x, dy, alpha=0.0, seq_len=0):
         """Gradients of sum(dy * y) + alpha-weighted sequence balance loss for the last forward pass
-        (same x, same routing).  Fills dx, the fp32 weight gradients and loss_bal; returns dx."""
+        (same x, same routing).  Fills dx, the fp32 weight gradients and loss_bal; returns dx.
+        Of a padded batch (n_tokens still holds its live count) they are the live tokens' gradients:
+        what lies in the padded rows of x and dy takes no part, and those of dx are zero."""
         if self.gather:
             raise ValueError("backward reads the permuted rows x_perm: build the layer with gather=False")
         if self.n_tokens is not None and alpha:
@@ -222,20 +224,38 @@ class MoeLayerGPU:
         combine_backward = L.moe_combine_local_backward if self.partial else L.moe_combine_backward
         dispatch_backward = L.moe_dispatch_local_backward if self.partial else L.moe_dispatch_backward
         combine_backward(cfg, dy, self.y_perm, self.inv, self.topk_w, self.dy_perm, self.d_topk_w)
+        scores = self.scores
+        if self.n_tokens is not None:
+            x, dy, scores = self._without_padding(x, dy)
         if self.save_gu:
             L.moe_expert_ffn_backward_saved(cfg, self.x_perm, x, self.offsets, self.weights, self.saved, self.dy_perm,
                                             dy, self.dx_perm, self.dx_shared, self.grads, self.ws_ffn_bwd)
         else:
             L.moe_expert_ffn_backward(cfg, self.x_perm, x, self.offsets, self.weights, self.dy_perm, dy,
                                       self.dx_perm, self.dx_shared, self.grads, self.ws_ffn_bwd)
-        L.moe_route_backward(self.cfg, x, self.w_router, self.scores, self.topk_idx, self.d_topk_w, alpha, seq_len,
+        L.moe_route_backward(self.cfg, x, self.w_router, scores, self.topk_idx, self.d_topk_w, alpha, seq_len,
                              self.dx_router, self.g_w_router, self.loss_bal, self.ws_route_bwd)
         dispatch_backward(cfg, self.dx_perm, self.dx_shared, self.dx_router, self.inv, self.dx)
         return self.dx
 
+    def _without_padding(self, x, dy):
+        """x, dy and the affinities with rows for the padded tokens that add exactly nothing.  The router's and the
+        shared experts' gradients contract over all T rows; a padded row's gate gradients are zero, but zero times
+        what lies there need not be."""
+        live = self.n_tokens.reshape(1).to(self.device, non_blocking=True)   # (pinned host memory will do too)
+        pad = (torch.arange(self.T, device=self.device) >= live).unsqueeze(1)
+        if self.c.S > 0:
+            dy = dy[:self.T].masked_fill(pad, 0)
+            if self.save_gu:
+                self.gs.masked_fill_(pad, 0)
+                self.us.masked_fill_(pad, 0)
+        scores = None if self.scores is None else self.scores.masked_fill(pad, 0.5)
+        return x[:self.T].masked_fill(pad, 0), dy, scores
+
     def forward(self, x, bias, gamma=None, scores_in=False, n_tokens=None):
         """One batch through the layer; with gamma set, bias is updated in place afterwards.
-        n_tokens: int32 device tensor of one element, the live tokens of a padded batch."""
+        n_tokens: int32 device tensor of one element, the live tokens of a padded batch; y of a padded token is the
+        shared experts' output for whatever its row of x holds."""
         self._check_batch(gamma, n_tokens)
         self.n_tokens = n_tokens
         self.route(x, bias, scores_in)

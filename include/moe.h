@@ -373,6 +373,10 @@ moe_status moe_dequantize_fp4(const uint8_t* codes, const uint8_t* scales, int32
  * called once with the sum of the ranks' d_topk_w, or by each rank with its own:
  * dx_router and dw_router are linear in d_topk_w and add up too, but the balance
  * term does not depend on it, so alpha is 0 on all ranks but one.
+ * moe_expert_ffn_backward* (of the shared experts) and moe_route_backward contract
+ * over all T rows: for a padded batch's gradients the rows of dy behind the live
+ * tokens have to be zero, and those of x, scores and saved->gs and us finite (of
+ * scores not zero either).
  * With T == 0 tensors without elements may be NULL in these four calls; they take
  * T below 2^23 (MOE_ERR_SHAPE).
  * moe_update_bias compares with T*k pairs over cfg's E experts: it is for whole

@@ -4,7 +4,9 @@ import pytest
 import torch
 
 from biased_top_routing_amd.runner import MoeLayerGPU, to_device
-from gpu_util import dev_f32, host, say
+from gpu_util import dev_f32, host, rel_inf, say
+from oracle.backward import backward_from_routing
+from oracle.layer import decode_act
 from workloads import MID
 from workloads.inputs import f32_to_bf16_bits, make_weights, make_x, rng
 
@@ -44,3 +46,117 @@ def test_shares_with_the_balance_loss():
         tol = steps * BF * np.abs(want).max()
         assert np.abs(want - without).max() > 10 * tol
         assert np.abs(one + two - want).max() <= tol
+
+
+GRADS = ("dx", "d_topk_w", "g_w_gate_up", "g_w_down", "g_ws_gate_up", "g_ws_down", "g_w_router")
+PADDED = {
+    "recomputed": (MID.with_(T=260, H=256, E=16, G=4, M=2, k=4, S=2, I=256), 133, {}),
+    "saved": (MID.with_(T=260, H=256, E=16, G=4, M=2, k=4, S=1, I=256), 133, dict(save_gu=True)),
+    "no shared experts": (MID.with_(T=100, H=320, E=10, G=2, M=1, k=3, S=0, I=128), 37, {}),
+    "share": (MID.with_(T=260, H=256, E=16, G=4, M=2, k=4, S=1, I=256), 133, dict(share=(5, 8))),
+    "none live": (MID.with_(T=70, H=256, E=16, G=4, M=2, k=4, S=1, I=128), 0, {}),
+    "all live": (MID.with_(T=70, H=256, E=16, G=4, M=2, k=4, S=1, I=128), 70, {}),
+}
+
+
+def _gradients(layer):
+    return {n: getattr(layer, n).clone() for n in GRADS if getattr(layer, n) is not None}
+
+
+def _same(a, b, what):
+    for n in a:
+        assert torch.equal(a[n].view(torch.int8), b[n].view(torch.int8)), f"{what}: {n}"
+
+
+@pytest.mark.parametrize("name", PADDED)
+def test_padded_training_step(name):
+    """What lies in the padded rows of x and dy reaches no gradient: NaN, infinities and numbers there give the bits
+    that zeros give, and the gradients are the live tokens' (against the oracle on those alone, normwise with the
+    2e-2 that bf16 operands are allowed in a whole batch's backward pass)."""
+    c, live, kw = PADDED[name]
+    wts = make_weights(c)
+    x, dy, bias = to_device(make_x(c)), to_device(_dy(c, 92)), dev_f32(wts.bias0)
+    n = torch.tensor([live], dtype=torch.int32, device="cuda")
+    layer = MoeLayerGPU(c, wts, **kw)
+    layer.alloc_backward()
+    say(f"padded training step, {name}")
+
+    def step(fill_x, fill_dy):
+        xs, ds = x.clone(), dy.clone()
+        xs[live:], ds[live:] = fill_x, fill_dy
+        before = xs.clone(), ds.clone()
+        layer.forward(xs, bias, n_tokens=n)
+        layer.backward(xs, ds)
+        torch.cuda.synchronize()
+        for now, then in zip((xs, ds), before):      # the caller's own
+            assert torch.equal(now.view(torch.int16), then.view(torch.int16))
+        return _gradients(layer)
+
+    clean = step(0.0, 0.0)
+    for fill_x, fill_dy in ((1.0, 1000.0), (float("nan"), 0.0), (0.5, float("nan")), (float("inf"), float("-inf"))):
+        _same(clean, step(fill_x, fill_dy), f"padded rows of x {fill_x}, of dy {fill_dy}")
+    for n_ in ("dx", "d_topk_w"):
+        assert not clean[n_][live:].any(), n_
+    if "share" in kw or live == 0:
+        if live == 0:
+            assert not any(v.any() for v in clean.values())
+        return
+    f64 = lambda a: decode_act(a).astype(np.float64)
+    idx = host(layer.topk_idx)[:live].astype(np.int64)
+    o = backward_from_routing(f64(make_x(c))[:live], f64(wts.w_router), wts.logit_offset, f64(wts.w_gate_up),
+                              f64(wts.w_down), [f64(a) for a in wts.ws_gate_up] if c.S else None,
+                              [f64(a) for a in wts.ws_down] if c.S else None, idx, f64(_dy(c, 92))[:live],
+                              c.route_scale)
+    got = {k: host(v) for k, v in clean.items()}
+    errs = {"dx": rel_inf(got["dx"][:live], o["dx"]), "d_topk_w": rel_inf(got["d_topk_w"][:live], o["dw"]),
+            "dw_router": rel_inf(got["g_w_router"], o["dw_router"])}
+    for e in range(c.E):
+        if (idx == e).any():
+            errs[f"dw_gate_up[{e}]"] = rel_inf(got["g_w_gate_up"][e], o["dw_gate_up"][e])
+            errs[f"dw_down[{e}]"] = rel_inf(got["g_w_down"][e], o["dw_down"][e])
+        else:
+            assert not got["g_w_gate_up"][e].any() and not got["g_w_down"][e].any()
+    if c.S:
+        errs["dws_gate_up"] = rel_inf(got["g_ws_gate_up"], o["dws_gate_up"])
+        errs["dws_down"] = rel_inf(got["g_ws_down"], o["dws_down"])
+    bad = {k: v for k, v in errs.items() if not v < 2e-2}
+    assert not bad, bad
+
+
+@pytest.mark.parametrize("save_gu", [False, True])
+def test_padded_training_step_replays(save_gu):
+    """Forward and backward of a padded batch in one graph follow the live count from replay to replay, with an eager
+    step's bits, whatever the padded rows hold."""
+    c = MID.with_(T=200, H=256, E=16, G=4, M=2, k=4, S=1, I=256)
+    wts = make_weights(c)
+    bias = dev_f32(wts.bias0)
+    eager, graph = MoeLayerGPU(c, wts, save_gu=save_gu), MoeLayerGPU(c, wts, save_gu=save_gu)
+    xg, dg = to_device(make_x(c)), to_device(_dy(c, 93))
+    ng = torch.tensor([c.T], dtype=torch.int32, device="cuda")
+    say(f"padded training step in a graph, save_gu={save_gu}")
+    graph.alloc_backward()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        graph.forward(xg, bias, n_tokens=ng)
+        graph.backward(xg, dg)
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        graph.forward(xg, bias, n_tokens=ng)
+        graph.backward(xg, dg)
+    for step, live in enumerate((200, 1, 0, 133, 200)):
+        xs, ds = to_device(make_x(c, step)), to_device(_dy(c, 94 + step))
+        xs[live:] = float("nan") if step % 2 else 1.0
+        ds[live:] = float("nan") if step % 2 == 0 else 1.0
+        xg.copy_(xs)
+        dg.copy_(ds)
+        ng.fill_(live)
+        eager.forward(xs, bias, n_tokens=torch.tensor([live], dtype=torch.int32, device="cuda"))
+        eager.backward(xs, ds)
+        want = _gradients(eager)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        _same(want, _gradients(graph), f"replay {step}")
+        assert all(torch.isfinite(v).all() for v in want.values()), step
