@@ -802,7 +802,8 @@ extern "C" moe_status moe_dispatch_local(const moe_cfg* cfg, int32_t first_exper
   } else if (!counts || !offsets) {
     return MOE_ERR_NULL;
   }
-  if (first_expert < 0) return MOE_ERR_SHAPE;
+  // (the kernels take the unsigned difference id - first_expert: with the share below 2^31 no negative id wraps into it)
+  if (first_expert < 0 || (int64_t)first_expert + cfg->E > (int64_t)1 << 31) return MOE_ERR_SHAPE;
   if (!ws) return MOE_ERR_NULL;
   if (ws_bytes < dispatch_ws_bytes(cfg)) return MOE_ERR_WORKSPACE;
   for (const void* q : {(const void*)n_tokens, (const void*)topk_idx, (const void*)counts, (const void*)offsets,

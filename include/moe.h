@@ -393,7 +393,7 @@ moe_status moe_dequantize_fp4(const uint8_t* codes, const uint8_t* scales, int32
  * expert in the share is topk_idx[t, j] - first_expert).  Any other value of
  * topk_idx, negative ones included, makes the pair absent.
  *
- *  first_expert  >= 0 (MOE_ERR_SHAPE otherwise)
+ *  first_expert  >= 0, first_expert + E at most 2^31 (MOE_ERR_SHAPE otherwise)
  *  n_tokens  device pointer to one int32, the live tokens of the batch (taken as
  *            0 when negative and as T when larger), or NULL: all T
  *  counts, offsets  over the present pairs (offsets[E] of them)
