@@ -159,11 +159,14 @@ _device_fn = _stream_fn = None
 
 def _bind_torch() -> None:
     """Torch's own current-device and current-stream queries, without the objects that torch.cuda wraps
-    them in (a call of a small kernel costs 4 us; torch.cuda.current_stream() took 2.8 of the binding's 5.5)."""
+    them in (a call of a small kernel costs 4 us; torch.cuda.current_stream() took 2.8 of the binding's 5.5).
+    They are no public names: where a torch lacks one, the public calls serve."""
     global _device_fn, _stream_fn
     import torch
     torch.cuda.init()
-    _device_fn, _stream_fn = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+    _device_fn = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    _stream_fn = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+                  or (lambda device: torch.cuda.current_stream(device).cuda_stream))
 
 
 def _device() -> int:
