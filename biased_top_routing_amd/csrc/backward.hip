@@ -302,7 +302,8 @@ __global__ __launch_bounds__(256) void seq_stats_kernel(const float* __restrict_
     rs = wave_sum(rs);
 #pragma unroll
     for (int i = 0; i < kMaxEPL; ++i) acc[i] += v[i] / rs;
-    if (lane < k) atomicAdd(&c_lds[idx[(int64_t)t * k + lane]], 1);   // integer counts: order-free
+    const int sel = lane < k ? idx[(int64_t)t * k + lane] : -1;
+    if ((unsigned)sel < (unsigned)E) atomicAdd(&c_lds[sel], 1);       // integer counts: order-free
   }
 #pragma unroll
   for (int i = 0; i < kMaxEPL; ++i) {
@@ -371,10 +372,11 @@ __global__ __launch_bounds__(256) void route_grad_kernel(const float* __restrict
   gs = wave_sum(gs);
 #pragma unroll
   for (int i = 0; i < kMaxEPL; ++i) ds[i] = ds[i] / rs - gs / (rs * rs);
-  // gates over the selected experts
-  const int sel = lane < k ? idx[(int64_t)t * k + lane] : 0;
-  const float ss = lane < k ? s[(int64_t)t * E + sel] : 0.f;
-  const float dwj = lane < k ? d_w[(int64_t)t * k + lane] : 0.f;
+  // gates over the selected experts (an id outside [0, E) is none)
+  int sel = lane < k ? idx[(int64_t)t * k + lane] : -1;
+  if ((unsigned)sel >= (unsigned)E) sel = -1;
+  const float ss = sel >= 0 ? s[(int64_t)t * E + sel] : 0.f;
+  const float dwj = sel >= 0 ? d_w[(int64_t)t * k + lane] : 0.f;
   const float S = wave_sum(ss);
   const float B1 = wave_sum(dwj * ss);
   const float dsel = scale / S * (dwj - B1 / S);

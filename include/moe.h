@@ -515,7 +515,10 @@ moe_status moe_expert_ffn_backward_saved(const moe_cfg* cfg, const void* x_perm,
  *           L_bal = alpha * mean over sequences of sum_e f_e P_e
  *   router  dlogit = ds * s (1 - s);  dx_router = dlogit W_r;  dw_router = dlogit^T x
  *  x [T, H], w_router [E, H] bf16; scores [T, E] fp32 affinities (moe_route's
- *  output); topk_idx [T, k]; d_topk_w [T, k] from moe_combine_backward;
+ *  output); topk_idx [T, k] as moe_route wrote it (an id outside [0, E) is passed
+ *  over, here and in the counts of the loss; pairs that a caller makes absent for
+ *  moe_dispatch_local keep their id here, their d_topk_w is 0);
+ *  d_topk_w [T, k] from moe_combine_backward;
  *  alpha >= 0 (0: no balance loss); seq_len 0 (= T) or a divisor of T;
  *  dx_router [T, H] fp32 out (may be NULL); dw_router [E, H] fp32 out;
  *  loss: one fp32 out (L_bal); ws of at least moe_workspace_bytes(cfg, MOE_WS_ROUTE_BWD).

@@ -3,8 +3,9 @@ import numpy as np
 import pytest
 import torch
 
+from biased_top_routing_amd import _lib as L
 from biased_top_routing_amd.runner import MoeLayerGPU, to_device
-from gpu_util import dev_f32, host, rel_inf, say
+from gpu_util import dev_f32, dev_i32, host, rel_inf, say
 from oracle.backward import backward_from_routing
 from oracle.layer import decode_act
 from workloads import MID
@@ -160,3 +161,42 @@ def test_padded_training_step_replays(save_gu):
         torch.cuda.synchronize()
         _same(want, _gradients(graph), f"replay {step}")
         assert all(torch.isfinite(v).all() for v in want.values()), step
+
+
+@pytest.mark.parametrize("E,k", [(16, 4), (70, 3), (512, 8)])
+def test_router_gradient_passes_over_foreign_ids(E, k):
+    """Ids outside [0, E) where no gate gradient comes from: the router's gradients have the bits that real ids give
+    there, and the loss counts the others (fp32 sums over a sequence: 1e-4, as for whole batches)."""
+    T, H, L_, alpha, scale = 96, 128, 32, 0.5, 2.5
+    g = rng(95, E, k)
+    cfg = L.make_cfg(T, H, E, 1, 1, k, 0, 128, 1, scale, "bf16", "bf16")
+    bits = lambda *s: to_device(f32_to_bf16_bits(g.standard_normal(s).astype(np.float32)))
+    x, w = bits(T, H), bits(E, H)
+    s = g.uniform(0.05, 0.95, (T, E)).astype(np.float32)
+    idx = np.argsort(g.random((T, E)), axis=1)[:, :k].astype(np.int32)
+    dead = g.random(T) < 0.4
+    dw = g.standard_normal((T, k)).astype(np.float32)
+    dw[dead] = 0
+    foreign = idx.copy()
+    foreign[dead] = g.choice(np.array([-1, E, 511 + 1, -2 ** 31, 2 ** 31 - 1], np.int32), (dead.sum(), k))
+    say(f"foreign ids E={E} k={k}")
+
+    def run(ids, a):
+        out = (torch.empty((T, H), dtype=torch.float32, device="cuda"),
+               torch.empty((E, H), dtype=torch.float32, device="cuda"), torch.empty(1, device="cuda"))
+        ws = torch.empty(L.moe_workspace_bytes(cfg, L.MOE_WS_ROUTE_BWD), dtype=torch.uint8, device="cuda")
+        L.moe_route_backward(cfg, x, w, dev_f32(s), dev_i32(ids), dev_f32(dw), a, L_, *out, ws)
+        torch.cuda.synchronize()
+        return out
+
+    for got, want in zip(run(foreign, 0.0), run(idx, 0.0)):
+        assert torch.equal(got, want)
+    P = s.astype(np.float64) / s.sum(1, dtype=np.float64, keepdims=True)
+    loss = 0.0
+    for b in range(T // L_):
+        rows = slice(b * L_, (b + 1) * L_)
+        count = np.bincount(idx[rows][~dead[rows]].reshape(-1), minlength=E)
+        loss += alpha / (T // L_) * (E / (k * L_) * count * P[rows].mean(0)).sum()
+    dx, dr, got = run(foreign, alpha)
+    assert torch.isfinite(dx).all() and torch.isfinite(dr).all()
+    assert abs(float(got) - loss) <= 1e-4 * loss
