@@ -356,7 +356,8 @@ __global__ __launch_bounds__(256) void permute_rows_kernel(const uint4* __restri
         const int64_t c = c0 + i * kWave + lane;
         if (c >= nchunk) continue;
         // (a share's rows: non-temporal, T = 16384, H = 7168, an eighth of the experts
-        // 92 -> 83 us the whole dispatch, every expert of T = 8192 230 -> 201 us)
+        // 92 -> 83 us the whole dispatch, every expert of T = 8192 230 -> 201 us, both with
+        // x partly in the memory-side cache; not measured with x cold, as the plain stores above)
         if constexpr (LOCAL)
           __builtin_nontemporal_store(u32x4_t{v[i].x, v[i].y, v[i].z, v[i].w},
                                       reinterpret_cast<u32x4_t*>(&dst[p * nchunk + c]));

@@ -102,7 +102,11 @@ constexpr int kFp8MaxKC = 64;
 // tile, 256 output columns per down tile.  The whole call in us at H = 7168, I = 2048,
 // 256 experts, 32 / 128 rows a tile: 8 rows an expert 1017 / 1052, 16 rows 1068 / 1080,
 // 20 rows 1102 / 1088, 24 rows 1152 / 1099; at H = 2048, I = 1408, 64 experts: 16 rows 81 /
-// 84, 24 rows 84 / 85.
+// 84, 24 rows 84 / 85: the border lies at about 19 rows in the one and past 24 in the other.
+//   The 32-row tiles are chosen on the host, from the capacity T * k, for the routed and the
+// shared experts together.  Not measured, and not told apart by the rule: a share or a padded
+// batch with few live rows in a large capacity (it gets 128-row tiles), and routed experts of
+// few rows beside long shared ones (these get 32-row tiles too).
 constexpr int kFp4RowsBM = 32, kFp4LowBM = 128, kFp4BM = 256, kFp4HighBM = 288;
 constexpr int kFp4RowsAvg = 20;
 constexpr int kFp4BNH = 128, kFp4BN2 = 256;
@@ -118,7 +122,8 @@ constexpr int kFp4BNH = 128, kFp4BN2 = 256;
 // s384 0.94 238 / 247.
 //   The table builder chooses: it knows the rows that are there (a share of a batch, or a
 // padded one, has fewer than T * k; 32 of 256 experts held, H = 7168, I = 2048, T = 512: 151
-// us, and 188 as T * k would have it).  It leaves the height in header entry kFp4TileRows;
+// us, and 188 as T * k would have it).  It counts the tiles of the routed segments alone; the
+// shared experts' take the height that follows.  It leaves the height in header entry kFp4TileRows;
 // the host sizes tables and grid for the lowest.  (One kernel for three heights is up to
 // 0.6% slower than one each.)
 __host__ __device__ inline int fp4_tile_rows(int n_low, int n, int n_high) {

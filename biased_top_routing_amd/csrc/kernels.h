@@ -5,7 +5,8 @@
 
 namespace moe {
 
-// Compute units of the current device, asked for once per device.
+// Compute units of the device that is current at the first call (asked for once: the
+// grids sized by it are right for any number, and the devices of a node are alike).
 int cu_count();
 
 moe_status launch_route_topk(const moe_cfg* c, const float* scores, const float* bias, int32_t* idx,

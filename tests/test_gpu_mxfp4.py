@@ -200,7 +200,7 @@ def _spread(bits, g):
 
 
 CASES = [
-    # (T, H, E, G, M, k, S, I): tiles of 32 rows (up to 24 rows an expert on average), 64 (56) and 256, odd
+    # (T, H, E, G, M, k, S, I): tiles of 32 rows (up to 20 rows an expert on average) and of 128 and more, odd
     # numbers of 128-wide K steps in either GEMM, one step only, several shared experts, ragged tiles, one token,
     # more experts than pairs, column tiles past the end
     (1, 256, 8, 2, 1, 2, 1, 128),
