@@ -16,8 +16,8 @@ import oracle.mxfp4 as mx
 
 pytestmark = pytest.mark.gpu
 
-ROUNDS = [
-    # (rows a tile, GEMM that takes several rounds, T, H, E, k, S, I)
+CASES = [
+    # (rows a tile, GEMM whose workgroups take several, T, H, E, k, S, I)
     (256, "gate/up", 130, 128, 6, 6, 1, 11008),
     (256, "gate/up", 130, 384, 6, 6, 1, 5120),
     (256, "gate/up", 250, 256, 5, 5, 2, 5120),
@@ -43,7 +43,7 @@ def _affinities(T, E, k):
     return s
 
 
-@pytest.mark.parametrize("rows,gemm,T,H,E,k,S,I", ROUNDS)
+@pytest.mark.parametrize("rows,gemm,T,H,E,k,S,I", CASES)
 def test_several_tiles_a_workgroup(rows, gemm, T, H, E, k, S, I):
     say(f"{rows}-row tiles, several a workgroup in {gemm}: T={T} H={H} E={E} k={k} S={S} I={I}")
     c = MID.with_(T=T, H=H, E=E, G=1, M=1, k=k, S=S, I=I, sigma=0.05, group_topr=1, wgt="mxfp4")
