@@ -17,12 +17,13 @@ HEADER = os.path.join(os.path.dirname(PKG), "include", "moe.h")
 
 MOE_OK, MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_LAUNCH = 0, -1, -2, -3, -4, -5
 MOE_ERR_SCRATCH = -6
-MOE_F32, MOE_BF16, MOE_FP8_E4M3, MOE_MXFP4 = 0, 1, 2, 3
-MOE_SCORES_IN = 1
+MOE_F32, MOE_BF16, MOE_FP8_E4M3, MOE_MXFP4, MOE_INT8 = 0, 1, 2, 3, 4
+MOE_SCORES_IN, MOE_SOFTMAX, MOE_GATES_RAW = 1, 2, 4
 MOE_FFN_ALL, MOE_FFN_GATE_UP, MOE_FFN_DOWN = 0, 1, 2
 MOE_WS_DISPATCH, MOE_WS_FFN, MOE_WS_FFN_BWD, MOE_WS_ROUTE_BWD, MOE_WS_ROUTE = 1, 2, 3, 4, 5
+MOE_WS_NORM_BWD, MOE_WS_ROUTE_BWD_SOFTMAX = 6, 7
 MOE_WSP_H, MOE_WSP_H_SCALE, MOE_WSP_H_SHARED, MOE_WSP_H_SHARED_SCALE = 0, 1, 2, 3
-_DTYPES = {"f32": MOE_F32, "bf16": MOE_BF16, "fp8_e4m3": MOE_FP8_E4M3, "mxfp4": MOE_MXFP4}
+_DTYPES = {"f32": MOE_F32, "bf16": MOE_BF16, "fp8_e4m3": MOE_FP8_E4M3, "mxfp4": MOE_MXFP4, "int8": MOE_INT8}
 
 
 class MoeError(RuntimeError):
@@ -88,6 +89,12 @@ def lib() -> ctypes.CDLL:
             "moe_combine_local": [cfgp, vp, vp, vp, vp, vp, vp],
             "moe_combine_local_backward": [cfgp, vp, vp, vp, vp, vp, vp, vp],
             "moe_dispatch_local_backward": [cfgp, vp, vp, vp, vp, vp, vp],
+            "moe_expert_ffn_codes": [cfgp, vp, vp, vp, vp, ctypes.POINTER(MoeExpertWeights), vp, vp, vp, sz,
+                                     ctypes.c_int, vp],
+            "moe_quantize_int8": [vp, i32, i32, i32, i32, vp, vp, vp],
+            "moe_norm": [cfgp, vp, vp, vp, vp, f32, vp, vp, vp, vp, vp],
+            "moe_norm_backward": [cfgp, vp, vp, vp, f32, vp, vp, vp, vp, vp, sz, vp],
+            "moe_route_backward_flags": [cfgp, u32, vp, vp, vp, vp, vp, f32, i32, vp, vp, vp, vp, sz, vp],
             "moe_quantize_fp4": [vp, i32, i32, i32, vp, vp, vp],
             "moe_dequantize_fp4": [vp, vp, i32, i32, i32, vp, vp],
             "moe_ffn_workspace_part": [cfgp, ctypes.c_int, ctypes.POINTER(sz), ctypes.POINTER(sz)],
@@ -340,6 +347,39 @@ def moe_dequantize_fp4(codes, scales, n_mat, rows, cols, dst, stream=None):
     """The bf16 values [n_mat, rows, cols] of MXFP4 codes and scale bytes."""
     _check("moe_dequantize_fp4", lib().moe_dequantize_fp4(_c(codes), _c(scales), n_mat, rows, cols, _c(dst),
                                                           _s(stream)))
+
+
+def moe_expert_ffn_codes(cfg, x_codes, x_scale, perm, offsets, weights: MoeExpertWeights, y_perm, y_shared, ws,
+                         phase=MOE_FFN_ALL, stream=None):
+    """moe_expert_ffn_gather on int8 or E4M3 codes [T, H] with their scales."""
+    _check("moe_expert_ffn_codes", lib().moe_expert_ffn_codes(
+        ctypes.byref(cfg), _c(x_codes), _c(x_scale), _c(perm), _c(offsets), ctypes.byref(weights), _c(y_perm),
+        _c(y_shared), _c(ws), _nbytes(ws), phase, _s(stream)))
+
+
+def moe_quantize_int8(src, n_mat, rows, cols, group, dst, scales, stream=None):
+    """bf16 [n_mat, rows, cols] -> int8 codes of the same shape and fp32 scales [n_mat / group, rows]."""
+    _check("moe_quantize_int8", lib().moe_quantize_int8(_c(src), n_mat, rows, cols, group, _c(dst), _c(scales),
+                                                        _s(stream)))
+
+
+def moe_norm(cfg, n_tokens, x, residual, weight, eps, h, y, codes=None, code_scale=None, stream=None):
+    """h = x + residual, y = h * weight / rms(h), and y as int8 or E4M3 codes."""
+    _check("moe_norm", lib().moe_norm(ctypes.byref(cfg), live_count(n_tokens), _c(x), _c(residual), _c(weight),
+                                      float(eps), _c(h), _c(y), _c(codes), _c(code_scale), _s(stream)))
+
+
+def moe_norm_backward(cfg, n_tokens, h, weight, eps, dy, dh, dx, dweight, ws, stream=None):
+    _check("moe_norm_backward", lib().moe_norm_backward(
+        ctypes.byref(cfg), live_count(n_tokens), _c(h), _c(weight), float(eps), _c(dy), _c(dh), _c(dx), _c(dweight),
+        _c(ws), _nbytes(ws), _s(stream)))
+
+
+def moe_route_backward_flags(cfg, flags, x, w_router, scores, topk_idx, d_topk_w, alpha, seq_len, dx_router, dw_router,
+                             loss, ws, stream=None):
+    _check("moe_route_backward_flags", lib().moe_route_backward_flags(
+        ctypes.byref(cfg), flags, _c(x), _c(w_router), _c(scores), _c(topk_idx), _c(d_topk_w), float(alpha),
+        int(seq_len), _c(dx_router), _c(dw_router), _c(loss), _c(ws), _nbytes(ws), _s(stream)))
 
 
 def moe_ffn_workspace_part(cfg, part) -> tuple:

@@ -5,12 +5,14 @@
 #include "common.h"
 #include "bwd_layout.h"
 #include "ffn_layout.h"
+#include "norm_layout.h"
 
 namespace moe {
 
 bool gemm_dtype_ok(const moe_cfg* c) {
   if (c->act == MOE_F32 && c->wgt == MOE_F32) return true;
-  if (c->act == MOE_BF16 && (c->wgt == MOE_BF16 || c->wgt == MOE_FP8_E4M3 || c->wgt == MOE_MXFP4))
+  if (c->act == MOE_BF16 && (c->wgt == MOE_BF16 || c->wgt == MOE_FP8_E4M3 || c->wgt == MOE_MXFP4 ||
+                              c->wgt == MOE_INT8))
     return true;
   return false;
 }
@@ -48,6 +50,10 @@ moe_status validate_cfg(const moe_cfg* c) {
     if ((int64_t)c->T * c->k * std::max(c->H, c->I) / 32 >= ((int64_t)1 << 31) ||
         (int64_t)c->T * std::max<int64_t>(c->H, (int64_t)c->S * c->I) / 32 >= ((int64_t)1 << 31))
       return MOE_ERR_SHAPE;
+  } else if (c->wgt == MOE_INT8) {  // whole 128-wide K slices; 32-bit sums; a wavefront a row to quantise
+    if (c->H % 128 || c->I % 128) return MOE_ERR_SHAPE;
+    if (c->H >= kInt8MaxK || (int64_t)(c->S > 1 ? c->S : 1) * c->I >= kInt8MaxK) return MOE_ERR_SHAPE;
+    if ((int64_t)c->T * c->k >= (int64_t)1 << 26) return MOE_ERR_SHAPE;
   } else {  // fp8 experts: K of every GEMM at most kFp8MaxKC chunks of 128
     if (c->H % 128 || c->I % 128) return MOE_ERR_SHAPE;
     if (c->H > 128 * kFp8MaxKC || (int64_t)(c->S > 1 ? c->S : 1) * c->I > 128 * kFp8MaxKC)
@@ -67,6 +73,8 @@ extern "C" size_t moe_workspace_bytes(const moe_cfg* cfg, int which) {
   if (which == MOE_WS_FFN) return FfnLayout(cfg).total;
   if (which == MOE_WS_FFN_BWD) return FfnBwdLayout(cfg).total;
   if (which == MOE_WS_ROUTE_BWD) return RouteBwdLayout(cfg, 0).total;
+  if (which == MOE_WS_NORM_BWD) return NormBwdLayout(cfg).total;
+  if (which == MOE_WS_ROUTE_BWD_SOFTMAX) return RouteBwdLayout(cfg, 0, 2).total;
   return 0;
 }
 

@@ -394,6 +394,80 @@ __global__ __launch_bounds__(256) void route_grad_kernel(const float* __restrict
   }
 }
 
+// ... with the flags of moe_route: ds_e of the gates (MOE_GATES_RAW: scale * dw, not through their sum) and of the
+// balance loss, through the softmax (dlogit_e = s_e (ds_e - sum s ds)) or the sigmoid.  dlogit is stored as the sum of
+// two bf16 numbers, the nearest and what it leaves (17 bits and more: the products of the router's gradients then stay
+// within 2^-17 of fp32 ones), in rows of 2 * Ep, zero behind E.
+template <bool SOFTMAX>
+__global__ __launch_bounds__(256) void route_grad_flags_kernel(const float* __restrict__ s,
+                                                               const int32_t* __restrict__ idx,
+                                                               const float* __restrict__ d_w,
+                                                               const float* __restrict__ coef, int T, int E, int Ep,
+                                                               int k, int L, float scale, bool raw,
+                                                               bf16_t* __restrict__ dlogit) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const int lane = threadIdx.x & 63;
+  const int t = blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (t >= T) return;
+  const int b = t / L;
+  float v[kMaxEPL], ds[kMaxEPL], rs = 0.f, gs = 0.f;
+#pragma unroll
+  for (int i = 0; i < kMaxEPL; ++i) {
+    const int e = lane + 64 * i;
+    v[i] = e < E ? s[(int64_t)t * E + e] : 0.f;
+    ds[i] = coef && e < E ? coef[(int64_t)b * E + e] : 0.f;   // d L_bal / d s'_te
+    rs += v[i];
+    gs += ds[i] * v[i];
+  }
+  rs = wave_sum(rs);
+  gs = wave_sum(gs);
+  // (all affinities 0: neither the normalised ones nor a gradient)
+#pragma unroll
+  for (int i = 0; i < kMaxEPL; ++i) ds[i] = coef && rs > 0.f ? (ds[i] - gs / rs) / rs : 0.f;
+  // gates over the selected experts (an id outside [0, E) is none)
+  int sel = lane < k ? idx[(int64_t)t * k + lane] : -1;
+  if ((unsigned)sel >= (unsigned)E) sel = -1;
+  const float ss = sel >= 0 ? s[(int64_t)t * E + sel] : 0.f;
+  const float dwj = sel >= 0 ? d_w[(int64_t)t * k + lane] : 0.f;
+  const float S = wave_sum(ss);
+  const float B1 = wave_sum(dwj * ss);
+  const float dsel = raw ? scale * dwj : S > 0.f ? scale / S * (dwj - B1 / S) : 0.f;
+  for (int j = 0; j < k; ++j) {
+    const int ej = __shfl(sel, j);
+    const float dj = __shfl(dsel, j);
+#pragma unroll
+    for (int i = 0; i < kMaxEPL; ++i)
+      if (ej == lane + 64 * i) ds[i] += dj;
+  }
+  float mean = 0.f;
+  if constexpr (SOFTMAX) {
+#pragma unroll
+    for (int i = 0; i < kMaxEPL; ++i) mean = fmaf(v[i], ds[i], mean);
+    mean = wave_sum(mean);
+  }
+  bf16_t* out = dlogit + (int64_t)t * 2 * Ep;
+#pragma unroll
+  for (int i = 0; i < kMaxEPL; ++i) {
+    const int e = lane + 64 * i;
+    if (e >= Ep) continue;
+    const float d = e < E ? SOFTMAX ? v[i] * (ds[i] - mean) : ds[i] * v[i] * (1.0f - v[i]) : 0.f;
+    const bf16_t hi = f32_to_bf16(d);
+    out[e] = hi;
+    out[Ep + e] = f32_to_bf16(d - bf16_to_f32(hi));
+  }
+#endif
+}
+
+// Two copies of the router weight [E, H], each in Ep rows, zero behind E.
+__global__ __launch_bounds__(256) void router_weight_twice_kernel(const uint4* __restrict__ w, int E, int Ep,
+                                                                  int64_t nchunk, uint4* __restrict__ out) {
+  const int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (q >= (int64_t)Ep * nchunk) return;
+  const uint4 v = q < (int64_t)E * nchunk ? w[q] : make_uint4(0, 0, 0, 0);
+  out[q] = v;
+  out[(int64_t)Ep * nchunk + q] = v;
+}
+
 bool bwd_dtypes_ok(const moe_cfg* c) { return c->act == MOE_BF16 && c->wgt == MOE_BF16; }
 
 // one lane per 16-byte chunk of a row, whole wavefronts, at most 1024 lanes
@@ -484,17 +558,29 @@ extern "C" moe_status moe_expert_ffn_backward_saved(const moe_cfg* cfg, const vo
                              ws_bytes, stream);
 }
 
-extern "C" moe_status moe_route_backward(const moe_cfg* cfg, const void* x, const void* w_router,
-                                         const float* scores, const int32_t* topk_idx, const float* d_topk_w,
-                                         float alpha, int32_t seq_len, float* dx_router, float* dw_router,
-                                         float* loss, void* ws, size_t ws_bytes, void* stream) {
+namespace {
+
+// Both entry points; with_flags: the call that takes moe_route's flags.
+moe_status route_backward(const moe_cfg* cfg, bool with_flags, uint32_t flags, const void* x, const void* w_router,
+                          const float* scores, const int32_t* topk_idx, const float* d_topk_w, float alpha,
+                          int32_t seq_len, float* dx_router, float* dw_router, float* loss, void* ws, size_t ws_bytes,
+                          void* stream) {
   moe_status st = validate_cfg(cfg);
   if (st != MOE_OK) return st;
   if (!bwd_dtypes_ok(cfg)) return MOE_ERR_UNSUPPORTED;
+  if (with_flags) {
+    if (!flags || (flags & ~(MOE_SOFTMAX | MOE_GATES_RAW))) return MOE_ERR_UNSUPPORTED;
+    // (one descriptor covers the two copies of the router weight, and one the 1024 rows of x of a partial sum)
+    if (align_up(cfg->E, 64) * (int64_t)cfg->H * 4 >= (int64_t)1 << 31 || cfg->H >= 1 << 20) return MOE_ERR_UNSUPPORTED;
+    if (misaligned(x, 16) || misaligned(w_router, 16) || misaligned(ws, 16) || misaligned(scores, 4) ||
+        misaligned(topk_idx, 4) || misaligned(d_topk_w, 4) || misaligned(dx_router, 4) || misaligned(dw_router, 4) ||
+        misaligned(loss, 4))
+      return MOE_ERR_UNSUPPORTED;
+  }
   if (!x || !w_router || !scores || !topk_idx || !d_topk_w || !dw_router || !loss || !ws) return MOE_ERR_NULL;
   if (!(alpha >= 0.0f) || !isfinite(alpha)) return MOE_ERR_SHAPE;
   if (seq_len < 0 || (seq_len > 0 && cfg->T % seq_len != 0)) return MOE_ERR_SHAPE;
-  const RouteBwdLayout L(cfg, seq_len);
+  const RouteBwdLayout L(cfg, seq_len, with_flags ? 2 : 1);
   if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
   hipStream_t s = as_stream(stream);
   char* base = static_cast<char*>(ws);
@@ -517,11 +603,47 @@ extern "C" moe_status moe_route_backward(const moe_cfg* cfg, const void* x, cons
   hipLaunchKernelGGL(seq_coef_kernel, dim3(1), dim3(256), 0, s, cnt, psum, cfg->E, cfg->k, L.seq_len,
                      bal ? L.nseq : 0, L.nchunk, alpha, coef, loss);
   if ((st = launch_status()) != MOE_OK) return st;
-  hipLaunchKernelGGL(route_grad_kernel, dim3((unsigned)((cfg->T + 3) / 4)), dim3(256), 0, s, scores, topk_idx,
-                     d_topk_w, bal ? coef : nullptr, cfg->T, cfg->E, cfg->k, L.seq_len, cfg->route_scale, dlogit);
+  const dim3 tokens((unsigned)((cfg->T + 3) / 4));
+  if (!with_flags) {
+    hipLaunchKernelGGL(route_grad_kernel, tokens, dim3(256), 0, s, scores, topk_idx, d_topk_w, bal ? coef : nullptr,
+                       cfg->T, cfg->E, cfg->k, L.seq_len, cfg->route_scale, dlogit);
+    if ((st = launch_status()) != MOE_OK) return st;
+    return launch_router_bwd_gemms(cfg, (const bf16_t*)x, (const bf16_t*)w_router, dlogit, cfg->E, 1, part, L.nsplit,
+                                   dw_router, dx_router, s);
+  }
+  auto grad = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, tokens, dim3(256), 0, s, scores, topk_idx, d_topk_w, bal ? coef : nullptr, cfg->T, cfg->E,
+                       L.Ep, cfg->k, L.seq_len, cfg->route_scale, (flags & MOE_GATES_RAW) != 0, dlogit);
+  };
+  if (flags & MOE_SOFTMAX) grad(route_grad_flags_kernel<true>);
+  else grad(route_grad_flags_kernel<false>);
   if ((st = launch_status()) != MOE_OK) return st;
-  return launch_router_bwd_gemms(cfg, (const bf16_t*)x, (const bf16_t*)w_router, dlogit, part, L.nsplit, dw_router,
-                                 dx_router, s);
+  bf16_t* w2 = reinterpret_cast<bf16_t*>(base + L.off_w);
+  if (dx_router) {
+    const int64_t nchunk = (int64_t)cfg->H / 8;
+    hipLaunchKernelGGL(router_weight_twice_kernel, dim3((unsigned)((L.Ep * nchunk + 255) / 256)), dim3(256), 0, s,
+                       (const uint4*)w_router, cfg->E, L.Ep, nchunk, (uint4*)w2);
+    if ((st = launch_status()) != MOE_OK) return st;
+  }
+  return launch_router_bwd_gemms(cfg, (const bf16_t*)x, w2, dlogit, L.Ep, 2, part, L.nsplit, dw_router, dx_router, s);
+}
+
+}  // namespace
+
+extern "C" moe_status moe_route_backward(const moe_cfg* cfg, const void* x, const void* w_router,
+                                         const float* scores, const int32_t* topk_idx, const float* d_topk_w,
+                                         float alpha, int32_t seq_len, float* dx_router, float* dw_router,
+                                         float* loss, void* ws, size_t ws_bytes, void* stream) {
+  return route_backward(cfg, false, 0, x, w_router, scores, topk_idx, d_topk_w, alpha, seq_len, dx_router, dw_router, loss,
+                        ws, ws_bytes, stream);
+}
+
+extern "C" moe_status moe_route_backward_flags(const moe_cfg* cfg, uint32_t flags, const void* x, const void* w_router,
+                                               const float* scores, const int32_t* topk_idx, const float* d_topk_w,
+                                               float alpha, int32_t seq_len, float* dx_router, float* dw_router,
+                                               float* loss, void* ws, size_t ws_bytes, void* stream) {
+  return route_backward(cfg, true, flags, x, w_router, scores, topk_idx, d_topk_w, alpha, seq_len, dx_router, dw_router,
+                        loss, ws, ws_bytes, stream);
 }
 
 extern "C" moe_status moe_dispatch_backward(const moe_cfg* cfg, const void* dx_perm, const void* dx_shared,

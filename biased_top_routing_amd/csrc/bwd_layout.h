@@ -84,9 +84,12 @@ constexpr int kRouterKSplit = 1024;  // token rows per split of the router-weigh
 
 struct RouteBwdLayout {
   int nseq, seq_len, nchunk, nsplit;
-  size_t off_cnt, off_psum, off_coef, off_dlogit, off_part, total;
+  int Ep;
+  size_t off_cnt, off_psum, off_coef, off_dlogit, off_part, off_w, total;
 
-  RouteBwdLayout(const moe_cfg* c, int seq) {
+  // terms 2: dlogit as the sum of two bf16 numbers, in rows of 2 * Ep (Ep: E rounded up to 64; columns [0, Ep) the
+  // leading terms, then the rest, zero behind E), for products with two copies of the router weight
+  RouteBwdLayout(const moe_cfg* c, int seq, int terms = 1) {
     seq_len = seq > 0 ? seq : (c->T > 0 ? c->T : 1);
     nseq = c->T / seq_len;
     nchunk = (seq_len + kSeqChunk - 1) / kSeqChunk;
@@ -99,8 +102,10 @@ struct RouteBwdLayout {
     off_cnt = take(chunks_max * c->E * 4);
     off_psum = take(chunks_max * c->E * 4);
     off_coef = take(seqs_max * c->E * 4);
-    off_dlogit = take((size_t)c->T * c->E * 2);
-    off_part = take((size_t)nsplit * c->E * c->H * 4);
+    Ep = terms == 1 ? c->E : (int)align_up(c->E, 64);
+    off_dlogit = take((size_t)c->T * terms * Ep * 2);
+    off_part = take((size_t)nsplit * terms * Ep * c->H * 4);
+    off_w = take(terms == 1 ? 0 : (size_t)2 * Ep * c->H * 2);
     total = o;
   }
 };

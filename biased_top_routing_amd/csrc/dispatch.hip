@@ -17,6 +17,7 @@
 #include "common.h"
 #include "ffn_layout.h"
 #include "fp4.h"
+#include "int8.h"
 #include "kernels.h"
 
 namespace moe {
@@ -475,6 +476,54 @@ __global__ __launch_bounds__(256) void permute_rows_fp4_kernel(const uint4* __re
 #endif
 }
 
+// int8 dispatch (int8.h): the token's row is read twice, for its largest magnitude and for its codes (the second
+// time from the cache), and the codes are stored to each of its k destination rows with the row's scale.
+template <int CPL, bool LOCAL>
+__global__ __launch_bounds__(256) void permute_rows_int8_kernel(const uint4* __restrict__ src,
+                                                                const int32_t* __restrict__ inv, int T, int k, int H,
+                                                                uint2* __restrict__ dst,
+                                                                float* __restrict__ dst_scale) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const int lane = threadIdx.x & 63;
+  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (t >= T) return;      // whole wavefront exits together
+  const int64_t nchunk = H / 8;
+  const int32_t myp = lane < k ? inv[t * k + lane] : LOCAL ? -1 : 0;
+  if (LOCAL && !__any(myp >= 0)) return;
+  uint4 v[CPL];
+  auto load = [&](int64_t c0) {
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) {
+      const int64_t c = c0 + i * kWave + lane;
+      v[i] = c < nchunk ? src[t * nchunk + c] : make_uint4(0, 0, 0, 0);
+    }
+  };
+  uint32_t m = 0;
+  for (int64_t c0 = 0; c0 < nchunk; c0 += (int64_t)CPL * kWave) {
+    load(c0);
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) m = max(m, chunk_amax(v[i]));
+  }
+  const Int8Row row(wave_max(m));
+  if (lane < k && (!LOCAL || myp >= 0)) dst_scale[myp] = row.scale;
+  for (int64_t c0 = 0; c0 < nchunk; c0 += (int64_t)CPL * kWave) {
+    load(c0);
+    uint2 q[CPL];
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) q[i] = chunk_codes(row, v[i]);
+    for (int j = 0; j < k; ++j) {
+      const int64_t p = __shfl(myp, j);
+      if (LOCAL && p < 0) continue;
+#pragma unroll
+      for (int i = 0; i < CPL; ++i) {
+        const int64_t c = c0 + i * kWave + lane;
+        if (c < nchunk) dst[p * nchunk + c] = q[i];
+      }
+    }
+  }
+#endif
+}
+
 // Row quantisation without permutation (shared-expert input, tests).
 __global__ __launch_bounds__(256) void quantize_rows_kernel(const uint4* __restrict__ src,
                                                             int64_t rows, int cols,
@@ -554,7 +603,7 @@ __global__ __launch_bounds__(256) void quantize_blocks_kernel(const bf16_t* __re
 
 // ---- a small share in one launch
 // Row formats of the copy.
-enum { kRowsCopy = 0, kRowsFp8 = 1, kRowsFp4 = 2, kRowsNone = 3 };
+enum { kRowsCopy = 0, kRowsFp8 = 1, kRowsFp4 = 2, kRowsNone = 3, kRowsInt8 = 4 };
 
 // Workgroup t < T does token t, workgroup T the counts.  A pair's row is the
 // number of pairs that come before it, ordered by (expert, pair id): with the
@@ -650,6 +699,25 @@ __global__ __launch_bounds__(kSmallThreads) void dispatch_small_kernel(
   bool any = false;
   for (int j = 0; j < k; ++j) any |= dest[j] >= 0;
   if (!any) return;
+  // int8: the row's largest magnitude first (a row of more than U chunks a lane is read again below)
+  __shared__ uint32_t top[4];
+  uint32_t amax = 0;
+  if constexpr (ROWS == kRowsInt8) {
+    for (int64_t c0 = 0; c0 < nchunk; c0 += U * kSmallThreads) {
+      if (c0 > 0) load(c0);
+#pragma unroll
+      for (int u = 0; u < U; ++u) amax = max(amax, chunk_amax(v[u]));
+    }
+    amax = wave_max(amax);
+    if (lane == 0) top[wave] = amax;
+    __syncthreads();
+    amax = max(max(top[0], top[1]), max(top[2], top[3]));
+    if (nchunk > U * kSmallThreads) load(0);
+  }
+  const Int8Row row8(amax);
+  if constexpr (ROWS == kRowsInt8) {
+    if (tid < k && dest[tid] >= 0) static_cast<float*>(x_scale)[dest[tid]] = row8.scale;
+  }
   for (int64_t c0 = 0; c0 < nchunk; c0 += U * kSmallThreads) {
     if (c0 > 0) load(c0);
 #pragma unroll
@@ -660,6 +728,7 @@ __global__ __launch_bounds__(kSmallThreads) void dispatch_small_kernel(
       float sc;
       uint32_t w4, sw;
       if constexpr (ROWS == kRowsFp8) w8 = quant_chunk_1x128(v[u], &sc);
+      if constexpr (ROWS == kRowsInt8) w8 = chunk_codes(row8, v[u]);
       if constexpr (ROWS == kRowsFp4) {
         uint32_t e;
         w4 = mx_quant_chunk(v[u], &e);
@@ -670,6 +739,7 @@ __global__ __launch_bounds__(kSmallThreads) void dispatch_small_kernel(
         const int64_t p = dest[j];
         if (p < 0) continue;
         if constexpr (ROWS == kRowsCopy) static_cast<uint4*>(x_perm)[p * nchunk + c] = v[u];
+        if constexpr (ROWS == kRowsInt8) static_cast<uint2*>(x_perm)[p * nchunk + c] = w8;
         if constexpr (ROWS == kRowsFp8) {
           static_cast<uint2*>(x_perm)[p * nchunk + c] = w8;
           if ((lane & 15) == 0) static_cast<float*>(x_scale)[p * (nchunk / 16) + c / 16] = sc;
@@ -696,6 +766,7 @@ static moe_status dispatch_small(const moe_cfg* cfg, const Window& win, const in
   if (!x_perm) go(dispatch_small_kernel<kRowsNone>);
   else if (cfg->wgt == MOE_MXFP4) go(dispatch_small_kernel<kRowsFp4>);
   else if (cfg->wgt == MOE_FP8_E4M3) go(dispatch_small_kernel<kRowsFp8>);
+  else if (cfg->wgt == MOE_INT8) go(dispatch_small_kernel<kRowsInt8>);
   else go(dispatch_small_kernel<kRowsCopy>);
   return launch_status();
 }
@@ -707,7 +778,7 @@ static moe_status dispatch_launch(const moe_cfg* cfg, const Window& win, const i
                                   int32_t* counts, int32_t* offsets, int32_t* perm, int32_t* inv, void* x_perm,
                                   float* x_perm_scale, int32_t* segc, hipStream_t s) {
   moe_status st;
-  const bool fp8 = cfg->wgt == MOE_FP8_E4M3, fp4 = cfg->wgt == MOE_MXFP4;
+  const bool fp8 = cfg->wgt == MOE_FP8_E4M3, fp4 = cfg->wgt == MOE_MXFP4, i8 = cfg->wgt == MOE_INT8;
   const int64_t N = pairs(cfg);
   const int64_t nseg = dispatch_segments(cfg);
   const int E = cfg->E;
@@ -721,6 +792,9 @@ static moe_status dispatch_launch(const moe_cfg* cfg, const Window& win, const i
     if (fp4) {
       hipLaunchKernelGGL((permute_rows_fp4_kernel<8, LOCAL>), dim3(tblocks), dim3(256), 0, s, (const uint4*)x, inv,
                          cfg->T, cfg->k, cfg->H, (uint32_t*)x_perm, (uint32_t*)x_perm_scale);
+    } else if (i8) {
+      hipLaunchKernelGGL((permute_rows_int8_kernel<8, LOCAL>), dim3(tblocks), dim3(256), 0, s, (const uint4*)x, inv,
+                         cfg->T, cfg->k, cfg->H, (uint2*)x_perm, x_perm_scale);
     } else if (fp8) {
       hipLaunchKernelGGL((permute_rows_fp8_kernel<8, LOCAL>), dim3(tblocks), dim3(256), 0, s, (const uint4*)x, inv,
                          cfg->T, cfg->k, cfg->H, (uint2*)x_perm, x_perm_scale);
@@ -766,11 +840,11 @@ static moe_status dispatch_check(const moe_cfg* cfg, const int32_t* topk_idx, co
                                  int32_t* offsets, int32_t* perm, int32_t* inv, void* x_perm, float* x_perm_scale) {
   moe_status st = validate_cfg(cfg);
   if (st != MOE_OK) return st;
-  const bool fp4 = cfg->wgt == MOE_MXFP4, scaled = fp4 || cfg->wgt == MOE_FP8_E4M3;
+  const bool fp4 = cfg->wgt == MOE_MXFP4, i8 = cfg->wgt == MOE_INT8, scaled = fp4 || i8 || cfg->wgt == MOE_FP8_E4M3;
   // x_perm == nullptr: indices only (the expert FFN gathers the rows itself)
   if (!topk_idx || !counts || !offsets || !perm || !inv) return MOE_ERR_NULL;
   if (x_perm && (!x || (scaled && !x_perm_scale))) return MOE_ERR_NULL;
-  if (fp4 && x_perm && (misaligned(x, 16) || misaligned(x_perm, 16) || misaligned(x_perm_scale, 4)))
+  if ((fp4 || i8) && x_perm && (misaligned(x, 16) || misaligned(x_perm, 16) || misaligned(x_perm_scale, 4)))
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }

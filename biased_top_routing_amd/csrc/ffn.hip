@@ -321,11 +321,25 @@ bool fp4_misaligned(const moe_cfg* c, const void* x_perm, const void* x_perm_sca
   return false;
 }
 
-// Both FFN entry points: routed gate/up rows from x_perm (perm == nullptr) or
-// gathered from x through perm.
+// The int8 kernels load 16-byte chunks of rows and codes and 4-byte scales (a row's h scale in one word).
+bool int8_misaligned(const moe_cfg* c, const void* x_perm, const float* x_perm_scale, const moe_expert_weights* w,
+                     const void* x, const void* x_codes, const float* x_scale, const void* y_perm, const void* y_shared,
+                     const void* ws) {
+  const bool s = c->S > 0;
+  for (const void* q : {x_perm, w->w_gate_up, w->w_down, s ? w->ws_gate_up : nullptr, s ? w->ws_down : nullptr, x, x_codes,
+                        y_perm, s ? y_shared : nullptr, ws})
+    if (misaligned(q, 16)) return true;
+  for (const float* q : {x_perm_scale, x_scale, w->w_gate_up_scale, w->w_down_scale, s ? w->ws_gate_up_scale : nullptr,
+                         s ? w->ws_down_scale : nullptr})
+    if (misaligned(q, 4)) return true;
+  return false;
+}
+
+// All FFN entry points: routed gate/up rows from x_perm (perm == nullptr) or
+// gathered from x through perm (FP8 and int8: from x_codes, x_scale where they are given).
 moe_status expert_ffn(const moe_cfg* cfg, const void* x_perm, const float* x_perm_scale,
                       const int32_t* perm, const int32_t* offsets, const moe_expert_weights* w,
-                      const void* x, void* y_perm, void* y_shared, const moe_ffn_saved* saved, void* ws,
+                      const void* x, const void* x_codes, const float* x_scale, void* y_perm, void* y_shared, const moe_ffn_saved* saved, void* ws,
                       size_t ws_bytes, int phase, void* stream) {
   moe_status st = validate_cfg(cfg);
   if (st != MOE_OK) return st;
@@ -334,9 +348,10 @@ moe_status expert_ffn(const moe_cfg* cfg, const void* x_perm, const float* x_per
   const bool gate_up = phase != MOE_FFN_DOWN;
   if (!w || !offsets || !y_perm || !ws || !w->w_gate_up || !w->w_down) return MOE_ERR_NULL;
   if (!perm && !x_perm) return MOE_ERR_NULL;
-  if (perm && gate_up && !x) return MOE_ERR_NULL;
-  if (cfg->S > 0 && (!x || !y_shared || !w->ws_gate_up || !w->ws_down)) return MOE_ERR_NULL;
-  const bool fp8 = cfg->wgt == MOE_FP8_E4M3, fp4 = cfg->wgt == MOE_MXFP4, scaled = fp8 || fp4;
+  if (perm && gate_up && !x && !x_codes) return MOE_ERR_NULL;
+  if (cfg->S > 0 && ((!x && !x_codes) || !y_shared || !w->ws_gate_up || !w->ws_down)) return MOE_ERR_NULL;
+  const bool fp8 = cfg->wgt == MOE_FP8_E4M3, fp4 = cfg->wgt == MOE_MXFP4, i8 = cfg->wgt == MOE_INT8,
+             scaled = fp8 || fp4 || i8;
   if (scaled && ((!perm && !x_perm_scale) || !w->w_gate_up_scale || !w->w_down_scale)) return MOE_ERR_NULL;
   if (scaled && cfg->S > 0 && (!w->ws_gate_up_scale || !w->ws_down_scale)) return MOE_ERR_NULL;
   if (saved) {
@@ -346,9 +361,11 @@ moe_status expert_ffn(const moe_cfg* cfg, const void* x_perm, const float* x_per
   // gathered rows are addressed by 32-bit byte offsets into x (one row past
   // the end marks a dropped row)
   if (perm && cfg->act != MOE_F32 &&
-      ((int64_t)cfg->T + 1) * cfg->H * (fp4 ? 1 : fp8 ? 2 : 2 * (int64_t)act_bytes(cfg)) / 2 > INT32_MAX)
+      ((int64_t)cfg->T + 1) * cfg->H * (fp4 ? 1 : fp8 || i8 ? 2 : 2 * (int64_t)act_bytes(cfg)) / 2 > INT32_MAX)
     return MOE_ERR_UNSUPPORTED;
   if (fp4 && fp4_misaligned(cfg, x_perm, x_perm_scale, w, x, y_perm, y_shared, ws)) return MOE_ERR_UNSUPPORTED;
+  if (i8 && int8_misaligned(cfg, x_perm, x_perm_scale, w, x, x_codes, x_scale, y_perm, y_shared, ws))
+    return MOE_ERR_UNSUPPORTED;
   if (ws_bytes < FfnLayout(cfg).total) return MOE_ERR_WORKSPACE;
   if (cfg->T == 0) return MOE_OK;
   hipStream_t s = as_stream(stream);
@@ -358,12 +375,15 @@ moe_status expert_ffn(const moe_cfg* cfg, const void* x_perm, const float* x_per
   if (fp4)
     return launch_ffn_fp4(cfg, (const uint8_t*)x_perm, (const uint8_t*)x_perm_scale, perm, offsets, w, (const bf16_t*)x,
                           (bf16_t*)y_perm, (bf16_t*)y_shared, ws, phase, s);
+  if (i8)
+    return launch_ffn_int8(cfg, (const uint8_t*)x_perm, x_perm_scale, perm, offsets, w, (const bf16_t*)x,
+                           (const uint8_t*)x_codes, x_scale, (bf16_t*)y_perm, (bf16_t*)y_shared, ws, phase, s);
   if (!fp8)
     return launch_ffn_bf16(cfg, (const bf16_t*)x_perm, perm, offsets, w, (const bf16_t*)x,
                            (bf16_t*)y_perm, (bf16_t*)y_shared, phase == MOE_FFN_DOWN ? nullptr : saved, ws,
                            phase, s);
   return launch_ffn_fp8(cfg, (const fp8_t*)x_perm, x_perm_scale, perm, offsets, w, (const bf16_t*)x,
-                        (bf16_t*)y_perm, (bf16_t*)y_shared, ws, phase, s);
+                        (const fp8_t*)x_codes, x_scale, (bf16_t*)y_perm, (bf16_t*)y_shared, ws, phase, s);
 }
 
 }  // namespace
@@ -373,7 +393,7 @@ extern "C" moe_status moe_expert_ffn(const moe_cfg* cfg, const void* x_perm, con
                                      void* y_perm, void* y_shared, void* ws, size_t ws_bytes, int phase,
                                      void* stream) {
   if (!x_perm) return MOE_ERR_NULL;
-  return expert_ffn(cfg, x_perm, x_perm_scale, nullptr, offsets, w, x, y_perm, y_shared, nullptr, ws, ws_bytes,
+  return expert_ffn(cfg, x_perm, x_perm_scale, nullptr, offsets, w, x, nullptr, nullptr, y_perm, y_shared, nullptr, ws, ws_bytes,
                     phase, stream);
 }
 
@@ -382,8 +402,21 @@ extern "C" moe_status moe_expert_ffn_gather(const moe_cfg* cfg, const void* x, c
                                             void* y_perm, void* y_shared, void* ws, size_t ws_bytes,
                                             int phase, void* stream) {
   if (!perm) return MOE_ERR_NULL;
-  return expert_ffn(cfg, nullptr, nullptr, perm, offsets, w, x, y_perm, y_shared, nullptr, ws, ws_bytes, phase,
-                    stream);
+  return expert_ffn(cfg, nullptr, nullptr, perm, offsets, w, x, nullptr, nullptr, y_perm, y_shared, nullptr, ws,
+                    ws_bytes, phase, stream);
+}
+
+extern "C" moe_status moe_expert_ffn_codes(const moe_cfg* cfg, const void* x_codes, const float* x_scale,
+                                           const int32_t* perm, const int32_t* offsets, const moe_expert_weights* w,
+                                           void* y_perm, void* y_shared, void* ws, size_t ws_bytes, int phase,
+                                           void* stream) {
+  const moe_status st = validate_cfg(cfg);
+  if (st != MOE_OK) return st;
+  if (cfg->wgt != MOE_INT8 && cfg->wgt != MOE_FP8_E4M3) return MOE_ERR_UNSUPPORTED;
+  if (!perm || !x_codes || !x_scale) return MOE_ERR_NULL;
+  if (misaligned(x_codes, 16) || misaligned(x_scale, 4)) return MOE_ERR_UNSUPPORTED;
+  return expert_ffn(cfg, nullptr, nullptr, perm, offsets, w, nullptr, x_codes, x_scale, y_perm, y_shared, nullptr, ws,
+                    ws_bytes, phase, stream);
 }
 
 extern "C" moe_status moe_expert_ffn_save(const moe_cfg* cfg, const void* x_perm, const int32_t* perm,
@@ -391,6 +424,6 @@ extern "C" moe_status moe_expert_ffn_save(const moe_cfg* cfg, const void* x_perm
                                           void* y_perm, void* y_shared, const moe_ffn_saved* saved, void* ws,
                                           size_t ws_bytes, int phase, void* stream) {
   if (!saved || (!x_perm && !perm)) return MOE_ERR_NULL;
-  return expert_ffn(cfg, x_perm, nullptr, x_perm ? nullptr : perm, offsets, w, x, y_perm, y_shared, saved, ws,
-                    ws_bytes, phase, stream);
+  return expert_ffn(cfg, x_perm, nullptr, x_perm ? nullptr : perm, offsets, w, x, nullptr, nullptr, y_perm, y_shared,
+                    saved, ws, ws_bytes, phase, stream);
 }

@@ -132,6 +132,13 @@ __host__ __device__ inline int fp4_tile_rows(int n_low, int n, int n_high) {
 }
 constexpr int kFp4TileRows = 6;
 
+// int8 GEMMs: tiles of 32 token rows where the pairs make at most 20 an expert, else 256; 128 h columns per
+// gate/up tile, 256 output columns per down tile.
+constexpr int kInt8RowsBM = 32, kInt8BM = 256;
+constexpr int kInt8RowsAvg = 20;
+constexpr int kInt8BNH = 128, kInt8BN2 = 256;
+constexpr int kInt8MaxK = 1 << 17;   // K of a GEMM stays below: 128 * 128 * K fits the accumulators
+
 // Row tiles per group in the tile order of a segment (see build_tiles_kernel).
 #ifndef MOE_GROUP_ROW_TILES
 #define MOE_GROUP_ROW_TILES 8
@@ -159,6 +166,7 @@ constexpr int kStripeGateUp = 8;
 constexpr int kStripeDown = 0;
 constexpr int kStripeFp8 = 2;
 constexpr int kStripeFp4 = 2;
+constexpr int kStripeInt8 = 2;
 
 // Position j of XCD xcd in runs of P consecutive entries dealt to the 8 XCDs in turn.
 __host__ __device__ inline int xcd_run_index(int j, int xcd, int P) {
@@ -214,25 +222,26 @@ struct FfnLayout {
   int64_t R1, Rs1, R2, Rs2;      // routed row-tile bounds, shared row tiles
   int64_t nt1, nt1s, nt2;        // column tiles: gate/up routed, gate/up shared, down
   int64_t max1, max2;            // tile-table capacities
-  size_t off_hdr, off_t1, off_t2, off_hp, off_hps, off_hs, off_hss, off_xq, off_xqs, total;
+  size_t off_hdr, off_t1, off_t2, off_hp, off_hps, off_hs, off_hss, off_xq, off_xqs, off_hb, off_hbs, total;
 
   explicit FfnLayout(const moe_cfg* c) {
     const int64_t P = pairs(c);
-    const bool f8 = c->wgt == MOE_FP8_E4M3, f4 = c->wgt == MOE_MXFP4;
+    const bool f8 = c->wgt == MOE_FP8_E4M3, f4 = c->wgt == MOE_MXFP4, i8 = c->wgt == MOE_INT8;
     const int bm4 = P <= (int64_t)kFp4RowsAvg * c->E  ? kFp4RowsBM
                                                       : kFp4LowBM;
+    const int bmi = P <= (int64_t)kInt8RowsAvg * c->E ? kInt8RowsBM : kInt8BM;
     dec = small_batch(c);
-    bm1 = f4 ? bm4 : f8 ? kFp8BM : dec ? kDecBM : kBM1;
-    bm1_alt = f4 || f8 || dec ? 0 : kBM1Alt;
+    bm1 = i8 ? bmi : f4 ? bm4 : f8 ? kFp8BM : dec ? kDecBM : kBM1;
+    bm1_alt = i8 || f4 || f8 || dec ? 0 : kBM1Alt;
     bm2_alt = 0;   // down tiles keep one height (320/256-row tiles of 8 wavefronts measured 1-2% slower)
-    bm2 = f4 ? bm4 : f8 ? kFp8BM : dec ? kDecBM : kBM2;
+    bm2 = i8 ? bmi : f4 ? bm4 : f8 ? kFp8BM : dec ? kDecBM : kBM2;
     R1 = P / bm1 + c->E;
     Rs1 = c->S > 0 ? (c->T + bm1 - 1) / bm1 : 0;
     R2 = P / bm2 + c->E;
-    if (f4) R1 = std::min(R1, P), R2 = std::min(R2, P);   // (few pairs: no more tiles than rows)
+    if (f4 || i8) R1 = std::min(R1, P), R2 = std::min(R2, P);   // (few pairs: no more tiles than rows)
     Rs2 = c->S > 0 ? (c->T + bm2 - 1) / bm2 : 0;
-    const int bnh = f4 ? kFp4BNH : f8 ? kFp8BNH : dec ? kDecBNH : kBNH;
-    const int bn2 = f4 ? kFp4BN2 : f8 ? kFp8BN2 : dec ? kDecBN2 : kBN2;
+    const int bnh = i8 ? kInt8BNH : f4 ? kFp4BNH : f8 ? kFp8BNH : dec ? kDecBNH : kBNH;
+    const int bn2 = i8 ? kInt8BN2 : f4 ? kFp4BN2 : f8 ? kFp8BN2 : dec ? kDecBN2 : kBN2;
     nt1 = (c->I + bnh - 1) / bnh;
     nt1s = ((int64_t)c->S * c->I + bnh - 1) / bnh;
     nt2 = (c->H + bn2 - 1) / bn2;
@@ -242,17 +251,20 @@ struct FfnLayout {
     off_hdr = o; o = align_up(o + 64, 256);
     off_t1 = o; o = align_up(o + (size_t)max1 * sizeof(TileDesc), 256);
     off_t2 = o; o = align_up(o + (size_t)max2 * sizeof(TileDesc), 256);
-    // h codes take 1 byte (FP8) or half a byte (MXFP4) an element; both formats keep
-    // 4 scale bytes per 128 elements (one fp32, four E8M0)
-    auto stored = [&](size_t n) { return f4 ? n / 2 : f8 ? n : n * act_bytes(c); };
-    auto scale = [&](size_t n) { return f4 || f8 ? n / 128 * 4 : 0; };
+    // h codes take 1 byte (FP8, int8) or half a byte (MXFP4) an element; FP8 and MXFP4 keep
+    // 4 scale bytes per 128 elements (one fp32, four E8M0), int8 one fp32 a row
+    auto stored = [&](size_t n) { return f4 ? n / 2 : f8 || i8 ? n : n * act_bytes(c); };
+    auto scale = [&](size_t n, size_t rows) { return i8 ? rows * 4 : f4 || f8 ? n / 128 * 4 : 0; };
     const size_t nh = (size_t)P * c->I, nhs = (size_t)c->T * c->S * c->I, nx = (size_t)c->T * c->H;
     off_hp = o; o = align_up(o + stored(nh), 256);
-    off_hps = o; o = align_up(o + scale(nh), 256);
+    off_hps = o; o = align_up(o + scale(nh, P), 256);
     off_hs = o; o = align_up(o + stored(nhs), 256);
-    off_hss = o; o = align_up(o + scale(nhs), 256);
-    off_xq = o; o = align_up(o + (f4 || f8 ? stored(nx) : 0), 256);
-    off_xqs = o; o = align_up(o + scale(nx), 256);
+    off_hss = o; o = align_up(o + scale(nhs, c->S > 0 ? c->T : 0), 256);
+    off_xq = o; o = align_up(o + (f4 || f8 || i8 ? stored(nx) : 0), 256);
+    off_xqs = o; o = align_up(o + scale(nx, c->T), 256);
+    // int8: h as the gate/up GEMM leaves it, in bf16
+    off_hb = o; o = align_up(o + (i8 ? nh * 2 : 0), 256);
+    off_hbs = o; o = align_up(o + (i8 ? nhs * 2 : 0), 256);
     total = o;
   }
 };

@@ -63,6 +63,8 @@ struct GemmParams {
   float* topk_w;            //   [T, k] out
   int G, M;                 //   expert groups, groups per token
   float route_scale;
+  bool logits;              // router: leave the logits, without the sigmoid
+  bool raw;                 // router top-k: gates not divided by their sum
   int T, H, E, S, I, k;
 };
 
@@ -394,8 +396,8 @@ __device__ __forceinline__ void gemm_tile(const GemmParams& p, bf16_t* lds, int 
           float sv = 0.f;
           if (col < ncols) {
             const float l = acc[mi][ni][r] + (p.offset ? p.offset[col] : 0.f);
-            sv = 1.0f / (1.0f + expf(-l));
-            if (out) out[row * ncols + col] = sv;
+            sv = p.logits ? l : 1.0f / (1.0f + expf(-l));
+            if (out && !p.logits) out[row * ncols + col] = sv;   // (a softmax's are left by the top-k)
           }
           sl[i * BN + col] = sv;
         }
@@ -406,7 +408,7 @@ __device__ __forceinline__ void gemm_tile(const GemmParams& p, bf16_t* lds, int 
           const int col = nt * BN + wn * NI * 32 + ni * 32 + lr;
           if (col < ncols) {
             const float l = acc[mi][ni][r] + (p.offset ? p.offset[col] : 0.f);
-            out[row * ncols + col] = 1.0f / (1.0f + expf(-l));
+            out[row * ncols + col] = p.logits ? l : 1.0f / (1.0f + expf(-l));
           }
         }
       }
@@ -471,7 +473,7 @@ __global__ __launch_bounds__(64 * kRsWaves) void router_splitk_kernel(const bf16
                                                                      const bf16_t* __restrict__ w,
                                                                      const float* __restrict__ offset,
                                                                      float* __restrict__ scores, int T, int H,
-                                                                     int E) {
+                                                                     int E, bool logits) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int NR = TM * TM / 64;       // accumulator values per lane
   constexpr int KS = 512 / TM;           // K per MFMA step (16 or 32)
@@ -509,7 +511,7 @@ __global__ __launch_bounds__(64 * kRsWaves) void router_splitk_kernel(const bf16
     const int t = t0 + i, e = e0 + l % TM;
     if (t < T && e < E) {
       const float lg = sum + (offset ? offset[e] : 0.f);
-      scores[(int64_t)t * E + e] = 1.0f / (1.0f + expf(-lg));
+      scores[(int64_t)t * E + e] = logits ? lg : 1.0f / (1.0f + expf(-lg));
     }
   }
 #endif
@@ -523,7 +525,8 @@ __global__ __launch_bounds__(64 * kRsWaves) void router_splitk_kernel(const bf16
 // so the [T, E] affinities need not be written and read back.  The GEMM part
 // adds the K slices in the order of the standalone router GEMM, so its
 // affinities, and with them the selection, are the same bit for bit.
-template <int EPL, int TOPR, int WM, int WN, int MI, int NI, int BK, int STAGES>
+// SOFTMAX: logits instead, of which the selection forms the affinities.
+template <int EPL, int TOPR, bool SOFTMAX, int WM, int WN, int MI, int NI, int BK, int STAGES>
 __global__ __launch_bounds__(64 * WM * WN) void router_topk_kernel(GemmParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int BM = WM * MI * 32, BN = WN * NI * 32;
@@ -543,8 +546,9 @@ __global__ __launch_bounds__(64 * WM * WN) void router_topk_kernel(GemmParams p)
   for (int tt = threadIdx.x / 16; tt < BM; tt += TPP) {   // the same trip count on every lane
     const bool valid = tt < rows;
     const int64_t t = row0 + (valid ? tt : 0);
-    topk16_token<EPL, TOPR>(sl + tt * BN, b, valid, p.G, p.M, p.k, p.route_scale, p.topk_idx + t * p.k,
-                            p.topk_w + t * p.k);
+    float* s_out = static_cast<float*>(p.out_routed);
+    topk16_token<EPL, TOPR, SOFTMAX>(sl + tt * BN, s_out ? s_out + t * p.E : nullptr, b, valid, p.G, p.M, p.k,
+                                     p.route_scale, p.raw, p.topk_idx + t * p.k, p.topk_w + t * p.k);
   }
 #endif
 }
@@ -606,10 +610,9 @@ bool router_topk_fusable(const moe_cfg* c) {
 template <int EPL, int TOPR>
 static void launch_router_topk_r(const moe_cfg* c, const GemmParams& p, hipStream_t st) {
   const dim3 grid((unsigned)((c->T + 63) / 64));
-  if constexpr (EPL <= 8)   // 64 tokens x 128 experts
-    hipLaunchKernelGGL((router_topk_kernel<EPL, TOPR, 2, 4, 1, 1, 64, 3>), grid, dim3(512), 0, st, p);
-  else                      // 64 tokens x 256 experts
-    hipLaunchKernelGGL((router_topk_kernel<EPL, TOPR, 2, 4, 1, 2, 64, 3>), grid, dim3(512), 0, st, p);
+  constexpr int NI = EPL <= 8 ? 1 : 2;   // 64 tokens x 128 or 256 experts
+  if (p.logits) hipLaunchKernelGGL((router_topk_kernel<EPL, TOPR, true, 2, 4, 1, NI, 64, 3>), grid, dim3(512), 0, st, p);
+  else hipLaunchKernelGGL((router_topk_kernel<EPL, TOPR, false, 2, 4, 1, NI, 64, 3>), grid, dim3(512), 0, st, p);
 }
 
 template <int EPL>
@@ -623,7 +626,8 @@ static void launch_router_topk_e(const moe_cfg* c, const GemmParams& p, hipStrea
 }
 
 moe_status launch_router_topk_bf16(const moe_cfg* c, const bf16_t* x, const bf16_t* w_router, const float* offset,
-                                   const float* bias, float* scores, int32_t* idx, float* w, hipStream_t st) {
+                                   const float* bias, float* scores, uint32_t flags, int32_t* idx, float* w,
+                                   hipStream_t st) {
   if (!router_topk_fusable(c)) return MOE_ERR_UNSUPPORTED;
   GemmParams p{};
   p.a_shared = x;
@@ -634,6 +638,8 @@ moe_status launch_router_topk_bf16(const moe_cfg* c, const bf16_t* x, const bf16
   p.topk_idx = idx;
   p.topk_w = w;
   p.G = c->G; p.M = c->M; p.route_scale = c->route_scale;
+  p.logits = flags & MOE_SOFTMAX;
+  p.raw = flags & MOE_GATES_RAW;
   p.T = c->T; p.H = c->H; p.E = c->E; p.S = c->S; p.I = c->I; p.k = c->k;
   switch (c->E / 16) {
     case 1: launch_router_topk_e<1>(c, p, st); break;
@@ -646,8 +652,9 @@ moe_status launch_router_topk_bf16(const moe_cfg* c, const bf16_t* x, const bf16
 }
 
 moe_status launch_router_bf16(const moe_cfg* c, const bf16_t* x, const bf16_t* w_router,
-                              const float* offset, float* scores, hipStream_t st) {
+                              const float* offset, float* scores, bool logits, hipStream_t st) {
   GemmParams p{};
+  p.logits = logits;
   p.a_shared = x;
   p.w_routed = w_router;
   p.offset = offset;
@@ -662,11 +669,11 @@ moe_status launch_router_bf16(const moe_cfg* c, const bf16_t* x, const bf16_t* w
   switch (router_tile(c)) {
     case kRtSplit16:
       hipLaunchKernelGGL(router_splitk_kernel<16>, dim3((unsigned)((c->T + 15) / 16), (unsigned)((c->E + 15) / 16)),
-                         dim3(64 * kRsWaves), 0, st, x, w_router, offset, scores, c->T, c->H, c->E);
+                         dim3(64 * kRsWaves), 0, st, x, w_router, offset, scores, c->T, c->H, c->E, logits);
       break;
     case kRtSplit32:
       hipLaunchKernelGGL(router_splitk_kernel<32>, dim3((unsigned)((c->T + 31) / 32), (unsigned)((c->E + 31) / 32)),
-                         dim3(64 * kRsWaves), 0, st, x, w_router, offset, scores, c->T, c->H, c->E);
+                         dim3(64 * kRsWaves), 0, st, x, w_router, offset, scores, c->T, c->H, c->E, logits);
       break;
     case kRt256: launch(RT256{}); break;
     case kRt128: launch(RT128{}); break;

@@ -497,13 +497,17 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void gemm_bwd_kernel(BwdParams p
 #endif   // __HIP_DEVICE_COMPILE__
 }
 
-// dW_r = sum over the splits of the partial sums, in split order.
+// dW_r = sum over the splits of the partial sums, in split order: n values, `stride` between the splits; second > 0:
+// and of the second terms' sums, that far behind the first.
 __global__ __launch_bounds__(256) void reduce_splits_kernel(const float* __restrict__ part, int nsplit,
-                                                            int64_t n, float* __restrict__ out) {
+                                                            int64_t n, int64_t stride, int64_t second,
+                                                            float* __restrict__ out) {
   const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (i >= n) return;
   float s = 0.f;
-  for (int k = 0; k < nsplit; ++k) s += part[(int64_t)k * n + i];
+  for (int k = 0; k < nsplit; ++k) s += part[(int64_t)k * stride + i];
+  if (second > 0)
+    for (int k = 0; k < nsplit; ++k) s += part[(int64_t)k * stride + second + i];
   out[i] = s;
 }
 
@@ -607,22 +611,23 @@ moe_status launch_ffn_bwd_bf16(const moe_cfg* c, const bf16_t* x_perm, const bf1
 }
 
 moe_status launch_router_bwd_gemms(const moe_cfg* c, const bf16_t* x, const bf16_t* w_router,
-                                   const bf16_t* dlogit, float* part, int nsplit, float* dw_router,
+                                   const bf16_t* dlogit, int Ep, int terms, float* part, int nsplit, float* dw_router,
                                    float* dx_router, hipStream_t st) {
   BwdParams p{};
-  p.T = c->T; p.H = c->H; p.E = c->E; p.S = c->S; p.I = c->I;
+  const int rows = terms * Ep;
+  p.T = c->T; p.H = c->H; p.E = rows; p.S = c->S; p.I = c->I;
   p.ksplit = kRouterKSplit;
   p.a_shared = dlogit;
   p.b_shared = x;
   p.out_routed = part;
-  const int64_t tiles = (int64_t)((c->E + kBwdBM - 1) / kBwdBM) * ((c->H + kBwdBN - 1) / kBwdBN);
+  const int64_t tiles = (int64_t)((rows + kBwdBM - 1) / kBwdBM) * ((c->H + kBwdBN - 1) / kBwdBN);
   hipLaunchKernelGGL((gemm_bwd_kernel<kDwR, MOE_BWD_TILE>), dim3((unsigned)(tiles * nsplit)), dim3(kBwdThreads),
                      0, st, p);
   moe_status s;
   if ((s = launch_status()) != MOE_OK) return s;
   const int64_t n = (int64_t)c->E * c->H;
   hipLaunchKernelGGL(reduce_splits_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, part, nsplit, n,
-                     dw_router);
+                     (int64_t)rows * c->H, terms == 2 ? (int64_t)Ep * c->H : 0, dw_router);
   if ((s = launch_status()) != MOE_OK) return s;
   if (dx_router) {
     p.b_shared = w_router;

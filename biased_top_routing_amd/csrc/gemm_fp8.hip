@@ -483,8 +483,8 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void gemm_fp8_kernel(Fp8Params p) 
 
 moe_status launch_ffn_fp8(const moe_cfg* c, const fp8_t* x_perm, const float* x_perm_scale,
                           const int32_t* perm, const int32_t* offsets, const moe_expert_weights* w,
-                          const bf16_t* x, bf16_t* y_perm, bf16_t* y_shared, void* ws, int phase,
-                          hipStream_t st) {
+                          const bf16_t* x, const fp8_t* x_codes, const float* x_scale, bf16_t* y_perm, bf16_t* y_shared,
+                          void* ws, int phase, hipStream_t st) {
   const FfnLayout L(c);
   char* base = static_cast<char*>(ws);
   const int32_t* hdr = reinterpret_cast<const int32_t*>(base + L.off_hdr);
@@ -500,12 +500,16 @@ moe_status launch_ffn_fp8(const moe_cfg* c, const fp8_t* x_perm, const float* x_
   p.T = c->T; p.H = c->H; p.E = c->E; p.S = c->S; p.I = c->I; p.k = c->k;
   if (phase == MOE_FFN_ALL || phase == MOE_FFN_GATE_UP) {
     if ((s = launch_build_tiles(c, offsets, ws, st)) != MOE_OK) return s;
-    // x once in E4M3 (1 x 128 scales): the shared experts' operand, and the
-    // routed one when its rows are gathered
-    if ((c->S > 0 || perm) && (s = launch_quantize_rows(x, c->T, c->H, xq, xqs, st)) != MOE_OK) return s;
+    // x once in E4M3 (1 x 128 scales), unless the caller has it: the shared experts'
+    // operand, and the routed one when its rows are gathered
+    if (!x_codes) {
+      if ((c->S > 0 || perm) && (s = launch_quantize_rows(x, c->T, c->H, xq, xqs, st)) != MOE_OK) return s;
+      x_codes = xq;
+      x_scale = xqs;
+    }
     p.perm = perm;
     p.a_routed = x_perm; p.sa_routed = x_perm_scale;
-    p.a_shared = xq; p.sa_shared = xqs;
+    p.a_shared = x_codes; p.sa_shared = x_scale;
     p.w_routed = (const fp8_t*)w->w_gate_up; p.sw_routed = w->w_gate_up_scale;
     p.w_shared = (const fp8_t*)w->ws_gate_up; p.sw_shared = w->ws_gate_up_scale;
     p.out_routed = hp; p.out_routed_scale = hps;

@@ -1,0 +1,77 @@
+// Symmetric int8 rows: a row with largest magnitude a stands for code * s with s = a / 127 and
+// code = the whole number nearest 127 v / a (ties to even), |code| <= 127.
+//
+// Every value quantised here is a bf16 number or the product of two, so 127 v is exact in fp32 (at
+// most 8 + 8 + 7 significant bits) and the quotient is the only rounding before the code: two values
+// would have to lie within 2^-24 of each other's quotient for that to move a code, and 16-bit numerators
+// and denominators do not.  The codes therefore do not depend on who computes them.
+#pragma once
+
+#include "common.h"
+
+namespace moe {
+
+#if defined(__HIP_DEVICE_COMPILE__)
+// |v| as an integer that orders like it; infinities and NaN from kInfBits up.
+constexpr uint32_t kInfBits = 0x7F800000u;
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+// What the codes of a row need of its largest magnitude (as bits).
+struct Int8Row {
+  float a, y, up;    // a power of two away from the largest magnitude, 1 / a, and 127 times that power
+  float scale;       // a / 127 of the row itself; 0 for a row of zeros, NaN for one with an infinity or a NaN
+  bool none;         // its codes are 0
+
+  __device__ __forceinline__ explicit Int8Row(uint32_t amax) {
+    const float m = __uint_as_float(amax);
+    none = amax == 0 || amax >= kInfBits;
+    scale = amax >= kInfBits ? __uint_as_float(0x7FC00000u) : __fdiv_rn(m, 127.0f);
+    // (the quotient is formed away from the ends of the range, where 127 v or 1 / a leave it)
+    const float p = m > 0x1p60f ? 0x1p-80f : m < 0x1p-60f ? 0x1p80f : 1.0f;
+    a = none ? 1.0f : m * p;
+    y = __fdiv_rn(1.0f, a);
+    up = none ? 0.0f : 127.0f * p;
+  }
+  // The code of v in the low byte of the result.  q = fl32(127 v / a) by one correction step (Markstein);
+  // adding 1.5 * 2^23 rounds it to a whole number, ties to even, whose two's complement ends the bits.
+  __device__ __forceinline__ uint32_t code(float v) const {
+    const float n = v * up, q0 = n * y;
+    const float q = fmaf(fmaf(-q0, a, n), y, q0);
+    return none ? 0u : __float_as_uint(q + 12582912.0f);
+  }
+  __device__ __forceinline__ uint32_t codes4(float v0, float v1, float v2, float v3) const {
+    const uint32_t lo = __builtin_amdgcn_perm(code(v1), code(v0), 0x0C0C0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(code(v3), code(v2), 0x04000C0Cu);
+    return lo | hi;
+  }
+};
+
+// 8 bf16 values of a 16-byte chunk.
+__device__ __forceinline__ void chunk_values(uint4 raw, float (&v)[8]) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ uint32_t chunk_amax(uint4 raw) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = max(m, max((w[i] << 16) & 0x7FFFFFFFu, w[i] & 0x7FFF0000u));
+  return m;
+}
+__device__ __forceinline__ uint2 chunk_codes(const Int8Row& r, uint4 raw) {
+  float v[8];
+  chunk_values(raw, v);
+  return make_uint2(r.codes4(v[0], v[1], v[2], v[3]), r.codes4(v[4], v[5], v[6], v[7]));
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t m) {
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d));
+  return m;
+}
+#endif
+
+}  // namespace moe

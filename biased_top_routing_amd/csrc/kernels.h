@@ -9,17 +9,21 @@ namespace moe {
 // grids sized by it are right for any number, and the devices of a node are alike).
 int cu_count();
 
-moe_status launch_route_topk(const moe_cfg* c, const float* scores, const float* bias, int32_t* idx,
-                             float* w, hipStream_t st);
+// The top-k of moe_route with its flags.  MOE_SOFTMAX: scores holds logits, and the affinities are left in s_out
+// (null: nowhere; it may be scores).
+moe_status launch_route_topk(const moe_cfg* c, const float* scores, float* s_out, const float* bias, uint32_t flags,
+                             int32_t* idx, float* w, hipStream_t st);
 
+// The router GEMM: sigmoid affinities, or the logits themselves.
 moe_status launch_router_bf16(const moe_cfg* c, const bf16_t* x, const bf16_t* w_router,
-                              const float* offset, float* scores, hipStream_t st);
+                              const float* offset, float* scores, bool logits, hipStream_t st);
 
-// Router GEMM + sigmoid + biased group-limited top-k + gates in one kernel
+// Router GEMM + affinities + biased group-limited top-k + gates in one kernel
 // (scores may be null); router_topk_fusable tells whether it covers c.
 bool router_topk_fusable(const moe_cfg* c);
 moe_status launch_router_topk_bf16(const moe_cfg* c, const bf16_t* x, const bf16_t* w_router, const float* offset,
-                                   const float* bias, float* scores, int32_t* idx, float* w, hipStream_t st);
+                                   const float* bias, float* scores, uint32_t flags, int32_t* idx, float* w,
+                                   hipStream_t st);
 
 // x_perm: the expert-sorted rows written by dispatch; or perm != nullptr: the
 // routed gate/up rows are gathered from x (row p = token perm[p] / k) and
@@ -36,13 +40,20 @@ moe_status launch_ffn_f32(const moe_cfg* c, const float* x_perm, const int32_t* 
 
 moe_status launch_ffn_fp8(const moe_cfg* c, const fp8_t* x_perm, const float* x_perm_scale,
                           const int32_t* perm, const int32_t* offsets, const moe_expert_weights* w,
-                          const bf16_t* x, bf16_t* y_perm, bf16_t* y_shared, void* ws, int phase,
-                          hipStream_t st);
+                          const bf16_t* x, const fp8_t* x_codes, const float* x_scale, bf16_t* y_perm, bf16_t* y_shared,
+                          void* ws, int phase, hipStream_t st);
 
 moe_status launch_ffn_fp4(const moe_cfg* c, const uint8_t* x_perm, const uint8_t* x_perm_scale,
                           const int32_t* perm, const int32_t* offsets, const moe_expert_weights* w,
                           const bf16_t* x, bf16_t* y_perm, bf16_t* y_shared, void* ws, int phase,
                           hipStream_t st);
+
+// x_codes, x_scale (here and above): x [T, H] quantised already (else null: quantised into the workspace where
+// it is needed).
+moe_status launch_ffn_int8(const moe_cfg* c, const uint8_t* x_perm, const float* x_perm_scale, const int32_t* perm,
+                           const int32_t* offsets, const moe_expert_weights* w, const bf16_t* x, const uint8_t* x_codes,
+                           const float* x_scale, bf16_t* y_perm, bf16_t* y_shared, void* ws, int phase,
+                           hipStream_t st);
 
 // Builds the tile tables of the grouped GEMMs from the per-expert offsets.
 moe_status launch_build_tiles(const moe_cfg* c, const int32_t* offsets, void* ws, hipStream_t st);
@@ -66,6 +77,10 @@ moe_status launch_build_tile_tables(const moe_cfg* c, const int32_t* offsets, in
 moe_status launch_quantize_rows(const bf16_t* src, int64_t rows, int cols, fp8_t* dst, float* scales,
                                 hipStream_t st);
 
+// Quantises rows of bf16 values to int8 with a scale a row; limit (nullable, on the device): only the first *limit.
+moe_status launch_quantize_rows_int8(const bf16_t* src, int64_t rows, int cols, const int32_t* limit, uint8_t* dst,
+                                     float* scales, hipStream_t st);
+
 // The gate/up GEMM storing its gate and up outputs (bf16, [rows, I] routed,
 // [T, S*I] shared) over a table built with the gate/up tile (kBM1 rows, kBNH
 // columns): the recomputation the backward pass starts from.
@@ -81,8 +96,9 @@ moe_status launch_ffn_bwd_bf16(const moe_cfg* c, const bf16_t* x_perm, const bf1
                                const moe_expert_weights* w, const moe_ffn_saved* saved, const bf16_t* dy_perm,
                                const bf16_t* dy, bf16_t* dx_perm, bf16_t* dx_shared, const moe_expert_grads* gr,
                                void* ws, hipStream_t st);
+// dlogit has `terms` blocks of Ep columns a row, whose sum it stands for, and w_router as many copies of Ep rows.
 moe_status launch_router_bwd_gemms(const moe_cfg* c, const bf16_t* x, const bf16_t* w_router,
-                                   const bf16_t* dlogit, float* part, int nsplit, float* dw_router,
+                                   const bf16_t* dlogit, int Ep, int terms, float* part, int nsplit, float* dw_router,
                                    float* dx_router, hipStream_t st);
 
 }  // namespace moe

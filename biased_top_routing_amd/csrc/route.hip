@@ -19,7 +19,7 @@ __global__ __launch_bounds__(256) void router_f32_kernel(const float* __restrict
                                                          const float* __restrict__ w,
                                                          const float* __restrict__ off,
                                                          float* __restrict__ scores, int T, int H,
-                                                         int E) {
+                                                         int E, bool logits) {
   const int64_t id = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (id >= (int64_t)T * E) return;
   const int t = (int)(id / E), e = (int)(id % E);
@@ -34,7 +34,7 @@ __global__ __launch_bounds__(256) void router_f32_kernel(const float* __restrict
     acc = fmaf(a.w, b.w, acc);
   }
   if (off) acc += off[e];
-  scores[id] = 1.0f / (1.0f + expf(-acc));
+  scores[id] = logits ? acc : 1.0f / (1.0f + expf(-acc));
 }
 
 // ------------------------------------------------------------------ top-k
@@ -44,11 +44,12 @@ __global__ __launch_bounds__(256) void router_f32_kernel(const float* __restrict
 //   first (one lane per group);  chosen groups = rank < M under (score desc,
 //   index asc);  then k rounds of a slice-wide max over 64-bit keys
 //   (order key of q, ~expert) restricted to the chosen groups;
-//   gates = scale * s / sum(s) over the selected experts.
-template <int EPL, int LPT>
+//   gates = scale * s / sum(s) over the selected experts (raw: scale * s).
+// SOFTMAX: `scores` holds logits, s is formed here and left in s_out (nullable; it may be `scores`).
+template <int EPL, int LPT, bool SOFTMAX>
 __global__ __launch_bounds__(256) void route_topk_kernel(
-    const float* __restrict__ scores, const float* __restrict__ bias, int T, int E, int G, int M,
-    int k, int topr, float scale, int32_t* __restrict__ idx_out, float* __restrict__ w_out) {
+    const float* scores, float* s_out, const float* __restrict__ bias, int T, int E, int G, int M,
+    int k, int topr, float scale, bool raw, int32_t* __restrict__ idx_out, float* __restrict__ w_out) {
   constexpr int TPW = kWave / LPT;   // tokens per wavefront
   constexpr int TPB = 4 * TPW;       // tokens per block
   extern __shared__ float lds[];
@@ -77,7 +78,32 @@ __global__ __launch_bounds__(256) void route_topk_kernel(
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
       const int e = sl * EPL + j;
-      s[j] = (valid && e < E) ? scores[(int64_t)t * E + e] : 0.f;
+      s[j] = (valid && e < E) ? scores[(int64_t)t * E + e] : SOFTMAX && valid ? -__builtin_huge_valf() : 0.f;
+    }
+    if constexpr (SOFTMAX) {
+      Softmax sm;
+      float m = s[0];
+#pragma unroll
+      for (int j = 1; j < EPL; ++j) m = fmaxf(m, s[j]);
+#pragma unroll
+      for (int off = LPT / 2; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
+      sm.set(m);
+      double ex[EPL], z = 0.0;
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) z += ex[j] = sm.term(s[j]);
+#pragma unroll
+      for (int off = LPT / 2; off > 0; off >>= 1) z += __shfl_xor(z, off);
+      sm.total(z);
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) {
+        s[j] = sm.share(ex[j]);
+        const int e = sl * EPL + j;
+        if (s_out && valid && e < E) s_out[(int64_t)t * E + e] = s[j];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+      const int e = sl * EPL + j;
       q[j] = s[j] + b[j];
       if (e < E) {
         q_l[e] = q[j];
@@ -148,7 +174,7 @@ __global__ __launch_bounds__(256) void route_topk_kernel(
     for (int off = LPT / 2; off > 0; off >>= 1) tot += __shfl_xor(tot, off);
     if (valid && sl < k) {
       idx_out[(int64_t)t * k + sl] = my_e;
-      w_out[(int64_t)t * k + sl] = scale * my_s / tot;
+      w_out[(int64_t)t * k + sl] = gate_of<SOFTMAX>(my_s, tot, scale, raw);
     }
     __syncthreads();   // LDS slots are reused by the next token
   }
@@ -157,10 +183,10 @@ __global__ __launch_bounds__(256) void route_topk_kernel(
 // Fast form for E = 16 * EPL with groups of whole lanes: one token per 16
 // lanes (four per wavefront), no LDS and no barrier; the per-token work is
 // topk16_token (route_topk.h), which the fused router kernel runs as well.
-template <int EPL, int TOPR>
+template <int EPL, int TOPR, bool SOFTMAX>
 __global__ __launch_bounds__(256) void route_topk16_kernel(
-    const float* __restrict__ scores, const float* __restrict__ bias, int T, int E, int G, int M,
-    int k, float scale, int32_t* __restrict__ idx_out, float* __restrict__ w_out) {
+    const float* scores, float* s_out, const float* __restrict__ bias, int T, int E, int G, int M,
+    int k, float scale, bool raw, int32_t* __restrict__ idx_out, float* __restrict__ w_out) {
   constexpr int LPT = 16;
   const int sl = threadIdx.x & (LPT - 1);
   float b[EPL];
@@ -173,59 +199,77 @@ __global__ __launch_bounds__(256) void route_topk16_kernel(
     //  token past T load nothing and store nothing)
     const bool valid = t < T;
     const int64_t tr = valid ? t : 0;
-    topk16_token<EPL, TOPR>(scores + tr * E, b, valid, G, M, k, scale, idx_out + tr * k, w_out + tr * k);
+    topk16_token<EPL, TOPR, SOFTMAX>(scores + tr * E, s_out ? s_out + tr * E : nullptr, b, valid, G, M, k, scale, raw,
+                                     idx_out + tr * k, w_out + tr * k);
   }
 }
 
+// What a top-k launch needs besides the configuration.
+struct TopkArgs {
+  const float* scores;   // affinities, or logits
+  float* s_out;          // softmax: the affinities out (nullable)
+  const float* bias;
+  bool raw;
+  int32_t* idx;
+  float* w;
+};
+
 template <int EPL, int TOPR>
-static void launch_topk16(const moe_cfg* c, const float* scores, const float* bias, int32_t* idx,
-                          float* w, hipStream_t st) {
+static void launch_topk16(const moe_cfg* c, const TopkArgs& a, bool softmax, hipStream_t st) {
   const int blocks = (int)std::min<int64_t>(((int64_t)c->T + 15) / 16, 16384);
-  hipLaunchKernelGGL((route_topk16_kernel<EPL, TOPR>), dim3(blocks), dim3(256), 0, st, scores, bias, c->T,
-                     c->E, c->G, c->M, c->k, c->route_scale, idx, w);
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(blocks), dim3(256), 0, st, a.scores, a.s_out, a.bias, c->T, c->E, c->G, c->M, c->k,
+                       c->route_scale, a.raw, a.idx, a.w);
+  };
+  if (softmax) go(route_topk16_kernel<EPL, TOPR, true>);
+  else go(route_topk16_kernel<EPL, TOPR, false>);
 }
 
 template <int EPL>
-static void launch_topk16_r(const moe_cfg* c, const float* scores, const float* bias, int32_t* idx,
-                            float* w, hipStream_t st) {
+static void launch_topk16_r(const moe_cfg* c, const TopkArgs& a, bool softmax, hipStream_t st) {
   switch (c->group_topr) {
-    case 1: launch_topk16<EPL, 1>(c, scores, bias, idx, w, st); break;
-    case 2: launch_topk16<EPL, 2>(c, scores, bias, idx, w, st); break;
-    case 3: launch_topk16<EPL, 3>(c, scores, bias, idx, w, st); break;
-    default: launch_topk16<EPL, 4>(c, scores, bias, idx, w, st); break;
+    case 1: launch_topk16<EPL, 1>(c, a, softmax, st); break;
+    case 2: launch_topk16<EPL, 2>(c, a, softmax, st); break;
+    case 3: launch_topk16<EPL, 3>(c, a, softmax, st); break;
+    default: launch_topk16<EPL, 4>(c, a, softmax, st); break;
   }
 }
 
 template <int EPL, int LPT>
-static void launch_topk(const moe_cfg* c, const float* scores, const float* bias, int32_t* idx,
-                        float* w, hipStream_t st) {
+static void launch_topk(const moe_cfg* c, const TopkArgs& a, bool softmax, hipStream_t st) {
   constexpr int TPB = 4 * (kWave / LPT);
   const int blocks = (int)std::min<int64_t>(((int64_t)c->T + TPB - 1) / TPB, 8192);
   const size_t lds = (size_t)TPB * (2 * c->E + 2 * c->G) * sizeof(float);
-  hipLaunchKernelGGL((route_topk_kernel<EPL, LPT>), dim3(blocks), dim3(256), lds, st, scores, bias,
-                     c->T, c->E, c->G, c->M, c->k, c->group_topr, c->route_scale, idx, w);
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(blocks), dim3(256), lds, st, a.scores, a.s_out, a.bias, c->T, c->E, c->G, c->M,
+                       c->k, c->group_topr, c->route_scale, a.raw, a.idx, a.w);
+  };
+  if (softmax) go(route_topk_kernel<EPL, LPT, true>);
+  else go(route_topk_kernel<EPL, LPT, false>);
 }
 
-moe_status launch_route_topk(const moe_cfg* c, const float* scores, const float* bias, int32_t* idx,
-                             float* w, hipStream_t st) {
+moe_status launch_route_topk(const moe_cfg* c, const float* scores, float* s_out, const float* bias, uint32_t flags,
+                             int32_t* idx, float* w, hipStream_t st) {
+  const TopkArgs a{scores, s_out, bias, (flags & MOE_GATES_RAW) != 0, idx, w};
+  const bool softmax = flags & MOE_SOFTMAX;
   if (topk16_fits(c)) {
     switch (c->E / 16) {
-      case 1: launch_topk16_r<1>(c, scores, bias, idx, w, st); break;
-      case 2: launch_topk16_r<2>(c, scores, bias, idx, w, st); break;
-      case 4: launch_topk16_r<4>(c, scores, bias, idx, w, st); break;
-      case 8: launch_topk16_r<8>(c, scores, bias, idx, w, st); break;
-      case 16: launch_topk16_r<16>(c, scores, bias, idx, w, st); break;
+      case 1: launch_topk16_r<1>(c, a, softmax, st); break;
+      case 2: launch_topk16_r<2>(c, a, softmax, st); break;
+      case 4: launch_topk16_r<4>(c, a, softmax, st); break;
+      case 8: launch_topk16_r<8>(c, a, softmax, st); break;
+      case 16: launch_topk16_r<16>(c, a, softmax, st); break;
       default: goto general;
     }
     return launch_status();
   }
 general:
-  if (c->E <= 16) launch_topk<1, 16>(c, scores, bias, idx, w, st);
-  else if (c->E <= 32) launch_topk<1, 32>(c, scores, bias, idx, w, st);
-  else if (c->E <= 64) launch_topk<1, 64>(c, scores, bias, idx, w, st);
-  else if (c->E <= 128) launch_topk<2, 64>(c, scores, bias, idx, w, st);
-  else if (c->E <= 256) launch_topk<4, 64>(c, scores, bias, idx, w, st);
-  else launch_topk<8, 64>(c, scores, bias, idx, w, st);
+  if (c->E <= 16) launch_topk<1, 16>(c, a, softmax, st);
+  else if (c->E <= 32) launch_topk<1, 32>(c, a, softmax, st);
+  else if (c->E <= 64) launch_topk<1, 64>(c, a, softmax, st);
+  else if (c->E <= 128) launch_topk<2, 64>(c, a, softmax, st);
+  else if (c->E <= 256) launch_topk<4, 64>(c, a, softmax, st);
+  else launch_topk<8, 64>(c, a, softmax, st);
   return launch_status();
 }
 
@@ -239,8 +283,9 @@ extern "C" moe_status moe_route(const moe_cfg* cfg, const void* x, const void* w
                                 void* stream) {
   moe_status st = validate_cfg(cfg);
   if (st != MOE_OK) return st;
-  if (flags & ~MOE_SCORES_IN) return MOE_ERR_UNSUPPORTED;
-  const bool scores_in = flags & MOE_SCORES_IN;
+  if (flags & ~(MOE_SCORES_IN | MOE_SOFTMAX | MOE_GATES_RAW)) return MOE_ERR_UNSUPPORTED;
+  const bool scores_in = flags & MOE_SCORES_IN, softmax = flags & MOE_SOFTMAX;
+  if (scores_in && softmax) return MOE_ERR_UNSUPPORTED;
   if (!bias || !topk_idx || !topk_w) return MOE_ERR_NULL;
   if (scores_in && !scores) return MOE_ERR_NULL;
   if (!scores_in && (!x || !w_router)) return MOE_ERR_NULL;
@@ -252,19 +297,19 @@ extern "C" moe_status moe_route(const moe_cfg* cfg, const void* x, const void* w
   hipStream_t s = as_stream(stream);
   if (!scores_in && router_topk_fusable(cfg))
     return launch_router_topk_bf16(cfg, (const bf16_t*)x, (const bf16_t*)w_router, logit_offset, bias, scores,
-                                   topk_idx, topk_w, s);
+                                   flags, topk_idx, topk_w, s);
   float* sc = scores ? scores : static_cast<float*>(ws);
   if (!scores_in) {
     if (cfg->act == MOE_F32) {
       const int64_t n = (int64_t)cfg->T * cfg->E;
       hipLaunchKernelGGL(router_f32_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s,
                          (const float*)x, (const float*)w_router, logit_offset, sc, cfg->T,
-                         cfg->H, cfg->E);
+                         cfg->H, cfg->E, softmax);
       if ((st = launch_status()) != MOE_OK) return st;
     } else {
-      st = launch_router_bf16(cfg, (const bf16_t*)x, (const bf16_t*)w_router, logit_offset, sc, s);
+      st = launch_router_bf16(cfg, (const bf16_t*)x, (const bf16_t*)w_router, logit_offset, sc, softmax, s);
       if (st != MOE_OK) return st;
     }
   }
-  return launch_route_topk(cfg, sc, bias, topk_idx, topk_w, s);
+  return launch_route_topk(cfg, sc, softmax ? scores : nullptr, bias, flags, topk_idx, topk_w, s);
 }

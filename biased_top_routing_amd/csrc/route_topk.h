@@ -32,6 +32,46 @@ __device__ __forceinline__ float dpp_f32(float v) {
   return __uint_as_float(dpp_u32<CTRL>(__float_as_uint(v)));
 }
 
+// Sum and maximum over the 16 lanes of a token, the same on each of them.
+__device__ __forceinline__ float max16(float v) {
+  v = fmaxf(v, dpp_f32<kDppXor1>(v));
+  v = fmaxf(v, dpp_f32<kDppXor2>(v));
+  v = fmaxf(v, dpp_f32<kDppHalfMirror>(v));
+  return fmaxf(v, dpp_f32<kDppMirror>(v));
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp_f64(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint64_t lo = dpp_u32<CTRL>((uint32_t)u), hi = dpp_u32<CTRL>((uint32_t)(u >> 32));
+  return __builtin_bit_cast(double, hi << 32 | lo);
+}
+__device__ __forceinline__ double sum16(double v) {
+  v += dpp_f64<kDppXor1>(v);
+  v += dpp_f64<kDppXor2>(v);
+  v += dpp_f64<kDppHalfMirror>(v);
+  return v + dpp_f64<kDppMirror>(v);
+}
+
+// Softmax of a token's logits, one affinity at a time: e^(l - top) over their sum.  The exponentials, their sum and
+// the quotient are formed in 64 bits and rounded once to fp32, so that affinities that differ keep their order and
+// do not depend on who computes them.  (T = 16384, E = 256: 4 million exponentials, some 4 us of the chip.)
+struct Softmax {
+  double top, inv;
+  // top and the sum over the token's logits, alike on all of its lanes
+  __device__ __forceinline__ void set(float m) { top = m == -__builtin_huge_valf() ? 0.0 : (double)m; }
+  __device__ __forceinline__ double term(float l) const { return exp((double)l - top); }
+  __device__ __forceinline__ void total(double z) { inv = z > 0.0 ? 1.0 / z : 0.0; }   // (all logits -inf: 0 everywhere)
+  __device__ __forceinline__ float share(double e) const { return (float)(e * inv); }
+};
+
+// The gate of a selected expert: its affinity, over the sum of the selected ones unless it is to stay raw.
+template <bool SOFTMAX>
+__device__ __forceinline__ float gate_of(float s, float total, float scale, bool raw) {
+  if (raw) return scale * s;
+  if (SOFTMAX && total == 0.f) return 0.f;   // (every selected expert masked)
+  return scale * s / total;
+}
+
 // Merge the partner's top-R list into this lane's (both descending).
 template <int CTRL, int R>
 __device__ __forceinline__ void merge_step(float (&top)[R]) {
@@ -65,9 +105,11 @@ __device__ __forceinline__ void merge_step(float (&top)[R]) {
 //   entry;  gates = scale * s / sum(s) over the winners, s read back from row.
 // Lane sl < k writes slot sl of idx_out / w_out (the token's output rows)
 // when `valid`; an invalid token's lanes only take part in the cross-lane moves.
-template <int EPL, int TOPR>
-__device__ __forceinline__ void topk16_token(const float* row, const float (&b)[EPL], bool valid, int G,
-                                             int M, int k, float scale, int32_t* idx_out, float* w_out) {
+// SOFTMAX: `row` holds logits, and the affinities are formed here (and left in s_out, unless it is null; it may be
+// row itself: the lanes of a token run in step, and every logit has been read by then).
+template <int EPL, int TOPR, bool SOFTMAX>
+__device__ __forceinline__ void topk16_token(const float* row, float* s_out, const float (&b)[EPL], bool valid, int G,
+                                             int M, int k, float scale, bool raw, int32_t* idx_out, float* w_out) {
   constexpr int LPT = 16;
   const int lane = threadIdx.x & (kWave - 1);
   const int sl = lane & (LPT - 1);
@@ -86,6 +128,19 @@ __device__ __forceinline__ void topk16_token(const float* row, const float (&b)[
   } else {
 #pragma unroll
     for (int j = 0; j < EPL; ++j) s[j] = valid ? mine[j] : 0.f;
+  }
+  Softmax sm;
+  if constexpr (SOFTMAX) {
+    float m = s[0];
+#pragma unroll
+    for (int j = 1; j < EPL; ++j) m = fmaxf(m, s[j]);
+    sm.set(max16(m));
+    double e[EPL], z = 0.0;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) z += e[j] = sm.term(s[j]);
+    sm.total(sum16(z));
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) s[j] = sm.share(e[j]);
   }
 #pragma unroll
   for (int j = 0; j < EPL; ++j) q[j] = s[j] + b[j];
@@ -145,7 +200,15 @@ __device__ __forceinline__ void topk16_token(const float* row, const float (&b)[
     for (int j = 0; j < EPL; ++j) key[j] = j == jw ? 0u : key[j];
     if (sl == r) my_e = (int)we;
   }
-  const float my_s = (valid && sl < k) ? row[my_e] : 0.f;
+  float my_s = (valid && sl < k) ? row[my_e] : 0.f;
+  if constexpr (SOFTMAX) {
+    if (valid && sl < k) my_s = sm.share(sm.term(my_s));
+    __builtin_amdgcn_wave_barrier();
+    if (valid && s_out) {
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) s_out[sl * EPL + j] = s[j];
+    }
+  }
   float tot = my_s;
   tot += dpp_f32<kDppXor1>(tot);
   tot += dpp_f32<kDppXor2>(tot);
@@ -153,7 +216,7 @@ __device__ __forceinline__ void topk16_token(const float* row, const float (&b)[
   tot += dpp_f32<kDppMirror>(tot);
   if (valid && sl < k) {
     idx_out[sl] = my_e;
-    w_out[sl] = scale * my_s / tot;
+    w_out[sl] = gate_of<SOFTMAX>(my_s, tot, scale, raw);
   }
 }
 

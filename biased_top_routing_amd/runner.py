@@ -20,6 +20,13 @@ way y (and dx) is this share's sum; the bias update needs the loads of the whole
 batch, so gamma is refused.  The shares of the ranks add up to the layer when what
 every rank could compute is given to one of them: the shared experts (the others'
 cfg has S = 0) and the balance loss (adds_balance=True; the others pass alpha = 0).
+
+With norm=w [H] the layer begins with a root-mean-square norm (moe_norm):
+forward(x, residual=r) adds r to x (the sum stays in .h, for the next block's
+residual), norms it, and routes and runs the experts on the result; with
+gather=True int8 and FP8 experts take their rows as the norm's codes
+(moe_expert_ffn_codes).  backward(dh=...) goes through the norm too.
+softmax=True and raw_gates=True are moe_route's MOE_SOFTMAX and MOE_GATES_RAW.
 """
 from __future__ import annotations
 
@@ -40,9 +47,14 @@ def to_device(arr, device="cuda"):
 
 
 class MoeLayerGPU:
+    norm = residual = graph_residual = codes = code_scale = None
+    route_flags = 0
+
     def __init__(self, cfg, weights, T=None, device="cuda", gather=False, save_gu=False, keep_scores=True, share=None,
-                 adds_balance=False):
+                 adds_balance=False, norm=None, eps=1e-6, softmax=False, raw_gates=False):
         self.c = cfg
+        self.route_flags = (L.MOE_SOFTMAX if softmax else 0) | (L.MOE_GATES_RAW if raw_gates else 0)
+        self.eps = eps
         self.share = share
         first, self.n_exp = (0, cfg.E) if share is None else (int(share[0]), int(share[1]))
         self.adds_balance = adds_balance or self.n_exp == cfg.E
@@ -58,15 +70,19 @@ class MoeLayerGPU:
         self.keep_scores = keep_scores
         self.fp8 = cfg.wgt == "fp8_e4m3"
         self.fp4 = cfg.wgt == "mxfp4"
+        self.int8 = cfg.wgt == "int8"
         self.act_dtype = torch.float32 if cfg.act == "f32" else torch.bfloat16
         dev = lambda a: to_device(a, device)
         self.w_router = dev(weights.w_router)
         self.logit_offset = dev(weights.logit_offset)
-        if self.fp8 or self.fp4:
+        self.norm = dev(norm) if isinstance(norm, np.ndarray) else norm
+        if self.norm is not None and (self.norm.shape != (cfg.H,) or self.norm.dtype != self.act_dtype):
+            raise ValueError(f"norm is a weight of {cfg.H} values of {self.act_dtype}")
+        if self.fp8 or self.fp4 or self.int8:
             self.w_gate_up, self.w_gate_up_scale = self._quantize(weights.w_gate_up[held])
             self.w_down, self.w_down_scale = self._quantize(weights.w_down[held])
             self.ws_gate_up, self.ws_gate_up_scale = self._quantize(weights.ws_gate_up)
-            self.ws_down, self.ws_down_scale = self._quantize(weights.ws_down)
+            self.ws_down, self.ws_down_scale = self._quantize(weights.ws_down, joint=True)
         else:
             self.w_gate_up, self.w_down = dev(weights.w_gate_up[held]), dev(weights.w_down[held])
             self.ws_gate_up, self.ws_down = dev(weights.ws_gate_up), dev(weights.ws_down)
@@ -76,10 +92,20 @@ class MoeLayerGPU:
                                         self.ws_down_scale)
         self.alloc(cfg.T if T is None else T)
 
-    def _quantize(self, w_np):
+    def _quantize(self, w_np, joint=False):
         """bf16 weights [n, rows, cols] -> E4M3 codes + one fp32 scale per 128 x 128 block, or MXFP4 codes
-        [n, rows, cols/2] + scale bytes [n, cols/128, rows, 4] (on the GPU)."""
+        [n, rows, cols/2] + scale bytes [n, cols/128, rows, 4], or int8 codes + one fp32 scale a row [n, rows]
+        (joint: [rows], over all n matrices) (on the GPU)."""
         n, rows, cols = w_np.shape
+        if self.int8:
+            codes = torch.empty((n, rows, cols), dtype=torch.int8, device=self.device)
+            scales = torch.empty((rows,) if joint else (n, rows), dtype=torch.float32, device=self.device)
+            if n:
+                src = to_device(w_np, self.device)
+                L.moe_quantize_int8(src, n, rows, cols, n if joint else 1, codes, scales)
+                torch.cuda.current_stream().synchronize()
+                del src
+            return codes, scales
         if self.fp4:
             codes = torch.empty((n, rows, cols // 2), dtype=torch.uint8, device=self.device)
             scales = torch.empty((n, cols // 128, rows, 4), dtype=torch.uint8, device=self.device)
@@ -121,6 +147,9 @@ class MoeLayerGPU:
         elif self.fp4:
             self.x_perm = torch.empty((P, c.H // 2), dtype=torch.uint8, device=d)
             self.x_perm_scale = torch.empty((c.H // 128, P, 4), dtype=torch.uint8, device=d)
+        elif self.int8:
+            self.x_perm = torch.empty((P, c.H), dtype=torch.int8, device=d)
+            self.x_perm_scale = torch.empty(P, dtype=f32, device=d)
         elif self.fp8:
             self.x_perm = torch.empty((P, c.H), dtype=torch.uint8, device=d)
             self.x_perm_scale = torch.empty((P, c.H // 128), dtype=f32, device=d)
@@ -133,6 +162,14 @@ class MoeLayerGPU:
         self.ws_dispatch = torch.empty(L.moe_workspace_bytes(self.cfg_x, L.MOE_WS_DISPATCH), dtype=torch.uint8,
                                        device=d)
         self.ws_ffn = torch.empty(L.moe_workspace_bytes(self.cfg_x, L.MOE_WS_FFN), dtype=torch.uint8, device=d)
+        self.codes = self.code_scale = None
+        if self.norm is not None:
+            # (zero: the rows behind the live tokens of a padded batch are not written)
+            self.h = torch.zeros((T, c.H), dtype=self.act_dtype, device=d)
+            self.xn = torch.zeros((T, c.H), dtype=self.act_dtype, device=d)
+            if self.gather and (self.int8 or self.fp8):
+                self.codes = torch.zeros((T, c.H), dtype=torch.int8 if self.int8 else torch.uint8, device=d)
+                self.code_scale = torch.zeros((T,) if self.int8 else (T, c.H // 128), dtype=f32, device=d)
         if self.save_gu:
             bf = torch.bfloat16
             self.g = torch.empty((P, c.I), dtype=bf, device=d)
@@ -142,11 +179,18 @@ class MoeLayerGPU:
             self.saved = L.ffn_saved(self.g, self.u, self.gs, self.us)
 
     # ---------------------------------------------------------------- the five calls
+    def add_and_norm(self, x, residual=None):
+        """The norm in front of the layer: self.h = x + residual (h = x without one), returns the normed rows."""
+        self.residual = residual
+        L.moe_norm(self.cfg, self.n_tokens, x, residual, self.norm, self.eps, None if residual is None else self.h,
+                   self.xn, self.codes, self.code_scale)
+        return self.xn
+
     def route(self, x, bias, scores_in=False):
         keep = self.keep_scores or scores_in
+        flags = self.route_flags & ~L.MOE_SOFTMAX | L.MOE_SCORES_IN if scores_in else self.route_flags
         L.moe_route(self.cfg, x, self.w_router, self.logit_offset, bias, self.scores if keep else None,
-                    L.MOE_SCORES_IN if scores_in else 0, self.topk_idx, self.topk_w,
-                    None if keep else self.ws_route)
+                    flags, self.topk_idx, self.topk_w, None if keep else self.ws_route)
 
     @property
     def partial(self):
@@ -166,6 +210,9 @@ class MoeLayerGPU:
         if self.save_gu:
             L.moe_expert_ffn_save(self.cfg_x, self.x_perm, self.perm, self.offsets, self.weights, x, self.y_perm,
                                   self.y_shared, self.saved, self.ws_ffn, phase)
+        elif self.codes is not None:
+            L.moe_expert_ffn_codes(self.cfg_x, self.codes, self.code_scale, self.perm, self.offsets, self.weights,
+                                   self.y_perm, self.y_shared, self.ws_ffn, phase)
         elif self.gather:
             L.moe_expert_ffn_gather(self.cfg_x, x, self.perm, self.offsets, self.weights, self.y_perm,
                                     self.y_shared, self.ws_ffn, phase)
@@ -202,15 +249,24 @@ class MoeLayerGPU:
         self.loss_bal = torch.empty(1, dtype=f32, device=d)
         self.grads = L.expert_grads(self.g_w_gate_up, self.g_w_down, self.g_ws_gate_up, self.g_ws_down)
         self.ws_ffn_bwd = torch.empty(L.moe_workspace_bytes(self.cfg_x, L.MOE_WS_FFN_BWD), dtype=torch.uint8, device=d)
-        self.ws_route_bwd = torch.empty(L.moe_workspace_bytes(self.cfg, L.MOE_WS_ROUTE_BWD), dtype=torch.uint8,
-                                        device=d)
+        kind = L.MOE_WS_ROUTE_BWD_SOFTMAX if self.route_flags else L.MOE_WS_ROUTE_BWD
+        self.ws_route_bwd = torch.empty(L.moe_workspace_bytes(self.cfg, kind), dtype=torch.uint8, device=d)
+        if self.norm is not None:
+            self.dx_in = torch.empty((T, c.H), dtype=bf, device=d)
+            self.g_norm = torch.empty(c.H, dtype=f32, device=d)
+            self.ws_norm_bwd = torch.empty(L.moe_workspace_bytes(self.cfg, L.MOE_WS_NORM_BWD), dtype=torch.uint8,
+                                           device=d)
         self._bwd_T = T
 
-    def backward(self, x, dy, alpha=0.0, seq_len=0):
+    def backward(self, x, dy, alpha=0.0, seq_len=0, dh=None):
         """Gradients of sum(dy * y) + alpha-weighted sequence balance loss for the last forward pass
         (same x, same routing).  Fills dx, the fp32 weight gradients and loss_bal; returns dx.
         Of a padded batch (n_tokens still holds its live count) they are the live tokens' gradients:
-        what lies in the padded rows of x and dy takes no part, and those of dx are zero."""
+        what lies in the padded rows of x and dy takes no part, and those of dx are zero.
+        With a norm dx is the gradient of x and of the residual, dh (or None) the one that reaches their sum from
+        elsewhere, and g_norm the norm weight's."""
+        if dh is not None and self.norm is None:
+            raise ValueError("dh is the gradient of the norm's input sum: the layer has no norm")
         if self.gather:
             raise ValueError("backward reads the permuted rows x_perm: build the layer with gather=False")
         if self.n_tokens is not None and alpha:
@@ -221,6 +277,9 @@ class MoeLayerGPU:
         if getattr(self, "_bwd_T", None) != self.T:
             self.alloc_backward()
         cfg = self.cfg_x
+        h = x if self.residual is None else self.h        # the norm's input
+        if self.norm is not None:
+            x = self.xn
         combine_backward = L.moe_combine_local_backward if self.partial else L.moe_combine_backward
         dispatch_backward = L.moe_dispatch_local_backward if self.partial else L.moe_dispatch_backward
         combine_backward(cfg, dy, self.y_perm, self.inv, self.topk_w, self.dy_perm, self.d_topk_w)
@@ -233,10 +292,19 @@ class MoeLayerGPU:
         else:
             L.moe_expert_ffn_backward(cfg, self.x_perm, x, self.offsets, self.weights, self.dy_perm, dy,
                                       self.dx_perm, self.dx_shared, self.grads, self.ws_ffn_bwd)
-        L.moe_route_backward(self.cfg, x, self.w_router, scores, self.topk_idx, self.d_topk_w, alpha, seq_len,
-                             self.dx_router, self.g_w_router, self.loss_bal, self.ws_route_bwd)
+        if self.route_flags:
+            L.moe_route_backward_flags(self.cfg, self.route_flags, x, self.w_router, scores, self.topk_idx, self.d_topk_w,
+                                       alpha, seq_len, self.dx_router, self.g_w_router, self.loss_bal,
+                                       self.ws_route_bwd)
+        else:
+            L.moe_route_backward(self.cfg, x, self.w_router, scores, self.topk_idx, self.d_topk_w, alpha, seq_len,
+                                 self.dx_router, self.g_w_router, self.loss_bal, self.ws_route_bwd)
         dispatch_backward(cfg, self.dx_perm, self.dx_shared, self.dx_router, self.inv, self.dx)
-        return self.dx
+        if self.norm is None:
+            return self.dx
+        L.moe_norm_backward(self.cfg, self.n_tokens, h, self.norm, self.eps, self.dx, dh, self.dx_in, self.g_norm,
+                            self.ws_norm_bwd)
+        return self.dx_in
 
     def _without_padding(self, x, dy):
         """x, dy and the affinities with rows for the padded tokens that add exactly nothing.  The router's and the
@@ -252,12 +320,15 @@ class MoeLayerGPU:
         scores = None if self.scores is None else self.scores.masked_fill(pad, 0.5)
         return x[:self.T].masked_fill(pad, 0), dy, scores
 
-    def forward(self, x, bias, gamma=None, scores_in=False, n_tokens=None):
+    def forward(self, x, bias, gamma=None, scores_in=False, n_tokens=None, residual=None):
         """One batch through the layer; with gamma set, bias is updated in place afterwards.
         n_tokens: int32 device tensor of one element, the live tokens of a padded batch; y of a padded token is the
-        shared experts' output for whatever its row of x holds."""
-        self._check_batch(gamma, n_tokens)
+        shared experts' output for whatever its row of x holds.
+        residual: [T, H], added to x before the norm (layers with a norm)."""
+        self._check_batch(gamma, n_tokens, residual)
         self.n_tokens = n_tokens
+        if self.norm is not None:
+            x = self.add_and_norm(x, residual)
         self.route(x, bias, scores_in)
         self.dispatch(x)
         self.expert_ffn(x)
@@ -266,35 +337,38 @@ class MoeLayerGPU:
             self.update_bias(bias, gamma)
         return self.y
 
-    def _check_batch(self, gamma, n_tokens):
+    def _check_batch(self, gamma, n_tokens, residual=None):
         """Refuses what forward() cannot run, before anything is launched."""
         L.live_count(n_tokens)
+        if residual is not None and self.norm is None:
+            raise ValueError("a residual is added before the norm: the layer has none")
         if gamma is not None and (self.share is not None or n_tokens is not None):
             raise ValueError("the bias update needs the loads of a whole batch over every expert")
 
     # ---------------------------------------------------------------- HIP graph
-    def capture(self, x, bias, gamma=None, n_tokens=None):
+    def capture(self, x, bias, gamma=None, n_tokens=None, residual=None):
         """Record one forward() over the tensors x and bias (and the bias update when
-        gamma is set) into a HIP graph; replay() reruns it on whatever they (and n_tokens) then hold.
+        gamma is set) into a HIP graph; replay() reruns it on whatever they (and n_tokens and residual) then hold.
         One graph serves every batch of this T: each launch is sized by capacity (the
         grouped GEMMs' tile tables are built on the device from the batch's routing)
         and no call allocates, copies or synchronises, so the recorded work is the
         same kernels forward() launches.  A warm-up pass (no bias update) on a side
         stream precedes the capture."""
-        self._check_batch(gamma, n_tokens)
+        self._check_batch(gamma, n_tokens, residual)
         side = torch.cuda.Stream()
         side.wait_stream(torch.cuda.current_stream())
         with torch.cuda.stream(side):
-            self.forward(x, bias, None, n_tokens=n_tokens)
+            self.forward(x, bias, None, n_tokens=n_tokens, residual=residual)
         torch.cuda.current_stream().wait_stream(side)
         self.graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(self.graph):
-            self.forward(x, bias, gamma, n_tokens=n_tokens)
-        self.graph_inputs = (x, bias, n_tokens)
+            self.forward(x, bias, gamma, n_tokens=n_tokens, residual=residual)
+        self.graph_inputs, self.graph_residual = (x, bias, n_tokens), residual
         return self.graph
 
     def replay(self):
         """One replay of the captured step on the current stream; returns y."""
         self.n_tokens = self.graph_inputs[2]     # backward() then takes the pairs that the graph's batch has
+        self.residual = self.graph_residual
         self.graph.replay()
         return self.y

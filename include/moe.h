@@ -23,6 +23,11 @@
  *    tensors pass through the `float*` scale arguments and members.  Codes,
  *    rows and workspaces must be 16-byte aligned and scale bytes 4-byte aligned
  *    (MOE_ERR_UNSUPPORTED otherwise).
+ *  - int8 matrices [rows, cols] are two tensors: codes [rows, cols] and one fp32
+ *    scale a row; row r stands for code * scale[r].  (A token's activations have one
+ *    scale, and so has an output channel of a weight matrix, whose rows are the
+ *    output channels.)  Codes, rows and workspaces must be 16-byte aligned and scales
+ *    4-byte aligned (MOE_ERR_UNSUPPORTED otherwise).
  *  - Every call validates all sizes and pointers on the host BEFORE touching the
  *    device and returns a negative moe_status on error (nothing is launched).  A
  *    failed launch returns MOE_ERR_LAUNCH.  Work is asynchronous on `stream`
@@ -57,7 +62,7 @@ typedef enum {
   MOE_ERR_SCRATCH = -6      /* sizes exceed the fixed scratch of a no-allocation entry point */
 } moe_status;
 
-typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_FP8_E4M3 = 2, MOE_MXFP4 = 3 } moe_dtype;
+typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_FP8_E4M3 = 2, MOE_MXFP4 = 3, MOE_INT8 = 4 } moe_dtype;
 
 /*
  * Layer configuration.
@@ -68,8 +73,8 @@ typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_FP8_E4M3 = 2, MOE_MXFP4 = 3 } moe_
  *              scores, added from the largest down (1 <= group_topr <= E/G, <= 8).
  *  route_scale: gates are route_scale * s_j / sum(s) over the selected experts.
  *  act / wgt (moe_dtype): (F32, F32) | (BF16, BF16) | (BF16, FP8_E4M3) |
- *              (BF16, MXFP4).  The router always runs in `act` precision;
- *              FP8_E4M3 and MXFP4 apply to the expert GEMMs only.
+ *              (BF16, MXFP4) | (BF16, INT8).  The router always runs in `act`
+ *              precision; FP8_E4M3, MXFP4 and INT8 apply to the expert GEMMs only.
  *  bias_eq_mode: 0 - an expert whose load equals T*k/E counts as underloaded
  *              (+gamma), so every bias moves each step; 1 - it is left unchanged.
  * Supported ranges (every call checks them first and returns MOE_ERR_SHAPE
@@ -82,7 +87,9 @@ typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_FP8_E4M3 = 2, MOE_MXFP4 = 3 } moe_
  *  grouped GEMMs count their tiles in 32 bits).  F32: H % 4 == 0, I % 4 == 0;
  *  BF16 experts: H % 64 == 0, I % 128 == 0; FP8 experts: H % 128 == 0,
  *  I % 128 == 0, H <= 8192 and max(S, 1)*I <= 8192 (64 scale blocks of K); MXFP4
- *  experts: H % 128 == 0, I % 128 == 0, T*k*max(H, I) and T*max(H, S*I) under 2^36.
+ *  experts: H % 128 == 0, I % 128 == 0, T*k*max(H, I) and T*max(H, S*I) under 2^36;
+ *  INT8 experts: H % 128 == 0, I % 128 == 0, H and max(S, 1)*I under 2^17 (sums in
+ *  32 bits), T*k under 2^26.
  */
 typedef struct {
   int32_t T, H, E, G, M, k, S, I;
@@ -95,6 +102,8 @@ typedef struct {
 
 /* moe_route flags */
 #define MOE_SCORES_IN 1u /* `scores` is an input: route on these fp32 affinities, skip the router GEMM */
+#define MOE_SOFTMAX 2u   /* affinities softmax(x w_router^T + o) over the E experts, in place of the sigmoid */
+#define MOE_GATES_RAW 4u /* gates route_scale * s_j, not divided by the sum over the selected experts */
 
 /*
  * moe_route - affinity and biased, group-limited top-k with gates.
@@ -134,6 +143,15 @@ typedef struct {
  * The router GEMM sums in a fixed order per batch size (repeated calls give
  * identical bits); small and large batches use different kernels, so the last
  * bits of a token's affinities can depend on T.
+ * MOE_SOFTMAX: the logits l = x w_router^T + o are fp32 numbers, the softmax over them
+ * is formed in 64 bits and rounded once to fp32: equal logits rank alike wherever they
+ * are computed, and affinities that differ keep their order.  An expert with l = -inf has
+ * s = 0 (a mask: an offset of -inf takes it out of service, though it may be selected
+ * where fewer than k others are allowed); a token whose logits are all -inf has s = 0
+ * everywhere.  Gates of a token whose selected affinities are all 0 are 0.  Logits of
+ * +inf or NaN give unspecified results.
+ * MOE_SOFTMAX cannot be combined with MOE_SCORES_IN (the affinities are there;
+ * MOE_ERR_UNSUPPORTED); MOE_GATES_RAW goes with all.
  * MOE_ERR_WORKSPACE: scores is NULL and ws is NULL or too small.
  */
 moe_status moe_route(const moe_cfg* cfg, const void* x, const void* w_router,
@@ -159,11 +177,12 @@ moe_status moe_route(const moe_cfg* cfg, const void* x, const void* w_router,
  *  inv       [T, k] int32 out: row of pair (t, j) in the permuted order
  *  x_perm    [T*k, H] out: row p = x[perm[p] / k]; act dtype, or E4M3 bytes when
  *            wgt == FP8_E4M3 (quantised per 1x128 tile: sc = amax/448, q = e4m3(v/sc)),
- *            or MXFP4 codes [T*k, H/2] (quantised as by moe_quantize_fp4).
+ *            or MXFP4 codes [T*k, H/2] (quantised as by moe_quantize_fp4), or int8
+ *            codes [T*k, H] (as by moe_quantize_int8).
  *            NULL: only counts, offsets, perm and inv are written (x and
  *            x_perm_scale may then be NULL too), for moe_expert_ffn_gather.
  *  x_perm_scale [T*k, H/128] fp32 out (FP8), scale bytes [H/128, T*k, 4] out
- *            (MXFP4), else NULL
+ *            (MXFP4), [T*k] fp32 out (INT8), else NULL
  *  ws, ws_bytes  workspace of at least moe_workspace_bytes(cfg, MOE_WS_DISPATCH)
  */
 moe_status moe_dispatch(const moe_cfg* cfg, const int32_t* topk_idx, const void* x,
@@ -196,7 +215,9 @@ moe_status moe_dispatch_noalloc(const moe_cfg* cfg, const int32_t* topk_idx, con
  * tensors hold E4M3 bytes, one fp32 scale per 128 x 128 block) or MXFP4 (each
  * expert's matrix as codes and scale bytes: w_gate_up [E, 2I, H/2] with
  * [E, H/128, 2I, 4], w_down [E, H, I/2] with [E, I/128, H, 4], alike for the
- * shared ones). */
+ * shared ones) or INT8 (codes of the weights' shapes, scales w_gate_up_scale [E, 2I],
+ * w_down_scale [E, H], ws_gate_up_scale [S, 2I] and ws_down_scale [H]: the shared experts
+ * are one FFN of S*I columns, whose W_d has one scale an output channel). */
 typedef struct {
   const void* w_gate_up;         /* [E, 2I, H]: gate rows [0, I), up rows [I, 2I) */
   const void* w_down;            /* [E, H, I] */
@@ -235,7 +256,9 @@ typedef struct {
  * Intermediates are rounded to the activation dtype (bf16) or, for FP8, to E4M3
  * per 1x128 tile of each row, or, for MXFP4, to E2M1 per 32 columns of each row
  * (as by moe_quantize_fp4, from the fp32 values); accumulation is fp32.  MXFP4
- * quantises x for the shared experts in the same way.
+ * quantises x for the shared experts in the same way.  INT8 rounds h to bf16 and then
+ * quantises each row of it, a shared row over its S*I columns (as by
+ * moe_quantize_int8); its sums are exact, in 32 bits.
  */
 moe_status moe_expert_ffn(const moe_cfg* cfg, const void* x_perm, const float* x_perm_scale,
                           const int32_t* offsets, const moe_expert_weights* w, const void* x,
@@ -258,12 +281,27 @@ moe_status moe_expert_ffn(const moe_cfg* cfg, const void* x_perm, const float* x
  *  perm, offsets  as written by moe_dispatch (which may then skip x_perm)
  *  w, y_perm, y_shared, ws, ws_bytes, phase  as for moe_expert_ffn
  * MOE_ERR_UNSUPPORTED when (T+1) * H * (bytes per element) exceeds 2^31 - 1
- * (the gathered rows are addressed by 32-bit byte offsets; bf16, FP8 and MXFP4).
+ * (the gathered rows are addressed by 32-bit byte offsets; bf16, FP8, MXFP4 and INT8).
  */
 moe_status moe_expert_ffn_gather(const moe_cfg* cfg, const void* x, const int32_t* perm,
                                  const int32_t* offsets, const moe_expert_weights* w,
                                  void* y_perm, void* y_shared, void* ws, size_t ws_bytes,
                                  int phase, void* stream);
+
+/*
+ * moe_expert_ffn_codes - moe_expert_ffn_gather on a batch that is quantised already
+ * (by moe_norm, say): the same results as its own quantisation gives, bit for bit,
+ * where the codes and scales are the same.  INT8 and FP8_E4M3 experts
+ * (MOE_ERR_UNSUPPORTED otherwise).
+ *
+ *  x_codes   [T, H] int8 or E4M3 codes
+ *  x_scale   [T] (INT8) or [T, H/128] (FP8) fp32
+ * The other arguments and errors are moe_expert_ffn_gather's.
+ */
+moe_status moe_expert_ffn_codes(const moe_cfg* cfg, const void* x_codes, const float* x_scale,
+                                const int32_t* perm, const int32_t* offsets, const moe_expert_weights* w,
+                                void* y_perm, void* y_shared, void* ws, size_t ws_bytes, int phase,
+                                void* stream);
 
 /* The SwiGLU inputs of the experts (bf16, caller-owned): g = X W_g^T and
  * u = X W_u^T, [T*k, I] in the expert-sorted row order of x_perm, and the
@@ -358,6 +396,72 @@ moe_status moe_quantize_fp4(const void* src_bf16, int32_t n_mat, int32_t rows, i
  */
 moe_status moe_dequantize_fp4(const uint8_t* codes, const uint8_t* scales, int32_t n_mat, int32_t rows,
                               int32_t cols, void* dst_bf16, void* stream);
+
+/*
+ * moe_quantize_int8 - int8 codes and row scales of bf16 matrices [n_mat, rows, cols]:
+ * the weight preparation of the INT8 experts, and what moe_dispatch does to the rows
+ * of x.
+ *  dst     [n_mat, rows, cols] codes out
+ *  scales  [n_mat / group, rows] fp32 out
+ * Row r of `group` neighbouring matrices has one scale: group 1 for w_gate_up, w_down
+ * and ws_gate_up, and S for ws_down.  scale = max|v| / 127, code = the whole number
+ * nearest 127 v / max|v| (ties to even): -127 to 127.  A row of zeros has scale 0 and
+ * codes 0; one that holds an infinity or a NaN has scale NaN and codes 0.
+ * cols must be a multiple of 8, n_mat of group, and n_mat / group * rows below 2^26
+ * (MOE_ERR_SHAPE).  src must be 16-byte aligned, dst 8-byte, scales 4-byte
+ * (MOE_ERR_UNSUPPORTED).
+ */
+moe_status moe_quantize_int8(const void* src_bf16, int32_t n_mat, int32_t rows, int32_t cols, int32_t group,
+                             int8_t* dst, float* scales, void* stream);
+
+/* ------------------------------------------------------------------------- norm
+ * The root-mean-square norm in front of the layer, with the residual's addition
+ * and the experts' 8-bit rows.  cfg gives T, H, act and wgt.
+ *   moe_norm -> moe_route (on y) -> moe_dispatch (indices) -> moe_expert_ffn_codes
+ * and behind the layer's backward calls moe_norm_backward.
+ * n_tokens as for moe_dispatch_local: the live tokens of a padded batch, on the
+ * device, or NULL.  T is below 2^23, rows 16-byte aligned, scales, dweight and
+ * n_tokens 4-byte (MOE_ERR_SHAPE, MOE_ERR_UNSUPPORTED).
+ *
+ * Follows: RMSNorm outputs are recomputed in the backward pass rather than kept
+ * (qwbw.cn essay, infrastructure section, memory optimisations): y is the norm of h
+ * as it is stored, so moe_norm of h without a residual gives its bits again.
+ */
+
+/*
+ * moe_norm - h = x + residual (in the activation type), y = h * weight * r with
+ * r = (mean_j h_j^2 + eps)^-1/2 over the row.
+ *  x         [T, H] act dtype
+ *  residual  [T, H] act dtype, or NULL: h = x
+ *  weight    [H] act dtype
+ *  eps       finite, > 0 (MOE_ERR_SHAPE otherwise)
+ *  h         [T, H] act dtype out, may be NULL, and may be residual or x (in place)
+ *  y         [T, H] act dtype out, may be NULL if codes are written
+ *  codes     [T, H] int8 or E4M3 codes out (wgt INT8 or FP8_E4M3, else
+ *            MOE_ERR_UNSUPPORTED), or NULL
+ *  code_scale [T] (INT8) or [T, H/128] (FP8) fp32 out, with codes
+ * Sums are held in fp32.  The codes are those of h * weight before r and before any
+ * rounding (both formats are free of a row's factor), by the rules of
+ * moe_quantize_int8, or of moe_quantize_fp8 with 1 x 128 tiles, and r is in the scales.
+ * Rows of all outputs behind the live tokens stay as they were.
+ */
+moe_status moe_norm(const moe_cfg* cfg, const int32_t* n_tokens, const void* x, const void* residual,
+                    const void* weight, float eps, void* h, void* y, void* codes, float* code_scale, void* stream);
+
+/*
+ * moe_norm_backward - gradients of y and of h: with u = h r and g = dy * weight,
+ *   dx[t]   = r (g - u mean_j(g_j u_j)) + dh[t]     (of x and of residual alike)
+ *   dweight = sum over the live tokens of dy * u
+ *  h, weight, eps  as in moe_norm (h its output; x where there was no residual)
+ *  dy        [T, H] act dtype: the gradient of y
+ *  dh        [T, H] act dtype: the gradient that reaches h itself, or NULL
+ *  dx        [T, H] act dtype out; rows behind the live tokens are zero; may be dy or dh
+ *  dweight   [H] fp32 out (summed in a fixed order)
+ *  ws, ws_bytes  at least moe_workspace_bytes(cfg, MOE_WS_NORM_BWD)
+ */
+moe_status moe_norm_backward(const moe_cfg* cfg, const int32_t* n_tokens, const void* h, const void* weight,
+                             float eps, const void* dy, const void* dh, void* dx, float* dweight, void* ws,
+                             size_t ws_bytes, void* stream);
 
 /* -------------------------------------------------------------- share of a batch
  * The dispatch and combine of a rank that holds some of the experts, and of a
@@ -529,6 +633,23 @@ moe_status moe_route_backward(const moe_cfg* cfg, const void* x, const void* w_r
                               void* stream);
 
 /*
+ * moe_route_backward_flags - moe_route_backward of a moe_route with `flags` (MOE_SOFTMAX,
+ * MOE_GATES_RAW or both; MOE_ERR_UNSUPPORTED otherwise).  scores are that call's output.
+ *   MOE_GATES_RAW   w_j = scale * s_j:  ds_j = scale * dw_j
+ *   MOE_SOFTMAX     dlogit_e = s_e (ds_e - sum_e' s_e' ds_e')
+ * Other than moe_route_backward, which rounds dlogit to bf16 for its products, this call
+ * carries it as the sum of two bf16 numbers (16 bits and more).
+ * A token whose selected affinities are all 0 gives no gradient through renormalised
+ * gates, one whose affinities are all 0 none at all.
+ *  ws of at least moe_workspace_bytes(cfg, MOE_WS_ROUTE_BWD_SOFTMAX); E*H*4 below 2^31
+ *  (MOE_ERR_UNSUPPORTED).  The other arguments and errors are moe_route_backward's.
+ */
+moe_status moe_route_backward_flags(const moe_cfg* cfg, uint32_t flags, const void* x, const void* w_router,
+                                    const float* scores, const int32_t* topk_idx, const float* d_topk_w,
+                                    float alpha, int32_t seq_len, float* dx_router, float* dw_router, float* loss,
+                                    void* ws, size_t ws_bytes, void* stream);
+
+/*
  * moe_dispatch_backward - the input gradient of the layer:
  *   dx[t] = sum_j dx_perm[inv[t,j]] + dx_shared[t] + dx_router[t]
  * accumulated in fp32 (slots in order, then the shared and router terms), dx
@@ -543,6 +664,8 @@ moe_status moe_dispatch_backward(const moe_cfg* cfg, const void* dx_perm, const 
 #define MOE_WS_FFN 2
 #define MOE_WS_FFN_BWD 3
 #define MOE_WS_ROUTE_BWD 4
+#define MOE_WS_NORM_BWD 6
+#define MOE_WS_ROUTE_BWD_SOFTMAX 7
 
 /* Bytes of workspace a call needs for this configuration (0 on an invalid cfg). */
 size_t moe_workspace_bytes(const moe_cfg* cfg, int which);
@@ -551,10 +674,11 @@ size_t moe_workspace_bytes(const moe_cfg* cfg, int which);
  * moe_ffn_workspace_part - where moe_expert_ffn keeps the SwiGLU intermediate h
  * inside its workspace, so that a caller can read it after MOE_FFN_GATE_UP (or
  * supply it before MOE_FFN_DOWN).  Parts:
- *   MOE_WSP_H               h of the routed rows [T*k, I], act dtype or E4M3
- *   MOE_WSP_H_SCALE         their 1x128 tile scales [T*k, I/128] fp32 (FP8 only)
+ *   MOE_WSP_H               h of the routed rows [T*k, I], act dtype, E4M3 or int8
+ *   MOE_WSP_H_SCALE         their 1x128 tile scales [T*k, I/128] fp32 (FP8), or row
+ *                           scales [T*k] (INT8)
  *   MOE_WSP_H_SHARED        h of the shared experts [T, S*I]
- *   MOE_WSP_H_SHARED_SCALE  their scales [T, S*I/128] fp32 (FP8 only)
+ *   MOE_WSP_H_SHARED_SCALE  their scales [T, S*I/128] (FP8) or [T] (INT8) fp32
  * Writes the byte offset from the start of the workspace and the byte size
  * (0 for a part this configuration does not hold).  Host only; no device call.
  */

@@ -70,6 +70,23 @@ def seq_balance_loss(s: np.ndarray, idx: np.ndarray, k: int, seq_len: int, alpha
     return loss, ds
 
 
+def route_backward(x, w_router, s, idx, dw, scale: float, alpha: float = 0.0, seq_len: int = 0, softmax: bool = True,
+                   raw: bool = False):
+    """Gradients of the gates (and of the balance loss) through the router, for affinities s [T, E] that are a
+    softmax or a sigmoid of the logits.  raw: gates scale * s.  Returns (dx, dw_router, loss)."""
+    x, s, dw = (np.asarray(v, F64) for v in (x, s, dw))
+    idx = np.asarray(idx, np.int64)
+    s_sel = np.take_along_axis(s, idx, axis=1)
+    ds = np.zeros(s.shape, F64)
+    np.put_along_axis(ds, idx, scale * dw if raw else gate_backward(s_sel, dw, scale), axis=1)
+    loss = 0.0
+    if alpha:
+        loss, more = seq_balance_loss(s, idx, idx.shape[1], seq_len or len(s), alpha)
+        ds = ds + more
+    dlogit = s * (ds - (s * ds).sum(axis=1, keepdims=True)) if softmax else ds * s * (1.0 - s)
+    return dlogit @ np.asarray(w_router, F64), dlogit.T @ x, loss
+
+
 def swiglu_backward(X: np.ndarray, w_gate_up: np.ndarray, w_down: np.ndarray, dY: np.ndarray):
     """Gradients of Y = W_d (silu(W_g X) * W_u X) for one expert on rows X [n, H].
 

@@ -44,6 +44,19 @@ def affinity(x: np.ndarray, w_router: np.ndarray, logit_offset=None) -> np.ndarr
     return s.astype(F32)
 
 
+def affinity_softmax(x: np.ndarray, w_router: np.ndarray, logit_offset=None) -> np.ndarray:
+    """s[t, :] = softmax of the logits <x_t, w_e> + o_e over all experts: the logits rounded to fp32, the softmax in
+    fp64 and rounded to fp32.  A logit of -inf gives 0, a token with no other the affinities 0."""
+    logits = np.asarray(x, F64) @ np.asarray(w_router, F64).T
+    if logit_offset is not None:
+        logits = logits + np.asarray(logit_offset, F64)[None, :]
+    logits = logits.astype(F32).astype(F64)
+    top = logits.max(axis=1, keepdims=True)
+    e = np.exp(logits - np.where(np.isfinite(top), top, 0.0))
+    z = e.sum(axis=1, keepdims=True)
+    return (e / np.where(z > 0, z, 1.0)).astype(F32)
+
+
 def _biased(s32: np.ndarray, bias: np.ndarray) -> np.ndarray:
     """q = fl32(s + b): one fp32 add per element."""
     return (np.asarray(s32, F32) + np.asarray(bias, F32)[None, :]).astype(F32)
@@ -61,11 +74,12 @@ def _group_scores(q: np.ndarray, n_groups: int, topr: int) -> np.ndarray:
 
 
 def route(s32: np.ndarray, bias: np.ndarray, n_groups: int, groups_per_token: int,
-          top_k: int, group_topr: int, route_scale: float):
+          top_k: int, group_topr: int, route_scale: float, raw: bool = False):
     """Biased, group-limited top-k.  Returns (idx int32 [T,k], w float64 [T,k]).
 
     idx[t, j] is the j-th selected expert (q descending, index ascending);
-    w[t, j] = scale * s[t, idx] / sum over the selected experts of s.
+    w[t, j] = scale * s[t, idx] / sum over the selected experts of s (0 where that is 0);
+    raw: scale * s[t, idx].
     """
     s32 = np.asarray(s32, F32)
     T, E = s32.shape
@@ -79,7 +93,10 @@ def route(s32: np.ndarray, bias: np.ndarray, n_groups: int, groups_per_token: in
     qm = np.where(allowed, q.astype(F64), -np.inf)
     idx = np.argsort(-qm, axis=1, kind="stable")[:, :top_k]
     sel = np.take_along_axis(s32.astype(F64), idx, axis=1)
-    w = route_scale * sel / sel.sum(axis=1, keepdims=True)
+    if raw:
+        return idx.astype(np.int32), route_scale * sel
+    total = sel.sum(axis=1, keepdims=True)
+    w = route_scale * sel / np.where(total > 0, total, 1.0)
     return idx.astype(np.int32), w
 
 
