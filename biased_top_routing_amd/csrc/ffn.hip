@@ -30,7 +30,7 @@ struct TileTables {
   int E, S, T, bm1, bm1_alt, bm2, bm2_alt, nt1, nt1s, nt2;
   TileDesc *t1, *t2;     // t2 == nullptr: the first table only
   int32_t* hdr;
-  bool fp4_choose;       // MXFP4: bm1 and bm2 are the lowest of the heights, the rows that are there decide
+  bool choose;           // MXFP4, int8: bm1 and bm2 are the lowest of the heights, the rows that are there decide
 };
 
 // Block b of nb blocks of 1024 threads.
@@ -49,13 +49,13 @@ __device__ void build_tiles_block(const int32_t* __restrict__ offsets, const Til
     row0 = offsets[tid];
     rows = offsets[tid + 1] - row0;
   }
-  if (p.fp4_choose) {                                   // the tiles of the routed segments at each height
+  if (p.choose) {                                   // the tiles of the routed segments at each height
     __shared__ int32_t tiles_s[3][16];
     int n[3] = {0, 0, 0};
     if (tid < E) {
-      n[0] = (rows + kFp4LowBM - 1) / kFp4LowBM;
-      n[1] = (rows + kFp4BM - 1) / kFp4BM;
-      n[2] = (rows + kFp4HighBM - 1) / kFp4HighBM;
+      n[0] = (rows + kTileLowBM - 1) / kTileLowBM;
+      n[1] = (rows + kTileBM - 1) / kTileBM;
+      n[2] = (rows + kTileHighBM - 1) / kTileHighBM;
     }
 #pragma unroll
     for (int h = 0; h < 3; ++h) {
@@ -69,7 +69,7 @@ __device__ void build_tiles_block(const int32_t* __restrict__ offsets, const Til
     for (int h = 0; h < 3; ++h)
 #pragma unroll
       for (int w = 0; w < 16; ++w) sum[h] += tiles_s[h][w];
-    bm1 = bm2 = fp4_tile_rows(sum[0], sum[1], sum[2]);
+    bm1 = bm2 = tile_rows_of(sum[0], sum[1], sum[2]);
   }
   int c1 = 0, c2 = 0;
   if (tid < nseg) {
@@ -106,7 +106,7 @@ __device__ void build_tiles_block(const int32_t* __restrict__ offsets, const Til
   if (tid == 0 && b == 0) {
     hdr[0] = total1;
     hdr[1] = t2 ? total2 : 0;
-    if (p.fp4_choose) hdr[kFp4TileRows] = bm1;
+    if (p.choose) hdr[kTileRows] = bm1;
     // tiles of the routed segments (they come first; the shared ones follow)
     hdr[4] = p.S > 0 ? pre1[E] : total1;
     hdr[5] = t2 ? (p.S > 0 ? pre2[E] : total2) : 0;
@@ -183,7 +183,7 @@ moe_status launch_build_tile_tables(const moe_cfg* c, const int32_t* offsets, in
 static TileTables ffn_tables(const moe_cfg* c, const FfnLayout& L, char* base) {
   return TileTables{c->E, c->S, c->T, L.bm1, L.bm1_alt, L.bm2, L.bm2_alt, (int)L.nt1, (int)L.nt1s, (int)L.nt2,
                     reinterpret_cast<TileDesc*>(base + L.off_t1), reinterpret_cast<TileDesc*>(base + L.off_t2),
-                    reinterpret_cast<int32_t*>(base + L.off_hdr), c->wgt == MOE_MXFP4 && L.bm1 != kFp4RowsBM};
+                    reinterpret_cast<int32_t*>(base + L.off_hdr), (c->wgt == MOE_MXFP4 && L.bm1 != kFp4RowsBM) || (c->wgt == MOE_INT8 && L.bm1 != kInt8RowsBM)};
 }
 
 moe_status launch_build_tiles(const moe_cfg* c, const int32_t* offsets, void* ws, hipStream_t st) {

@@ -107,7 +107,7 @@ constexpr int kFp8MaxKC = 64;
 // shared experts together.  Not measured, and not told apart by the rule: a share or a padded
 // batch with few live rows in a large capacity (it gets 128-row tiles), and routed experts of
 // few rows beside long shared ones (these get 32-row tiles too).
-constexpr int kFp4RowsBM = 32, kFp4LowBM = 128, kFp4BM = 256, kFp4HighBM = 288;
+constexpr int kFp4RowsBM = 32, kTileLowBM = 128, kTileBM = 256, kTileHighBM = 288;
 constexpr int kFp4RowsAvg = 20;
 constexpr int kFp4BNH = 128, kFp4BN2 = 256;
 // A tile of 128 rows has two slices of loads in flight instead of one and takes less
@@ -123,18 +123,18 @@ constexpr int kFp4BNH = 128, kFp4BN2 = 256;
 //   The table builder chooses: it knows the rows that are there (a share of a batch, or a
 // padded one, has fewer than T * k; 32 of 256 experts held, H = 7168, I = 2048, T = 512: 151
 // us, and 188 as T * k would have it).  It counts the tiles of the routed segments alone; the
-// shared experts' take the height that follows.  It leaves the height in header entry kFp4TileRows;
+// shared experts' take the height that follows.  It leaves the height in header entry kTileRows;
 // the host sizes tables and grid for the lowest.  (One kernel for three heights is up to
 // 0.6% slower than one each.)
-__host__ __device__ inline int fp4_tile_rows(int n_low, int n, int n_high) {
-  if ((int64_t)5 * n_low <= (int64_t)7 * n) return kFp4LowBM;
-  return (int64_t)10 * n_high <= (int64_t)9 * n ? kFp4HighBM : kFp4BM;
+__host__ __device__ inline int tile_rows_of(int n_low, int n, int n_high) {
+  if ((int64_t)5 * n_low <= (int64_t)7 * n) return kTileLowBM;
+  return (int64_t)10 * n_high <= (int64_t)9 * n ? kTileHighBM : kTileBM;
 }
-constexpr int kFp4TileRows = 6;
+constexpr int kTileRows = 6;
 
-// int8 GEMMs: tiles of 32 token rows where the pairs make at most 20 an expert, else 256; 128 h columns per
-// gate/up tile, 256 output columns per down tile.
-constexpr int kInt8RowsBM = 32, kInt8BM = 256;
+// int8 GEMMs: tiles of 32 token rows where the pairs make at most 20 an expert, else of the heights above by the same
+// rule; 128 h columns per gate/up tile, 256 output columns per down tile.
+constexpr int kInt8RowsBM = 32;
 constexpr int kInt8RowsAvg = 20;
 constexpr int kInt8BNH = 128, kInt8BN2 = 256;
 constexpr int kInt8MaxK = 1 << 17;   // K of a GEMM stays below: 128 * 128 * K fits the accumulators
@@ -228,8 +228,8 @@ struct FfnLayout {
     const int64_t P = pairs(c);
     const bool f8 = c->wgt == MOE_FP8_E4M3, f4 = c->wgt == MOE_MXFP4, i8 = c->wgt == MOE_INT8;
     const int bm4 = P <= (int64_t)kFp4RowsAvg * c->E  ? kFp4RowsBM
-                                                      : kFp4LowBM;
-    const int bmi = P <= (int64_t)kInt8RowsAvg * c->E ? kInt8RowsBM : kInt8BM;
+                                                      : kTileLowBM;
+    const int bmi = P <= (int64_t)kInt8RowsAvg * c->E ? kInt8RowsBM : kTileLowBM;
     dec = small_batch(c);
     bm1 = i8 ? bmi : f4 ? bm4 : f8 ? kFp8BM : dec ? kDecBM : kBM1;
     bm1_alt = i8 || f4 || f8 || dec ? 0 : kBM1Alt;

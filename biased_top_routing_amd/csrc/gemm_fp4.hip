@@ -641,9 +641,9 @@ __global__ __launch_bounds__(kFp4Threads, 1) void gemm_fp4_kernel(Fp4Params p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   __shared__ __attribute__((aligned(16))) uint8_t lds[kFp4Lds];
   const int bm = __builtin_amdgcn_readfirstlane(*p.tile_rows);
-  if (bm == kFp4LowBM) gemm_fp4_tiles<MODE, kFp4LowBM, 3>(p, lds);
-  else if (bm == kFp4BM) gemm_fp4_tiles<MODE, kFp4BM, 2>(p, lds);
-  else gemm_fp4_tiles<MODE, kFp4HighBM, 2>(p, lds);
+  if (bm == kTileLowBM) gemm_fp4_tiles<MODE, kTileLowBM, 3>(p, lds);
+  else if (bm == kTileBM) gemm_fp4_tiles<MODE, kTileBM, 2>(p, lds);
+  else gemm_fp4_tiles<MODE, kTileHighBM, 2>(p, lds);
 #endif
 }
 
@@ -802,7 +802,7 @@ moe_status launch_ffn_fp4(const moe_cfg* c, const uint8_t* x_perm, const uint8_t
   auto bytes = [](const void* q) { return static_cast<const uint8_t*>(q); };
   moe_status s;
   Fp4Params p{};
-  p.tile_rows = hdr + kFp4TileRows;
+  p.tile_rows = hdr + kTileRows;
   p.T = c->T; p.H = c->H; p.E = c->E; p.S = c->S; p.I = c->I; p.k = c->k;
   if (phase == MOE_FFN_ALL || phase == MOE_FFN_GATE_UP) {
     // the tile tables, and x once in MXFP4: the shared experts' operand, and the routed one when its rows are gathered

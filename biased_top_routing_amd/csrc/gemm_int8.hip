@@ -37,12 +37,13 @@ struct Int8Params {
   bf16_t* out_shared;
   const TileDesc* tiles;
   const int32_t* ntiles;
+  const int32_t* tile_rows;   // rows per tile
   const int32_t* perm;        // gate/up: non-null -> routed rows gathered from a_shared / sa_shared
   int T, H, E, S, I, k;
 };
 
 #if defined(__HIP_DEVICE_COMPILE__)
-constexpr int NI8 = 4;          // MFMA column blocks of a wavefront
+constexpr int NI8 = 4;          // MFMA column blocks of a wavefront (few rows)
 typedef __attribute__((address_space(3))) void lds_void_t;
 
 __device__ __forceinline__ i32x4_t mfma_i8(i32x4_t w, i32x4_t a, i32x4_t c) {
@@ -105,14 +106,15 @@ struct OperandsI8 {
   }
 };
 
-// The order of a wavefront's columns: block ni, MFMA row 4 g + r is column 8 g + 4 (ni mod 2) + r of its 32 gate
-// columns (ni < 2) or of the up columns BN / 2 further on, or of its first or second 32 output columns, so that a
-// lane holds 8 neighbouring columns of a row in two blocks: 16 bytes of bf16.  The tile column whose LDS row lane
-// l16 reads is col_lane + col_off.
+// The order of a wavefront's columns: blocks ni and ni + 1 (ni even) share 32 neighbouring columns, MFMA row 4 g + r
+// of block ni being column 8 g + 4 (ni mod 2) + r of them, so that a lane holds 8 neighbouring columns of a row in two
+// blocks: 16 bytes of bf16.  The first half of a gate/up wavefront's blocks are gate columns, the other half the up
+// columns BN / 2 further on.  The tile column whose LDS row lane l16 reads is col_lane + col_off.
 __device__ __forceinline__ int col_lane(int l16) { return 8 * (l16 >> 2) + (l16 & 3); }
-template <int MODE, int BN>
+template <int MODE, int NI, int BN>
 __device__ __forceinline__ constexpr int col_off(int ni) {
-  return (ni / 2) * (MODE == kGateUpI8 ? BN / 2 : 32) + (ni % 2) * 4;
+  if (MODE == kGateUpI8) return (ni / (NI / 2)) * (BN / 2) + (ni % (NI / 2)) / 2 * 32 + (ni % 2) * 4;
+  return (ni / 2) * 32 + (ni % 2) * 4;
 }
 // Physical 16-byte chunk of logical chunk c of 8 in LDS row r of the weights: 8 lanes' rows (4, and 4 that lie 8
 // further on) meet no bank twice.
@@ -125,11 +127,297 @@ __device__ __forceinline__ void lds_barrier() {
 }
 #endif
 
+// ------------------------------------------------------------------ large batches
+constexpr int kInt8Threads = 512;
+constexpr int kInt8Lds = 147456;
+
+#if defined(__HIP_DEVICE_COMPILE__)
+// v as a value that the compiler cannot compute ahead of this point (what a tile's begin and epilogue derive from the
+// lane would otherwise be computed before the loops and held, or spilled, through them).
+__device__ __forceinline__ int opaque(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+// The GEMM over tiles of BM rows.
+template <int MODE, int BM, int STAGES>
+__device__ __forceinline__ void gemm_int8_tiles(const Int8Params& p, uint8_t* lds) {
+  constexpr int WM = 2, WN = 4, NT = kInt8Threads, NW = NT / 64, BN = 256;
+  constexpr int MI = BM / (WM * 16), NI = BN / (WN * 16), HALF = NI / 2;
+  static_assert(WM * WN == NW && WM * MI * 16 == BM && BN == kInt8BN2, "tile shape");
+  constexpr int BK = 128, CPR = BK / 16;               // bytes (two K steps) and 16-byte chunks of a row per slice
+  constexpr int RPL = NT / CPR;                        // rows a load of all threads covers
+  // loads per thread per slice; an odd number of 32 rows: A's last load is the first half of the wavefronts' alone
+  constexpr int A_CH = (BM + RPL - 1) / RPL, B_CH = BN / RPL, PER = A_CH + B_CH;
+  constexpr bool A_HALF = BM % RPL != 0;
+  static_assert(RPL % 16 == 0 && BN % RPL == 0 && BM % (RPL / 2) == 0 && (!A_HALF || STAGES == 2), "the loads of a slice");
+  constexpr int B_OFF = BM * BK, STAGE = B_OFF + BN * BK;
+  static_assert(STAGES * STAGE <= kInt8Lds, "LDS");
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  const int l16 = lane & 15, g = lane >> 4;
+
+  // ------------------------------------------------------------ this workgroup's tiles
+  // XCD x = b mod 8 takes an equal contiguous share of the shared tiles and then one of the routed tiles; its
+  // workgroups take them in turn.
+  const int n_real = __builtin_amdgcn_readfirstlane(p.ntiles[0]), n_rt = __builtin_amdgcn_readfirstlane(p.ntiles[4]);
+  const int xcd = blockIdx.x & 7, per_s = (n_real - n_rt + 7) >> 3, per_r = (n_rt + 7) >> 3;
+  const int s_cnt = min(max(n_real - n_rt - xcd * per_s, 0), per_s);
+  const int r_cnt = min(max(n_rt - xcd * per_r, 0), per_r);
+  const int step = gridDim.x >> 3;
+  // the n-th of this workgroup: round n takes the next `step` positions of the share, turned by 5 n (an expert's row
+  // tiles of one column follow each other, the last one shorter: without the turn a workgroup might get only long
+  // ones)
+  auto place = [&](int n) { return n * step + ((int)(blockIdx.x >> 3) + 5 * n) % step; };
+  auto entry = [&](int q) { return q < s_cnt ? n_rt + xcd * per_s + q : xcd * per_r + q - s_cnt; };
+  const int q_end = s_cnt + r_cnt;
+  int nq = 0;                                          // the tile being loaded
+  if (place(0) >= q_end) return;
+
+  // ------------------------------------------------------------ the loads
+  // The stream of slices runs STAGES - 1 slices ahead of the products, through the tiles.
+  int ls = 0;                                          // stage the next slice goes to
+  int left = 0;                                        // slices of the tile to load yet
+  int in_l = 0, nk1 = 1;                               // slices of its current expert to load yet, of each
+  int ak = 0, wk = 0, w_skip = 0;                      // scalar offsets of the next slice; to the next expert's first
+  // A: an offset a load where rows are gathered, else one and the rows' distance; W: one, the rows' distance, and
+  // what lies between gate and up rows
+  constexpr int A_OFF = MODE == kGateUpI8 ? A_CH : 1;
+  int a_off[A_OFF], b_off = 0, a_dist = 0, w_dist = 0, w_gap = 0;
+  int pn[A_OFF];                                       // perm entries of this lane's rows in the tile after it
+  const uint8_t *baseA = nullptr, *baseW = nullptr;
+  int bytesA = 0, bytesW = 0;                          // 0 when the stream has ended: its loads are dropped
+  const int lr = tid / CPR;
+  auto load_perm = [&](int q) {
+    if (MODE != kGateUpI8 || p.perm == nullptr || q >= q_end) return;
+    const TileDesc d = tile_at(p, entry(q));
+    if (d.seg == p.E) return;
+    const __amdgpu_buffer_rsrc_t r = make_rsrc(p.perm + d.row0, d.rows * 4);
+#pragma unroll
+    for (int i = 0; i < A_OFF; ++i) pn[i] = __builtin_amdgcn_raw_buffer_load_b32(r, (lr + i * RPL) * 4, 0, 0);
+  };
+  // the next tile's loads begin, if there is one
+  auto next_tile = [&]() {
+    const int q = place(nq);
+    left = 0x7FFFFFFF;
+    ak = wk = 0;
+    bytesA = bytesW = 0;
+    if (q >= q_end) return;
+    const TileDesc d = tile_at(p, entry(q));
+    const OperandsI8<MODE> o(p, d);
+    const int ca = swz<CPR>(lr, tid % CPR) * 16, cw = swz_w(lr, tid % CPR) * 16;
+    // (rows past the tile's lie past the descriptor: the range check drops their loads)
+    if constexpr (MODE == kGateUpI8) {
+#pragma unroll
+      for (int i = 0; i < A_CH; ++i) {
+        const int r = lr + i * RPL;
+        a_off[i] = (r >= d.rows ? o.a_rows + 1 : o.gather ? pn[i] / p.k : r) * o.lda + ca;
+      }
+    } else {
+      a_off[0] = lr * o.lda + ca;
+      a_dist = RPL * o.lda;
+    }
+    b_off = o.ex * o.w_one + (o.c0 + lr) * o.ldw + cw;
+    w_dist = RPL * o.ldw;
+    w_gap = MODE == kGateUpI8 ? (p.I - 128) * o.ldw : 0;
+    baseA = o.A; bytesA = o.a_bytes;
+    baseW = o.W; bytesW = o.w_bytes;
+    w_skip = o.w_one - o.nk1 * BK;
+    in_l = nk1 = o.nk1;
+    left = o.nk1 * o.nexp;
+    load_perm(place(++nq));
+  };
+  // Load i of PER of the stream's next slice.  (Only offsets that lie inside the descriptor whatever the lane go
+  // through the scalar offset.)
+  struct Stream {                                      // (in scalar registers)
+    __amdgpu_buffer_rsrc_t a, w;
+    int ak, wk;
+  };
+  auto stream = [&]() {
+    return Stream{make_rsrc(baseA, bytesA), make_rsrc(baseW, bytesW), __builtin_amdgcn_readfirstlane(ak),
+                  __builtin_amdgcn_readfirstlane(wk)};
+  };
+  auto load_part = [&](const Stream& s, int i) {
+    lds_void_t* dst = (lds_void_t*)(lds + ls * STAGE + wave * 1024 + (i < A_CH ? i * NT * 16 : B_OFF + (i - A_CH) * NT * 16));
+    if (A_HALF && i == A_CH - 1 && wave >= NW / 2) return;
+    if (i < A_CH)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(s.a, dst, 16, MODE == kGateUpI8 ? a_off[i % A_OFF] : a_off[0] + i * a_dist,
+                                               s.ak, 0, 0);
+    else
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          s.w, dst, 16, b_off + (i - A_CH) * w_dist + ((i - A_CH) * RPL >= 128 ? w_gap : 0), s.wk, 0, 0);
+  };
+  // After a slice's loads.
+  auto advance = [&]() {
+    ak += BK;
+    wk += BK;
+    --left;
+    ls = ls == STAGES - 1 ? 0 : ls + 1;
+    if (MODE == kDownI8 && --in_l == 0) {              // the next shared expert's K range
+      in_l = nk1;
+      wk += w_skip;
+    }
+  };
+
+  // ------------------------------------------------------------ the products
+  // this lane's fragments in a stage: tile rows arow0 + 16 mi and brow + col_off(ni); lane group g supplies the
+  // elements [16g, 16g + 16) of a step (the swizzles are the same for every block, and a row's second step is 64 bytes
+  // away by exclusive or)
+  const int arow0 = wm * MI * 16 + l16;
+  const int brow = wn * (MODE == kGateUpI8 ? BN / WN / 2 : BN / WN) + col_lane(l16);
+  const int a_lane = arow0 * BK + swz<CPR>(l16, g) * 16;
+  const int b_lane = B_OFF + brow * BK + swz_w(col_lane(l16), g) * 16;
+  constexpr int NB = MI % 3 == 0 ? 3 : 4, D = 2, R = NB - D;   // A fragments held, read ahead, multiplied over the barrier
+  static_assert(MI % NB == 0 && MI >= NI, "the buffers rotate within a step; B's next step is read in one");
+  i32x4_t fa[NB], fb[2][NI];                           // fragments of token rows; of the weights, in either K step
+  auto read_a = [&](const uint8_t* stage, int kk, int mi) {
+    fa[mi % NB] = *reinterpret_cast<const i32x4_t*>(stage + (a_lane ^ (kk * 64)) + mi * 16 * BK);
+  };
+  auto read_b = [&](const uint8_t* stage, int kk, int ni) {
+    fb[kk][ni] = *reinterpret_cast<const i32x4_t*>(stage + (b_lane ^ (kk * 64)) + col_off<MODE, NI, BN>(ni) * BK);
+  };
+  int cs = 0;                                          // stage of the current slice
+  auto read_first = [&]() {                            // a slice's first fragments
+    const uint8_t* here = lds + cs * STAGE;
+#pragma unroll
+    for (int ni = 0; ni < NI; ++ni) read_b(here, 0, ni);
+#pragma unroll
+    for (int i = 0; i < D; ++i) read_a(here, 0, i);
+  };
+  auto load_slice = [&]() {
+    if (left == 0) next_tile();
+    const Stream s = stream();
+#pragma unroll
+    for (int i = 0; i < PER; ++i) load_part(s, i);
+    advance();
+  };
+  // What follows a slice's reads: the next slice has landed, everywhere, and this one's stage is free.
+  auto turn = [&]() {
+    wait_vm<PER * (STAGES - 2)>();
+    lds_barrier();
+    cs = cs == STAGES - 1 ? 0 : cs + 1;
+  };
+  load_perm(place(0));
+#pragma unroll
+  for (int i = 0; i < STAGES - 1; ++i) load_slice();
+  wait_vm<PER * (STAGES - 2)>();
+  lds_barrier();
+
+  const int steps1 = (MODE == kDownI8 ? p.I : p.H) / BK;   // slices of an expert
+  for (int nc = 0, qc = place(0); qc < q_end; qc = place(++nc)) {
+    const TileDesc cd = tile_at(p, entry(qc));
+    const int slices = MODE == kDownI8 && cd.seg == p.E ? p.S * steps1 : steps1;
+    if (wm * MI * 16 >= cd.rows) {                     // no rows for this wavefront: it only loads
+      for (int kt = 0; kt < slices; ++kt) {
+        load_slice();
+        turn();
+      }
+      continue;
+    }
+    const OperandsI8<MODE> o(p, cd);
+    const int cl = wn * (MODE == kGateUpI8 ? BN / WN / 2 : BN / WN) + 8 * g;
+    // the scales of this lane's columns and rows
+    float sw[NI][4], sa[MI];
+#pragma unroll
+    for (int ni = 0; ni < NI; ++ni) {
+      const int c = cl + col_off<MODE, NI, BN>(ni);    // (4 columns: all there, or none)
+      const float* q = o.SW + (MODE == kGateUpI8 ? o.template wrow<BN>(p, 0, c) : min(o.c0 + c, o.ncols - 4));
+#pragma unroll
+      for (int r = 0; r < 4; ++r) sw[ni][r] = q[r];
+    }
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi) {
+      const int i = min(arow0 + mi * 16, cd.rows - 1);
+      sa[mi] = o.SA[o.gather ? p.perm[cd.row0 + i] / p.k : i];
+    }
+    i32x4_t acc[MI][NI];
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+      for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = i32x4_t{0, 0, 0, 0};
+    // row block mi of a K step, what else is to be issued between the products
+    auto multiply = [&](int mi, const i32x4_t (&b)[NI], auto also) {
+#pragma unroll
+      for (int ni = 0; ni < NI; ++ni) {
+        acc[mi][ni] = mfma_i8(b[ni], fa[mi % NB], acc[mi][ni]);
+        also(ni);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    read_first();
+    for (int kt = 0; kt < slices; ++kt) {
+      if (left == 0) next_tile();
+      const uint8_t* here = lds + cs * STAGE;
+      const Stream s = stream();
+      // the slice's first K step, the loads of the slice to come between its products
+#pragma unroll
+      for (int mi = 0; mi < MI; ++mi)
+        multiply(mi, fb[0], [&](int ni) {
+          if (ni == 0) read_a(here, mi + D < MI ? 0 : 1, (mi + D) % MI);
+          if (ni == 1 && mi < NI) read_b(here, 1, mi);
+          const int i = PER * mi / MI + ni - 2;
+          if (ni >= 2 && i < PER * (mi + 1) / MI) load_part(s, i);
+        });
+      advance();
+      // the second, its last R row blocks over the barrier and the next slice's first reads
+#pragma unroll
+      for (int mi = 0; mi < MI - R; ++mi)
+        multiply(mi, fb[1], [&](int ni) {
+          if (ni == 0 && mi + D < MI) read_a(here, 1, mi + D);
+        });
+      turn();
+      read_first();                                    // (not into the buffers in use; after a tile's last slice unused)
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < R; ++i) multiply(MI - R + i, fb[1], [](int) {});
+    }
+    static_assert(PER <= 2 * MI && NI == 4, "the loads fit between the products");
+    // acc[mi][ni][r] holds C[i][j] with i = arow0 + 16 mi (token row), j in the order of col_off
+    bf16_t* out = o.shared ? p.out_shared : p.out_routed;
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi) {
+      const int i = arow0 + mi * 16;
+      bf16_t* row = out + (cd.row0 + i) * (int64_t)o.ncols;
+#pragma unroll
+      for (int b = 0; b < (MODE == kGateUpI8 ? HALF / 2 : NI / 2); ++b) {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int ni = 2 * b + e / 4;
+          v[e] = (float)acc[mi][ni][e % 4] * (sa[mi] * sw[ni][e % 4]);
+          if constexpr (MODE == kGateUpI8) {
+            const float u = (float)acc[mi][ni + HALF][e % 4] * (sa[mi] * sw[ni + HALF][e % 4]);
+            v[e] = v[e] * gate_sigmoid(v[e]) * u;
+          }
+        }
+        const int col = (MODE == kGateUpI8 ? cd.nt * 128 : cd.nt * 256) + cl + b * 32;
+        if (i < cd.rows && (MODE == kGateUpI8 || col < o.ncols))
+          *reinterpret_cast<uint4*>(row + col) = make_uint4(cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]),
+                                                           cvt_bf16x2(v[4], v[5]), cvt_bf16x2(v[6], v[7]));
+      }
+    }
+  }
+}
+#endif
+
+// The table's builder chose the tiles' height from the rows that are there.
+template <int MODE>
+__global__ __launch_bounds__(kInt8Threads, 1) void gemm_int8_kernel(Int8Params p) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kInt8Lds];
+  const int bm = __builtin_amdgcn_readfirstlane(*p.tile_rows);
+  if (bm == kTileLowBM) gemm_int8_tiles<MODE, kTileLowBM, 3>(p, lds);
+  else if (bm == kTileBM) gemm_int8_tiles<MODE, kTileBM, 2>(p, lds);
+  else gemm_int8_tiles<MODE, kTileHighBM, 2>(p, lds);
+#endif
+}
+
+// ------------------------------------------------------------------ few rows per expert
 // One workgroup of WM x WN wavefronts a tile (PARTS > 1: a part of one) of WM * MI * 16 token rows x WN * 64
 // weight rows.  K advances 128 bytes a slice through a ring of STAGES LDS stages filled by direct-to-LDS loads
 // (16-byte chunks, XOR swizzle per row), one barrier a slice.
 template <int MODE, int WM, int WN, int MI, int STAGES, int PARTS>
-__global__ __launch_bounds__(64 * WM * WN, 1) void gemm_int8_kernel(Int8Params p) {
+__global__ __launch_bounds__(64 * WM * WN, 1) void gemm_int8_rows_kernel(Int8Params p) {
   constexpr int NT = 64 * WM * WN, BM = WM * MI * 16, BN = WN * 64, BK = 128, CPR = BK / 16;
   static_assert(PARTS * BN == kInt8BN2 && BN / 2 * PARTS == kInt8BNH, "the tiles of the table, in parts");
   constexpr int A_CH = BM * CPR / NT, B_CH = BN * CPR / NT, PER = A_CH + B_CH;   // loads per thread per slice
@@ -197,7 +485,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void gemm_int8_kernel(Int8Params p
         i32x4_t fb[NI8];
 #pragma unroll
         for (int ni = 0; ni < NI8; ++ni)
-          fb[ni] = *reinterpret_cast<const i32x4_t*>(base + (BM + brow + col_off<MODE, BN>(ni)) * BK +
+          fb[ni] = *reinterpret_cast<const i32x4_t*>(base + (BM + brow + col_off<MODE, NI8, BN>(ni)) * BK +
                                                      swz_w(col_lane(l16), kk * 4 + g) * 16);
 #pragma unroll
         for (int mi = 0; mi < MI; ++mi) {
@@ -217,7 +505,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void gemm_int8_kernel(Int8Params p
   for (int ni = 0; ni < NI8; ++ni)
 #pragma unroll
     for (int r = 0; r < 4; ++r)
-      sw[ni][r] = o.SW[o.template wrow<BN>(p, part, wn * (MODE == kGateUpI8 ? 32 : 64) + 8 * g + col_off<MODE, BN>(ni) + r)];
+      sw[ni][r] = o.SW[o.template wrow<BN>(p, part, wn * (MODE == kGateUpI8 ? 32 : 64) + 8 * g + col_off<MODE, NI8, BN>(ni) + r)];
 #pragma unroll
   for (int mi = 0; mi < MI; ++mi) {
     const int i = arow0 + mi * 16;
@@ -253,10 +541,15 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void gemm_int8_kernel(Int8Params p
 
 template <int MODE>
 moe_status launch_gemm_int8(const FfnLayout& L, int64_t max_tiles, const Int8Params& p, hipStream_t st) {
-  const unsigned grid = (unsigned)grouped_grid(max_tiles, kStripeInt8);
-  if (grid == 0) return MOE_OK;
-  if (L.bm1 == kInt8RowsBM) hipLaunchKernelGGL((gemm_int8_kernel<MODE, 1, 1, 2, 4, 4>), dim3(4 * grid), dim3(64), 0, st, p);
-  else hipLaunchKernelGGL((gemm_int8_kernel<MODE, 2, 4, 8, 2, 1>), dim3(grid), dim3(512), 0, st, p);
+  if (max_tiles == 0) return MOE_OK;
+  if (L.bm1 == kInt8RowsBM) {
+    const unsigned parts = 4 * (unsigned)grouped_grid(max_tiles, kStripeInt8);
+    hipLaunchKernelGGL((gemm_int8_rows_kernel<MODE, 1, 1, 2, 4, 4>), dim3(parts), dim3(64), 0, st, p);
+    return launch_status();
+  }
+  // one workgroup a CU (its LDS leaves no room for two), whole rounds of the 8 XCDs
+  const int64_t grid = std::min<int64_t>(std::max(cu_count() / 8 * 8, 8), (int64_t)align_up((size_t)max_tiles, 8));
+  hipLaunchKernelGGL(gemm_int8_kernel<MODE>, dim3((unsigned)grid), dim3(kInt8Threads), 0, st, p);
   return launch_status();
 }
 
@@ -275,6 +568,7 @@ moe_status launch_ffn_int8(const moe_cfg* c, const uint8_t* x_perm, const float*
   bf16_t* hbs = reinterpret_cast<bf16_t*>(base + L.off_hbs);
   moe_status s;
   Int8Params p{};
+  p.tile_rows = hdr + kTileRows;
   p.T = c->T; p.H = c->H; p.E = c->E; p.S = c->S; p.I = c->I; p.k = c->k;
   if (phase == MOE_FFN_ALL || phase == MOE_FFN_GATE_UP) {
     if ((s = launch_build_tiles(c, offsets, ws, st)) != MOE_OK) return s;
