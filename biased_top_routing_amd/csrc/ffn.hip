@@ -10,6 +10,7 @@
 #include "common.h"
 #include "ffn_layout.h"
 #include "fp4.h"
+#include "int8.h"
 #include "kernels.h"
 
 namespace moe {
@@ -26,11 +27,12 @@ namespace moe {
 // their weight rows are shared in that XCD's L2, also for segments far larger
 // than the number of tiles in flight.  Every workgroup computes the prefix sums over segments in LDS
 // (at most 513 segments) and writes its own share of the entries.
+enum { kChooseNone = 0, kChooseFp4 = 1, kChooseInt8 = 2 };
 struct TileTables {
   int E, S, T, bm1, bm1_alt, bm2, bm2_alt, nt1, nt1s, nt2;
   TileDesc *t1, *t2;     // t2 == nullptr: the first table only
   int32_t* hdr;
-  bool choose;           // MXFP4, int8: bm1 and bm2 are the lowest of the heights, the rows that are there decide
+  int choose;            // MXFP4, int8: bm1 and bm2 are the lowest of the heights, the rows that are there decide
 };
 
 // Block b of nb blocks of 1024 threads.
@@ -69,7 +71,7 @@ __device__ void build_tiles_block(const int32_t* __restrict__ offsets, const Til
     for (int h = 0; h < 3; ++h)
 #pragma unroll
       for (int w = 0; w < 16; ++w) sum[h] += tiles_s[h][w];
-    bm1 = bm2 = tile_rows_of(sum[0], sum[1], sum[2]);
+    bm1 = bm2 = p.choose == kChooseInt8 ? int8_tile_rows(sum[0], sum[2]) : fp4_tile_rows(sum[0], sum[1], sum[2]);
   }
   int c1 = 0, c2 = 0;
   if (tid < nseg) {
@@ -167,6 +169,23 @@ __global__ __launch_bounds__(1024) void build_tiles_quantize_fp4_kernel(const in
 #endif
 }
 
+// The tables of an int8 call and x in int8 (int8.h): the other blocks quantise 16 rows each.
+__global__ __launch_bounds__(1024) void build_tiles_quantize_int8_kernel(const int32_t* __restrict__ offsets,
+                                                                        TileTables p, int nb,
+                                                                        const uint4* __restrict__ x, int rows,
+                                                                        int64_t nchunk, uint2* __restrict__ dst,
+                                                                        float* __restrict__ scales) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  if ((int)blockIdx.x < nb) {
+    build_tiles_block(offsets, p, blockIdx.x, nb);
+    return;
+  }
+  const int64_t row = ((int64_t)blockIdx.x - nb) * 16 + (threadIdx.x >> 6);
+  if (row < rows)
+    int8_row<8>(x + row * nchunk, nchunk, [](int64_t q) { return q; }, dst + row * nchunk, scales + row);
+#endif
+}
+
 // Blocks that fill the larger of two tables of at most max1 and max2 entries.
 static unsigned table_blocks(int64_t max1, int64_t max2) {
   return (unsigned)std::min<int64_t>(std::max<int64_t>((std::max(max1, max2) + 1023) / 1024, 1), 64);
@@ -175,7 +194,7 @@ static unsigned table_blocks(int64_t max1, int64_t max2) {
 moe_status launch_build_tile_tables(const moe_cfg* c, const int32_t* offsets, int bm1, int bm1_alt, int nt1,
                                     int nt1s, TileDesc* t1, int64_t max1, int bm2, int bm2_alt, int nt2, TileDesc* t2,
                                     int64_t max2, int32_t* hdr, hipStream_t st) {
-  const TileTables p{c->E, c->S, c->T, bm1, bm1_alt, bm2, bm2_alt, nt1, nt1s, nt2, t1, t2, hdr, false};
+  const TileTables p{c->E, c->S, c->T, bm1, bm1_alt, bm2, bm2_alt, nt1, nt1s, nt2, t1, t2, hdr, kChooseNone};
   hipLaunchKernelGGL(build_tiles_kernel, dim3(table_blocks(max1, max2)), dim3(1024), 0, st, offsets, p);
   return launch_status();
 }
@@ -183,7 +202,7 @@ moe_status launch_build_tile_tables(const moe_cfg* c, const int32_t* offsets, in
 static TileTables ffn_tables(const moe_cfg* c, const FfnLayout& L, char* base) {
   return TileTables{c->E, c->S, c->T, L.bm1, L.bm1_alt, L.bm2, L.bm2_alt, (int)L.nt1, (int)L.nt1s, (int)L.nt2,
                     reinterpret_cast<TileDesc*>(base + L.off_t1), reinterpret_cast<TileDesc*>(base + L.off_t2),
-                    reinterpret_cast<int32_t*>(base + L.off_hdr), (c->wgt == MOE_MXFP4 && L.bm1 != kFp4RowsBM) || (c->wgt == MOE_INT8 && L.bm1 != kInt8RowsBM)};
+                    reinterpret_cast<int32_t*>(base + L.off_hdr), L.bm1 != kTileLowBM ? kChooseNone : c->wgt == MOE_MXFP4 ? kChooseFp4 : c->wgt == MOE_INT8 ? kChooseInt8 : kChooseNone};
 }
 
 moe_status launch_build_tiles(const moe_cfg* c, const int32_t* offsets, void* ws, hipStream_t st) {
@@ -202,6 +221,17 @@ moe_status launch_build_tiles_quantize_fp4(const moe_cfg* c, const int32_t* offs
   hipLaunchKernelGGL(build_tiles_quantize_fp4_kernel, dim3(nb + (unsigned)((blocks + 3) / 4)), dim3(1024), 0, st,
                      offsets, ffn_tables(c, L, base), (int)nb, (const uint4*)x, c->T, c->H, blocks,
                      (uint32_t*)(base + L.off_xq), (uint32_t*)(base + L.off_xqs));
+  return launch_status();
+}
+
+moe_status launch_build_tiles_quantize_int8(const moe_cfg* c, const int32_t* offsets, const bf16_t* x, void* ws,
+                                            hipStream_t st) {
+  const FfnLayout L(c);
+  char* base = static_cast<char*>(ws);
+  const unsigned nb = table_blocks(L.max1, L.max2);
+  hipLaunchKernelGGL(build_tiles_quantize_int8_kernel, dim3(nb + (unsigned)(((int64_t)c->T + 15) / 16)), dim3(1024), 0, st,
+                     offsets, ffn_tables(c, L, base), (int)nb, (const uint4*)x, c->T, (int64_t)c->H / 8,
+                     (uint2*)(base + L.off_xq), (float*)(base + L.off_xqs));
   return launch_status();
 }
 

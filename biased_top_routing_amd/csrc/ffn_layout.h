@@ -126,14 +126,23 @@ constexpr int kFp4BNH = 128, kFp4BN2 = 256;
 // shared experts' take the height that follows.  It leaves the height in header entry kTileRows;
 // the host sizes tables and grid for the lowest.  (One kernel for three heights is up to
 // 0.6% slower than one each.)
-__host__ __device__ inline int tile_rows_of(int n_low, int n, int n_high) {
+__host__ __device__ inline int fp4_tile_rows(int n_low, int n, int n_high) {
   if ((int64_t)5 * n_low <= (int64_t)7 * n) return kTileLowBM;
   return (int64_t)10 * n_high <= (int64_t)9 * n ? kTileHighBM : kTileBM;
 }
+__host__ __device__ inline int int8_tile_rows(int n_low, int n_high) {
+  return (int64_t)8 * n_low <= (int64_t)15 * n_high ? kTileLowBM : kTileHighBM;
+}
 constexpr int kTileRows = 6;
 
-// int8 GEMMs: tiles of 32 token rows where the pairs make at most 20 an expert, else of the heights above by the same
-// rule; 128 h columns per gate/up tile, 256 output columns per down tile.
+// int8 GEMMs: tiles of 32 token rows where the pairs make at most 20 an expert, else 128 or 288 rows, chosen by the
+// table builder as above; 128 h columns per gate/up tile, 256 output columns per down tile.
+//   A tile of 288 rows takes about twice the time of one of 128 (three stages of loads against two, and less of them
+// a product), and less where it holds few rows: it is right where 128-row tiles would be more than 1.875 times as many.
+// The whole call in us with 128 / 288 rows a tile, tiles' ratio (H = 7168, I = 2048, 256 experts, rows an expert even,
+// v; H = 2048, I = 1408, 64 experts, even, e, or Zipf 1.1, s): v112 1.06 2484 / 2760, v128 1.48 2797 / 2855, v256 2.49
+// 3910 / 3690, v384 1.75 5220 / 5170, v512 2.23 6687 / 6235, s131 1.34 219 / 258, s215 1.58 262 / 300, s384 1.85 394 /
+// 413, s768 2.10 702 / 679, e281 2.33 255 / 261, e384 1.77 396 / 382.  256 rows were never the best of three (v512 6840).
 constexpr int kInt8RowsBM = 32;
 constexpr int kInt8RowsAvg = 20;
 constexpr int kInt8BNH = 128, kInt8BN2 = 256;

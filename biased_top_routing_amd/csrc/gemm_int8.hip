@@ -152,7 +152,7 @@ __device__ __forceinline__ void gemm_int8_tiles(const Int8Params& p, uint8_t* ld
   constexpr bool A_HALF = BM % RPL != 0;
   static_assert(RPL % 16 == 0 && BN % RPL == 0 && BM % (RPL / 2) == 0 && (!A_HALF || STAGES == 2), "the loads of a slice");
   constexpr int B_OFF = BM * BK, STAGE = B_OFF + BN * BK;
-  static_assert(STAGES * STAGE <= kInt8Lds, "LDS");
+  static_assert(STAGES * STAGE <= kInt8Lds && B_CH >= 2, "LDS; the pieces that the down GEMM's outputs pass through");
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
   const int l16 = lane & 15, g = lane >> 4;
@@ -373,27 +373,50 @@ __device__ __forceinline__ void gemm_int8_tiles(const Int8Params& p, uint8_t* ld
     }
     static_assert(PER <= 2 * MI && NI == 4, "the loads fit between the products");
     // acc[mi][ni][r] holds C[i][j] with i = arow0 + 16 mi (token row), j in the order of col_off
-    bf16_t* out = o.shared ? p.out_shared : p.out_routed;
+    bf16_t* out = (o.shared ? p.out_shared : p.out_routed) + cd.row0 * (int64_t)o.ncols;
+    const int lane = opaque(threadIdx.x) & 63, l16 = lane & 15, g = lane >> 4;
+    auto packed = [](const float (&v)[8]) {
+      return make_uint4(cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]), cvt_bf16x2(v[4], v[5]), cvt_bf16x2(v[6], v[7]));
+    };
 #pragma unroll
     for (int mi = 0; mi < MI; ++mi) {
-      const int i = arow0 + mi * 16;
-      bf16_t* row = out + (cd.row0 + i) * (int64_t)o.ncols;
-#pragma unroll
-      for (int b = 0; b < (MODE == kGateUpI8 ? HALF / 2 : NI / 2); ++b) {
-        float v[8];
+      float v[8];
+      if constexpr (MODE == kGateUpI8) {
+        const int i = wm * MI * 16 + l16 + mi * 16;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const int ni = 2 * b + e / 4;
-          v[e] = (float)acc[mi][ni][e % 4] * (sa[mi] * sw[ni][e % 4]);
-          if constexpr (MODE == kGateUpI8) {
-            const float u = (float)acc[mi][ni + HALF][e % 4] * (sa[mi] * sw[ni + HALF][e % 4]);
-            v[e] = v[e] * gate_sigmoid(v[e]) * u;
-          }
+          const float gv = (float)acc[mi][e / 4][e % 4] * (sa[mi] * sw[e / 4][e % 4]);
+          const float uv = (float)acc[mi][e / 4 + HALF][e % 4] * (sa[mi] * sw[e / 4 + HALF][e % 4]);
+          v[e] = gv * gate_sigmoid(gv) * uv;
         }
-        const int col = (MODE == kGateUpI8 ? cd.nt * 128 : cd.nt * 256) + cl + b * 32;
-        if (i < cd.rows && (MODE == kGateUpI8 || col < o.ncols))
-          *reinterpret_cast<uint4*>(row + col) = make_uint4(cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]),
-                                                           cvt_bf16x2(v[4], v[5]), cvt_bf16x2(v[6], v[7]));
+        if (i < cd.rows) *reinterpret_cast<uint4*>(out + i * (int64_t)o.ncols + cd.nt * 128 + cl) = packed(v);
+      } else {
+        // 16 rows x 64 columns through two 1 KB pieces of the stage that is filled next, which only this wavefront's
+        // own loads fill (8 rows each, 16-byte chunks XOR swizzled), so that whole 128-byte row segments are stored
+        // (1.5% faster than halves of them).  (It reads back only what it wrote; its LDS operations complete in order.)
+        uint8_t* stg = lds + ls * STAGE + B_OFF + wave * 1024;
+#pragma unroll
+        for (int b = 0; b < NI; b += 2) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = (float)acc[mi][b + e / 4][e % 4] * (sa[mi] * sw[b + e / 4][e % 4]);
+          *reinterpret_cast<uint4*>(stg + (l16 >> 3) * NW * 1024 + (l16 & 7) * 128 + ((2 * b + g) ^ (l16 & 7)) * 16) =
+              packed(v);
+        }
+        __builtin_amdgcn_s_waitcnt(kLgkmWaitZero);
+        __builtin_amdgcn_wave_barrier();
+        const int col = cd.nt * 256 + wn * 64 + (lane & 7) * 8;   // (ncols is a multiple of 128: whole segments)
+#pragma unroll
+        for (int it = 0; it < 2; ++it) {
+          const int i = wm * MI * 16 + mi * 16 + it * 8 + (lane >> 3);
+          const uint4 y = *reinterpret_cast<const uint4*>(stg + it * NW * 1024 + (lane >> 3) * 128 +
+                                                         ((lane & 7) ^ (lane >> 3)) * 16);
+          typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
+          if (i < cd.rows && col < o.ncols)            // (non-temporal: 1% faster)
+            __builtin_nontemporal_store(u32x4_t{y.x, y.y, y.z, y.w},
+                                        reinterpret_cast<u32x4_t*>(out + i * (int64_t)o.ncols + col));
+        }
+        __builtin_amdgcn_s_waitcnt(kLgkmWaitZero);
+        __builtin_amdgcn_wave_barrier();
       }
     }
   }
@@ -407,12 +430,15 @@ __global__ __launch_bounds__(kInt8Threads, 1) void gemm_int8_kernel(Int8Params p
   __shared__ __attribute__((aligned(16))) uint8_t lds[kInt8Lds];
   const int bm = __builtin_amdgcn_readfirstlane(*p.tile_rows);
   if (bm == kTileLowBM) gemm_int8_tiles<MODE, kTileLowBM, 3>(p, lds);
-  else if (bm == kTileBM) gemm_int8_tiles<MODE, kTileBM, 2>(p, lds);
   else gemm_int8_tiles<MODE, kTileHighBM, 2>(p, lds);
 #endif
 }
 
 // ------------------------------------------------------------------ few rows per expert
+// The weights are read once, and past the caches (non-temporal loads: T = 128, H = 7168, 256 experts the whole call 1831
+// -> 1650 us, 6.9 TB/s; T = 1 97 -> 87; 4 / 3 stages a workgroup 87 / 81).
+constexpr int kNonTemporal = 2;
+
 // One workgroup of WM x WN wavefronts a tile (PARTS > 1: a part of one) of WM * MI * 16 token rows x WN * 64
 // weight rows.  K advances 128 bytes a slice through a ring of STAGES LDS stages filled by direct-to-LDS loads
 // (16-byte chunks, XOR swizzle per row), one barrier a slice.
@@ -457,7 +483,8 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void gemm_int8_rows_kernel(Int8Par
       __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void_t*)(sb + i * NT * 16), 16, a_off[i], ak, 0, 0);
 #pragma unroll
     for (int i = 0; i < B_CH; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void_t*)(sb + BM * BK + i * NT * 16), 16, b_off[i], wk, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void_t*)(sb + BM * BK + i * NT * 16), 16, b_off[i], wk, 0,
+                                               kNonTemporal);
   };
 #pragma unroll
   for (int s = 0; s < STAGES - 1; ++s)
@@ -544,7 +571,7 @@ moe_status launch_gemm_int8(const FfnLayout& L, int64_t max_tiles, const Int8Par
   if (max_tiles == 0) return MOE_OK;
   if (L.bm1 == kInt8RowsBM) {
     const unsigned parts = 4 * (unsigned)grouped_grid(max_tiles, kStripeInt8);
-    hipLaunchKernelGGL((gemm_int8_rows_kernel<MODE, 1, 1, 2, 4, 4>), dim3(parts), dim3(64), 0, st, p);
+    hipLaunchKernelGGL((gemm_int8_rows_kernel<MODE, 1, 1, 2, 3, 4>), dim3(parts), dim3(64), 0, st, p);
     return launch_status();
   }
   // one workgroup a CU (its LDS leaves no room for two), whole rounds of the 8 XCDs
@@ -571,11 +598,12 @@ moe_status launch_ffn_int8(const moe_cfg* c, const uint8_t* x_perm, const float*
   p.tile_rows = hdr + kTileRows;
   p.T = c->T; p.H = c->H; p.E = c->E; p.S = c->S; p.I = c->I; p.k = c->k;
   if (phase == MOE_FFN_ALL || phase == MOE_FFN_GATE_UP) {
-    if ((s = launch_build_tiles(c, offsets, ws, st)) != MOE_OK) return s;
-    // x once in int8: the shared experts' operand, and the routed one when its rows are gathered
-    if (!x_codes && (c->S > 0 || perm)) {
-      s = launch_quantize_rows_int8(x, c->T, c->H, nullptr, base + L.off_xq, floats(L.off_xqs), st);
-      if (s != MOE_OK) return s;
+    // the tile tables, and x once in int8, unless the caller has it: the shared experts' operand, and the routed one
+    // when its rows are gathered
+    const bool quantise = !x_codes && (c->S > 0 || perm);
+    s = quantise ? launch_build_tiles_quantize_int8(c, offsets, x, ws, st) : launch_build_tiles(c, offsets, ws, st);
+    if (s != MOE_OK) return s;
+    if (quantise) {
       x_codes = base + L.off_xq;
       x_scale = floats(L.off_xqs);
     }
@@ -589,11 +617,10 @@ moe_status launch_ffn_int8(const moe_cfg* c, const uint8_t* x_perm, const float*
     p.ntiles = hdr;
     if ((s = launch_gemm_int8<kGateUpI8>(L, L.max1, p, st)) != MOE_OK) return s;
     // (rows behind the last present pair of a share hold nothing)
-    s = launch_quantize_rows_int8(hb, pairs(c), c->I, offsets + c->E, base + L.off_hp, floats(L.off_hps), st);
+    s = launch_quantize_int8_pair(
+        Int8Rows{hb, pairs(c), c->I, base + L.off_hp, floats(L.off_hps)},
+        Int8Rows{hbs, c->S > 0 ? c->T : 0, c->S * c->I, base + L.off_hs, floats(L.off_hss)}, offsets + c->E, st);
     if (s != MOE_OK) return s;
-    if (c->S > 0 && (s = launch_quantize_rows_int8(hbs, c->T, c->S * c->I, nullptr, base + L.off_hs, floats(L.off_hss),
-                                                   st)) != MOE_OK)
-      return s;
   }
   if (phase == MOE_FFN_ALL || phase == MOE_FFN_DOWN) {
     p.perm = nullptr;

@@ -11,6 +11,8 @@
 
 namespace moe {
 
+constexpr int kInt8Held = 16;   // chunks of a row that a lane keeps: rows of up to 8192 columns are read once
+
 #if defined(__HIP_DEVICE_COMPILE__)
 // |v| as an integer that orders like it; infinities and NaN from kInfBits up.
 constexpr uint32_t kInfBits = 0x7F800000u;
@@ -71,6 +73,38 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t m) {
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d));
   return m;
+}
+// A row of n chunks by one wavefront: chunk q is src[at(q)], its codes go to dst[at(q)].  The chunks are read once and
+// kept where they fit HELD a lane, else read again.
+template <int HELD, class At>
+__device__ __forceinline__ void int8_row(const uint4* __restrict__ src, int64_t n, At at, uint2* __restrict__ dst,
+                                         float* __restrict__ scale) {
+  const int lane = threadIdx.x & 63;
+  uint4 v[HELD];
+  auto load = [&](int64_t q0) {
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) {
+      const int64_t q = q0 + i * kWave + lane;
+      if (q0 + i * kWave < n) v[i] = src[at(q < n ? q : n - 1)];
+      else v[i] = make_uint4(0, 0, 0, 0);
+    }
+  };
+  uint32_t m = 0;
+  for (int64_t q0 = 0; q0 < n; q0 += HELD * kWave) {
+    load(q0);
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) m = max(m, chunk_amax(v[i]));
+  }
+  const Int8Row c(wave_max(m));
+  for (int64_t q0 = 0; q0 < n; q0 += HELD * kWave) {
+    if (n > HELD * kWave) load(q0);
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) {
+      const int64_t q = q0 + i * kWave + lane;
+      if (q < n) dst[at(q)] = chunk_codes(c, v[i]);
+    }
+  }
+  if (lane == 0) *scale = c.scale;
 }
 #endif
 

@@ -61,6 +61,10 @@ moe_status launch_build_tiles(const moe_cfg* c, const int32_t* offsets, void* ws
 moe_status launch_build_tiles_quantize_fp4(const moe_cfg* c, const int32_t* offsets, const bf16_t* x, void* ws,
                                            hipStream_t st);
 
+// The same, and x [T, H] quantised to int8 into the workspace.
+moe_status launch_build_tiles_quantize_int8(const moe_cfg* c, const int32_t* offsets, const bf16_t* x, void* ws,
+                                            hipStream_t st);
+
 struct TileDesc;
 // Two tables (t1: row height bm1, or bm1_alt for a segment that needs no more
 // tiles of that height (bm1_alt = 0: never), nt1 column tiles per routed
@@ -77,9 +81,16 @@ moe_status launch_build_tile_tables(const moe_cfg* c, const int32_t* offsets, in
 moe_status launch_quantize_rows(const bf16_t* src, int64_t rows, int cols, fp8_t* dst, float* scales,
                                 hipStream_t st);
 
-// Quantises rows of bf16 values to int8 with a scale a row; limit (nullable, on the device): only the first *limit.
-moe_status launch_quantize_rows_int8(const bf16_t* src, int64_t rows, int cols, const int32_t* limit, uint8_t* dst,
-                                     float* scales, hipStream_t st);
+// Rows of bf16 values to be quantised to int8 with a scale a row: two sets, of the first one the rows up to *limit (on
+// the device).
+struct Int8Rows {
+  const bf16_t* src;
+  int64_t rows;
+  int cols;
+  uint8_t* dst;
+  float* scales;
+};
+moe_status launch_quantize_int8_pair(const Int8Rows& a, const Int8Rows& b, const int32_t* limit, hipStream_t st);
 
 // The gate/up GEMM storing its gate and up outputs (bf16, [rows, I] routed,
 // [T, S*I] shared) over a table built with the gate/up tile (kBM1 rows, kBNH

@@ -1,5 +1,7 @@
 // Quantisation of bf16 rows to int8 codes with one scale a row (int8.h): the weight preparation of the
 // int8 experts, their activations, and the SwiGLU intermediates between their two GEMMs.
+#include <algorithm>
+
 #include "common.h"
 #include "int8.h"
 #include "kernels.h"
@@ -7,58 +9,46 @@
 namespace moe {
 namespace {
 
-// One wavefront a row: the row's chunks of 16 bytes are read once and kept where they fit kHeld a lane (8192
-// columns), else read again.  A row may consist of `group` pieces of nchunk chunks, `stride` chunks apart (the
-// same row of `group` matrices).  limit (nullable): rows from *limit on are left alone.
-constexpr int kHeld = 16;
-
-__global__ __launch_bounds__(256) void quantize_int8_kernel(const uint4* __restrict__ src, int64_t rows,
-                                                            int rows_mat, int group, int64_t nchunk,
-                                                            const int32_t* __restrict__ limit,
-                                                            uint2* __restrict__ dst, float* __restrict__ scales) {
+// One wavefront a row.  A row may consist of `group` pieces of nchunk chunks, `stride` chunks apart (the same row of
+// `group` matrices).
+__global__ __launch_bounds__(256) void quantize_int8_kernel(const uint4* __restrict__ src, int64_t rows, int rows_mat,
+                                                            int group, int64_t nchunk, uint2* __restrict__ dst,
+                                                            float* __restrict__ scales) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  const int lane = threadIdx.x & 63;
   const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (row >= rows || (limit && row >= *limit)) return;
-  const int64_t mat = row / rows_mat, r = row % rows_mat;
-  const int64_t first = (mat * group * rows_mat + r) * nchunk, stride = rows_mat * nchunk;
-  const int64_t n = group * nchunk;
-  auto at = [&](int64_t q) { return group == 1 ? first + q : first + q / nchunk * stride + q % nchunk; };
-  uint4 v[kHeld];
-  auto load = [&](int64_t q0) {
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-      const int64_t q = q0 + i * kWave + lane;
-      if (q0 + i * kWave < n) v[i] = src[at(q < n ? q : n - 1)];
-      else v[i] = make_uint4(0, 0, 0, 0);
-    }
-  };
-  uint32_t m = 0;
-  for (int64_t q0 = 0; q0 < n; q0 += kHeld * kWave) {
-    load(q0);
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) m = max(m, chunk_amax(v[i]));
-  }
-  const Int8Row c(wave_max(m));
-  for (int64_t q0 = 0; q0 < n; q0 += kHeld * kWave) {
-    if (n > kHeld * kWave) load(q0);
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-      const int64_t q = q0 + i * kWave + lane;
-      if (q < n) dst[at(q)] = chunk_codes(c, v[i]);
-    }
-  }
-  if (lane == 0) scales[row] = c.scale;
+  if (row >= rows) return;
+  const int64_t first = (row / rows_mat * group * rows_mat + row % rows_mat) * nchunk, stride = rows_mat * nchunk;
+  int8_row<kInt8Held>(src, group * nchunk,
+                      [&](int64_t q) { return group == 1 ? first + q : first + q / nchunk * stride + q % nchunk; }, dst,
+                      scales + row);
+#endif
+}
+
+// Two sets of rows, the first one's up to *limit (h of the routed rows, of which a share has fewer than there is room
+// for, and of the shared experts: one launch of 4.4 us saved a call).  HELD 4 for rows of at most 2048 columns.
+template <int HELD>
+__global__ __launch_bounds__(256) void quantize_int8_pair_kernel(Int8Rows a, Int8Rows b, int64_t a_blocks,
+                                                                 const int32_t* __restrict__ limit) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const bool second = blockIdx.x >= a_blocks;
+  const Int8Rows& s = second ? b : a;
+  const int64_t row = ((int64_t)blockIdx.x - (second ? a_blocks : 0)) * 4 + (threadIdx.x >> 6);
+  if (row >= (second ? s.rows : (int64_t)*limit)) return;
+  const int64_t n = s.cols / 8;
+  int8_row<HELD>((const uint4*)s.src + row * n, n, [](int64_t q) { return q; }, (uint2*)s.dst + row * n, s.scales + row);
 #endif
 }
 
 }  // namespace
 
-moe_status launch_quantize_rows_int8(const bf16_t* src, int64_t rows, int cols, const int32_t* limit, uint8_t* dst,
-                                     float* scales, hipStream_t st) {
-  if (rows == 0) return MOE_OK;
-  hipLaunchKernelGGL(quantize_int8_kernel, dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, st, (const uint4*)src, rows,
-                     (int)(rows < INT32_MAX ? rows : INT32_MAX), 1, (int64_t)cols / 8, limit, (uint2*)dst, scales);
+moe_status launch_quantize_int8_pair(const Int8Rows& a, const Int8Rows& b, const int32_t* limit, hipStream_t st) {
+  const int64_t na = (a.rows + 3) / 4, nb = (b.rows + 3) / 4;
+  if (na + nb == 0) return MOE_OK;
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(na + nb)), dim3(256), 0, st, a, b, na, limit);
+  };
+  if (std::max(a.cols, b.cols) <= 2048) go(quantize_int8_pair_kernel<4>);
+  else go(quantize_int8_pair_kernel<kInt8Held>);
   return launch_status();
 }
 
@@ -75,7 +65,6 @@ extern "C" moe_status moe_quantize_int8(const void* src_bf16, int32_t n_mat, int
   if (!src_bf16 || !dst || !scales) return MOE_ERR_NULL;
   if (misaligned(src_bf16, 16) || misaligned(dst, 8) || misaligned(scales, 4)) return MOE_ERR_UNSUPPORTED;
   hipLaunchKernelGGL(quantize_int8_kernel, dim3((unsigned)((n + 3) / 4)), dim3(256), 0, as_stream(stream),
-                     (const uint4*)src_bf16, n, rows, group, (int64_t)cols / 8, (const int32_t*)nullptr, (uint2*)dst,
-                     scales);
+                     (const uint4*)src_bf16, n, rows, group, (int64_t)cols / 8, (uint2*)dst, scales);
   return launch_status();
 }
