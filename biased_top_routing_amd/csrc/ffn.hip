@@ -56,7 +56,7 @@ __device__ void build_tiles_block(const int32_t* __restrict__ offsets, const Til
     int n[3] = {0, 0, 0};
     if (tid < E) {
       n[0] = (rows + kTileLowBM - 1) / kTileLowBM;
-      n[1] = (rows + kTileBM - 1) / kTileBM;
+      n[1] = p.choose == kChooseInt8 ? rows > 0 : (rows + kTileBM - 1) / kTileBM;
       n[2] = (rows + kTileHighBM - 1) / kTileHighBM;
     }
 #pragma unroll
@@ -71,7 +71,12 @@ __device__ void build_tiles_block(const int32_t* __restrict__ offsets, const Til
     for (int h = 0; h < 3; ++h)
 #pragma unroll
       for (int w = 0; w < 16; ++w) sum[h] += tiles_s[h][w];
-    bm1 = bm2 = p.choose == kChooseInt8 ? int8_tile_rows(sum[0], sum[2]) : fp4_tile_rows(sum[0], sum[1], sum[2]);
+    if (p.choose == kChooseInt8) {
+      bm1 = bm2 = int8_tile_rows(sum[0], sum[2]);
+      if (tid == 0 && b == 0) hdr[kTileOnce] = int8_weights_once(sum[0], sum[1]);
+    } else {
+      bm1 = bm2 = fp4_tile_rows(sum[0], sum[1], sum[2]);
+    }
   }
   int c1 = 0, c2 = 0;
   if (tid < nseg) {

@@ -133,10 +133,17 @@ __host__ __device__ inline int fp4_tile_rows(int n_low, int n, int n_high) {
 __host__ __device__ inline int int8_tile_rows(int n_low, int n_high) {
   return (int64_t)8 * n_low <= (int64_t)15 * n_high ? kTileLowBM : kTileHighBM;
 }
-constexpr int kTileRows = 6;
+// Whether nearly every 128-row tile of int8 weights is the only one of its expert: its weights are then read past the
+// caches, for nobody else will (the whole call in us with and without, first layer above: v32 1.00 tiles an expert 1919
+// / 2040, v64 1.00 2094 / 2153, v112 1.07 2428 / 2441; where experts have several tiles it costs: s384 430 / 416).
+__host__ __device__ inline int int8_weights_once(int n_low, int n_experts) {
+  return (int64_t)4 * n_low <= (int64_t)5 * n_experts;
+}
+constexpr int kTileRows = 6, kTileOnce = 7;
 
-// int8 GEMMs: tiles of 32 token rows where the pairs make at most 20 an expert, else 128 or 288 rows, chosen by the
-// table builder as above; 128 h columns per gate/up tile, 256 output columns per down tile.
+// int8 GEMMs: tiles of 32 token rows where the pairs make at most 12 an expert (32 / 128 rows a tile, us, the layers
+// below: v8 1726 / 1737, v16 1836 / 1825, e9 118 / 118, e19 129 / 117), else 128 or 288 rows, chosen by the table builder
+// as above; 128 h columns per gate/up tile, 256 output columns per down tile.
 //   A tile of 288 rows takes about twice the time of one of 128 (three stages of loads against two, and less of them
 // a product), and less where it holds few rows: it is right where 128-row tiles would be more than 1.875 times as many.
 // The whole call in us with 128 / 288 rows a tile, tiles' ratio (H = 7168, I = 2048, 256 experts, rows an expert even,
@@ -144,7 +151,7 @@ constexpr int kTileRows = 6;
 // 3910 / 3690, v384 1.75 5220 / 5170, v512 2.23 6687 / 6235, s131 1.34 219 / 258, s215 1.58 262 / 300, s384 1.85 394 /
 // 413, s768 2.10 702 / 679, e281 2.33 255 / 261, e384 1.77 396 / 382.  256 rows were never the best of three (v512 6840).
 constexpr int kInt8RowsBM = 32;
-constexpr int kInt8RowsAvg = 20;
+constexpr int kInt8RowsAvg = 12;
 constexpr int kInt8BNH = 128, kInt8BN2 = 256;
 constexpr int kInt8MaxK = 1 << 17;   // K of a GEMM stays below: 128 * 128 * K fits the accumulators
 

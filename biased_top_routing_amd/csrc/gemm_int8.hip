@@ -22,6 +22,8 @@ typedef int i32x4_t __attribute__((ext_vector_type(4)));
 
 namespace {
 
+constexpr int kNonTemporal = 2;   // the loads' cache policy
+
 enum { kGateUpI8 = 1, kDownI8 = 2 };
 
 struct Int8Params {
@@ -37,7 +39,7 @@ struct Int8Params {
   bf16_t* out_shared;
   const TileDesc* tiles;
   const int32_t* ntiles;
-  const int32_t* tile_rows;   // rows per tile
+  const int32_t* tile_rows;   // rows per tile, and whether weights are read once (header entries kTileRows, kTileOnce)
   const int32_t* perm;        // gate/up: non-null -> routed rows gathered from a_shared / sa_shared
   int T, H, E, S, I, k;
 };
@@ -139,8 +141,8 @@ __device__ __forceinline__ int opaque(int v) {
   return v;
 }
 
-// The GEMM over tiles of BM rows.
-template <int MODE, int BM, int STAGES>
+// The GEMM over tiles of BM rows; ONCE: weights past the caches.
+template <int MODE, int BM, int STAGES, bool ONCE>
 __device__ __forceinline__ void gemm_int8_tiles(const Int8Params& p, uint8_t* lds) {
   constexpr int WM = 2, WN = 4, NT = kInt8Threads, NW = NT / 64, BN = 256;
   constexpr int MI = BM / (WM * 16), NI = BN / (WN * 16), HALF = NI / 2;
@@ -245,7 +247,8 @@ __device__ __forceinline__ void gemm_int8_tiles(const Int8Params& p, uint8_t* ld
                                                s.ak, 0, 0);
     else
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          s.w, dst, 16, b_off + (i - A_CH) * w_dist + ((i - A_CH) * RPL >= 128 ? w_gap : 0), s.wk, 0, 0);
+          s.w, dst, 16, b_off + (i - A_CH) * w_dist + ((i - A_CH) * RPL >= 128 ? w_gap : 0), s.wk, 0,
+          ONCE ? kNonTemporal : 0);
   };
   // After a slice's loads.
   auto advance = [&]() {
@@ -429,16 +432,16 @@ __global__ __launch_bounds__(kInt8Threads, 1) void gemm_int8_kernel(Int8Params p
 #if defined(__HIP_DEVICE_COMPILE__)
   __shared__ __attribute__((aligned(16))) uint8_t lds[kInt8Lds];
   const int bm = __builtin_amdgcn_readfirstlane(*p.tile_rows);
-  if (bm == kTileLowBM) gemm_int8_tiles<MODE, kTileLowBM, 3>(p, lds);
-  else gemm_int8_tiles<MODE, kTileHighBM, 2>(p, lds);
+  const int once = __builtin_amdgcn_readfirstlane(p.tile_rows[kTileOnce - kTileRows]);
+  if (bm != kTileLowBM) gemm_int8_tiles<MODE, kTileHighBM, 2, false>(p, lds);
+  else if (once) gemm_int8_tiles<MODE, kTileLowBM, 3, true>(p, lds);
+  else gemm_int8_tiles<MODE, kTileLowBM, 3, false>(p, lds);
 #endif
 }
 
 // ------------------------------------------------------------------ few rows per expert
 // The weights are read once, and past the caches (non-temporal loads: T = 128, H = 7168, 256 experts the whole call 1831
 // -> 1650 us, 6.9 TB/s; T = 1 97 -> 87; 4 / 3 stages a workgroup 87 / 81).
-constexpr int kNonTemporal = 2;
-
 // One workgroup of WM x WN wavefronts a tile (PARTS > 1: a part of one) of WM * MI * 16 token rows x WN * 64
 // weight rows.  K advances 128 bytes a slice through a ring of STAGES LDS stages filled by direct-to-LDS loads
 // (16-byte chunks, XOR swizzle per row), one barrier a slice.
