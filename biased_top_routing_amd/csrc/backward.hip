@@ -458,14 +458,50 @@ __global__ __launch_bounds__(256) void route_grad_flags_kernel(const float* __re
 #endif
 }
 
-// Two copies of the router weight [E, H], each in Ep rows, zero behind E.
-__global__ __launch_bounds__(256) void router_weight_twice_kernel(const uint4* __restrict__ w, int E, int Ep,
-                                                                  int64_t nchunk, uint4* __restrict__ out) {
-  const int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (q >= (int64_t)Ep * nchunk) return;
-  const uint4 v = q < (int64_t)E * nchunk ? w[q] : make_uint4(0, 0, 0, 0);
-  out[q] = v;
-  out[(int64_t)Ep * nchunk + q] = v;
+// seq_coef_kernel spread over the chip: workgroup (b, 64 experts from e0), each of its wavefronts a quarter of the
+// sequence's chunks, and the partial loss of the 64 in part_loss (T = 16384, E = 256, 4 sequences: 71 us by one
+// workgroup).
+__global__ __launch_bounds__(256) void seq_coef_part_kernel(const int32_t* __restrict__ cnt,
+                                                            const float* __restrict__ psum, int E, int k, int L,
+                                                            int nseq, int nchunk, float alpha, float* __restrict__ coef,
+                                                            float* __restrict__ part_loss) {
+  const int ne = (E + 63) / 64, b = blockIdx.x / ne, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int e = blockIdx.x % ne * 64 + lane;
+  __shared__ int c_s[4][64];
+  __shared__ float p_s[4][64];
+  int c = 0;
+  float ps = 0.f;
+  if (e < E)
+    for (int ch = wave; ch < nchunk; ch += 4) {
+      c += cnt[((int64_t)b * nchunk + ch) * E + e];
+      ps += psum[((int64_t)b * nchunk + ch) * E + e];
+    }
+  c_s[wave][lane] = c;
+  p_s[wave][lane] = ps;
+  __syncthreads();
+  if (wave > 0) return;
+  c = c_s[0][lane] + c_s[1][lane] + c_s[2][lane] + c_s[3][lane];
+  ps = p_s[0][lane] + p_s[1][lane] + p_s[2][lane] + p_s[3][lane];
+  const float f = (float)E / ((float)k * (float)L) * (float)c;
+  if (e < E) coef[(int64_t)b * E + e] = alpha / (float)nseq * f / (float)L;
+  const float sum = wave_sum(e < E ? f * (ps / (float)L) : 0.f);
+  if (lane == 0) part_loss[blockIdx.x] = sum;
+}
+
+// loss = alpha / nseq * the sum of n partial losses, in a fixed order.
+__global__ __launch_bounds__(1024) void seq_loss_kernel(const float* __restrict__ part_loss, int n, float alpha,
+                                                        int nseq, float* __restrict__ loss) {
+  __shared__ float s[16];
+  float v = 0.f;
+  for (int i = threadIdx.x; i < n; i += 1024) v += part_loss[i];
+  v = wave_sum(v);
+  if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    v = 0.f;
+    for (int i = 0; i < 16; ++i) v += s[i];
+    *loss = n > 0 ? alpha / (float)nseq * v : 0.f;
+  }
 }
 
 bool bwd_dtypes_ok(const moe_cfg* c) { return c->act == MOE_BF16 && c->wgt == MOE_BF16; }
@@ -570,10 +606,8 @@ moe_status route_backward(const moe_cfg* cfg, bool with_flags, uint32_t flags, c
   if (!bwd_dtypes_ok(cfg)) return MOE_ERR_UNSUPPORTED;
   if (with_flags) {
     if (!flags || (flags & ~(MOE_SOFTMAX | MOE_GATES_RAW))) return MOE_ERR_UNSUPPORTED;
-    // (one descriptor covers the two copies of the router weight, and one the 1024 rows of x of a partial sum)
-    if (align_up(cfg->E, 64) * (int64_t)cfg->H * 4 >= (int64_t)1 << 31 || cfg->H >= 1 << 20) return MOE_ERR_UNSUPPORTED;
     if (misaligned(x, 16) || misaligned(w_router, 16) || misaligned(ws, 16) || misaligned(scores, 4) ||
-        misaligned(topk_idx, 4) || misaligned(d_topk_w, 4) || misaligned(dx_router, 4) || misaligned(dw_router, 4) ||
+        misaligned(topk_idx, 4) || misaligned(d_topk_w, 4) || misaligned(dx_router, 4) || misaligned(dw_router, 16) ||
         misaligned(loss, 4))
       return MOE_ERR_UNSUPPORTED;
   }
@@ -581,6 +615,7 @@ moe_status route_backward(const moe_cfg* cfg, bool with_flags, uint32_t flags, c
   if (!(alpha >= 0.0f) || !isfinite(alpha)) return MOE_ERR_SHAPE;
   if (seq_len < 0 || (seq_len > 0 && cfg->T % seq_len != 0)) return MOE_ERR_SHAPE;
   const RouteBwdLayout L(cfg, seq_len, with_flags ? 2 : 1);
+  if (with_flags && (cfg->T >= 1 << 23 || (int64_t)L.nseq * ((cfg->E + 63) / 64) >= 1 << 24)) return MOE_ERR_SHAPE;
   if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
   hipStream_t s = as_stream(stream);
   char* base = static_cast<char*>(ws);
@@ -600,16 +635,25 @@ moe_status route_backward(const moe_cfg* cfg, bool with_flags, uint32_t flags, c
                        cfg->T, cfg->E, cfg->k, L.seq_len, L.nchunk, cnt, psum);
     if ((st = launch_status()) != MOE_OK) return st;
   }
-  hipLaunchKernelGGL(seq_coef_kernel, dim3(1), dim3(256), 0, s, cnt, psum, cfg->E, cfg->k, L.seq_len,
-                     bal ? L.nseq : 0, L.nchunk, alpha, coef, loss);
+  if (with_flags) {
+    float* part_loss = reinterpret_cast<float*>(base + L.off_loss);
+    const int np = bal ? L.nseq * ((cfg->E + 63) / 64) : 0;
+    if (bal)
+      hipLaunchKernelGGL(seq_coef_part_kernel, dim3((unsigned)np), dim3(256), 0, s, cnt, psum, cfg->E, cfg->k, L.seq_len,
+                         L.nseq, L.nchunk, alpha, coef, part_loss);
+    hipLaunchKernelGGL(seq_loss_kernel, dim3(1), dim3(1024), 0, s, part_loss, np, alpha, L.nseq, loss);
+  } else {
+    hipLaunchKernelGGL(seq_coef_kernel, dim3(1), dim3(256), 0, s, cnt, psum, cfg->E, cfg->k, L.seq_len,
+                       bal ? L.nseq : 0, L.nchunk, alpha, coef, loss);
+  }
   if ((st = launch_status()) != MOE_OK) return st;
   const dim3 tokens((unsigned)((cfg->T + 3) / 4));
   if (!with_flags) {
     hipLaunchKernelGGL(route_grad_kernel, tokens, dim3(256), 0, s, scores, topk_idx, d_topk_w, bal ? coef : nullptr,
                        cfg->T, cfg->E, cfg->k, L.seq_len, cfg->route_scale, dlogit);
     if ((st = launch_status()) != MOE_OK) return st;
-    return launch_router_bwd_gemms(cfg, (const bf16_t*)x, (const bf16_t*)w_router, dlogit, cfg->E, 1, part, L.nsplit,
-                                   dw_router, dx_router, s);
+    return launch_router_bwd_gemms(cfg, (const bf16_t*)x, (const bf16_t*)w_router, dlogit, part, L.nsplit, dw_router,
+                                   dx_router, s);
   }
   auto grad = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, tokens, dim3(256), 0, s, scores, topk_idx, d_topk_w, bal ? coef : nullptr, cfg->T, cfg->E,
@@ -618,14 +662,7 @@ moe_status route_backward(const moe_cfg* cfg, bool with_flags, uint32_t flags, c
   if (flags & MOE_SOFTMAX) grad(route_grad_flags_kernel<true>);
   else grad(route_grad_flags_kernel<false>);
   if ((st = launch_status()) != MOE_OK) return st;
-  bf16_t* w2 = reinterpret_cast<bf16_t*>(base + L.off_w);
-  if (dx_router) {
-    const int64_t nchunk = (int64_t)cfg->H / 8;
-    hipLaunchKernelGGL(router_weight_twice_kernel, dim3((unsigned)((L.Ep * nchunk + 255) / 256)), dim3(256), 0, s,
-                       (const uint4*)w_router, cfg->E, L.Ep, nchunk, (uint4*)w2);
-    if ((st = launch_status()) != MOE_OK) return st;
-  }
-  return launch_router_bwd_gemms(cfg, (const bf16_t*)x, w2, dlogit, L.Ep, 2, part, L.nsplit, dw_router, dx_router, s);
+  return launch_router_bwd_gemms2(cfg, L, (const bf16_t*)x, (const bf16_t*)w_router, dlogit, part, dw_router, dx_router, s);
 }
 
 }  // namespace

@@ -1,6 +1,8 @@
 // Workspace layouts of the backward calls (host and device agree on them).
 #pragma once
 
+#include <algorithm>
+
 #include "common.h"
 #include "ffn_layout.h"
 
@@ -83,17 +85,18 @@ constexpr int kSeqChunk = 64;      // tokens per statistics chunk
 constexpr int kRouterKSplit = 1024;  // token rows per split of the router-weight gradient
 
 struct RouteBwdLayout {
-  int nseq, seq_len, nchunk, nsplit;
-  int Ep;
-  size_t off_cnt, off_psum, off_coef, off_dlogit, off_part, off_w, total;
+  int nseq, seq_len, nchunk, nsplit, ksplit, Ep;
+  size_t off_cnt, off_psum, off_coef, off_loss, off_dlogit, off_part, total;
 
   // terms 2: dlogit as the sum of two bf16 numbers, in rows of 2 * Ep (Ep: E rounded up to 64; columns [0, Ep) the
-  // leading terms, then the rest, zero behind E), for products with two copies of the router weight
+  // leading terms, then the rest, zero behind E)
   RouteBwdLayout(const moe_cfg* c, int seq, int terms = 1) {
     seq_len = seq > 0 ? seq : (c->T > 0 ? c->T : 1);
     nseq = c->T / seq_len;
     nchunk = (seq_len + kSeqChunk - 1) / kSeqChunk;
-    nsplit = (c->T + kRouterKSplit - 1) / kRouterKSplit;
+    Ep = terms == 1 ? c->E : (int)align_up(c->E, 64);
+    ksplit = terms == 1 ? kRouterKSplit : router_ksplit(c->T, Ep, c->H);
+    nsplit = (c->T + ksplit - 1) / ksplit;
     // sizes from bounds that hold for every sequence length (nseq * nchunk <=
     // T + T / 64 + 1, nseq <= T), so the workspace size does not depend on it
     const size_t chunks_max = (size_t)c->T + c->T / kSeqChunk + 1, seqs_max = (size_t)(c->T > 0 ? c->T : 1);
@@ -102,11 +105,17 @@ struct RouteBwdLayout {
     off_cnt = take(chunks_max * c->E * 4);
     off_psum = take(chunks_max * c->E * 4);
     off_coef = take(seqs_max * c->E * 4);
-    Ep = terms == 1 ? c->E : (int)align_up(c->E, 64);
+    off_loss = take(terms == 1 ? 0 : seqs_max * (Ep / 64) * 4);
     off_dlogit = take((size_t)c->T * terms * Ep * 2);
-    off_part = take((size_t)nsplit * terms * Ep * c->H * 4);
-    off_w = take(terms == 1 ? 0 : (size_t)2 * Ep * c->H * 2);
+    off_part = take((size_t)nsplit * Ep * c->H * 4);
     total = o;
+  }
+  // Token rows a partial sum of dW_r: whole 64-row slices, such that the tiles of 256 x 256 make about one workgroup a
+  // CU (fewer leave CUs idle, more write and read more partial sums), and 32-bit offsets into the split's rows.
+  static int router_ksplit(int64_t T, int64_t Ep, int64_t H) {
+    const int64_t tiles = (Ep + 255) / 256 * ((H + 255) / 256), splits = std::max<int64_t>(1, 256 / tiles);
+    const int64_t most = std::max<int64_t>(64, ((int64_t)1 << 30) / (std::max(H, 2 * Ep) * 2) / 64 * 64);
+    return (int)std::min<int64_t>(most, std::max<int64_t>(64, ((T + splits - 1) / splits + 63) / 64 * 64));
   }
 };
 

@@ -30,6 +30,12 @@
 //         M-contiguous; rows past the segment's end read as zero); fp32 stores.
 //   kDwR  K-segmented over fixed splits of the T tokens (fp32 partial sums,
 //         reduced in order afterwards, so the result does not depend on timing).
+//   kDxR2 / kDwR2  the same with dlogit as the sum of two bf16 numbers (rows of
+//         2 Ep columns, Ep = p.E a multiple of 64, the leading terms first): the
+//         walk over K passes over W_r, or over the split's tokens, once for either,
+//         into the same accumulators.  (As products of twice the size, with two
+//         copies of W_r and two sets of partial sums: T = 16384, E = 256, H = 7168
+//         dW_r and its reduction 256 us.)
 #include "bwd_layout.h"
 #include "common.h"
 #include "ffn_layout.h"
@@ -38,7 +44,9 @@
 
 namespace moe {
 
-enum { kDh = 0, kDx = 1, kDxR = 2, kDwGu = 3, kDwD = 4, kDwR = 5 };
+enum { kDh = 0, kDx = 1, kDxR = 2, kDwGu = 3, kDwD = 4, kDwR = 5, kDwR2 = 6, kDxR2 = -1 };
+constexpr bool is_dxr(int kind) { return kind == kDxR || kind == kDxR2; }
+constexpr bool is_dwr(int kind) { return kind == kDwR || kind == kDwR2; }
 constexpr int dw_stripe(int kind) { return kind == kDwGu ? kStripeDwGu : kStripeDwD; }
 constexpr bool kseg_kind(int kind) { return kind >= kDwGu; }
 
@@ -59,7 +67,8 @@ struct BwdParams {
   const int32_t* ntiles;
   const int32_t* offsets;   // K-segmented kinds: the experts' token-row segments
   int T, H, E, S, I;
-  int ksplit;               // kDwR: token rows per split
+  int ksplit;               // kDwR, kDwR2: token rows per split
+  int w_rows;               // kDxR2: rows of W_r (at most E)
 };
 
 typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
@@ -117,7 +126,8 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void gemm_bwd_kernel(BwdParams p
   const bf16_t* A = nullptr;
   const bf16_t* B = nullptr;
   int lda = 0, ldb = 0, a_bytes = 0, b_bytes = 0;
-  if constexpr (KIND == kDxR) {
+  if constexpr (is_dxr(KIND)) {
+    constexpr int TERMS = KIND == kDxR2 ? 2 : 1;
     const int ntn = (p.H + BN - 1) / BN;
     const int rt = blockIdx.x / ntn, nt = blockIdx.x % ntn;
     m0 = rt * BM;
@@ -125,12 +135,12 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void gemm_bwd_kernel(BwdParams p
     if (mvalid <= 0) return;
     n0 = nt * BN;
     N = p.H;
-    A = p.a_shared + (int64_t)m0 * p.E;
-    lda = p.E;
-    K = p.E;
+    lda = TERMS * p.E;
+    A = p.a_shared + (int64_t)m0 * lda;
+    K = lda;
     B = p.b_shared;
     ldb = p.H;
-    b_bytes = p.E * p.H * 2;
+    b_bytes = (TERMS == 2 ? p.w_rows : p.E) * p.H * 2;
   } else if constexpr (!KSEG) {
     const int L = grouped_tile<0>(p.ntiles);
     if (L < 0) return;
@@ -162,7 +172,7 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void gemm_bwd_kernel(BwdParams p
     // K-segmented: one tile of one gradient; M x N and the token rows it reduces over
     int M, local, ntn;
     int64_t krow0 = 0;
-    if constexpr (KIND == kDwR) {
+    if constexpr (is_dwr(KIND)) {
       M = p.E;
       N = p.H;
       const int mtn = (M + BM - 1) / BM;
@@ -172,8 +182,8 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void gemm_bwd_kernel(BwdParams p
       krow0 = (int64_t)split * p.ksplit;
       K = min(p.ksplit, p.T - (int)krow0);
       if (K < 0) return;
-      A = p.a_shared + krow0 * p.E;
-      lda = p.E;
+      lda = (KIND == kDwR2 ? 2 : 1) * p.E;
+      A = p.a_shared + krow0 * lda;
       B = p.b_shared + krow0 * p.H;
       ldb = p.H;
     } else {
@@ -253,12 +263,18 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void gemm_bwd_kernel(BwdParams p
     b_off[i] = (r * ldb + cmap) * 2;
   }
   const __amdgpu_buffer_rsrc_t rsrc_a_kc = make_rsrc(A, A_MC ? 0 : mvalid * lda * 2);
+  // slices of one term; the second term's: dW_r's tokens once more, dlogit Ep columns on; dx's W_r once more
+  const int nk1 = (K + BK - 1) / BK;
 #define MOE_ISSUE_BWD(stage_, k0_)                                                                    \
   {                                                                                                   \
-    const int k0v = (k0_);                                                                            \
+    const int kq = (k0_);                                                                             \
+    const bool again = (KIND == kDwR2 && kq >= nk1 * BK) || (KIND == kDxR2 && kq >= p.E);             \
+    const int k0v = KIND == kDwR2 && again ? kq - nk1 * BK : kq;                                      \
+    const int a_on = KIND == kDwR2 && again ? p.E : 0;                                                \
     bf16_t* sb = lds + (stage_) * STAGE;                                                              \
     if constexpr (A_MC) {                                                                             \
-      const __amdgpu_buffer_rsrc_t ra = make_rsrc(A + (int64_t)k0v * lda, max(0, a_bytes - k0v * lda * 2)); \
+      const __amdgpu_buffer_rsrc_t ra =                                                               \
+          make_rsrc(A + (int64_t)k0v * lda + a_on, max(0, a_bytes - (k0v * lda + a_on) * 2));         \
       _Pragma("unroll") for (int i = 0; i < A_CH; ++i)                                                \
           __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void_t*)(sb + (i * NW + wave) * 512), 16,  \
                                                    a_off[i], 0, 0, 0);                                \
@@ -267,7 +283,8 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void gemm_bwd_kernel(BwdParams p
           __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc_a_kc, (lds_void_t*)(sb + (i * NW + wave) * 512), \
                                                    16, a_off[i], k0v * 2, 0, 0);                      \
     }                                                                                                 \
-    const __amdgpu_buffer_rsrc_t rb = make_rsrc(B + (int64_t)k0v * ldb, max(0, b_bytes - k0v * ldb * 2)); \
+    const int kb = KIND == kDxR2 && again ? kq - p.E : k0v;                                           \
+    const __amdgpu_buffer_rsrc_t rb = make_rsrc(B + (int64_t)kb * ldb, max(0, b_bytes - kb * ldb * 2)); \
     _Pragma("unroll") for (int i = 0; i < B_CH; ++i)                                                  \
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void_t*)(sb + BM * BK + (i * NW + wave) * 512), \
                                                  16, b_off[i], 0, 0, 0);                              \
@@ -286,7 +303,7 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void gemm_bwd_kernel(BwdParams p
   for (int mi = 0; mi < MI; ++mi) a_rd[mi] = wm * MI * 32 + mi * 32 + lr;
   const bool has_rows = wm * MI * 32 < mvalid;
 
-  const int nk = (K + BK - 1) / BK;
+  const int nk = (KIND == kDwR2 ? 2 : 1) * nk1;
 #pragma unroll
   for (int s = 0; s < STAGES - 1; ++s)
     if (s < nk) MOE_ISSUE_BWD(s, s * BK);
@@ -478,7 +495,7 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void gemm_bwd_kernel(BwdParams p
         const int col = n0 + wn * NI * 32 + ni * 32 + lr;
         if (col >= N) continue;
         const float v = acc[mi][ni][r];
-        if constexpr (KIND == kDxR) {
+        if constexpr (is_dxr(KIND)) {
           static_cast<float*>(p.out_shared)[row * N + col] = v;
         } else if constexpr (KIND == kDwGu) {
           float* o = shared ? static_cast<float*>(p.out_shared)
@@ -497,17 +514,27 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void gemm_bwd_kernel(BwdParams p
 #endif   // __HIP_DEVICE_COMPILE__
 }
 
-// dW_r = sum over the splits of the partial sums, in split order: n values, `stride` between the splits; second > 0:
-// and of the second terms' sums, that far behind the first.
+// dW_r = sum over the splits of the partial sums, in split order.
 __global__ __launch_bounds__(256) void reduce_splits_kernel(const float* __restrict__ part, int nsplit,
-                                                            int64_t n, int64_t stride, int64_t second,
-                                                            float* __restrict__ out) {
+                                                            int64_t n, float* __restrict__ out) {
   const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (i >= n) return;
   float s = 0.f;
-  for (int k = 0; k < nsplit; ++k) s += part[(int64_t)k * stride + i];
-  if (second > 0)
-    for (int k = 0; k < nsplit; ++k) s += part[(int64_t)k * stride + second + i];
+  for (int k = 0; k < nsplit; ++k) s += part[(int64_t)k * n + i];
+  out[i] = s;
+}
+
+// ... of n float4 each, `stride` apart.
+__global__ __launch_bounds__(256) void reduce_splits4_kernel(const float4* __restrict__ part, int nsplit, int64_t n,
+                                                             int64_t stride, float4* __restrict__ out) {
+  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= n) return;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int k = 0; k < nsplit; ++k) {
+    const float4 v = part[(int64_t)k * stride + i];
+    s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+  }
   out[i] = s;
 }
 
@@ -611,23 +638,22 @@ moe_status launch_ffn_bwd_bf16(const moe_cfg* c, const bf16_t* x_perm, const bf1
 }
 
 moe_status launch_router_bwd_gemms(const moe_cfg* c, const bf16_t* x, const bf16_t* w_router,
-                                   const bf16_t* dlogit, int Ep, int terms, float* part, int nsplit, float* dw_router,
+                                   const bf16_t* dlogit, float* part, int nsplit, float* dw_router,
                                    float* dx_router, hipStream_t st) {
   BwdParams p{};
-  const int rows = terms * Ep;
-  p.T = c->T; p.H = c->H; p.E = rows; p.S = c->S; p.I = c->I;
+  p.T = c->T; p.H = c->H; p.E = c->E; p.S = c->S; p.I = c->I;
   p.ksplit = kRouterKSplit;
   p.a_shared = dlogit;
   p.b_shared = x;
   p.out_routed = part;
-  const int64_t tiles = (int64_t)((rows + kBwdBM - 1) / kBwdBM) * ((c->H + kBwdBN - 1) / kBwdBN);
+  const int64_t tiles = (int64_t)((c->E + kBwdBM - 1) / kBwdBM) * ((c->H + kBwdBN - 1) / kBwdBN);
   hipLaunchKernelGGL((gemm_bwd_kernel<kDwR, MOE_BWD_TILE>), dim3((unsigned)(tiles * nsplit)), dim3(kBwdThreads),
                      0, st, p);
   moe_status s;
   if ((s = launch_status()) != MOE_OK) return s;
   const int64_t n = (int64_t)c->E * c->H;
   hipLaunchKernelGGL(reduce_splits_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, part, nsplit, n,
-                     (int64_t)rows * c->H, terms == 2 ? (int64_t)Ep * c->H : 0, dw_router);
+                     dw_router);
   if ((s = launch_status()) != MOE_OK) return s;
   if (dx_router) {
     p.b_shared = w_router;
@@ -638,6 +664,33 @@ moe_status launch_router_bwd_gemms(const moe_cfg* c, const bf16_t* x, const bf16
     if ((s = launch_status()) != MOE_OK) return s;
   }
   return MOE_OK;
+}
+
+moe_status launch_router_bwd_gemms2(const moe_cfg* c, const RouteBwdLayout& L, const bf16_t* x, const bf16_t* w_router,
+                                    const bf16_t* dlogit, float* part, float* dw_router, float* dx_router,
+                                    hipStream_t st) {
+  BwdParams p{};
+  p.T = c->T; p.H = c->H; p.E = L.Ep; p.S = c->S; p.I = c->I;
+  p.ksplit = L.ksplit;
+  p.w_rows = c->E;
+  p.a_shared = dlogit;
+  p.b_shared = x;
+  p.out_routed = part;
+  const int64_t tiles = (int64_t)((L.Ep + kBwdBM - 1) / kBwdBM) * ((c->H + kBwdBN - 1) / kBwdBN);
+  hipLaunchKernelGGL((gemm_bwd_kernel<kDwR2, MOE_BWD_TILE>), dim3((unsigned)(tiles * L.nsplit)), dim3(kBwdThreads), 0, st,
+                     p);
+  moe_status s;
+  if ((s = launch_status()) != MOE_OK) return s;
+  const int64_t n = (int64_t)c->E * c->H;              // (the rows behind E are not summed)
+  hipLaunchKernelGGL(reduce_splits4_kernel, dim3((unsigned)((n / 4 + 255) / 256)), dim3(256), 0, st, (const float4*)part,
+                     L.nsplit, n / 4, (int64_t)L.Ep * c->H / 4, (float4*)dw_router);
+  if ((s = launch_status()) != MOE_OK || !dx_router) return s;
+  p.b_shared = w_router;
+  p.out_shared = dx_router;
+  const int64_t rt = (c->T + kBwdBM - 1) / kBwdBM;
+  hipLaunchKernelGGL((gemm_bwd_kernel<kDxR2, MOE_BWD_TILE>), dim3((unsigned)(rt * ((c->H + kBwdBN - 1) / kBwdBN))),
+                     dim3(kBwdThreads), 0, st, p);
+  return launch_status();
 }
 
 }  // namespace moe

@@ -107,9 +107,13 @@ moe_status launch_ffn_bwd_bf16(const moe_cfg* c, const bf16_t* x_perm, const bf1
                                const moe_expert_weights* w, const moe_ffn_saved* saved, const bf16_t* dy_perm,
                                const bf16_t* dy, bf16_t* dx_perm, bf16_t* dx_shared, const moe_expert_grads* gr,
                                void* ws, hipStream_t st);
-// dlogit has `terms` blocks of Ep columns a row, whose sum it stands for, and w_router as many copies of Ep rows.
 moe_status launch_router_bwd_gemms(const moe_cfg* c, const bf16_t* x, const bf16_t* w_router,
-                                   const bf16_t* dlogit, int Ep, int terms, float* part, int nsplit, float* dw_router,
+                                   const bf16_t* dlogit, float* part, int nsplit, float* dw_router,
                                    float* dx_router, hipStream_t st);
+// The router part with dlogit in two terms, rows of 2 * L.Ep.
+struct RouteBwdLayout;
+moe_status launch_router_bwd_gemms2(const moe_cfg* c, const RouteBwdLayout& L, const bf16_t* x, const bf16_t* w_router,
+                                    const bf16_t* dlogit, float* part, float* dw_router, float* dx_router,
+                                    hipStream_t st);
 
 }  // namespace moe

@@ -641,8 +641,10 @@ moe_status moe_route_backward(const moe_cfg* cfg, const void* x, const void* w_r
  * carries it as the sum of two bf16 numbers (16 bits and more).
  * A token whose selected affinities are all 0 gives no gradient through renormalised
  * gates, one whose affinities are all 0 none at all.
- *  ws of at least moe_workspace_bytes(cfg, MOE_WS_ROUTE_BWD_SOFTMAX); E*H*4 below 2^31
- *  (MOE_ERR_UNSUPPORTED).  The other arguments and errors are moe_route_backward's.
+ *  ws of at least moe_workspace_bytes(cfg, MOE_WS_ROUTE_BWD_SOFTMAX).  x, w_router,
+ *  dw_router and ws must be 16-byte aligned, the rest 4-byte (MOE_ERR_UNSUPPORTED); T below
+ *  2^23, and T / seq_len * ceil(E / 64) below 2^24 (MOE_ERR_SHAPE).
+ *  The other arguments and errors are moe_route_backward's.
  */
 moe_status moe_route_backward_flags(const moe_cfg* cfg, uint32_t flags, const void* x, const void* w_router,
                                     const float* scores, const int32_t* topk_idx, const float* d_topk_w,

@@ -170,4 +170,3 @@ def test_route_backward_flags_refusals():
     assert bwd(alpha=-1.0) == bwd(seq=3) == bwd(alpha=float("inf")) == L.MOE_ERR_SHAPE
     assert bwd(n=need - 1) == L.MOE_ERR_WORKSPACE
     assert bwd(c=L.cfg_from(V3_FP8), n=BIG) == bwd(c=L.cfg_from(TINY), n=BIG) == L.MOE_ERR_UNSUPPORTED
-    assert bwd(c=L.cfg_from(MID, E=64, H=1 << 20, I=128, S=0, k=1, T=64), n=BIG) == L.MOE_ERR_UNSUPPORTED
