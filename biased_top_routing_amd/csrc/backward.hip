@@ -12,6 +12,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "bwd_layout.h"
 #include "common.h"
@@ -275,9 +276,20 @@ dim3 local_block(int64_t nchunk) {
 
 constexpr int kMaxEPL = 8;   // experts per lane: E <= 512
 
+// f(EPL) with the experts a lane that E needs, rounded up to a power of two
+template <typename F>
+void by_epl(int E, F f) {
+  if (E <= 64) f(std::integral_constant<int, 1>{});
+  else if (E <= 128) f(std::integral_constant<int, 2>{});
+  else if (E <= 256) f(std::integral_constant<int, 4>{});
+  else f(std::integral_constant<int, kMaxEPL>{});
+}
+
 // Statistics of one chunk of kSeqChunk tokens of one sequence: per expert, how
 // often it was selected and the sum of its normalised affinity s_te / sum_e' s_te'.
-// Each wave takes every fourth token; the waves' sums are added in order.
+// Each wave takes every fourth token, the rows of four of them loaded at once; the waves' sums are added in order.
+// EPL: experts a lane, E <= 64 * EPL.
+template <int EPL>
 __global__ __launch_bounds__(256) void seq_stats_kernel(const float* __restrict__ s, const int32_t* __restrict__ idx,
                                                         int T, int E, int k, int L, int nchunk,
                                                         int32_t* __restrict__ cnt, float* __restrict__ psum) {
@@ -288,25 +300,37 @@ __global__ __launch_bounds__(256) void seq_stats_kernel(const float* __restrict_
   const int t0 = b * L + ch * kSeqChunk, t1 = min(b * L + L, t0 + kSeqChunk);
   for (int e = threadIdx.x; e < E; e += blockDim.x) c_lds[e] = 0;
   __syncthreads();
-  float acc[kMaxEPL];
+  constexpr int TU = 4;
+  float acc[EPL];
 #pragma unroll
-  for (int i = 0; i < kMaxEPL; ++i) acc[i] = 0.f;
-  for (int t = t0 + wave; t < t1; t += 4) {
-    float v[kMaxEPL], rs = 0.f;
+  for (int i = 0; i < EPL; ++i) acc[i] = 0.f;
+  for (int tb = t0 + wave; tb < t1; tb += 4 * TU) {
+    float v[TU][EPL];
+    int sel[TU];
 #pragma unroll
-    for (int i = 0; i < kMaxEPL; ++i) {
-      const int e = lane + 64 * i;
-      v[i] = e < E ? s[(int64_t)t * E + e] : 0.f;
-      rs += v[i];
+    for (int u = 0; u < TU; ++u) {
+      const int t = tb + 4 * u;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        const int e = lane + 64 * i;
+        v[u][i] = t < t1 && e < E ? s[(int64_t)t * E + e] : 0.f;
+      }
+      sel[u] = t < t1 && lane < k ? idx[(int64_t)t * k + lane] : -1;
     }
-    rs = wave_sum(rs);
 #pragma unroll
-    for (int i = 0; i < kMaxEPL; ++i) acc[i] += v[i] / rs;
-    const int sel = lane < k ? idx[(int64_t)t * k + lane] : -1;
-    if ((unsigned)sel < (unsigned)E) atomicAdd(&c_lds[sel], 1);       // integer counts: order-free
+    for (int u = 0; u < TU; ++u) {
+      if (tb + 4 * u >= t1) break;
+      float rs = 0.f;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) rs += v[u][i];
+      rs = wave_sum(rs);
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) acc[i] += v[u][i] / rs;
+      if ((unsigned)sel[u] < (unsigned)E) atomicAdd(&c_lds[sel[u]], 1);       // integer counts: order-free
+    }
   }
 #pragma unroll
-  for (int i = 0; i < kMaxEPL; ++i) {
+  for (int i = 0; i < EPL; ++i) {
     const int e = lane + 64 * i;
     if (e < E) p_lds[wave][e] = acc[i];
   }
@@ -398,7 +422,7 @@ __global__ __launch_bounds__(256) void route_grad_kernel(const float* __restrict
 // balance loss, through the softmax (dlogit_e = s_e (ds_e - sum s ds)) or the sigmoid.  dlogit is stored as the sum of
 // two bf16 numbers, the nearest and what it leaves (17 bits and more: the products of the router's gradients then stay
 // within 2^-17 of fp32 ones), in rows of 2 * Ep, zero behind E.
-template <bool SOFTMAX>
+template <bool SOFTMAX, int EPL>
 __global__ __launch_bounds__(256) void route_grad_flags_kernel(const float* __restrict__ s,
                                                                const int32_t* __restrict__ idx,
                                                                const float* __restrict__ d_w,
@@ -410,9 +434,9 @@ __global__ __launch_bounds__(256) void route_grad_flags_kernel(const float* __re
   const int t = blockIdx.x * 4 + (threadIdx.x >> 6);
   if (t >= T) return;
   const int b = t / L;
-  float v[kMaxEPL], ds[kMaxEPL], rs = 0.f, gs = 0.f;
+  float v[EPL], ds[EPL], rs = 0.f, gs = 0.f;
 #pragma unroll
-  for (int i = 0; i < kMaxEPL; ++i) {
+  for (int i = 0; i < EPL; ++i) {
     const int e = lane + 64 * i;
     v[i] = e < E ? s[(int64_t)t * E + e] : 0.f;
     ds[i] = coef && e < E ? coef[(int64_t)b * E + e] : 0.f;   // d L_bal / d s'_te
@@ -423,7 +447,7 @@ __global__ __launch_bounds__(256) void route_grad_flags_kernel(const float* __re
   gs = wave_sum(gs);
   // (all affinities 0: neither the normalised ones nor a gradient)
 #pragma unroll
-  for (int i = 0; i < kMaxEPL; ++i) ds[i] = coef && rs > 0.f ? (ds[i] - gs / rs) / rs : 0.f;
+  for (int i = 0; i < EPL; ++i) ds[i] = coef && rs > 0.f ? (ds[i] - gs / rs) / rs : 0.f;
   // gates over the selected experts (an id outside [0, E) is none)
   int sel = lane < k ? idx[(int64_t)t * k + lane] : -1;
   if ((unsigned)sel >= (unsigned)E) sel = -1;
@@ -433,21 +457,21 @@ __global__ __launch_bounds__(256) void route_grad_flags_kernel(const float* __re
   const float B1 = wave_sum(dwj * ss);
   const float dsel = raw ? scale * dwj : S > 0.f ? scale / S * (dwj - B1 / S) : 0.f;
   for (int j = 0; j < k; ++j) {
-    const int ej = __shfl(sel, j);
-    const float dj = __shfl(dsel, j);
+    const int ej = __builtin_amdgcn_readlane(sel, j);
+    const float dj = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(dsel), j));
 #pragma unroll
-    for (int i = 0; i < kMaxEPL; ++i)
+    for (int i = 0; i < EPL; ++i)
       if (ej == lane + 64 * i) ds[i] += dj;
   }
   float mean = 0.f;
   if constexpr (SOFTMAX) {
 #pragma unroll
-    for (int i = 0; i < kMaxEPL; ++i) mean = fmaf(v[i], ds[i], mean);
+    for (int i = 0; i < EPL; ++i) mean = fmaf(v[i], ds[i], mean);
     mean = wave_sum(mean);
   }
   bf16_t* out = dlogit + (int64_t)t * 2 * Ep;
 #pragma unroll
-  for (int i = 0; i < kMaxEPL; ++i) {
+  for (int i = 0; i < EPL; ++i) {
     const int e = lane + 64 * i;
     if (e >= Ep) continue;
     const float d = e < E ? SOFTMAX ? v[i] * (ds[i] - mean) : ds[i] * v[i] * (1.0f - v[i]) : 0.f;
@@ -631,8 +655,10 @@ moe_status route_backward(const moe_cfg* cfg, bool with_flags, uint32_t flags, c
   }
   const bool bal = alpha > 0.0f;
   if (bal) {
-    hipLaunchKernelGGL(seq_stats_kernel, dim3((unsigned)(L.nseq * L.nchunk)), dim3(256), 0, s, scores, topk_idx,
-                       cfg->T, cfg->E, cfg->k, L.seq_len, L.nchunk, cnt, psum);
+    by_epl(cfg->E, [&](auto epl) {
+      hipLaunchKernelGGL((seq_stats_kernel<decltype(epl)::value>), dim3((unsigned)(L.nseq * L.nchunk)), dim3(256), 0, s,
+                         scores, topk_idx, cfg->T, cfg->E, cfg->k, L.seq_len, L.nchunk, cnt, psum);
+    });
     if ((st = launch_status()) != MOE_OK) return st;
   }
   if (with_flags) {
@@ -655,12 +681,14 @@ moe_status route_backward(const moe_cfg* cfg, bool with_flags, uint32_t flags, c
     return launch_router_bwd_gemms(cfg, (const bf16_t*)x, (const bf16_t*)w_router, dlogit, part, L.nsplit, dw_router,
                                    dx_router, s);
   }
-  auto grad = [&](auto kernel) {
+  auto launch = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, tokens, dim3(256), 0, s, scores, topk_idx, d_topk_w, bal ? coef : nullptr, cfg->T, cfg->E,
                        L.Ep, cfg->k, L.seq_len, cfg->route_scale, (flags & MOE_GATES_RAW) != 0, dlogit);
   };
-  if (flags & MOE_SOFTMAX) grad(route_grad_flags_kernel<true>);
-  else grad(route_grad_flags_kernel<false>);
+  by_epl(cfg->E, [&](auto epl) {
+    if (flags & MOE_SOFTMAX) launch(route_grad_flags_kernel<true, decltype(epl)::value>);
+    else launch(route_grad_flags_kernel<false, decltype(epl)::value>);
+  });
   if ((st = launch_status()) != MOE_OK) return st;
   return launch_router_bwd_gemms2(cfg, L, (const bf16_t*)x, (const bf16_t*)w_router, dlogit, part, dw_router, dx_router, s);
 }
