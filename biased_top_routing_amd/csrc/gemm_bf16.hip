@@ -459,14 +459,20 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void gemm_bf16_kernel(GemmParams
 
 // Router GEMM for small batches, whose token-tile grid would leave most CUs
 // idle (decode: T = 128 gives two 64-token tiles, each walking all of K):
-// a workgroup computes a TM x TN tile of (tokens, experts) with MFMA blocks of
-// TM x TN (32 x 32 x 16 or 16 x 16 x 32 bf16), each of its 16 wavefronts takes
-// one sixteenth of K straight from memory into operand registers (no operand is
-// shared between wavefronts, so nothing is staged in LDS), and the 16 partial
-// tiles are added through LDS in wavefront order (a fixed order: repeated calls
-// give identical bits; the summation order, and so the last bits of the
-// affinities, differ from the large-batch tiles).  Token and expert rows past
-// the ends are clamped to the last valid row and their results not stored.
+// a workgroup computes a TM x TM tile of (tokens, experts) with MFMA blocks of
+// TM x TM (32 x 32 x 16 or 16 x 16 x 32 bf16), each of its 16 wavefronts takes
+// one sixteenth of K, and the 16 partial tiles are added through LDS in
+// wavefront order (a fixed order: repeated calls give identical bits; the
+// summation order, and so the last bits of the affinities, differ from the
+// large-batch tiles).  No operand is shared between wavefronts, but each goes
+// through LDS all the same: an operand's lanes next to each other hold
+// different rows, and loaded so into registers every lane is an access of its
+// own to the vector cache, 64 of them a load, which bound the kernel (448 loads
+// a CU at E = 256, H = 7168); a direct-to-LDS load in which four lanes take 64
+// bytes of a row makes 16.  (The routing of T = 128 / 512 / 2048 tokens there
+// 20.8 -> 13.7, 33 -> 23.6 and 70 -> 41 us; more slices in flight, with one
+// workgroup a CU, gain 0.2 us at T = 128 and lose 1 us at T = 2048, E = 64.)
+// Rows past the ends are read as zeros and their results not stored.
 constexpr int kRsWaves = 16;
 template <int TM>   // 32: 32 x 32 x 16 blocks; 16: 16 x 16 x 32 blocks
 __global__ __launch_bounds__(64 * kRsWaves) void router_splitk_kernel(const bf16_t* __restrict__ x,
@@ -477,34 +483,72 @@ __global__ __launch_bounds__(64 * kRsWaves) void router_splitk_kernel(const bf16
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int NR = TM * TM / 64;       // accumulator values per lane
   constexpr int KS = 512 / TM;           // K per MFMA step (16 or 32)
-  __shared__ float red[kRsWaves][NR][64];
+  constexpr int SLICES = 32 / TM;        // (64 KB of LDS: two workgroups a CU)
+  constexpr int SPS = TM / 16;           // steps of a slice: 32 elements (64 bytes) of every row
+  constexpr int SLICE = TM * 32;         // elements of an operand's slice
+  __shared__ __attribute__((aligned(16))) bf16_t lds[kRsWaves][SLICES][2][SLICE];
+  static_assert(NR * 64 * 2 <= SLICES * 2 * SLICE, "a wavefront's partial tile fits its slices");
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int lr = lane % TM, kg = lane / TM;
   const int t0 = blockIdx.x * TM, e0 = blockIdx.y * TM;
-  // operand lane l: row l % TM, K elements 8 (l / TM) .. + 7 of each step
-  const bf16_t* xa = x + (int64_t)min(t0 + lr, T - 1) * H + 8 * kg;
-  const bf16_t* wb = w + (int64_t)min(e0 + lr, E - 1) * H + 8 * kg;
+  typedef __attribute__((address_space(3))) void lds_void_t;
+  const __amdgpu_buffer_rsrc_t ra = make_rsrc(x + (int64_t)t0 * H, min(TM, T - t0) * H * 2);
+  const __amdgpu_buffer_rsrc_t rw = make_rsrc(w + (int64_t)e0 * H, min(TM, E - e0) * H * 2);
+  const int off = lane / 4 * H * 2 + swz<4>(lane / 4, lane % 4) * 16;
   const int nks = H / KS;
-  const int ks0 = wave * nks / kRsWaves, ks1 = (wave + 1) * nks / kRsWaves;
+  const int ks0 = __builtin_amdgcn_readfirstlane(wave * nks / kRsWaves);
+  const int ks1 = __builtin_amdgcn_readfirstlane((wave + 1) * nks / kRsWaves);
+  auto issue = [&](int slot, int ks) {
+    bf16_t* dst = lds[wave][slot][0];
+#pragma unroll
+    for (int i = 0; i < SPS; ++i) {                        // 16 rows a load (their chunks alike: 16 rows on)
+      const int o = off + i * 16 * H * 2;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void_t*)(dst + i * 512), 16, o, ks * KS * 2, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void_t*)(dst + SLICE + i * 512), 16, o, ks * KS * 2, 0, 0);
+    }
+  };
   typedef float accv_t __attribute__((ext_vector_type(NR)));
   accv_t acc;
 #pragma unroll
   for (int r = 0; r < NR; ++r) acc[r] = 0.f;
-#pragma unroll 4
-  for (int ks = ks0; ks < ks1; ++ks) {
-    const bf16x8_t a = *reinterpret_cast<const bf16x8_t*>(xa + ks * KS);
-    const bf16x8_t b = *reinterpret_cast<const bf16x8_t*>(wb + ks * KS);
-    if constexpr (TM == 32) acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, acc, 0, 0, 0);
-    else acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, acc, 0, 0, 0);
-  }
 #pragma unroll
-  for (int r = 0; r < NR; ++r) red[wave][r][lane] = acc[r];
+  for (int s = 0; s < SLICES; ++s)
+    if (ks0 + s * SPS < ks1) issue(s, ks0 + s * SPS);
+  int slot = 0;
+  for (int ks = ks0; ks < ks1; ks += SPS) {
+    if (ks + (SLICES - 1) * SPS < ks1) wait_vm<2 * SPS * (SLICES - 1)>();   // (the later slices are still on their way)
+    else wait_vm<0>();
+    __builtin_amdgcn_wave_barrier();
+    // operand lane l: row l % TM, K elements 8 (l / TM) .. + 7 of each step
+    bf16x8_t a[SPS], b[SPS];
+#pragma unroll
+    for (int s = 0; s < SPS; ++s) {
+      const int at = lr * 32 + swz<4>(lr, s * (64 / TM) + kg) * 8;
+      a[s] = *reinterpret_cast<const bf16x8_t*>(lds[wave][slot][0] + at);
+      b[s] = *reinterpret_cast<const bf16x8_t*>(lds[wave][slot][1] + at);
+    }
+#pragma unroll
+    for (int s = 0; s < SPS; ++s) {
+      if (s && ks + s >= ks1) break;                       // (an odd number of steps: the next wavefront's)
+      if constexpr (TM == 32) acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[s], b[s], acc, 0, 0, 0);
+      else acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[s], b[s], acc, 0, 0, 0);
+    }
+    __builtin_amdgcn_s_waitcnt(kLgkmWaitZero);             // the slot is read before it is loaded again
+    __builtin_amdgcn_wave_barrier();
+    if (ks + SLICES * SPS < ks1) issue(slot, ks + SLICES * SPS);
+    slot = slot == SLICES - 1 ? 0 : slot + 1;
+  }
+  // each wavefront's partial tile over its own slices
+  float* red = reinterpret_cast<float*>(lds);
+  constexpr int RW = SLICES * SLICE;                       // floats of a wavefront's slices
+#pragma unroll
+  for (int r = 0; r < NR; ++r) red[wave * RW + r * 64 + lane] = acc[r];
   __syncthreads();
   for (int q = threadIdx.x; q < NR * 64; q += 64 * kRsWaves) {
     const int r = q >> 6, l = q & 63;
     float sum = 0.f;
 #pragma unroll
-    for (int v = 0; v < kRsWaves; ++v) sum += red[v][r][l];
+    for (int v = 0; v < kRsWaves; ++v) sum += red[v * RW + q];
     // acc[r] of lane l: 32 x 32 blocks row 8 (r / 4) + 4 (l / 32) + r % 4;
     // 16 x 16 blocks row 4 (l / 16) + r; column l % TM
     const int i = TM == 32 ? 8 * (r >> 2) + 4 * (l >> 5) + (r & 3) : 4 * (l >> 4) + r;
