@@ -308,6 +308,7 @@ __global__ __launch_bounds__(1024) void norm_bwd_sum_kernel(const float* __restr
   const int j = blockIdx.x * 64 + lane;
   float v = 0.f;
   if (j < H)
+#pragma unroll 8
     for (int b = q; b < nb; b += 16) v += part[(int64_t)b * H + j];
   s[q][lane] = v;
   __syncthreads();

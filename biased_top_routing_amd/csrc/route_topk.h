@@ -72,6 +72,17 @@ __device__ __forceinline__ float gate_of(float s, float total, float scale, bool
   return scale * s / total;
 }
 
+// v into a descending list of the R largest.
+template <int R>
+__device__ __forceinline__ void insert_top(float (&top)[R], float v) {
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const float hi = fmaxf(top[i], v), lo = fminf(top[i], v);
+    top[i] = hi;
+    v = lo;
+  }
+}
+
 // Merge the partner's top-R list into this lane's (both descending).
 template <int CTRL, int R>
 __device__ __forceinline__ void merge_step(float (&top)[R]) {
@@ -79,15 +90,7 @@ __device__ __forceinline__ void merge_step(float (&top)[R]) {
 #pragma unroll
   for (int i = 0; i < R; ++i) other[i] = dpp_f32<CTRL>(top[i]);
 #pragma unroll
-  for (int i2 = 0; i2 < R; ++i2) {
-    float v = other[i2];
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const float hi = fmaxf(top[i], v), lo = fminf(top[i], v);
-      top[i] = hi;
-      v = lo;
-    }
-  }
+  for (int i = 0; i < R; ++i) insert_top(top, other[i]);
 }
 
 // One token per 16 lanes (the caller's wavefront holds four such slices, all
@@ -149,15 +152,7 @@ __device__ __forceinline__ void topk16_token(const float* row, float* s_out, con
 #pragma unroll
   for (int i = 0; i < TOPR; ++i) top[i] = -__builtin_huge_valf();
 #pragma unroll
-  for (int j = 0; j < EPL; ++j) {
-    float v = q[j];
-#pragma unroll
-    for (int i = 0; i < TOPR; ++i) {
-      const float hi = fmaxf(top[i], v), lo = fminf(top[i], v);
-      top[i] = hi;
-      v = lo;
-    }
-  }
+  for (int j = 0; j < EPL; ++j) insert_top(top, q[j]);
   // the LG lanes of a group (an aligned block of 1, 2, 4, 8 or 16 lanes)
   if (LG >= 2) merge_step<kDppXor1>(top);
   if (LG >= 4) merge_step<kDppXor2>(top);
@@ -217,6 +212,108 @@ __device__ __forceinline__ void topk16_token(const float* row, float* s_out, con
   if (valid && sl < k) {
     idx_out[sl] = my_e;
     w_out[sl] = gate_of<SOFTMAX>(my_s, tot, scale, raw);
+  }
+}
+
+// The same of one token by a whole wavefront, for batches whose 16-lane slices would leave most of the chip idle: a
+// quarter of the experts a lane, and what the lanes agree on in scalar registers.  The same operations in the same
+// order but for the sum of a softmax, which is in 64 bits.  E = 64 * EPL, lane l holds experts [l*EPL, (l+1)*EPL),
+// G divides 64; k <= 16.
+template <int EPL, int TOPR, bool SOFTMAX>
+__device__ __forceinline__ void topk64_token(const float* row, float* s_out, const float (&b)[EPL], int G, int M, int k,
+                                             float scale, bool raw, int32_t* idx_out, float* w_out) {
+  const int lane = threadIdx.x & (kWave - 1), LG = kWave / G, grp = lane / LG;
+  auto at = [](float v, int l) { return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), l)); };
+  float s[EPL], q[EPL];
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) s[j] = row[lane * EPL + j];
+  if constexpr (SOFTMAX) {
+    Softmax sm;
+    float m = s[0];
+#pragma unroll
+    for (int j = 1; j < EPL; ++j) m = fmaxf(m, s[j]);
+    m = max16(m);
+    sm.set(fmaxf(fmaxf(at(m, 0), at(m, 16)), fmaxf(at(m, 32), at(m, 48))));
+    double e[EPL], z = 0.0;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) z += e[j] = sm.term(s[j]);
+    z = sum16(z);
+    z += __shfl_xor(z, 16);
+    sm.total(z + __shfl_xor(z, 32));
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) s[j] = sm.share(e[j]);
+    if (s_out) {
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) s_out[lane * EPL + j] = s[j];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) q[j] = s[j] + b[j];
+  // ---- group scores
+  float top[TOPR];
+#pragma unroll
+  for (int i = 0; i < TOPR; ++i) top[i] = -__builtin_huge_valf();
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) insert_top(top, q[j]);
+  if (LG >= 2) merge_step<kDppXor1>(top);
+  if (LG >= 4) merge_step<kDppXor2>(top);
+  if (LG >= 8) merge_step<kDppHalfMirror>(top);
+  if (LG >= 16) merge_step<kDppMirror>(top);
+  for (int x = 16; x < LG; x *= 2) {
+    float other[TOPR];
+#pragma unroll
+    for (int i = 0; i < TOPR; ++i) other[i] = __shfl_xor(top[i], x);
+#pragma unroll
+    for (int i = 0; i < TOPR; ++i) insert_top(top, other[i]);
+  }
+  float gs = top[0];
+#pragma unroll
+  for (int i = 1; i < TOPR; ++i) gs = gs + top[i];
+  int rank = 0;
+  for (int h = 0; h < G; ++h) {
+    const float o = at(gs, h * LG);
+    rank += (o > gs) || (o == gs && h < grp);
+  }
+  // ---- k rounds of the largest key, the lowest expert among equals
+  uint32_t key[EPL];
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) key[j] = rank < M ? float_order_key(q[j]) : 0u;
+  int my_e = 0;
+  float my_s = 0.f;
+  for (int r = 0; r < k; ++r) {
+    uint32_t m = key[0];
+#pragma unroll
+    for (int j = 1; j < EPL; ++j) m = max(m, key[j]);
+    m = max(m, dpp_u32<kDppXor1>(m));
+    m = max(m, dpp_u32<kDppXor2>(m));
+    m = max(m, dpp_u32<kDppHalfMirror>(m));
+    m = max(m, dpp_u32<kDppMirror>(m));
+    const uint32_t m0 = __builtin_amdgcn_readlane(m, 0), m1 = __builtin_amdgcn_readlane(m, 16);
+    const uint32_t m2 = __builtin_amdgcn_readlane(m, 32), m3 = __builtin_amdgcn_readlane(m, 48);
+    m = max(max(m0, m1), max(m2, m3));
+    int jl = EPL;
+    float sl = 0.f;
+#pragma unroll
+    for (int j = EPL - 1; j >= 0; --j) {
+      jl = key[j] == m ? j : jl;
+      sl = key[j] == m ? s[j] : sl;
+    }
+    const int win = __ffsll((unsigned long long)__ballot(jl < EPL)) - 1;   // (some lane holds the largest key)
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) key[j] = lane == win && j == jl ? 0u : key[j];
+    const int we = win * EPL + __builtin_amdgcn_readlane(jl, win);
+    const float ws = at(sl, win);
+    my_e = lane == r ? we : my_e;
+    my_s = lane == r ? ws : my_s;
+  }
+  float tot = my_s;
+  tot += dpp_f32<kDppXor1>(tot);
+  tot += dpp_f32<kDppXor2>(tot);
+  tot += dpp_f32<kDppHalfMirror>(tot);
+  tot += dpp_f32<kDppMirror>(tot);
+  if (lane < k) {
+    idx_out[lane] = my_e;
+    w_out[lane] = gate_of<SOFTMAX>(my_s, tot, scale, raw);
   }
 }
 

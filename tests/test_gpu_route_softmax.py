@@ -86,6 +86,33 @@ def test_softmax_routing(T, H, E, G, M, k, topr, act, mask):
         assert (np.abs(gates - gr) <= 40 * EPS32 * gr).all()
 
 
+@pytest.mark.parametrize("E,G,M,k,topr", [(256, 8, 4, 8, 2), (256, 1, 1, 16, 4), (128, 16, 3, 6, 1), (128, 2, 1, 1, 3),
+                                          (256, 16, 16, 16, 4)])
+@pytest.mark.parametrize("flags", [0, L.MOE_GATES_RAW])
+def test_the_selection_of_a_token_does_not_depend_on_the_batch(E, G, M, k, topr, flags):
+    """Few tokens are selected by a wavefront each, many by 16 lanes each: the same experts and gates, bit for bit, with
+    ties, affinities of zero and masked experts among them."""
+    T = 2049
+    g = rng(124, E, G, k)
+    s = (g.integers(0, 9, (T, E)) / 8).astype(np.float32)
+    s[::2] = g.random((s[::2].shape), dtype=np.float32)
+    s[5] = 0.0
+    bias = (g.integers(-2, 3, E) / 8).astype(np.float32)
+    bias[g.integers(0, E, E // 8)] = -np.inf
+    out = []
+    for n in (T, T - 1, 70, 1):
+        cfg = L.make_cfg(T=n, H=64, E=E, k=k, G=G, M=M, S=0, I=128, group_topr=topr, act="bf16")
+        sd = dev_f32(s[:n])
+        idx = torch.full((n, k), -1, dtype=torch.int32, device="cuda")
+        w = torch.full((n, k), -1.0, device="cuda")
+        L.moe_route(cfg, None, None, None, dev_f32(bias), sd, L.MOE_SCORES_IN | flags, idx, w, None)
+        out.append((host(idx), host(w)))
+    with np.errstate(invalid="ignore"):
+        for idx, w in out[1:]:
+            np.testing.assert_array_equal(idx, out[0][0][:len(idx)])
+            np.testing.assert_array_equal(w.view(np.uint32), out[0][1][:len(w)].view(np.uint32))
+
+
 def test_a_token_that_no_expert_may_take():
     """Every logit -inf: affinities and gates of 0, the experts chosen by the bias alone."""
     for T, E, G in ((3, 16, 4), (2100, 256, 8), (5, 13, 1)):
