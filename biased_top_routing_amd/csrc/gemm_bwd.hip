@@ -31,11 +31,15 @@
 //   kDwR  K-segmented over fixed splits of the T tokens (fp32 partial sums,
 //         reduced in order afterwards, so the result does not depend on timing).
 //   kDxR2 / kDwR2  the same with dlogit as the sum of two bf16 numbers (rows of
-//         2 Ep columns, Ep = p.E a multiple of 64, the leading terms first): the
-//         walk over K passes over W_r, or over the split's tokens, once for either,
-//         into the same accumulators.  (As products of twice the size, with two
-//         copies of W_r and two sets of partial sums: T = 16384, E = 256, H = 7168
-//         dW_r and its reduction 256 us.)
+//         2 Ep columns, Ep = p.E a multiple of 64, the leading terms first; 17
+//         bits and more, where one bf16 of 8 would put 2^-9 into every gradient):
+//         a slice holds both terms of half its depth of K and W_r's rows, or the
+//         tokens', of that once, so that both meet the same operand registers in
+//         the same accumulators.  T = 16384, E = 256, H = 7168: dW_r 109 us, dx
+//         145, 1.1 and 0.8 PFLOP/s, where dx stores 470 MB besides.  (As products
+//         of twice the size, with two sets of partial sums: dW_r 256 us; a walk
+//         over K that passes over the second operand once for either term: 121 and
+//         166 us, bound by the reads of it from LDS.)
 #include "bwd_layout.h"
 #include "common.h"
 #include "ffn_layout.h"
@@ -103,10 +107,12 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void gemm_bwd_kernel(BwdParams p
   constexpr int NW = WM * WN, NT = 64 * NW;
   constexpr int BM = WM * MI * 32, BN = WN * NI * 32;
   constexpr int CPK = BK / 8;          // 16-byte chunks per K-contiguous row of a slice
-  constexpr int A_CH = BM * CPK / NT, B_CH = BN * CPK / NT, PER = A_CH + B_CH;
-  constexpr int STAGE = (BM + BN) * BK;
+  // K of B in a slice: both terms of a dlogit, BK / 2 of K each, lie in A's part of it and meet the same B
+  constexpr int TERMS = KIND == kDwR2 || KIND == kDxR2 ? 2 : 1, BKB = BK / TERMS;
+  constexpr int A_CH = BM * CPK / NT, B_CH = BN * (BKB / 8) / NT, PER = A_CH + B_CH;
+  constexpr int STAGE = BM * BK + BN * BKB;
   static_assert(BK == 32 || BK == 64, "K slices of 32 or 64");
-  static_assert(BM * CPK % NT == 0 && BN * CPK % NT == 0, "whole loads per thread");
+  static_assert(BM * CPK % NT == 0 && BN * (BKB / 8) % NT == 0 && BKB % 16 == 0, "whole loads per thread");
   static_assert(BM % 128 == 0 && BN % 128 == 0, "M-contiguous slices of at least 16 chunks per row");
 #if defined(__HIP_DEVICE_COMPILE__)
   // kDx, kDh: each wavefront's (MI*32) x (NI*32) outputs are staged in LDS for
@@ -127,7 +133,6 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void gemm_bwd_kernel(BwdParams p
   const bf16_t* B = nullptr;
   int lda = 0, ldb = 0, a_bytes = 0, b_bytes = 0;
   if constexpr (is_dxr(KIND)) {
-    constexpr int TERMS = KIND == kDxR2 ? 2 : 1;
     const int ntn = (p.H + BN - 1) / BN;
     const int rt = blockIdx.x / ntn, nt = blockIdx.x % ntn;
     m0 = rt * BM;
@@ -137,7 +142,7 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void gemm_bwd_kernel(BwdParams p
     N = p.H;
     lda = TERMS * p.E;
     A = p.a_shared + (int64_t)m0 * lda;
-    K = lda;
+    K = p.E;
     B = p.b_shared;
     ldb = p.H;
     b_bytes = (TERMS == 2 ? p.w_rows : p.E) * p.H * 2;
@@ -247,10 +252,11 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void gemm_bwd_kernel(BwdParams p
     if constexpr (A_MC) {
       constexpr int CPR = BM / 8;
       const int r = q / CPR, pc = q % CPR;
-      a_off[i] = (r * lda + m0 + ((pc ^ mc_key(r)) << 3)) * 2;
+      a_off[i] = (r % BKB * lda + r / BKB * p.E + m0 + ((pc ^ mc_key(r)) << 3)) * 2;
     } else {
       const int r = q / CPK, pc = q % CPK;
-      a_off[i] = ((r < mvalid ? r : mvalid + 1) * lda + (swz<CPK>(r, pc) << 3)) * 2;
+      const int kc = swz<CPK>(r, pc) << 3;
+      a_off[i] = ((r < mvalid ? r : mvalid + 1) * lda + kc % BKB + kc / BKB * p.E) * 2;
     }
   }
 #pragma unroll
@@ -263,18 +269,13 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void gemm_bwd_kernel(BwdParams p
     b_off[i] = (r * ldb + cmap) * 2;
   }
   const __amdgpu_buffer_rsrc_t rsrc_a_kc = make_rsrc(A, A_MC ? 0 : mvalid * lda * 2);
-  // slices of one term; the second term's: dW_r's tokens once more, dlogit Ep columns on; dx's W_r once more
-  const int nk1 = (K + BK - 1) / BK;
 #define MOE_ISSUE_BWD(stage_, k0_)                                                                    \
   {                                                                                                   \
-    const int kq = (k0_);                                                                             \
-    const bool again = (KIND == kDwR2 && kq >= nk1 * BK) || (KIND == kDxR2 && kq >= p.E);             \
-    const int k0v = KIND == kDwR2 && again ? kq - nk1 * BK : kq;                                      \
-    const int a_on = KIND == kDwR2 && again ? p.E : 0;                                                \
+    const int k0v = (k0_);                                                                            \
     bf16_t* sb = lds + (stage_) * STAGE;                                                              \
     if constexpr (A_MC) {                                                                             \
       const __amdgpu_buffer_rsrc_t ra =                                                               \
-          make_rsrc(A + (int64_t)k0v * lda + a_on, max(0, a_bytes - (k0v * lda + a_on) * 2));         \
+          make_rsrc(A + (int64_t)k0v * lda, max(0, a_bytes - k0v * lda * 2));                         \
       _Pragma("unroll") for (int i = 0; i < A_CH; ++i)                                                \
           __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void_t*)(sb + (i * NW + wave) * 512), 16,  \
                                                    a_off[i], 0, 0, 0);                                \
@@ -283,8 +284,7 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void gemm_bwd_kernel(BwdParams p
           __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc_a_kc, (lds_void_t*)(sb + (i * NW + wave) * 512), \
                                                    16, a_off[i], k0v * 2, 0, 0);                      \
     }                                                                                                 \
-    const int kb = KIND == kDxR2 && again ? kq - p.E : k0v;                                           \
-    const __amdgpu_buffer_rsrc_t rb = make_rsrc(B + (int64_t)kb * ldb, max(0, b_bytes - kb * ldb * 2)); \
+    const __amdgpu_buffer_rsrc_t rb = make_rsrc(B + (int64_t)k0v * ldb, max(0, b_bytes - k0v * ldb * 2)); \
     _Pragma("unroll") for (int i = 0; i < B_CH; ++i)                                                  \
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void_t*)(sb + BM * BK + (i * NW + wave) * 512), \
                                                  16, b_off[i], 0, 0, 0);                              \
@@ -303,27 +303,29 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void gemm_bwd_kernel(BwdParams p
   for (int mi = 0; mi < MI; ++mi) a_rd[mi] = wm * MI * 32 + mi * 32 + lr;
   const bool has_rows = wm * MI * 32 < mvalid;
 
-  const int nk = (KIND == kDwR2 ? 2 : 1) * nk1;
+  const int nk = (K + BKB - 1) / BKB;
 #pragma unroll
   for (int s = 0; s < STAGES - 1; ++s)
-    if (s < nk) MOE_ISSUE_BWD(s, s * BK);
+    if (s < nk) MOE_ISSUE_BWD(s, s * BKB);
   int cur = 0;
   for (int kt = 0; kt < nk; ++kt) {
     wait_slices<PER>(min(nk - 1, kt + STAGES - 2) - kt);
     asm volatile("s_barrier" ::: "memory");
     const bf16_t* base = lds + cur * STAGE;
     const bf16_t* bbase = base + BM * BK;
-    constexpr int KK = BK / 16;
+    constexpr int KK = BK / 16, KKB = BKB / 16;
     // Every transposing read of this slice is issued before the next slice's
     // direct-to-LDS loads: issued after them, the compiler makes the first one
     // wait for those loads (vmcnt(0)), which serialises loads and MFMAs.
-    bf16x8_t fbs[KK][NI];
+    bf16x8_t fbs[KKB][NI];
     bf16x8_t fas[A_MC ? KK : 1][MI];
     if (has_rows) {
 #pragma unroll
       for (int kk = 0; kk < KK; ++kk) {
+        if (kk < KKB) {
 #pragma unroll
-        for (int ni = 0; ni < NI; ++ni) fbs[kk][ni] = mc_frag<BN>(bbase, kk, wn * NI * 32 + ni * 32, lane);
+          for (int ni = 0; ni < NI; ++ni) fbs[kk % KKB][ni] = mc_frag<BN>(bbase, kk, wn * NI * 32 + ni * 32, lane);
+        }
         if constexpr (A_MC) {
 #pragma unroll
           for (int mi = 0; mi < MI; ++mi) fas[kk][mi] = mc_frag<BM>(base, kk, wm * MI * 32 + mi * 32, lane);
@@ -333,7 +335,7 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void gemm_bwd_kernel(BwdParams p
     __builtin_amdgcn_sched_barrier(0);
     if (kt + STAGES - 1 < nk) {
       const int st = cur == 0 ? STAGES - 1 : cur - 1;
-      MOE_ISSUE_BWD(st, (kt + STAGES - 1) * BK);
+      MOE_ISSUE_BWD(st, (kt + STAGES - 1) * BKB);
     }
     if (has_rows) {
       if constexpr (A_MC) {
@@ -343,7 +345,7 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void gemm_bwd_kernel(BwdParams p
           for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
             for (int ni = 0; ni < NI; ++ni)
-              acc[mi][ni] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fas[kk][mi], fbs[kk][ni], acc[mi][ni], 0, 0, 0);
+              acc[mi][ni] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fas[kk][mi], fbs[kk % KKB][ni], acc[mi][ni], 0, 0, 0);
         }
       } else {
         // K-contiguous A: ds_read_b128 fragments, double-buffered across the k-steps
@@ -365,7 +367,7 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void gemm_bwd_kernel(BwdParams p
           for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
             for (int ni = 0; ni < NI; ++ni)
-              acc[mi][ni] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[cb][mi], fbs[kk][ni], acc[mi][ni], 0, 0, 0);
+              acc[mi][ni] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[cb][mi], fbs[kk % KKB][ni], acc[mi][ni], 0, 0, 0);
           __builtin_amdgcn_sched_barrier(0);
         }
       }
@@ -563,8 +565,8 @@ using DxTile = BwdTile<MOE_BWD_DX_TILE>;
 static_assert(DxTile::BM == kBwdBM && DxTile::BN == kBwdBN, "dx tile shape (the tile tables use kBwdBM x kBwdBN)");
 
 // dx of the routing's two-term gradient (sizes at its launch).
-#define MOE_BWD_DXR2_WIDE 2, 4, 2, 2, 2, 32, 2
-#define MOE_BWD_DXR2 2, 4, 2, 1, 2, 64, 2
+#define MOE_BWD_DXR2_WIDE 2, 4, 2, 2, 2, 64, 2
+#define MOE_BWD_DXR2 4, 2, 1, 2, 2, 64, 2
 using DxR2Wide = BwdTile<MOE_BWD_DXR2_WIDE>;
 using DxR2 = BwdTile<MOE_BWD_DXR2>;
 
@@ -696,7 +698,86 @@ moe_status launch_router_bwd_gemms2(const moe_cfg* c, const RouteBwdLayout& L, c
   p.out_shared = dx_router;
   // Short products (2 * Ep deep) under fp32 stores that nothing reads soon, past the caches (cached: 375 against 352 us
   // for all the gradients at T = 16384, E = 256, H = 7168): two workgroups a CU, one computing while the other stores.
-  // Tiles of 128 x 256 where they make four rounds of the 256 CUs (343 us there, 128 x 128 354, one workgroup of
+  // Tiles of 128 x 256 where they make four rounds of the 256 CUs (303 us there, 128 x 128 308, one workgroup of
+  // 256 x 256 318), else 128 x 128 (T = 4096, E = 64, H = 2048: 36.1 us, 128 x 256 37.7).
+  auto tiles_of = [](int64_t m, int64_t n) {
+    return ((m + WgTile::BM - 1) / WgTile::BM) * ((n + WgTile::BN - 1) / WgTile::BN);
+  };
+  const int64_t SI = (int64_t)c->S * c->I;
+  p.a_routed = dgu; p.a_shared = dgus;
+  p.b_routed = x_perm; p.b_shared = x;
+  p.out_routed = gr->w_gate_up; p.out_shared = gr->ws_gate_up;
+  {
+    const int64_t n_sh = c->S > 0 ? tiles_of(2 * SI, c->H) : 0;
+    const int64_t n = dw_grid(n_sh, c->E * tiles_of(2 * c->I, c->H), dw_stripe(kDwGu));
+    hipLaunchKernelGGL((gemm_bwd_kernel<kDwGu, MOE_BWD_WG_TILE>), dim3((unsigned)n), dim3(WgTile::THREADS), 0, st, p);
+    if ((s = launch_status()) != MOE_OK) return s;
+  }
+  p.a_routed = dy_perm; p.a_shared = dy;
+  p.b_routed = h; p.b_shared = hs;
+  p.out_routed = gr->w_down; p.out_shared = gr->ws_down;
+  {
+    const int64_t n_sh = c->S > 0 ? tiles_of(c->H, SI) : 0;
+    const int64_t n = dw_grid(n_sh, c->E * tiles_of(c->H, c->I), dw_stripe(kDwD));
+    hipLaunchKernelGGL((gemm_bwd_kernel<kDwD, MOE_BWD_WG_TILE>), dim3((unsigned)n), dim3(WgTile::THREADS), 0, st, p);
+    if ((s = launch_status()) != MOE_OK) return s;
+  }
+  return MOE_OK;
+}
+
+moe_status launch_router_bwd_gemms(const moe_cfg* c, const bf16_t* x, const bf16_t* w_router,
+                                   const bf16_t* dlogit, float* part, int nsplit, float* dw_router,
+                                   float* dx_router, hipStream_t st) {
+  BwdParams p{};
+  p.T = c->T; p.H = c->H; p.E = c->E; p.S = c->S; p.I = c->I;
+  p.ksplit = kRouterKSplit;
+  p.a_shared = dlogit;
+  p.b_shared = x;
+  p.out_routed = part;
+  const int64_t tiles = (int64_t)((c->E + kBwdBM - 1) / kBwdBM) * ((c->H + kBwdBN - 1) / kBwdBN);
+  hipLaunchKernelGGL((gemm_bwd_kernel<kDwR, MOE_BWD_TILE>), dim3((unsigned)(tiles * nsplit)), dim3(kBwdThreads),
+                     0, st, p);
+  moe_status s;
+  if ((s = launch_status()) != MOE_OK) return s;
+  const int64_t n = (int64_t)c->E * c->H;
+  hipLaunchKernelGGL(reduce_splits_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, part, nsplit, n,
+                     dw_router);
+  if ((s = launch_status()) != MOE_OK) return s;
+  if (dx_router) {
+    p.b_shared = w_router;
+    p.out_shared = dx_router;
+    const int64_t rt = (c->T + kBwdBM - 1) / kBwdBM;
+    hipLaunchKernelGGL((gemm_bwd_kernel<kDxR, MOE_BWD_TILE>), dim3((unsigned)(rt * ((c->H + kBwdBN - 1) / kBwdBN))),
+                       dim3(kBwdThreads), 0, st, p);
+    if ((s = launch_status()) != MOE_OK) return s;
+  }
+  return MOE_OK;
+}
+
+moe_status launch_router_bwd_gemms2(const moe_cfg* c, const RouteBwdLayout& L, const bf16_t* x, const bf16_t* w_router,
+                                    const bf16_t* dlogit, float* part, float* dw_router, float* dx_router,
+                                    hipStream_t st) {
+  BwdParams p{};
+  p.T = c->T; p.H = c->H; p.E = L.Ep; p.S = c->S; p.I = c->I;
+  p.ksplit = L.ksplit;
+  p.w_rows = c->E;
+  p.a_shared = dlogit;
+  p.b_shared = x;
+  p.out_routed = part;
+  const int64_t tiles = (int64_t)((L.Ep + kBwdBM - 1) / kBwdBM) * ((c->H + kBwdBN - 1) / kBwdBN);
+  hipLaunchKernelGGL((gemm_bwd_kernel<kDwR2, MOE_BWD_TILE>), dim3((unsigned)(tiles * L.nsplit)), dim3(kBwdThreads), 0, st,
+                     p);
+  moe_status s;
+  if ((s = launch_status()) != MOE_OK) return s;
+  const int64_t n = (int64_t)c->E * c->H;              // (the rows behind E are not summed)
+  hipLaunchKernelGGL(reduce_splits4_kernel, dim3((unsigned)((n / 4 + 255) / 256)), dim3(256), 0, st, (const float4*)part,
+                     L.nsplit, n / 4, (int64_t)L.Ep * c->H / 4, (float4*)dw_router);
+  if ((s = launch_status()) != MOE_OK || !dx_router) return s;
+  p.b_shared = w_router;
+  p.out_shared = dx_router;
+  // Short products (2 * Ep deep) under fp32 stores that nothing reads soon, past the caches (cached: 375 against 352 us
+  // for all the gradients at T = 16384, E = 256, H = 7168): two workgroups a CU, one computing while the other stores.
+XX
   // 256 x 256 352), else 128 x 128 (T = 4096, E = 64, H = 2048: 38.6 us, 128 x 256 40.8).
   auto tiles_of = [&](auto tile) {
     using X = decltype(tile);
