@@ -700,85 +700,6 @@ moe_status launch_router_bwd_gemms2(const moe_cfg* c, const RouteBwdLayout& L, c
   // for all the gradients at T = 16384, E = 256, H = 7168): two workgroups a CU, one computing while the other stores.
   // Tiles of 128 x 256 where they make four rounds of the 256 CUs (303 us there, 128 x 128 308, one workgroup of
   // 256 x 256 318), else 128 x 128 (T = 4096, E = 64, H = 2048: 36.1 us, 128 x 256 37.7).
-  auto tiles_of = [](int64_t m, int64_t n) {
-    return ((m + WgTile::BM - 1) / WgTile::BM) * ((n + WgTile::BN - 1) / WgTile::BN);
-  };
-  const int64_t SI = (int64_t)c->S * c->I;
-  p.a_routed = dgu; p.a_shared = dgus;
-  p.b_routed = x_perm; p.b_shared = x;
-  p.out_routed = gr->w_gate_up; p.out_shared = gr->ws_gate_up;
-  {
-    const int64_t n_sh = c->S > 0 ? tiles_of(2 * SI, c->H) : 0;
-    const int64_t n = dw_grid(n_sh, c->E * tiles_of(2 * c->I, c->H), dw_stripe(kDwGu));
-    hipLaunchKernelGGL((gemm_bwd_kernel<kDwGu, MOE_BWD_WG_TILE>), dim3((unsigned)n), dim3(WgTile::THREADS), 0, st, p);
-    if ((s = launch_status()) != MOE_OK) return s;
-  }
-  p.a_routed = dy_perm; p.a_shared = dy;
-  p.b_routed = h; p.b_shared = hs;
-  p.out_routed = gr->w_down; p.out_shared = gr->ws_down;
-  {
-    const int64_t n_sh = c->S > 0 ? tiles_of(c->H, SI) : 0;
-    const int64_t n = dw_grid(n_sh, c->E * tiles_of(c->H, c->I), dw_stripe(kDwD));
-    hipLaunchKernelGGL((gemm_bwd_kernel<kDwD, MOE_BWD_WG_TILE>), dim3((unsigned)n), dim3(WgTile::THREADS), 0, st, p);
-    if ((s = launch_status()) != MOE_OK) return s;
-  }
-  return MOE_OK;
-}
-
-moe_status launch_router_bwd_gemms(const moe_cfg* c, const bf16_t* x, const bf16_t* w_router,
-                                   const bf16_t* dlogit, float* part, int nsplit, float* dw_router,
-                                   float* dx_router, hipStream_t st) {
-  BwdParams p{};
-  p.T = c->T; p.H = c->H; p.E = c->E; p.S = c->S; p.I = c->I;
-  p.ksplit = kRouterKSplit;
-  p.a_shared = dlogit;
-  p.b_shared = x;
-  p.out_routed = part;
-  const int64_t tiles = (int64_t)((c->E + kBwdBM - 1) / kBwdBM) * ((c->H + kBwdBN - 1) / kBwdBN);
-  hipLaunchKernelGGL((gemm_bwd_kernel<kDwR, MOE_BWD_TILE>), dim3((unsigned)(tiles * nsplit)), dim3(kBwdThreads),
-                     0, st, p);
-  moe_status s;
-  if ((s = launch_status()) != MOE_OK) return s;
-  const int64_t n = (int64_t)c->E * c->H;
-  hipLaunchKernelGGL(reduce_splits_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, part, nsplit, n,
-                     dw_router);
-  if ((s = launch_status()) != MOE_OK) return s;
-  if (dx_router) {
-    p.b_shared = w_router;
-    p.out_shared = dx_router;
-    const int64_t rt = (c->T + kBwdBM - 1) / kBwdBM;
-    hipLaunchKernelGGL((gemm_bwd_kernel<kDxR, MOE_BWD_TILE>), dim3((unsigned)(rt * ((c->H + kBwdBN - 1) / kBwdBN))),
-                       dim3(kBwdThreads), 0, st, p);
-    if ((s = launch_status()) != MOE_OK) return s;
-  }
-  return MOE_OK;
-}
-
-moe_status launch_router_bwd_gemms2(const moe_cfg* c, const RouteBwdLayout& L, const bf16_t* x, const bf16_t* w_router,
-                                    const bf16_t* dlogit, float* part, float* dw_router, float* dx_router,
-                                    hipStream_t st) {
-  BwdParams p{};
-  p.T = c->T; p.H = c->H; p.E = L.Ep; p.S = c->S; p.I = c->I;
-  p.ksplit = L.ksplit;
-  p.w_rows = c->E;
-  p.a_shared = dlogit;
-  p.b_shared = x;
-  p.out_routed = part;
-  const int64_t tiles = (int64_t)((L.Ep + kBwdBM - 1) / kBwdBM) * ((c->H + kBwdBN - 1) / kBwdBN);
-  hipLaunchKernelGGL((gemm_bwd_kernel<kDwR2, MOE_BWD_TILE>), dim3((unsigned)(tiles * L.nsplit)), dim3(kBwdThreads), 0, st,
-                     p);
-  moe_status s;
-  if ((s = launch_status()) != MOE_OK) return s;
-  const int64_t n = (int64_t)c->E * c->H;              // (the rows behind E are not summed)
-  hipLaunchKernelGGL(reduce_splits4_kernel, dim3((unsigned)((n / 4 + 255) / 256)), dim3(256), 0, st, (const float4*)part,
-                     L.nsplit, n / 4, (int64_t)L.Ep * c->H / 4, (float4*)dw_router);
-  if ((s = launch_status()) != MOE_OK || !dx_router) return s;
-  p.b_shared = w_router;
-  p.out_shared = dx_router;
-  // Short products (2 * Ep deep) under fp32 stores that nothing reads soon, past the caches (cached: 375 against 352 us
-  // for all the gradients at T = 16384, E = 256, H = 7168): two workgroups a CU, one computing while the other stores.
-XX
-  // 256 x 256 352), else 128 x 128 (T = 4096, E = 64, H = 2048: 38.6 us, 128 x 256 40.8).
   auto tiles_of = [&](auto tile) {
     using X = decltype(tile);
     return (int64_t)((c->T + X::BM - 1) / X::BM) * ((c->H + X::BN - 1) / X::BN);
