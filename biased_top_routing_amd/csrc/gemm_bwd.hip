@@ -36,10 +36,11 @@
 //         a slice holds both terms of half its depth of K and W_r's rows, or the
 //         tokens', of that once, so that both meet the same operand registers in
 //         the same accumulators.  T = 16384, E = 256, H = 7168: dW_r 109 us, dx
-//         145, 1.1 and 0.8 PFLOP/s, where dx stores 470 MB besides.  (As products
-//         of twice the size, with two sets of partial sums: dW_r 256 us; a walk
-//         over K that passes over the second operand once for either term: 121 and
-//         166 us, bound by the reads of it from LDS.)
+//         121, 1.1 and 1.0 PFLOP/s, where dx stores 470 MB besides; the MFMAs are
+//         busy half the time.  (As products of twice the size, with two sets of
+//         partial sums: dW_r 256 us; a walk over K that passes over the second
+//         operand once for either term: 121 and 166 us, bound by the reads of it
+//         from LDS.)
 #include "bwd_layout.h"
 #include "common.h"
 #include "ffn_layout.h"
@@ -485,6 +486,23 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void gemm_bwd_kernel(BwdParams p
   // The weight gradients (45 GB of fp32 at the V3-like shape, never re-read by
   // this layer) are stored non-temporally: measured 2-5% faster than plain
   // stores, which also displace the operand panels from the L2.
+  if constexpr (KIND == kDxR2) {
+    // (one 32-bit addition a store, dx 145 -> 121 us; rows and columns past the ends lie past the descriptor's range)
+    const __amdgpu_buffer_rsrc_t ro = make_rsrc(static_cast<float*>(p.out_shared) + (int64_t)m0 * N, mvalid * N * 4);
+#pragma unroll
+    for (int ni = 0; ni < NI; ++ni) {
+      const int col = n0 + wn * NI * 32 + ni * 32 + lr;
+      const uint32_t at = col < N ? (uint32_t)((wm * MI * 32 + 4 * kh) * N + col) * 4 : 0x80000000u;
+#pragma unroll
+      for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(acc[mi][ni][r]), ro,
+                                                at + (uint32_t)((mi * 32 + 8 * (r >> 2) + (r & 3)) * N * 4), 0,
+                                                kNonTemporal);
+    }
+    return;
+  }
 #pragma unroll
   for (int mi = 0; mi < MI; ++mi) {
 #pragma unroll
@@ -497,9 +515,8 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void gemm_bwd_kernel(BwdParams p
         const int col = n0 + wn * NI * 32 + ni * 32 + lr;
         if (col >= N) continue;
         const float v = acc[mi][ni][r];
-        if constexpr (is_dxr(KIND)) {
-          if constexpr (KIND == kDxR2) __builtin_nontemporal_store(v, &static_cast<float*>(p.out_shared)[row * N + col]);
-          else static_cast<float*>(p.out_shared)[row * N + col] = v;
+        if constexpr (KIND == kDxR) {
+          static_cast<float*>(p.out_shared)[row * N + col] = v;
         } else if constexpr (KIND == kDwGu) {
           float* o = shared ? static_cast<float*>(p.out_shared)
                             : static_cast<float*>(p.out_routed) + (int64_t)seg * 2 * p.I * p.H;
@@ -699,7 +716,7 @@ moe_status launch_router_bwd_gemms2(const moe_cfg* c, const RouteBwdLayout& L, c
   // Short products (2 * Ep deep) under fp32 stores that nothing reads soon, past the caches (cached: 375 against 352 us
   // for all the gradients at T = 16384, E = 256, H = 7168): two workgroups a CU, one computing while the other stores.
   // Tiles of 128 x 256 where they make four rounds of the 256 CUs (303 us there, 128 x 128 308, one workgroup of
-  // 256 x 256 318), else 128 x 128 (T = 4096, E = 64, H = 2048: 36.1 us, 128 x 256 37.7).
+  // 256 x 256 318, each before its stores took one addition), else 128 x 128 (T = 4096, E = 64, H = 2048: 36.1 us, 128 x 256 37.7).
   auto tiles_of = [&](auto tile) {
     using X = decltype(tile);
     return (int64_t)((c->T + X::BM - 1) / X::BM) * ((c->H + X::BN - 1) / X::BN);

@@ -22,6 +22,9 @@ constexpr int kVmWaitOneStage() {
 // this wave (vmcnt and expcnt left at their maxima).
 constexpr int kLgkmWaitZero = 0xF | (0x3 << 14) | (0x7 << 4);
 
+// Cache policy of buffer loads and stores of what is not needed again soon.
+constexpr int kNonTemporal = 2;
+
 // Word 3 of a raw buffer descriptor (32-bit data format, no swizzle).
 constexpr int kBufferWord3 = 0x00020000;
 

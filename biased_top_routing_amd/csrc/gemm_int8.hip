@@ -22,8 +22,6 @@ typedef int i32x4_t __attribute__((ext_vector_type(4)));
 
 namespace {
 
-constexpr int kNonTemporal = 2;   // the loads' cache policy
-
 enum { kGateUpI8 = 1, kDownI8 = 2 };
 
 struct Int8Params {
