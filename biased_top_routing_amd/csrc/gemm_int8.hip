@@ -8,6 +8,17 @@
 //            needs all of its columns, which several workgroups compute: the rows are quantised between the GEMMs)
 //   down     y = C sh sw, stored as bf16.  The shared experts are one FFN of S I columns: their K ranges follow
 //            each other in one accumulator, so W_d has one scale a channel for all of them.
+//
+// Large batches: resident workgroups of 8 wavefronts, one a CU, each 144 or 64 rows x 64 columns of a tile of 288 or
+// 128 x 256, whose direct-to-LDS loads run ahead through the tiles.  288 rows (2 stages of 128 columns, all that LDS
+// holds) load the fewest bytes an operation; 128 rows (3 stages) waste fewer of short segments: the table's builder
+// counts both and chooses (int8_tile_rows, ffn_layout.h).  T = 16384, H = 7168, 256 experts, 8 + 1 a token, I = 2048:
+// gate/up 3.9 ms, down 2.15 ms, 2.1 POP/s over the whole call, at 1.8 GHz with the MFMAs busy 64% and 56% (a product of
+// two large square matrices by the library reaches 2.3).  16 x 16 x 64 blocks: from registers alone they reach 4.2 to
+// 4.3 POP/s on such operands, 32 x 32 x 32 ones 3.6 (4.9 either on zeros: the clock follows the power).
+// Few rows an expert (the rule beside kInt8RowsAvg): 32-row tiles, bound by reading the weights once, 6.9 TB/s.
+// 4 wavefronts of 128 x 128 7.0 ms a call against 6.2, loads staged through registers 6.8, weights touched ahead in
+// the L2 7.3 to 8.5, loads issued before the stores 6.6; another K order a tile and another XCD run, none.
 #include <algorithm>
 
 #include "common.h"

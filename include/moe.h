@@ -89,7 +89,7 @@ typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_FP8_E4M3 = 2, MOE_MXFP4 = 3, MOE_I
  *  I % 128 == 0, H <= 8192 and max(S, 1)*I <= 8192 (64 scale blocks of K); MXFP4
  *  experts: H % 128 == 0, I % 128 == 0, T*k*max(H, I) and T*max(H, S*I) under 2^36;
  *  INT8 experts: H % 128 == 0, I % 128 == 0, H and max(S, 1)*I under 2^17 (sums in
- *  32 bits), T*k under 2^26.
+ *  32 bits), T*(k+1) under 2^26.
  */
 typedef struct {
   int32_t T, H, E, G, M, k, S, I;

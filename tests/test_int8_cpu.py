@@ -64,7 +64,7 @@ def _cfg(**kw):
     ({}, True), (dict(act="f32"), False), (dict(H=2048 + 64), False), (dict(I=1408 + 64), False),
     (dict(S=0, E=8, G=1, M=1, k=1, I=128, H=(1 << 17) - 128), True), (dict(S=0, E=8, G=1, M=1, k=1, I=128, H=1 << 17), False),
     (dict(S=93, I=1408, H=128), True), (dict(S=94, I=1408, H=128), False),
-    (dict(T=(1 << 26) // 6, H=128, I=128), True), (dict(T=(1 << 26) // 6 + 1, H=128, I=128), False),
+    (dict(T=(1 << 26) // 7, H=128, I=128), True), (dict(T=(1 << 26) // 7 + 1, H=128, I=128), False),
 ])
 def test_configurations(kw, ok):
     assert (L.moe_workspace_bytes(_cfg(**kw), L.MOE_WS_FFN) > 0) == ok
