@@ -5,7 +5,9 @@
 //   E4M3: per 1 x 128 tile, scale = r max|h w| / 448
 //   backward, u = h r, g = dy w:  dx = r (g - u mean(g u)) + dh,  dw = sum_t dy u
 // Both read and write each element once: they are bound by memory.  A row's chunks of 16 bytes stay in
-// registers between its sums and its outputs.
+// registers between its sums and its outputs.  H = 7168, bf16: 32011 rows with residual, E4M3 codes and the normed rows
+// 364 us, 5.7 TB/s read and written (a large copy: 4.8); gradients of 16384 rows with dh 180 us, 5.3 TB/s; one row with
+// int8 codes 4.0 us in its kernel.
 #include <algorithm>
 
 #include "common.h"
@@ -210,16 +212,18 @@ __global__ __launch_bounds__(1024) void norm_bwd_rows_kernel(const int32_t* __re
 }
 
 // Workgroup (b, panel) takes the rows b, b + gridDim.x, ...: dx of the panel's columns, and its sum of dy u over
-// those rows in part[b].  FUSED: one panel holds the row, and the workgroup forms r and m itself.
-template <bool F32, bool FUSED>
+// those rows in part[b].  FUSED: one panel holds the row, and the workgroup forms r and m itself.  NW wavefronts a row;
+// NW == 1: every wavefront takes rows of its own, and their sums are added in order at the end.
+template <bool F32, bool FUSED, int NW>
 __global__ __launch_bounds__(kNormBwdThreads) void norm_bwd_kernel(
     const int32_t* __restrict__ n_tokens, const uint4* __restrict__ h, const uint4* __restrict__ weight, float eps,
     const uint4* dy, const uint4* dh, const float2* __restrict__ rm, int T, int H, uint4* dx, float* __restrict__ part) {
 #if defined(__HIP_DEVICE_COMPILE__)
   using C = Chunk<F32>;
-  constexpr int N = C::N, TH = kNormBwdThreads, CPL = kNormBwdChunks;
+  constexpr int N = C::N, TH = 64 * NW, CPL = kNormBwdChunks, ROWS = kNormBwdThreads / TH;
+  static_assert(NW == 1 || ROWS == 1, "the wavefronts of a row meet at the workgroup's barrier");
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int nchunk = H / N, c0 = blockIdx.y * TH * CPL + threadIdx.x;
+  const int nchunk = H / N, c0 = blockIdx.y * TH * CPL + threadIdx.x % TH;
   const int live = live_rows(n_tokens, T);
   float dw[CPL][N];
   uint4 wv[CPL];
@@ -229,9 +233,9 @@ __global__ __launch_bounds__(kNormBwdThreads) void norm_bwd_kernel(
 #pragma unroll
     for (int j = 0; j < N; ++j) dw[i][j] = 0.f;
   }
-  __shared__ float hh_s[2][TH / 64], gh_s[2][TH / 64];
+  __shared__ float hh_s[2][NW], gh_s[2][NW];
   int turn = 0;                                         // (two sets: a row's sums are read while the next are written)
-  for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
+  for (int64_t t = (int64_t)blockIdx.x * ROWS + threadIdx.x / TH; t < T; t += (int64_t)gridDim.x * ROWS) {
     const int64_t at = t * nchunk;
     if (t >= live) {
 #pragma unroll
@@ -261,12 +265,14 @@ __global__ __launch_bounds__(kNormBwdThreads) void norm_bwd_kernel(
       }
       hh = wave_sum(hh);
       gh = wave_sum(gh);
-      if (lane == 0) hh_s[turn][wave] = hh, gh_s[turn][wave] = gh;
-      __syncthreads();
-      hh = gh = 0.f;
+      if constexpr (NW > 1) {
+        if (lane == 0) hh_s[turn][wave] = hh, gh_s[turn][wave] = gh;
+        __syncthreads();
+        hh = gh = 0.f;
 #pragma unroll
-      for (int i = 0; i < TH / 64; ++i) hh += hh_s[turn][i], gh += gh_s[turn][i];
-      turn ^= 1;
+        for (int i = 0; i < NW; ++i) hh += hh_s[turn][i], gh += gh_s[turn][i];
+        turn ^= 1;
+      }
       r = inv_rms(hh, H, eps);
       m = __fdiv_rn(gh * r, (float)H);
     } else {
@@ -289,6 +295,22 @@ __global__ __launch_bounds__(kNormBwdThreads) void norm_bwd_kernel(
       }
       dx[at + c0 + i * TH] = C::put(e);
     }
+  }
+  if constexpr (ROWS > 1) {                             // the first wavefront adds the others' sums to its own
+    __shared__ float dw_s[ROWS - 1][CPL][N][64];
+    if (wave > 0) {
+#pragma unroll
+      for (int i = 0; i < CPL; ++i)
+#pragma unroll
+        for (int j = 0; j < N; ++j) dw_s[wave - 1][i][j][lane] = dw[i][j];
+    }
+    __syncthreads();
+    if (wave > 0) return;
+#pragma unroll
+    for (int i = 0; i < CPL; ++i)
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        for (int w = 0; w < ROWS - 1; ++w) dw[i][j] += dw_s[w][i][j][lane];
   }
 #pragma unroll
   for (int i = 0; i < CPL; ++i) {
@@ -343,6 +365,14 @@ extern "C" moe_status moe_norm(const moe_cfg* cfg, const int32_t* n_tokens, cons
   for (const void* q : {x, residual, weight, (const void*)h, (const void*)y, (const void*)codes})
     if (misaligned(q, 16)) return MOE_ERR_UNSUPPORTED;
   if (misaligned(code_scale, 4)) return MOE_ERR_UNSUPPORTED;
+  // Just enough lanes for a row, so that what is in flight on a CU is many rows' loads: the lane's chunks and the
+  // wavefronts of a row by its length alone.  With residual, int8 codes and normed rows, us, wavefronts x chunks a lane:
+  //              1 x 4   1 x 16   2 x 4   4 x 4   8 x 2   8 x 4
+  //   4096 x 1024  8.7     16.2     9.9    12.3    14.9    19.1
+  //   4096 x 2048 14.2     23.4    14.9    16.9    17.9    20.6
+  //   4096 x 4096 29.5     36.7    23.8    25.3    26.0    27.4   (1 x 4 reads h again)
+  //    512 x 7168 17.0     17.8    11.0     8.2     7.4     8.0
+  //  16384 x 7168  245      239     218     189     184     184
   const int64_t nchunk = (int64_t)cfg->H * act_bytes(cfg) / 16;
   auto go = [&](auto kernel, int rows, int threads) {
     hipLaunchKernelGGL(kernel, dim3((unsigned)((cfg->T + rows - 1) / rows)), dim3(threads), 0, as_stream(stream), n_tokens,
@@ -352,7 +382,9 @@ extern "C" moe_status moe_norm(const moe_cfg* cfg, const int32_t* n_tokens, cons
   auto shape = [&](auto f, auto c) {
     constexpr bool F = decltype(f)::value;
     constexpr int C = decltype(c)::value;
-    if (nchunk <= 1024 && cfg->T >= kNormWaveRows) go(norm_kernel<F, C, 1, 16>, 4, 256);
+    if (nchunk <= 256) go(norm_kernel<F, C, 1, 4>, 4, 256);
+    else if (nchunk <= 512) go(norm_kernel<F, C, 2, 4>, 1, 128);
+    else if (nchunk <= 1024) go(norm_kernel<F, C, 8, 2>, 1, 512);
     else go(norm_kernel<F, C, 8, 4>, 1, 512);
   };
   using std::integral_constant;
@@ -381,16 +413,18 @@ extern "C" moe_status moe_norm_backward(const moe_cfg* cfg, const int32_t* n_tok
   auto go = [&](auto f) {
     constexpr bool F = decltype(f)::value;
     const dim3 grid((unsigned)L.blocks, (unsigned)L.panels);
+    auto panel = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, grid, dim3(kNormBwdThreads), 0, s, n_tokens, (const uint4*)h, (const uint4*)weight, eps,
+                         (const uint4*)dy, (const uint4*)dh, rm, cfg->T, cfg->H, (uint4*)dx, part);
+    };
     if (L.panels > 1) {
       hipLaunchKernelGGL(norm_bwd_rows_kernel<F>, dim3((unsigned)cfg->T), dim3(1024), 0, s, n_tokens, (const uint4*)h,
                          (const uint4*)weight, eps, (const uint4*)dy, cfg->T, cfg->H, rm);
-      hipLaunchKernelGGL((norm_bwd_kernel<F, false>), grid, dim3(kNormBwdThreads), 0, s, n_tokens, (const uint4*)h,
-                         (const uint4*)weight, eps, (const uint4*)dy, (const uint4*)dh, rm, cfg->T, cfg->H, (uint4*)dx,
-                         part);
+      panel(norm_bwd_kernel<F, false, 4>);
+    } else if (L.rows > 1) {
+      panel(norm_bwd_kernel<F, true, 1>);
     } else {
-      hipLaunchKernelGGL((norm_bwd_kernel<F, true>), grid, dim3(kNormBwdThreads), 0, s, n_tokens, (const uint4*)h,
-                         (const uint4*)weight, eps, (const uint4*)dy, (const uint4*)dh, rm, cfg->T, cfg->H, (uint4*)dx,
-                         part);
+      panel(norm_bwd_kernel<F, true, 4>);
     }
   };
   if (cfg->T > 0) {

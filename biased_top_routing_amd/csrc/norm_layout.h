@@ -7,21 +7,19 @@
 
 namespace moe {
 
-// moe_norm: from this many rows on a wavefront a row fills the chip, below it a workgroup of 8 wavefronts a row.
-constexpr int kNormWaveRows = 2048;
-
 // moe_norm_backward: a workgroup of 256 lanes x 4 chunks of 16 bytes holds a row, or a panel of a longer one; each
 // of at most kNormBwdBlocks workgroups (a panel) leaves a partial sum of dweight.
 constexpr int kNormBwdThreads = 256, kNormBwdChunks = 4, kNormBwdBlocks = 512;
 
 struct NormBwdLayout {
-  int blocks, panels;
+  int blocks, panels, rows;   // rows: that a workgroup works on at a time
   size_t off_rm, off_part, total;
 
   explicit NormBwdLayout(const moe_cfg* c) {
     const int64_t chunks = (int64_t)c->H * (int64_t)act_bytes(c) / 16, panel = kNormBwdThreads * kNormBwdChunks;
     panels = (int)((chunks + panel - 1) / panel);
-    blocks = std::max(1, std::min(c->T, kNormBwdBlocks));
+    rows = chunks <= panel / 4 ? 4 : 1;
+    blocks = std::max(1, std::min((int)(((int64_t)c->T + rows - 1) / rows), kNormBwdBlocks));
     size_t o = 0;
     auto take = [&](size_t bytes) { const size_t at = o; o = align_up(o + bytes, 256); return at; };
     off_rm = take(panels > 1 ? (size_t)c->T * 8 : 0);

@@ -61,6 +61,10 @@ FORWARD = [
     (77, 132, "f32", None, True, True, 70),
     (2100, 1000, "f32", None, False, True, None),
     (4, 20004, "f32", None, True, True, 3),
+    (70, 2048, "bf16", "int8", True, True, None),       # one and two wavefronts a row, exactly and hardly filled
+    (9, 4096, "bf16", "int8", True, True, None),
+    (2300, 2176, "bf16", "fp8_e4m3", True, True, 2299),
+    (50, 2048, "f32", None, True, True, None),
 ]
 
 
@@ -159,6 +163,9 @@ BACKWARD = [
     (256, 128, "f32", True, 201),
     (530, 4096, "f32", True, None),
     (9, 9000, "f32", True, 8),
+    (2600, 512, "bf16", True, 2499),                     # a wavefront a row
+    (2051, 2048, "bf16", False, None),
+    (2049, 1024, "f32", True, None),
 ]
 
 
