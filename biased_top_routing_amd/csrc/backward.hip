@@ -18,6 +18,7 @@
 #include "common.h"
 #include "ffn_layout.h"
 #include "kernels.h"
+#include "route_topk.h"
 
 namespace moe {
 
@@ -287,7 +288,7 @@ void by_epl(int E, F f) {
 
 // Statistics of one chunk of kSeqChunk tokens of one sequence: per expert, how
 // often it was selected and the sum of its normalised affinity s_te / sum_e' s_te'.
-// Each wave takes every fourth token, the rows of four of them loaded at once; the waves' sums are added in order.
+// Each wave takes every fourth token, the rows of TU of them loaded at once; the waves' sums are added in order.
 // EPL: experts a lane, E <= 64 * EPL.
 template <int EPL>
 __global__ __launch_bounds__(256) void seq_stats_kernel(const float* __restrict__ s, const int32_t* __restrict__ idx,
@@ -300,7 +301,7 @@ __global__ __launch_bounds__(256) void seq_stats_kernel(const float* __restrict_
   const int t0 = b * L + ch * kSeqChunk, t1 = min(b * L + L, t0 + kSeqChunk);
   for (int e = threadIdx.x; e < E; e += blockDim.x) c_lds[e] = 0;
   __syncthreads();
-  constexpr int TU = 4;
+  constexpr int TU = EPL >= 8 ? 4 : EPL >= 4 ? 8 : 16;
   float acc[EPL];
 #pragma unroll
   for (int i = 0; i < EPL; ++i) acc[i] = 0.f;
@@ -418,6 +419,18 @@ __global__ __launch_bounds__(256) void route_grad_kernel(const float* __restrict
   }
 }
 
+#if defined(__HIP_DEVICE_COMPILE__)
+// The sum over a wavefront, by DPP and four scalar reads (six shuffles go through LDS).
+__device__ __forceinline__ float row_sum(float v) {
+  v += dpp_f32<kDppXor1>(v);
+  v += dpp_f32<kDppXor2>(v);
+  v += dpp_f32<kDppHalfMirror>(v);
+  v += dpp_f32<kDppMirror>(v);
+  auto at = [&](int l) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), l)); };
+  return (at(0) + at(16)) + (at(32) + at(48));
+}
+#endif
+
 // ... with the flags of moe_route: ds_e of the gates (MOE_GATES_RAW: scale * dw, not through their sum) and of the
 // balance loss, through the softmax (dlogit_e = s_e (ds_e - sum s ds)) or the sigmoid.  dlogit is stored as the sum of
 // two bf16 numbers, the nearest and what it leaves (17 bits and more: the products of the router's gradients then stay
@@ -443,8 +456,8 @@ __global__ __launch_bounds__(256) void route_grad_flags_kernel(const float* __re
     rs += v[i];
     gs += ds[i] * v[i];
   }
-  rs = wave_sum(rs);
-  gs = wave_sum(gs);
+  rs = row_sum(rs);
+  gs = row_sum(gs);
   // (all affinities 0: neither the normalised ones nor a gradient)
 #pragma unroll
   for (int i = 0; i < EPL; ++i) ds[i] = coef && rs > 0.f ? (ds[i] - gs / rs) / rs : 0.f;
@@ -453,8 +466,8 @@ __global__ __launch_bounds__(256) void route_grad_flags_kernel(const float* __re
   if ((unsigned)sel >= (unsigned)E) sel = -1;
   const float ss = sel >= 0 ? s[(int64_t)t * E + sel] : 0.f;
   const float dwj = sel >= 0 ? d_w[(int64_t)t * k + lane] : 0.f;
-  const float S = wave_sum(ss);
-  const float B1 = wave_sum(dwj * ss);
+  const float S = row_sum(ss);
+  const float B1 = row_sum(dwj * ss);
   const float dsel = raw ? scale * dwj : S > 0.f ? scale / S * (dwj - B1 / S) : 0.f;
   for (int j = 0; j < k; ++j) {
     const int ej = __builtin_amdgcn_readlane(sel, j);
@@ -467,7 +480,7 @@ __global__ __launch_bounds__(256) void route_grad_flags_kernel(const float* __re
   if constexpr (SOFTMAX) {
 #pragma unroll
     for (int i = 0; i < EPL; ++i) mean = fmaf(v[i], ds[i], mean);
-    mean = wave_sum(mean);
+    mean = row_sum(mean);
   }
   bf16_t* out = dlogit + (int64_t)t * 2 * Ep;
 #pragma unroll
@@ -496,6 +509,7 @@ __global__ __launch_bounds__(256) void seq_coef_part_kernel(const int32_t* __res
   int c = 0;
   float ps = 0.f;
   if (e < E)
+#pragma unroll 8
     for (int ch = wave; ch < nchunk; ch += 4) {
       c += cnt[((int64_t)b * nchunk + ch) * E + e];
       ps += psum[((int64_t)b * nchunk + ch) * E + e];
