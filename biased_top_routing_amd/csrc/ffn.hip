@@ -205,9 +205,11 @@ moe_status launch_build_tile_tables(const moe_cfg* c, const int32_t* offsets, in
 }
 
 static TileTables ffn_tables(const moe_cfg* c, const FfnLayout& L, char* base) {
+  const int choose = L.bm1 != kTileLowBM ? kChooseNone
+                     : c->wgt == MOE_MXFP4 ? kChooseFp4 : c->wgt == MOE_INT8 ? kChooseInt8 : kChooseNone;
   return TileTables{c->E, c->S, c->T, L.bm1, L.bm1_alt, L.bm2, L.bm2_alt, (int)L.nt1, (int)L.nt1s, (int)L.nt2,
                     reinterpret_cast<TileDesc*>(base + L.off_t1), reinterpret_cast<TileDesc*>(base + L.off_t2),
-                    reinterpret_cast<int32_t*>(base + L.off_hdr), L.bm1 != kTileLowBM ? kChooseNone : c->wgt == MOE_MXFP4 ? kChooseFp4 : c->wgt == MOE_INT8 ? kChooseInt8 : kChooseNone};
+                    reinterpret_cast<int32_t*>(base + L.off_hdr), choose};
 }
 
 moe_status launch_build_tiles(const moe_cfg* c, const int32_t* offsets, void* ws, hipStream_t st) {
@@ -374,7 +376,8 @@ bool int8_misaligned(const moe_cfg* c, const void* x_perm, const float* x_perm_s
 // gathered from x through perm (FP8 and int8: from x_codes, x_scale where they are given).
 moe_status expert_ffn(const moe_cfg* cfg, const void* x_perm, const float* x_perm_scale,
                       const int32_t* perm, const int32_t* offsets, const moe_expert_weights* w,
-                      const void* x, const void* x_codes, const float* x_scale, void* y_perm, void* y_shared, const moe_ffn_saved* saved, void* ws,
+                      const void* x, const void* x_codes, const float* x_scale, void* y_perm, void* y_shared,
+                      const moe_ffn_saved* saved, void* ws,
                       size_t ws_bytes, int phase, void* stream) {
   moe_status st = validate_cfg(cfg);
   if (st != MOE_OK) return st;
@@ -428,7 +431,8 @@ extern "C" moe_status moe_expert_ffn(const moe_cfg* cfg, const void* x_perm, con
                                      void* y_perm, void* y_shared, void* ws, size_t ws_bytes, int phase,
                                      void* stream) {
   if (!x_perm) return MOE_ERR_NULL;
-  return expert_ffn(cfg, x_perm, x_perm_scale, nullptr, offsets, w, x, nullptr, nullptr, y_perm, y_shared, nullptr, ws, ws_bytes,
+  return expert_ffn(cfg, x_perm, x_perm_scale, nullptr, offsets, w, x, nullptr, nullptr, y_perm, y_shared, nullptr, ws,
+                    ws_bytes,
                     phase, stream);
 }
 

@@ -716,7 +716,8 @@ moe_status launch_router_bwd_gemms2(const moe_cfg* c, const RouteBwdLayout& L, c
   // Short products (2 * Ep deep) under fp32 stores that nothing reads soon, past the caches (cached: 375 against 352 us
   // for all the gradients at T = 16384, E = 256, H = 7168): two workgroups a CU, one computing while the other stores.
   // Tiles of 128 x 256 where they make four rounds of the 256 CUs (303 us there, 128 x 128 308, one workgroup of
-  // 256 x 256 318, each before its stores took one addition), else 128 x 128 (T = 4096, E = 64, H = 2048: 36.1 us, 128 x 256 37.7).
+  // 256 x 256 318, each before its stores took one addition), else 128 x 128 (T = 4096, E = 64, H = 2048: 36.1 us,
+  // 128 x 256 37.7).
   auto tiles_of = [&](auto tile) {
     using X = decltype(tile);
     return (int64_t)((c->T + X::BM - 1) / X::BM) * ((c->H + X::BN - 1) / X::BN);

@@ -249,7 +249,8 @@ __device__ __forceinline__ void gemm_int8_tiles(const Int8Params& p, uint8_t* ld
                   __builtin_amdgcn_readfirstlane(wk)};
   };
   auto load_part = [&](const Stream& s, int i) {
-    lds_void_t* dst = (lds_void_t*)(lds + ls * STAGE + wave * 1024 + (i < A_CH ? i * NT * 16 : B_OFF + (i - A_CH) * NT * 16));
+    lds_void_t* dst =
+        (lds_void_t*)(lds + ls * STAGE + wave * 1024 + (i < A_CH ? i * NT * 16 : B_OFF + (i - A_CH) * NT * 16));
     if (A_HALF && i == A_CH - 1 && wave >= NW / 2) return;
     if (i < A_CH)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(s.a, dst, 16, MODE == kGateUpI8 ? a_off[i % A_OFF] : a_off[0] + i * a_dist,
@@ -544,7 +545,8 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void gemm_int8_rows_kernel(Int8Par
   for (int ni = 0; ni < NI8; ++ni)
 #pragma unroll
     for (int r = 0; r < 4; ++r)
-      sw[ni][r] = o.SW[o.template wrow<BN>(p, part, wn * (MODE == kGateUpI8 ? 32 : 64) + 8 * g + col_off<MODE, NI8, BN>(ni) + r)];
+      sw[ni][r] = o.SW[o.template wrow<BN>(
+          p, part, wn * (MODE == kGateUpI8 ? 32 : 64) + 8 * g + col_off<MODE, NI8, BN>(ni) + r)];
 #pragma unroll
   for (int mi = 0; mi < MI; ++mi) {
     const int i = arow0 + mi * 16;

@@ -176,8 +176,9 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void norm_kernel(
 
 // ------------------------------------------------------------------ gradients
 // r and m = mean(g u) of every live row (rows too long for the registers of one workgroup).
+constexpr int kNormRowsThreads = 512;   // (2^23 rows make a grid of fewer than 2^32 lanes)
 template <bool F32>
-__global__ __launch_bounds__(1024) void norm_bwd_rows_kernel(const int32_t* __restrict__ n_tokens,
+__global__ __launch_bounds__(kNormRowsThreads) void norm_bwd_rows_kernel(const int32_t* __restrict__ n_tokens,
                                                              const uint4* __restrict__ h,
                                                              const uint4* __restrict__ weight, float eps,
                                                              const uint4* __restrict__ dy, int T, int H,
@@ -189,7 +190,7 @@ __global__ __launch_bounds__(1024) void norm_bwd_rows_kernel(const int32_t* __re
   if (t >= live_rows(n_tokens, T)) return;
   const int nchunk = H / N, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   float hh = 0.f, gh = 0.f;
-  for (int c = threadIdx.x; c < nchunk; c += 1024) {
+  for (int c = threadIdx.x; c < nchunk; c += kNormRowsThreads) {
     float a[N], d[N], w[N];
     C::get(h[t * nchunk + c], a);
     C::get(dy[t * nchunk + c], d);
@@ -199,12 +200,13 @@ __global__ __launch_bounds__(1024) void norm_bwd_rows_kernel(const int32_t* __re
   }
   hh = wave_sum(hh);
   gh = wave_sum(gh);
-  __shared__ float hh_s[16], gh_s[16];
+  constexpr int NW = kNormRowsThreads / 64;
+  __shared__ float hh_s[NW], gh_s[NW];
   if (lane == 0) hh_s[wave] = hh, gh_s[wave] = gh;
   __syncthreads();
   if (threadIdx.x == 0) {
     hh = gh = 0.f;
-    for (int i = 0; i < 16; ++i) hh += hh_s[i], gh += gh_s[i];
+    for (int i = 0; i < NW; ++i) hh += hh_s[i], gh += gh_s[i];
     const float r = inv_rms(hh, H, eps);
     rm[t] = make_float2(r, __fdiv_rn(gh * r, (float)H));
   }
@@ -418,8 +420,8 @@ extern "C" moe_status moe_norm_backward(const moe_cfg* cfg, const int32_t* n_tok
                          (const uint4*)dy, (const uint4*)dh, rm, cfg->T, cfg->H, (uint4*)dx, part);
     };
     if (L.panels > 1) {
-      hipLaunchKernelGGL(norm_bwd_rows_kernel<F>, dim3((unsigned)cfg->T), dim3(1024), 0, s, n_tokens, (const uint4*)h,
-                         (const uint4*)weight, eps, (const uint4*)dy, cfg->T, cfg->H, rm);
+      hipLaunchKernelGGL(norm_bwd_rows_kernel<F>, dim3((unsigned)cfg->T), dim3(kNormRowsThreads), 0, s, n_tokens,
+                         (const uint4*)h, (const uint4*)weight, eps, (const uint4*)dy, cfg->T, cfg->H, rm);
       panel(norm_bwd_kernel<F, false, 4>);
     } else if (L.rows > 1) {
       panel(norm_bwd_kernel<F, true, 1>);

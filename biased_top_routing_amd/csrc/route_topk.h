@@ -60,7 +60,7 @@ struct Softmax {
   // top and the sum over the token's logits, alike on all of its lanes
   __device__ __forceinline__ void set(float m) { top = m == -__builtin_huge_valf() ? 0.0 : (double)m; }
   __device__ __forceinline__ double term(float l) const { return exp((double)l - top); }
-  __device__ __forceinline__ void total(double z) { inv = z > 0.0 ? 1.0 / z : 0.0; }   // (all logits -inf: 0 everywhere)
+  __device__ __forceinline__ void total(double z) { inv = z == 0.0 ? 0.0 : 1.0 / z; }   // (all logits -inf: 0 everywhere)
   __device__ __forceinline__ float share(double e) const { return (float)(e * inv); }
 };
 

@@ -267,6 +267,8 @@ class MoeLayerGPU:
         elsewhere, and g_norm the norm weight's."""
         if dh is not None and self.norm is None:
             raise ValueError("dh is the gradient of the norm's input sum: the layer has no norm")
+        if dh is not None:
+            self._check_rows("dh", dh)
         if self.gather:
             raise ValueError("backward reads the permuted rows x_perm: build the layer with gather=False")
         if self.n_tokens is not None and alpha:
@@ -326,6 +328,8 @@ class MoeLayerGPU:
         shared experts' output for whatever its row of x holds.
         residual: [T, H], added to x before the norm (layers with a norm)."""
         self._check_batch(gamma, n_tokens, residual)
+        if self.norm is not None:
+            self._check_rows("x", x)
         self.n_tokens = n_tokens
         if self.norm is not None:
             x = self.add_and_norm(x, residual)
@@ -340,10 +344,17 @@ class MoeLayerGPU:
     def _check_batch(self, gamma, n_tokens, residual=None):
         """Refuses what forward() cannot run, before anything is launched."""
         L.live_count(n_tokens)
-        if residual is not None and self.norm is None:
-            raise ValueError("a residual is added before the norm: the layer has none")
+        if residual is not None:
+            if self.norm is None:
+                raise ValueError("a residual is added before the norm: the layer has none")
+            self._check_rows("residual", residual)
         if gamma is not None and (self.share is not None or n_tokens is not None):
             raise ValueError("the bias update needs the loads of a whole batch over every expert")
+
+    def _check_rows(self, name, t):
+        if t.dim() != 2 or t.shape[0] < self.T or t.shape[1] != self.c.H or t.dtype != self.act_dtype:
+            raise ValueError(f"{name} of shape {tuple(t.shape)}, {t.dtype}: needs {self.T} rows of {self.c.H}, "
+                             f"{self.act_dtype}")
 
     # ---------------------------------------------------------------- HIP graph
     def capture(self, x, bias, gamma=None, n_tokens=None, residual=None):

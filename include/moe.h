@@ -131,7 +131,8 @@ typedef struct {
  *               where no kernel keeps them on chip); ignored otherwise (may be NULL)
  * Groups are chosen first (the M largest group scores, ties to the lower group),
  * then the k largest s + b among the experts of the chosen groups.
- * NaN scores give unspecified indices.
+ * NaN scores give unspecified indices (below E).  With MOE_SOFTMAX a logit that is NaN
+ * or +infinity makes its row's affinities NaN.
  * For mid-size bf16 batches (too large for the split-K router, too small for
  * router tiles of 128 tokens to fill the chip; E = 256: 2049 <= T < 16384) with
  * E = 16, 32, 64, 128 or 256 in groups of a power-of-two number of 16-lane

@@ -86,6 +86,24 @@ def test_softmax_routing(T, H, E, G, M, k, topr, act, mask):
         assert (np.abs(gates - gr) <= 40 * EPS32 * gr).all()
 
 
+@pytest.mark.parametrize("T,E,G,k", [(9, 256, 8, 8), (2100, 256, 8, 8), (9, 64, 4, 6), (5000, 64, 4, 6), (9, 60, 5, 20)])
+def test_a_row_with_a_nan_or_an_infinity(T, E, G, k):
+    """Its affinities are NaN, its experts some of the E, and no other row changes."""
+    x, w, bias = _inputs(T, 64, E, "bf16")
+    cfg = L.make_cfg(T, 64, E, G, G, k, 0, 128, 2, 1.0, "bf16", "bf16")
+    say(f"softmax of NaN T={T} E={E}")
+    run = lambda a: _route(cfg, to_device(f32_to_bf16_bits(a)), to_device(f32_to_bf16_bits(w)), None, dev_f32(bias),
+                           L.MOE_SOFTMAX, True)
+    want = run(x)
+    bad = x.copy()
+    bad[1, 5], bad[T - 1, 0] = np.nan, np.inf
+    s, idx, gates = run(bad)
+    assert np.isnan(s[[1, T - 1]]).all() and np.isnan(gates[[1, T - 1]]).all() and (idx >= 0).all() and (idx < E).all()
+    for got, ref in zip((s, idx, gates), want):
+        rest = np.delete(np.arange(T), [1, T - 1])
+        assert (got[rest] == ref[rest]).all()
+
+
 @pytest.mark.parametrize("E,G,M,k,topr", [(256, 8, 4, 8, 2), (256, 1, 1, 16, 4), (128, 16, 3, 6, 1), (128, 2, 1, 1, 3),
                                           (256, 16, 16, 16, 4)])
 @pytest.mark.parametrize("flags", [0, L.MOE_GATES_RAW])

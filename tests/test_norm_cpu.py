@@ -138,6 +138,21 @@ def test_runner_refusals():
         layer.backward(None, None, dh=object())
 
 
+def test_runner_refuses_rows_of_another_shape():
+    layer = MoeLayerGPU.__new__(MoeLayerGPU)
+    layer.c, layer.share, layer.gather, layer.n_tokens, layer.adds_balance = MID, None, False, None, True
+    layer.T, layer.act_dtype, layer.norm = 8, torch.bfloat16, object()
+    rows = lambda *shape, dtype=torch.bfloat16: torch.zeros(shape, dtype=dtype)
+    good = rows(8, MID.H)
+    for bad in (rows(7, MID.H), rows(8, MID.H - 8), rows(8 * MID.H), rows(8, MID.H, dtype=torch.float32)):
+        with pytest.raises(ValueError, match="residual of shape"):
+            layer.forward(good, None, residual=bad)
+        with pytest.raises(ValueError, match="x of shape"):
+            layer.forward(bad, None, residual=good)
+        with pytest.raises(ValueError, match="dh of shape"):
+            layer.backward(good, good, dh=bad)
+
+
 # ---------------------------------------------------------------- refusals: routing flags
 def test_route_flags():
     cfg = L.cfg_from(MID)
