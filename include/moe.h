@@ -131,8 +131,7 @@ typedef struct {
  *               where no kernel keeps them on chip); ignored otherwise (may be NULL)
  * Groups are chosen first (the M largest group scores, ties to the lower group),
  * then the k largest s + b among the experts of the chosen groups.
- * NaN scores give unspecified indices (below E).  With MOE_SOFTMAX a logit that is NaN
- * or +infinity makes its row's affinities NaN.
+ * NaN scores give unspecified indices (below E).
  * For mid-size bf16 batches (too large for the split-K router, too small for
  * router tiles of 128 tokens to fill the chip; E = 256: 2049 <= T < 16384) with
  * E = 16, 32, 64, 128 or 256 in groups of a power-of-two number of 16-lane
@@ -149,8 +148,8 @@ typedef struct {
  * are computed, and affinities that differ keep their order.  An expert with l = -inf has
  * s = 0 (a mask: an offset of -inf takes it out of service, though it may be selected
  * where fewer than k others are allowed); a token whose logits are all -inf has s = 0
- * everywhere.  Gates of a token whose selected affinities are all 0 are 0.  Logits of
- * +inf or NaN give unspecified results.
+ * everywhere.  Gates of a token whose selected affinities are all 0 are 0.  A logit of
+ * +inf or NaN makes s of its token NaN.
  * MOE_SOFTMAX cannot be combined with MOE_SCORES_IN (the affinities are there;
  * MOE_ERR_UNSUPPORTED); MOE_GATES_RAW goes with all.
  * MOE_ERR_WORKSPACE: scores is NULL and ws is NULL or too small.

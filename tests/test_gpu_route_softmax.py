@@ -172,6 +172,9 @@ BACKWARD = [
     (1100, 384, 256, 8, 0.01, 0),
     (257, 64, 300, 16, 0.0, 0),
     (2048, 128, 512, 8, 0.05, 512),
+    (1200, 64, 16, 2, 0.05, 1),            # 1200 partial losses, 1024 and 1032
+    (256, 64, 256, 4, 0.05, 1),
+    (129, 64, 512, 4, 0.05, 1),
 ]
 
 
