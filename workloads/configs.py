@@ -30,7 +30,7 @@ class MoeConfig:
     group_topr: int   # group score = sum of the top-r biased scores in the group
     route_scale: float
     act: str          # "f32" | "bf16"
-    wgt: str          # "f32" | "bf16" | "fp8_e4m3"
+    wgt: str          # "f32" | "bf16" | "fp8_e4m3" | "mxfp4" | "int8"
     sigma: float      # std-dev of every weight tensor
     offset_kind: Optional[str]   # None | "normal" | "zipf"
     zipf_s: float
