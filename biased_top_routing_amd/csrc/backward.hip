@@ -287,7 +287,8 @@ void by_epl(int E, F f) {
 }
 
 // Statistics of one chunk of kSeqChunk tokens of one sequence: per expert, how
-// often it was selected and the sum of its normalised affinity s_te / sum_e' s_te'.
+// often it was selected and the sum of its normalised affinity s_te / sum_e' s_te'
+// (of a token whose affinities are all 0: nothing).
 // Each wave takes every fourth token, the rows of TU of them loaded at once; the waves' sums are added in order.
 // EPL: experts a lane, E <= 64 * EPL.
 template <int EPL>
@@ -326,7 +327,7 @@ __global__ __launch_bounds__(256) void seq_stats_kernel(const float* __restrict_
       for (int i = 0; i < EPL; ++i) rs += v[u][i];
       rs = wave_sum(rs);
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) acc[i] += v[u][i] / rs;
+      for (int i = 0; i < EPL; ++i) acc[i] += rs == 0.f ? 0.f : v[u][i] / rs;
       if ((unsigned)sel[u] < (unsigned)E) atomicAdd(&c_lds[sel[u]], 1);       // integer counts: order-free
     }
   }
@@ -396,7 +397,7 @@ __global__ __launch_bounds__(256) void route_grad_kernel(const float* __restrict
   rs = wave_sum(rs);
   gs = wave_sum(gs);
 #pragma unroll
-  for (int i = 0; i < kMaxEPL; ++i) ds[i] = ds[i] / rs - gs / (rs * rs);
+  for (int i = 0; i < kMaxEPL; ++i) ds[i] = rs == 0.f ? 0.f : ds[i] / rs - gs / (rs * rs);
   // gates over the selected experts (an id outside [0, E) is none)
   int sel = lane < k ? idx[(int64_t)t * k + lane] : -1;
   if ((unsigned)sel >= (unsigned)E) sel = -1;
@@ -404,7 +405,7 @@ __global__ __launch_bounds__(256) void route_grad_kernel(const float* __restrict
   const float dwj = sel >= 0 ? d_w[(int64_t)t * k + lane] : 0.f;
   const float S = wave_sum(ss);
   const float B1 = wave_sum(dwj * ss);
-  const float dsel = scale / S * (dwj - B1 / S);
+  const float dsel = S == 0.f ? 0.f : scale / S * (dwj - B1 / S);   // (no affinity at all: no gradient)
   for (int j = 0; j < k; ++j) {
     const int ej = __shfl(sel, j);
     const float dj = __shfl(dsel, j);
@@ -477,7 +478,7 @@ __global__ __launch_bounds__(256) void route_grad_flags_kernel(const float* __re
   gs = row_sum(gs);
   // (all affinities 0: neither the normalised ones nor a gradient)
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) ds[i] = coef && rs > 0.f ? (ds[i] - gs / rs) / rs : 0.f;
+  for (int i = 0; i < EPL; ++i) ds[i] = coef && rs != 0.f ? (ds[i] - gs / rs) / rs : 0.f;
   // gates over the selected experts (an id outside [0, E) is none)
   int sel = lane < k ? idx[(int64_t)t * k + lane] : -1;
   if ((unsigned)sel >= (unsigned)E) sel = -1;
@@ -485,7 +486,7 @@ __global__ __launch_bounds__(256) void route_grad_flags_kernel(const float* __re
   const float dwj = sel >= 0 ? d_w[(int64_t)t * k + lane] : 0.f;
   const float S = row_sum(ss);
   const float B1 = row_sum(dwj * ss);
-  const float dsel = raw ? scale * dwj : S > 0.f ? scale / S * (dwj - B1 / S) : 0.f;
+  const float dsel = raw ? scale * dwj : S != 0.f ? scale / S * (dwj - B1 / S) : 0.f;
   for (int j = 0; j < k; ++j) {
     const int ej = __builtin_amdgcn_readlane(sel, j);
     const float dj = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(dsel), j));

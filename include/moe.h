@@ -479,8 +479,7 @@ moe_status moe_norm_backward(const moe_cfg* cfg, const int32_t* n_tokens, const 
  * term does not depend on it, so alpha is 0 on all ranks but one.
  * moe_expert_ffn_backward* (of the shared experts) and moe_route_backward contract
  * over all T rows: for a padded batch's gradients the rows of dy behind the live
- * tokens have to be zero, and those of x, scores and saved->gs and us finite (of
- * scores not zero either).
+ * tokens have to be zero, and those of x, scores and saved->gs and us finite.
  * With T == 0 tensors without elements may be NULL in these four calls; they take
  * T below 2^23 (MOE_ERR_SHAPE).
  * moe_update_bias compares with T*k pairs over cfg's E experts: it is for whole
@@ -617,6 +616,8 @@ moe_status moe_expert_ffn_backward_saved(const moe_cfg* cfg, const void* x_perm,
  *           sequences of seq_len consecutive tokens; per sequence
  *           f_e = E / (k L) * (selections of e), P_e = mean_t s_te / sum_e' s_te',
  *           L_bal = alpha * mean over sequences of sum_e f_e P_e
+ *           (a token whose affinities are all 0 adds nothing to P_e and gets no
+ *           gradient; one whose selected affinities are all 0 none through its gates)
  *   router  dlogit = ds * s (1 - s);  dx_router = dlogit W_r;  dw_router = dlogit^T x
  *  x [T, H], w_router [E, H] bf16; scores [T, E] fp32 affinities (moe_route's
  *  output); topk_idx [T, k] as moe_route wrote it (an id outside [0, E) is passed
@@ -639,8 +640,6 @@ moe_status moe_route_backward(const moe_cfg* cfg, const void* x, const void* w_r
  *   MOE_SOFTMAX     dlogit_e = s_e (ds_e - sum_e' s_e' ds_e')
  * Other than moe_route_backward, which rounds dlogit to bf16 for its products, this call
  * carries it as the sum of two bf16 numbers (16 bits and more).
- * A token whose selected affinities are all 0 gives no gradient through renormalised
- * gates, one whose affinities are all 0 none at all.
  *  ws of at least moe_workspace_bytes(cfg, MOE_WS_ROUTE_BWD_SOFTMAX).  x, w_router,
  *  dw_router and ws must be 16-byte aligned, the rest 4-byte (MOE_ERR_UNSUPPORTED); T below
  *  2^23, and T / seq_len * ceil(E / 64) below 2^24 (MOE_ERR_SHAPE).

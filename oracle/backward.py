@@ -40,22 +40,25 @@ def gate_backward(s_sel: np.ndarray, dw: np.ndarray, scale: float) -> np.ndarray
     """d loss / d s at the selected experts, given d loss / d w.
 
     w_j = c s_j / S with S = sum_j s_j, so dw_j/ds_i = c (delta_ij / S - s_j / S^2) and
-    ds_i = (c / S) (dw_i - sum_j dw_j s_j / S).   s_sel, dw: [T, k]."""
+    ds_i = (c / S) (dw_i - sum_j dw_j s_j / S); 0 where S is.   s_sel, dw: [T, k]."""
     s_sel = np.asarray(s_sel, F64)
     dw = np.asarray(dw, F64)
     S = s_sel.sum(axis=1, keepdims=True)
-    return (scale / S) * (dw - (dw * s_sel).sum(axis=1, keepdims=True) / S)
+    one = np.where(S == 0, 1.0, S)
+    return np.where(S == 0, 0.0, (scale / one) * (dw - (dw * s_sel).sum(axis=1, keepdims=True) / one))
 
 
 def seq_balance_loss(s: np.ndarray, idx: np.ndarray, k: int, seq_len: int, alpha: float):
-    """(loss, d loss / d s [T, E]) of the sequence-wise balance loss read above."""
+    """(loss, d loss / d s [T, E]) of the sequence-wise balance loss read above.  A token whose affinities are all 0
+    adds nothing to P and gets no gradient (its selections count in f)."""
     s = np.asarray(s, F64)
     T, E = s.shape
     assert T % seq_len == 0, "whole sequences"
     B = T // seq_len
     hit = np.zeros((T, E), F64)
     np.put_along_axis(hit, np.asarray(idx, np.int64), 1.0, axis=1)
-    row_sum = s.sum(axis=1, keepdims=True)
+    total = s.sum(axis=1, keepdims=True)
+    row_sum = np.where(total == 0, 1.0, total)
     sn = s / row_sum                                        # s'_te
     loss = 0.0
     g = np.zeros((T, E), F64)                               # d loss / d s'
@@ -67,7 +70,7 @@ def seq_balance_loss(s: np.ndarray, idx: np.ndarray, k: int, seq_len: int, alpha
         g[rows] = alpha / B * f[None, :] / seq_len
     # s' = s / sum(s): ds_i = g_i / S - sum_e g_e s_e / S^2
     ds = g / row_sum - (g * s).sum(axis=1, keepdims=True) / row_sum ** 2
-    return loss, ds
+    return loss, np.where(total == 0, 0.0, ds)
 
 
 def route_backward(x, w_router, s, idx, dw, scale: float, alpha: float = 0.0, seq_len: int = 0, softmax: bool = True,
