@@ -558,6 +558,16 @@ __global__ __launch_bounds__(1024) void seq_loss_kernel(SeqLoss seq) {
   }
 }
 
+// Weight gradients of a batch without tokens.
+__global__ __launch_bounds__(256) void zero_kernel(float* __restrict__ p, int64_t n) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) p[i] = 0.f;
+}
+
+moe_status launch_zero(float* p, int64_t n, hipStream_t st) {
+  hipLaunchKernelGGL(zero_kernel, dim3((unsigned)std::min<int64_t>((n + 255) / 256, 2048)), dim3(256), 0, st, p, n);
+  return launch_status();
+}
+
 bool bwd_dtypes_ok(const moe_cfg* c) { return c->act == MOE_BF16 && c->wgt == MOE_BF16; }
 
 // one lane per 16-byte chunk of a row, whole wavefronts, at most 1024 lanes
@@ -681,7 +691,8 @@ moe_status route_backward(const moe_cfg* cfg, bool with_flags, uint32_t flags, c
   if (cfg->T == 0) {
     hipLaunchKernelGGL(seq_coef_kernel, dim3(1), dim3(256), 0, s, cnt, psum, cfg->E, cfg->k, 1, 0, 0, 0.0f, coef,
                        loss);
-    return launch_status();
+    if ((st = launch_status()) != MOE_OK) return st;
+    return launch_zero(dw_router, (int64_t)cfg->E * cfg->H, s);
   }
   const bool bal = alpha > 0.0f;
   if (bal) {

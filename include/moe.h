@@ -625,7 +625,7 @@ moe_status moe_expert_ffn_backward_saved(const moe_cfg* cfg, const void* x_perm,
  *  moe_dispatch_local keep their id here, their d_topk_w is 0);
  *  d_topk_w [T, k] from moe_combine_backward;
  *  alpha >= 0 (0: no balance loss); seq_len 0 (= T) or a divisor of T;
- *  dx_router [T, H] fp32 out (may be NULL); dw_router [E, H] fp32 out;
+ *  dx_router [T, H] fp32 out (may be NULL); dw_router [E, H] fp32 out (zero with T == 0);
  *  loss: one fp32 out (L_bal); ws of at least moe_workspace_bytes(cfg, MOE_WS_ROUTE_BWD).
  */
 moe_status moe_route_backward(const moe_cfg* cfg, const void* x, const void* w_router, const float* scores,

@@ -81,3 +81,27 @@ def test_a_token_without_affinities(T, H, E, k, alpha, seq, flags):
     assert (dx[none] == 0).all()
     assert abs(loss - lr) <= (T + E + 40) * EPS32 * abs(lr) and (lr > 0) == (alpha > 0)
     assert (np.abs(dx - dxr) <= tx).all() and (np.abs(dw - dwr) <= tw).all()
+
+
+@pytest.mark.parametrize("flags", FLAGS)
+@pytest.mark.parametrize("H,E", [(64, 1), (192, 13), (4096, 512)])
+def test_an_empty_batch(H, E, flags):
+    """Sums over no token: a weight gradient and a loss of 0, and nothing written behind them."""
+    say(f"route backward, empty batch, H={H} E={E} flags={flags}")
+    cfg = L.make_cfg(0, H, E, 1, 1, 1, 0, 128, 1, 2.5, "bf16", "bf16")
+    nan = lambda n: torch.full((n,), float("nan"), device="cuda")
+    one = torch.zeros(16, dtype=torch.bfloat16, device="cuda")            # (there has to be some address)
+    ids = torch.zeros(4, dtype=torch.int32, device="cuda")
+    for alpha, with_dx in ((0.0, True), (0.5, False)):
+        dw, loss, dx = nan(E * H + 4), nan(2), nan(4)
+        kind = L.MOE_WS_ROUTE_BWD if flags is None else L.MOE_WS_ROUTE_BWD_SOFTMAX
+        ws = torch.full((L.moe_workspace_bytes(cfg, kind),), 0xFF, dtype=torch.uint8, device="cuda")
+        args = (one, one, nan(4), ids, nan(4), alpha, 0, dx if with_dx else None, dw, loss, ws)
+        if flags is None:
+            L.moe_route_backward(cfg, *args)
+        else:
+            L.moe_route_backward_flags(cfg, flags, *args)
+        torch.cuda.synchronize()
+        dw, loss = host(dw), host(loss)
+        assert (dw[:E * H] == 0).all() and np.isnan(dw[E * H:]).all()
+        assert loss[0] == 0 and np.isnan(loss[1]) and np.isnan(host(dx)).all()
