@@ -631,7 +631,14 @@ moe_status expert_ffn_backward(const moe_cfg* cfg, const void* x_perm, const voi
     return MOE_ERR_UNSUPPORTED;
   if (saved && (!saved->g || !saved->u || (cfg->S > 0 && (!saved->gs || !saved->us)))) return MOE_ERR_NULL;
   if (ws_bytes < FfnBwdLayout(cfg).total) return MOE_ERR_WORKSPACE;
-  if (cfg->T == 0) return MOE_OK;
+  if (cfg->T == 0) {
+    const int64_t down = (int64_t)cfg->H * cfg->I;         // (gate and up together: twice as many)
+    const hipStream_t s = as_stream(stream);
+    if ((st = launch_zero(grads->w_gate_up, 2 * cfg->E * down, s)) != MOE_OK) return st;
+    if ((st = launch_zero(grads->w_down, cfg->E * down, s)) != MOE_OK || cfg->S == 0) return st;
+    if ((st = launch_zero(grads->ws_gate_up, 2 * cfg->S * down, s)) != MOE_OK) return st;
+    return launch_zero(grads->ws_down, cfg->S * down, s);
+  }
   return launch_ffn_bwd_bf16(cfg, (const bf16_t*)x_perm, (const bf16_t*)x, offsets, w, saved,
                              (const bf16_t*)dy_perm, (const bf16_t*)dy, (bf16_t*)dx_perm, (bf16_t*)dx_shared, grads,
                              ws, as_stream(stream));

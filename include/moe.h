@@ -584,7 +584,7 @@ typedef struct {
  *  moe_combine_backward; dy [T, H];
  *  dx_perm [T*k, H] out (routed rows' input gradient, permuted order);
  *  dx_shared [T, H] out (S > 0); grads out (every member non-NULL; the shared
- *  ones when S > 0); ws of at least moe_workspace_bytes(cfg, MOE_WS_FFN_BWD).
+ *  ones when S > 0; zero with T == 0); ws of at least moe_workspace_bytes(cfg, MOE_WS_FFN_BWD).
  * MOE_ERR_UNSUPPORTED when T * max(H, 2 * max(S, 1) * I) * 2 bytes exceeds
  * 2^31 - 1 (operand rows are addressed by 32-bit offsets within a segment).
  */

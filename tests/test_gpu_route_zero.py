@@ -105,3 +105,30 @@ def test_an_empty_batch(H, E, flags):
         dw, loss = host(dw), host(loss)
         assert (dw[:E * H] == 0).all() and np.isnan(dw[E * H:]).all()
         assert loss[0] == 0 and np.isnan(loss[1]) and np.isnan(host(dx)).all()
+
+
+@pytest.mark.parametrize("S", [0, 2])
+@pytest.mark.parametrize("saved", [False, True])
+def test_the_experts_gradients_of_an_empty_batch(S, saved):
+    say(f"expert gradients, empty batch, S={S} saved={saved}")
+    E, H, I = 3, 192, 128
+    cfg = L.make_cfg(0, H, E, 1, 1, 1, S, I, 1, 1.0, "bf16", "bf16")
+    nan = lambda n: torch.full((n + 4,), float("nan"), device="cuda")
+    sizes = [E * 2 * I * H, E * H * I] + ([S * 2 * I * H, S * H * I] if S else [])
+    out = [nan(n) for n in sizes]
+    grads = L.expert_grads(*(out if S else out + [None, None]))
+    one = torch.zeros(64, dtype=torch.bfloat16, device="cuda")            # (there has to be some address)
+    sh = (one, one) if S else (None, None)
+    w = L.expert_weights(one, one, *sh)
+    offsets = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    ws = torch.full((L.moe_workspace_bytes(cfg, L.MOE_WS_FFN_BWD),), 0xFF, dtype=torch.uint8, device="cuda")
+    if saved:
+        keep = L.ffn_saved(one, one, *sh)
+        L.moe_expert_ffn_backward_saved(cfg, one, one, offsets, w, keep, one, one, one, one, grads, ws)
+    else:
+        L.moe_expert_ffn_backward(cfg, one, one, offsets, w, one, one, one, one, grads, ws)
+    torch.cuda.synchronize()
+    for t, n in zip(out, sizes):
+        g = host(t)
+        assert (g[:n] == 0).all() and np.isnan(g[n:]).all()
+    assert (host(one) == 0).all()
