@@ -174,7 +174,7 @@ __global__ __launch_bounds__(256) void route_topk_kernel(
     for (int off = LPT / 2; off > 0; off >>= 1) tot += __shfl_xor(tot, off);
     if (valid && sl < k) {
       idx_out[(int64_t)t * k + sl] = my_e;
-      w_out[(int64_t)t * k + sl] = gate_of<SOFTMAX>(my_s, tot, scale, raw);
+      w_out[(int64_t)t * k + sl] = gate_of(my_s, tot, scale, raw);
     }
     __syncthreads();   // LDS slots are reused by the next token
   }

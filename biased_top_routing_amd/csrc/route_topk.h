@@ -64,11 +64,11 @@ struct Softmax {
   __device__ __forceinline__ float share(double e) const { return (float)(e * inv); }
 };
 
-// The gate of a selected expert: its affinity, over the sum of the selected ones unless it is to stay raw.
-template <bool SOFTMAX>
+// The gate of a selected expert: its affinity, over the sum of the selected ones unless it is to stay raw; 0 where
+// there is none (masked experts, or affinities that underflow).
 __device__ __forceinline__ float gate_of(float s, float total, float scale, bool raw) {
   if (raw) return scale * s;
-  if (SOFTMAX && total == 0.f) return 0.f;   // (every selected expert masked)
+  if (s == 0.f && total == 0.f) return 0.f;
   return scale * s / total;
 }
 
@@ -211,7 +211,7 @@ __device__ __forceinline__ void topk16_token(const float* row, float* s_out, con
   tot += dpp_f32<kDppMirror>(tot);
   if (valid && sl < k) {
     idx_out[sl] = my_e;
-    w_out[sl] = gate_of<SOFTMAX>(my_s, tot, scale, raw);
+    w_out[sl] = gate_of(my_s, tot, scale, raw);
   }
 }
 
@@ -313,7 +313,7 @@ __device__ __forceinline__ void topk64_token(const float* row, float* s_out, con
   tot += dpp_f32<kDppMirror>(tot);
   if (lane < k) {
     idx_out[lane] = my_e;
-    w_out[lane] = gate_of<SOFTMAX>(my_s, tot, scale, raw);
+    w_out[lane] = gate_of(my_s, tot, scale, raw);
   }
 }
 

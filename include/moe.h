@@ -125,7 +125,8 @@ typedef struct {
  *               no router gradient)
  *  topk_idx     [T, k] int32 out: selected experts, ordered by s + b descending,
  *               ties to the lower expert index (-0.0 ranks as +0.0)
- *  topk_w       [T, k] fp32 out: route_scale * s_j / sum_j s_j
+ *  topk_w       [T, k] fp32 out: route_scale * s_j / sum_j s_j (0 where the selected
+ *               affinities are all 0)
  *  ws, ws_bytes workspace of at least moe_workspace_bytes(cfg, MOE_WS_ROUTE)
  *               bytes, required when scores is NULL (it stages the affinities
  *               where no kernel keeps them on chip); ignored otherwise (may be NULL)
@@ -148,8 +149,7 @@ typedef struct {
  * are computed, and affinities that differ keep their order.  An expert with l = -inf has
  * s = 0 (a mask: an offset of -inf takes it out of service, though it may be selected
  * where fewer than k others are allowed); a token whose logits are all -inf has s = 0
- * everywhere.  Gates of a token whose selected affinities are all 0 are 0.  A logit of
- * +inf or NaN makes s of its token NaN.
+ * everywhere.  A logit of +inf or NaN makes s of its token NaN.
  * MOE_SOFTMAX cannot be combined with MOE_SCORES_IN (the affinities are there;
  * MOE_ERR_UNSUPPORTED); MOE_GATES_RAW goes with all.
  * MOE_ERR_WORKSPACE: scores is NULL and ws is NULL or too small.

@@ -1,4 +1,5 @@
-"""GPU parity of the router's gradients where a token has no affinity at all (every logit -inf), and of empty batches.
+"""GPU parity of the routing and its gradients where a token has no affinity at all (every logit -inf), and of empty
+batches.
 
 Bounds (fixed before the first run).  The loss: (T + E + 40) 2^-24 of itself, as for batches without such tokens.
 Gradients: dlogit is off by 100 2^-24 of the magnitudes that make it up, and by half a step of what it is stored as: one
@@ -132,3 +133,44 @@ def test_the_experts_gradients_of_an_empty_batch(S, saved):
         g = host(t)
         assert (g[:n] == 0).all() and np.isnan(g[n:]).all()
     assert (host(one) == 0).all()
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("T,E,G,k", [(9, 256, 8, 8), (2100, 256, 8, 8), (17000, 256, 8, 8), (9, 64, 4, 6), (5000, 16, 4, 4),
+                                     (9, 60, 5, 20), (70, 300, 3, 32)])
+def test_gates_of_a_token_without_affinities(T, E, G, k, act):
+    """Gates of 0 on every path: affinities given (a softmax's own with masked tokens among them), a sigmoid of masked
+    logits, and a softmax.  The other tokens' gates are what they are without such tokens, bit for bit."""
+    if act == "f32" and T > 3000:
+        return
+    say(f"gates without affinities T={T} E={E} {act}")
+    g = rng(203, T, E)
+    s = g.random((T, E)).astype(np.float32)
+    none = np.array([1, T - 1])
+    bias = (g.uniform(-0.1, 0.1, E)).astype(np.float32)
+    cfg = L.make_cfg(T, 64, E, G, G, k, 0, 128, 1, 2.5, act, act)
+    run = lambda flags, x, w, o, sc: _route(cfg, flags, x, w, o, bias, sc)
+    want_i, want_g = run(L.MOE_SCORES_IN, None, None, None, s)
+    masked = s.copy()
+    masked[none] = 0
+    idx, gates = run(L.MOE_SCORES_IN, None, None, None, masked)
+    rest = np.delete(np.arange(T), none)
+    ir, _ = oracle.route(masked, bias, G, G, k, 1, 2.5)
+    assert (idx == ir).all() and (gates[none] == 0).all()
+    assert (gates[rest] == want_g[rest]).all() and (idx[rest] == want_i[rest]).all()
+    up = dev_f32 if act == "f32" else (lambda a: to_device(f32_to_bf16_bits(a)))
+    x, w = up(_grid(g, T, 64, 1.0, 2.0 ** -3, 32)), up(_grid(g, E, 64, 0.2, 2.0 ** -11, 61))
+    o = dev_f32(np.full(E, -np.inf))
+    for flags in (0, L.MOE_SOFTMAX):
+        idx, gates = run(flags, x, w, o, None)
+        ir, _ = oracle.route(np.zeros((1, E), np.float32), bias, G, G, k, 1, 2.5)
+        assert (gates == 0).all() and (idx == ir).all()
+
+
+def _route(cfg, flags, x, w, o, bias, s):
+    idx = torch.full((cfg.T, cfg.k), -1, dtype=torch.int32, device="cuda")
+    gates = torch.full((cfg.T, cfg.k), float("nan"), device="cuda")
+    ws = torch.empty(L.moe_workspace_bytes(cfg, L.MOE_WS_ROUTE), dtype=torch.uint8, device="cuda")
+    L.moe_route(cfg, x, w, o, dev_f32(bias), None if s is None else dev_f32(s), flags, idx, gates, ws)
+    torch.cuda.synchronize()
+    return host(idx), host(gates)
