@@ -90,8 +90,8 @@ def route(s32: np.ndarray, bias: np.ndarray, n_groups: int, groups_per_token: in
     chosen = np.argsort(-gs, axis=1, kind="stable")[:, :groups_per_token]
     group_of = np.arange(E) // gsz
     allowed = (group_of[None, :, None] == chosen[:, None, :]).any(axis=2)
-    qm = np.where(allowed, q.astype(F64), -np.inf)
-    idx = np.argsort(-qm, axis=1, kind="stable")[:, :top_k]
+    # allowed experts first (a bias of -inf ranks them behind the others, but before those of other groups)
+    idx = np.lexsort((-q.astype(F64), ~allowed), axis=1)[:, :top_k]
     sel = np.take_along_axis(s32.astype(F64), idx, axis=1)
     if raw:
         return idx.astype(np.int32), route_scale * sel
