@@ -132,6 +132,12 @@ typedef struct {
  *               where no kernel keeps them on chip); ignored otherwise (may be NULL)
  * Groups are chosen first (the M largest group scores, ties to the lower group),
  * then the k largest s + b among the experts of the chosen groups.
+ * An expert is taken out of service by a bias of -inf: it is selected only where the
+ * chosen groups hold fewer than k others, and a group with fewer than group_topr others
+ * ranks behind all that have as many.  moe_update_bias leaves such a bias as it is.  An
+ * offset of -inf (s = 0) does not do this by itself, for the ranking is by s + b: an
+ * expert without load gains gamma a step and would come back.  It belongs beside the bias
+ * where the gates and the softmax's other affinities are not to count the expert.
  * NaN scores give unspecified indices (below E).
  * For mid-size bf16 batches (too large for the split-K router, too small for
  * router tiles of 128 tokens to fill the chip; E = 256: 2049 <= T < 16384) with
@@ -147,8 +153,7 @@ typedef struct {
  * MOE_SOFTMAX: the logits l = x w_router^T + o are fp32 numbers, the softmax over them
  * is formed in 64 bits and rounded once to fp32: equal logits rank alike wherever they
  * are computed, and affinities that differ keep their order.  An expert with l = -inf has
- * s = 0 (a mask: an offset of -inf takes it out of service, though it may be selected
- * where fewer than k others are allowed); a token whose logits are all -inf has s = 0
+ * s = 0 and no share in the sum; a token whose logits are all -inf has s = 0
  * everywhere.  A logit of +inf or NaN makes s of its token NaN.
  * MOE_SOFTMAX cannot be combined with MOE_SCORES_IN (the affinities are there;
  * MOE_ERR_UNSUPPORTED); MOE_GATES_RAW goes with all.
