@@ -12,53 +12,13 @@ import torch
 import oracle
 from biased_top_routing_amd import _lib as L
 from biased_top_routing_amd.runner import to_device
-from gpu_util import dev_f32, dev_i32, host, say
+from gpu_util import dev_f32, host, say
+from route_grad_util import EPS32, backward, bounds, grid
 from workloads.inputs import f32_to_bf16_bits, rng
 
 pytestmark = pytest.mark.gpu
 
-EPS32 = 2.0 ** -24
 FLAGS = [None, L.MOE_SOFTMAX, L.MOE_SOFTMAX | L.MOE_GATES_RAW, L.MOE_GATES_RAW]   # None: moe_route_backward
-
-
-def _grid(g, n, H, sigma, unit, most):
-    return (np.clip(np.rint(g.standard_normal((n, H)) * sigma / unit), -most, most) * unit).astype(np.float32)
-
-
-def backward(cfg, flags, x, w, s, idx, dg, alpha, seq, with_dx=True):
-    """dx, dw and the loss of either entry point, into outputs and a workspace full of NaN."""
-    kind = L.MOE_WS_ROUTE_BWD if flags is None else L.MOE_WS_ROUTE_BWD_SOFTMAX
-    ws = torch.full((L.moe_workspace_bytes(cfg, kind),), 0xFF, dtype=torch.uint8, device="cuda")
-    dx = torch.full((max(cfg.T, 1), cfg.H), float("nan"), device="cuda") if with_dx else None
-    dw, loss = (torch.full(sh, float("nan"), device="cuda") for sh in ((cfg.E, cfg.H), (1,)))
-    args = (to_device(f32_to_bf16_bits(x)), to_device(f32_to_bf16_bits(w)), dev_f32(s), dev_i32(idx), dev_f32(dg), alpha,
-            seq, dx, dw, loss, ws)
-    if flags is None:
-        L.moe_route_backward(cfg, *args)
-    else:
-        L.moe_route_backward_flags(cfg, flags, *args)
-    torch.cuda.synchronize()
-    return None if dx is None else host(dx), host(dw), float(host(loss)[0])
-
-
-def bounds(x, w, s, idx, dg, alpha, softmax, raw, terms):
-    """What dx and dw may be off by."""
-    T, E = s.shape
-    k = idx.shape[1]
-    p = s.astype(np.float64)
-    sel = np.take_along_axis(p, idx.astype(np.int64), 1)
-    S = sel.sum(axis=1, keepdims=True)
-    one = np.where(S == 0, 1.0, S)
-    a = 2.5 * np.abs(dg) if raw else 2.5 / one * (np.abs(dg) + (np.abs(dg) * sel).sum(axis=1, keepdims=True) / one)
-    A = np.zeros((T, E))
-    np.put_along_axis(A, idx.astype(np.int64), a, axis=1)
-    if alpha:
-        total = p.sum(axis=1, keepdims=True)
-        A += np.where(total == 0, 0.0, 2 * alpha * (E / k) / T / np.where(total == 0, 1.0, total))
-    mag = p * (A + (p * A).sum(axis=1, keepdims=True)) if softmax else p * A
-    dl = (100 * EPS32 + (2.0 ** -8 if terms == 1 else 2.0 ** -17)) * mag
-    aw, ax = np.abs(w).astype(np.float64), np.abs(x).astype(np.float64)
-    return (dl + (2 * E + 8) * EPS32 * mag) @ aw, (dl + (2 * T + 8) * EPS32 * mag).T @ ax
 
 
 @pytest.mark.parametrize("flags", FLAGS)
@@ -67,7 +27,7 @@ def bounds(x, w, s, idx, dg, alpha, softmax, raw, terms):
 def test_a_token_without_affinities(T, H, E, k, alpha, seq, flags):
     say(f"route backward, tokens without affinities, T={T} E={E} alpha={alpha} flags={flags}")
     g = rng(202, T, H, E)
-    x, w = _grid(g, T, H, 1.0, 2.0 ** -3, 32), _grid(g, E, H, 1.5 / np.sqrt(H), 2.0 ** -11, 61)
+    x, w = grid(g, T, H, 1.0, 2.0 ** -3, 32), grid(g, E, H, 1.5 / np.sqrt(H), 2.0 ** -11, 61)
     softmax, raw = bool((flags or 0) & L.MOE_SOFTMAX), bool((flags or 0) & L.MOE_GATES_RAW)
     s = oracle.affinity_softmax(x, w) if softmax else oracle.affinity(x, w)
     none = np.array([0, T // 2, T - 1])
@@ -159,7 +119,7 @@ def test_gates_of_a_token_without_affinities(T, E, G, k, act):
     assert (idx == ir).all() and (gates[none] == 0).all()
     assert (gates[rest] == want_g[rest]).all() and (idx[rest] == want_i[rest]).all()
     up = dev_f32 if act == "f32" else (lambda a: to_device(f32_to_bf16_bits(a)))
-    x, w = up(_grid(g, T, 64, 1.0, 2.0 ** -3, 32)), up(_grid(g, E, 64, 0.2, 2.0 ** -11, 61))
+    x, w = up(grid(g, T, 64, 1.0, 2.0 ** -3, 32)), up(grid(g, E, 64, 0.2, 2.0 ** -11, 61))
     o = dev_f32(np.full(E, -np.inf))
     for flags in (0, L.MOE_SOFTMAX):
         idx, gates = run(flags, x, w, o, None)
