@@ -444,7 +444,8 @@ struct SeqLoss {
 constexpr int kLossInline = 1024;
 
 // ... with the flags of moe_route: ds_e of the gates (MOE_GATES_RAW: scale * dw, not through their sum) and of the
-// balance loss, through the softmax (dlogit_e = s_e (ds_e - sum s ds)) or the sigmoid.  dlogit is stored as the sum of
+// balance loss, through the softmax (dlogit_e = s_e (ds_e - sum s ds)) or the sigmoid.  The products d_e = s_e ds_e are
+// formed, of the affinities' shares s / sum s: ds itself has no bound where the sum is small.  dlogit is stored as the sum of
 // two bf16 numbers, the nearest and what it leaves (17 bits and more: the products of the router's gradients then stay
 // within 2^-17 of fp32 ones), in rows of 2 * Ep, zero behind E.
 template <bool SOFTMAX, int EPL>
@@ -465,50 +466,57 @@ __global__ __launch_bounds__(256) void route_grad_flags_kernel(const float* __re
     if (lane == 0) *seq.loss = seq.n > 0 ? seq.scale * v : 0.f;
   }
   const int b = t / L;
-  float v[EPL], ds[EPL], rs = 0.f, gs = 0.f;
+  float v[EPL], d[EPL], rs = 0.f;
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
     const int e = lane + 64 * i;
     v[i] = e < E ? s[(int64_t)t * E + e] : 0.f;
-    ds[i] = coef && e < E ? coef[(int64_t)b * E + e] : 0.f;   // d L_bal / d s'_te
+    d[i] = coef && e < E ? coef[(int64_t)b * E + e] : 0.f;   // d L_bal / d s'_te
     rs += v[i];
-    gs += ds[i] * v[i];
   }
-  rs = row_sum(rs);
-  gs = row_sum(gs);
-  // (all affinities 0: neither the normalised ones nor a gradient)
+  if (coef) {
+    float n[EPL], mean = 0.f;
+    rs = row_sum(rs);
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) ds[i] = coef && rs != 0.f ? (ds[i] - gs / rs) / rs : 0.f;
+    for (int i = 0; i < EPL; ++i) {
+      n[i] = rs != 0.f ? v[i] / rs : 0.f;                     // (all affinities 0: none of the gradient either)
+      mean = fmaf(n[i], d[i], mean);
+    }
+    mean = row_sum(mean);
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) d[i] = n[i] * (d[i] - mean);
+  }
   // gates over the selected experts (an id outside [0, E) is none)
   int sel = lane < k ? idx[(int64_t)t * k + lane] : -1;
   if ((unsigned)sel >= (unsigned)E) sel = -1;
   const float ss = sel >= 0 ? s[(int64_t)t * E + sel] : 0.f;
   const float dwj = sel >= 0 ? d_w[(int64_t)t * k + lane] : 0.f;
   const float S = row_sum(ss);
-  const float B1 = row_sum(dwj * ss);
-  const float dsel = raw ? scale * dwj : S != 0.f ? scale / S * (dwj - B1 / S) : 0.f;
+  const float share = raw ? ss : S != 0.f ? ss / S : 0.f;
+  const float B = raw ? 0.f : row_sum(dwj * share);
+  const float dsel = scale * share * (dwj - B);
   for (int j = 0; j < k; ++j) {
     const int ej = __builtin_amdgcn_readlane(sel, j);
     const float dj = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(dsel), j));
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
-      if (ej == lane + 64 * i) ds[i] += dj;
+      if (ej == lane + 64 * i) d[i] += dj;
   }
-  float mean = 0.f;
+  float sum = 0.f;
   if constexpr (SOFTMAX) {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) mean = fmaf(v[i], ds[i], mean);
-    mean = row_sum(mean);
+    for (int i = 0; i < EPL; ++i) sum += d[i];
+    sum = row_sum(sum);
   }
   bf16_t* out = dlogit + (int64_t)t * 2 * Ep;
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
     const int e = lane + 64 * i;
     if (e >= Ep) continue;
-    const float d = e < E ? SOFTMAX ? v[i] * (ds[i] - mean) : ds[i] * v[i] * (1.0f - v[i]) : 0.f;
-    const bf16_t hi = f32_to_bf16(d);
+    const float dl = e < E ? SOFTMAX ? d[i] - v[i] * sum : d[i] * (1.0f - v[i]) : 0.f;
+    const bf16_t hi = f32_to_bf16(dl);
     out[e] = hi;
-    out[Ep + e] = f32_to_bf16(d - bf16_to_f32(hi));
+    out[Ep + e] = f32_to_bf16(dl - bf16_to_f32(hi));
   }
 #endif
 }

@@ -47,6 +47,8 @@ def bounds(x, w, s, idx, dg, alpha, softmax, raw, terms, rows=slice(None)):
         total = p.sum(axis=1, keepdims=True)
         A += np.where(total == 0, 0.0, 2 * alpha * (E / k) / T / np.where(total == 0, 1.0, total))
     mag = p * (A + (p * A).sum(axis=1, keepdims=True)) if softmax else p * A
-    dl = (100 * EPS32 + (2.0 ** -8 if terms == 1 else 2.0 ** -17)) * mag
+    # (below 2^-126 fp32 and bf16 have fewer bits, down to none, and a matrix product may take such a number for 0: it and
+    # its second term are off by up to themselves, 2^-126 each.  It counts where dlogit itself has vanished.)
+    dl = (100 * EPS32 + (2.0 ** -8 if terms == 1 else 2.0 ** -17)) * mag + 2 * 2.0 ** -126
     aw, ax = np.abs(w).astype(np.float64), np.abs(x).astype(np.float64)
     return (dl + (2 * E + 8) * EPS32 * mag)[rows] @ aw, (dl + (2 * T + 8) * EPS32 * mag).T @ ax

@@ -134,3 +134,30 @@ def _route(cfg, flags, x, w, o, bias, s):
     L.moe_route(cfg, x, w, o, dev_f32(bias), None if s is None else dev_f32(s), flags, idx, gates, ws)
     torch.cuda.synchronize()
     return host(idx), host(gates)
+
+
+@pytest.mark.parametrize("small", [2.0 ** -126, 1e-40, 2.0 ** -146])
+@pytest.mark.parametrize("T,E,k,alpha,flags", [(8, 16, 1, 0.0, L.MOE_SOFTMAX), (70, 64, 4, 0.0, L.MOE_SOFTMAX),
+                                               (70, 256, 8, 0.2, L.MOE_SOFTMAX), (40, 100, 3, 0.2, L.MOE_GATES_RAW)])
+def test_gradients_of_vanishing_affinities(T, E, k, alpha, flags, small):
+    """Tokens whose selected affinities (a softmax under a bias that forces them), or all of them (a sigmoid), are next to
+    nothing: gates and normalised affinities are their ratios, and the gradient has the size of those."""
+    say(f"route backward, affinities of {small}, T={T} E={E} k={k} flags={flags}")
+    g = rng(204, T, E, k)
+    softmax, raw, H = flags == L.MOE_SOFTMAX, flags == L.MOE_GATES_RAW, 64
+    x, w = grid(g, T, H, 1.0, 2.0 ** -3, 32), grid(g, E, H, 0.2, 2.0 ** -11, 61)
+    s = (small * g.integers(1, 9, (T, E))).astype(np.float32)
+    if softmax:
+        s[:, E - 1] = 1
+    idx = np.stack([g.permutation(E - 1)[:k] for _ in range(T)]).astype(np.int32)
+    dg = g.standard_normal((T, k)).astype(np.float32)
+    cfg = L.make_cfg(T, H, E, 1, 1, k, 0, 128, 1, 2.5, "bf16", "bf16")
+    dx, dw, loss = backward(cfg, flags, x, w, s, idx, dg, alpha, 0)
+    dxr, dwr, lr = oracle.route_backward(x, w, s, idx, dg, 2.5, alpha, 0, softmax, raw)
+    tx, tw = bounds(x, w, s, idx, dg, alpha, softmax, raw, 2)
+    assert (np.abs(dx - dxr) <= tx).all() and (np.abs(dw - dwr) <= tw).all()
+    # (a rounding below 2^-126 is off by half a step of 2^-149, not by 2^-24 of the number: E sums of T + 40 shares, each
+    # times f <= E / k and alpha / T.  It counts where the loss itself has vanished.)
+    under = (T + E + 40) * 2.0 ** -150 * E * (E / k)
+    assert abs(loss - lr) <= (T + E + 40) * EPS32 * abs(lr) + under
+    assert np.abs(dxr).max() > (1e-6 if k > 1 else -1)    # (no vanishing gradient; with one expert its gate is a constant)
