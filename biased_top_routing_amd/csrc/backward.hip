@@ -392,9 +392,14 @@ __global__ __launch_bounds__(256) void route_grad_kernel(const float* __restrict
     v[i] = e < E ? s[(int64_t)t * E + e] : 0.f;
     ds[i] = coef && e < E ? coef[(int64_t)b * E + e] : 0.f;   // d L_bal / d s'_te
     rs += v[i];
-    gs += ds[i] * v[i];
   }
   rs = wave_sum(rs);
+  // (ds grows as the sums shrink: where one leaves the range, the affinities are taken 2^80 times as large and ds by as much
+  // smaller; what is a number without it keeps its bits)
+  const float up_r = rs < 0x1p-60f ? 0x1p80f : 1.0f;
+  rs *= up_r;
+#pragma unroll
+  for (int i = 0; i < kMaxEPL; ++i) gs += ds[i] * (v[i] * up_r);
   gs = wave_sum(gs);
 #pragma unroll
   for (int i = 0; i < kMaxEPL; ++i) ds[i] = rs == 0.f ? 0.f : ds[i] / rs - gs / (rs * rs);
@@ -403,8 +408,12 @@ __global__ __launch_bounds__(256) void route_grad_kernel(const float* __restrict
   if ((unsigned)sel >= (unsigned)E) sel = -1;
   const float ss = sel >= 0 ? s[(int64_t)t * E + sel] : 0.f;
   const float dwj = sel >= 0 ? d_w[(int64_t)t * k + lane] : 0.f;
-  const float S = wave_sum(ss);
-  const float B1 = wave_sum(dwj * ss);
+  float S = wave_sum(ss);
+  const float up = S == 0.f ? up_r : S < 0x1p-60f ? 0x1p80f : 1.0f, to_up = up_r / up;
+  S *= up;
+  const float B1 = wave_sum(dwj * (ss * up));
+#pragma unroll
+  for (int i = 0; i < kMaxEPL; ++i) ds[i] *= to_up;
   const float dsel = S == 0.f ? 0.f : scale / S * (dwj - B1 / S);   // (no affinity at all: no gradient)
   for (int j = 0; j < k; ++j) {
     const int ej = __shfl(sel, j);
@@ -416,7 +425,7 @@ __global__ __launch_bounds__(256) void route_grad_kernel(const float* __restrict
 #pragma unroll
   for (int i = 0; i < kMaxEPL; ++i) {
     const int e = lane + 64 * i;
-    if (e < E) dlogit[(int64_t)t * E + e] = f32_to_bf16(ds[i] * v[i] * (1.0f - v[i]));
+    if (e < E) dlogit[(int64_t)t * E + e] = f32_to_bf16(ds[i] * (v[i] * up) * (1.0f - v[i]));
   }
 }
 

@@ -138,7 +138,8 @@ def _route(cfg, flags, x, w, o, bias, s):
 
 @pytest.mark.parametrize("small", [2.0 ** -126, 1e-40, 2.0 ** -146])
 @pytest.mark.parametrize("T,E,k,alpha,flags", [(8, 16, 1, 0.0, L.MOE_SOFTMAX), (70, 64, 4, 0.0, L.MOE_SOFTMAX),
-                                               (70, 256, 8, 0.2, L.MOE_SOFTMAX), (40, 100, 3, 0.2, L.MOE_GATES_RAW)])
+                                               (70, 256, 8, 0.2, L.MOE_SOFTMAX), (40, 100, 3, 0.2, L.MOE_GATES_RAW),
+                                               (8, 16, 1, 0.0, None), (70, 64, 4, 0.0, None), (70, 256, 8, 0.2, None)])
 def test_gradients_of_vanishing_affinities(T, E, k, alpha, flags, small):
     """Tokens whose selected affinities (a softmax under a bias that forces them), or all of them (a sigmoid), are next to
     nothing: gates and normalised affinities are their ratios, and the gradient has the size of those."""
@@ -154,7 +155,7 @@ def test_gradients_of_vanishing_affinities(T, E, k, alpha, flags, small):
     cfg = L.make_cfg(T, H, E, 1, 1, k, 0, 128, 1, 2.5, "bf16", "bf16")
     dx, dw, loss = backward(cfg, flags, x, w, s, idx, dg, alpha, 0)
     dxr, dwr, lr = oracle.route_backward(x, w, s, idx, dg, 2.5, alpha, 0, softmax, raw)
-    tx, tw = bounds(x, w, s, idx, dg, alpha, softmax, raw, 2)
+    tx, tw = bounds(x, w, s, idx, dg, alpha, softmax, raw, 1 if flags is None else 2)
     assert (np.abs(dx - dxr) <= tx).all() and (np.abs(dw - dwr) <= tw).all()
     # (a rounding below 2^-126 is off by half a step of 2^-149, not by 2^-24 of the number: E sums of T + 40 shares, each
     # times f <= E / k and alpha / T.  It counts where the loss itself has vanished.)
