@@ -152,7 +152,8 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void norm_kernel(
         for (int j = 0; j < N; ++j) m = fmaxf(m, fabsf(p[j]));
 #pragma unroll
         for (int d = 8; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
-        const float sc = m == 0.f ? 1.0f : __fdiv_rn(m, 448.0f), inv = __fdiv_rn(1.0f, sc);
+        // (a tile below the smallest bf16 number counts as zeros: its scale has too few bits, or none, to divide by)
+        const float sc = m < 0x1p-133f ? 1.0f : __fdiv_rn(m, 448.0f), inv = __fdiv_rn(1.0f, sc);
         float q[N];
 #pragma unroll
         for (int j = 0; j < N; ++j) q[j] = div_by_scale(p[j], sc, inv);

@@ -448,6 +448,7 @@ moe_status moe_quantize_int8(const void* src_bf16, int32_t n_mat, int32_t rows, 
  * Sums are held in fp32.  The codes are those of h * weight before r and before any
  * rounding (both formats are free of a row's factor), by the rules of
  * moe_quantize_int8, or of moe_quantize_fp8 with 1 x 128 tiles, and r is in the scales.
+ * (A tile of products below 2^-133, the smallest bf16 number, counts as one of zeros.)
  * Rows of all outputs behind the live tokens stay as they were.
  */
 moe_status moe_norm(const moe_cfg* cfg, const int32_t* n_tokens, const void* x, const void* residual,
