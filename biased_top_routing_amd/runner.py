@@ -269,6 +269,8 @@ class MoeLayerGPU:
             raise ValueError("dh is the gradient of the norm's input sum: the layer has no norm")
         if dh is not None:
             self._check_rows("dh", dh)
+        if self.norm is not None and self.residual is None:
+            self._check_rows("x", x)                      # (the norm's input; with a residual that is self.h)
         if self.gather:
             raise ValueError("backward reads the permuted rows x_perm: build the layer with gather=False")
         if self.n_tokens is not None and alpha:
