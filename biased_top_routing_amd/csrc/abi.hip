@@ -53,7 +53,8 @@ moe_status validate_cfg(const moe_cfg* c) {
   } else if (c->wgt == MOE_INT8) {  // whole 128-wide K slices; 32-bit sums; a wavefront a row to quantise
     if (c->H % 128 || c->I % 128) return MOE_ERR_SHAPE;
     if (c->H >= kInt8MaxK || (int64_t)(c->S > 1 ? c->S : 1) * c->I >= kInt8MaxK) return MOE_ERR_SHAPE;
-    if ((int64_t)c->T * (c->k + 1) >= (int64_t)1 << 26) return MOE_ERR_SHAPE;
+    // (launch_quantize_int8_pair: four rows a workgroup of 256, fewer than 2^32 lanes)
+    if (((int64_t)c->T * c->k + 3) / 4 + ((int64_t)c->T + 3) / 4 >= (int64_t)1 << 24) return MOE_ERR_SHAPE;
   } else {  // fp8 experts: K of every GEMM at most kFp8MaxKC chunks of 128
     if (c->H % 128 || c->I % 128) return MOE_ERR_SHAPE;
     if (c->H > 128 * kFp8MaxKC || (int64_t)(c->S > 1 ? c->S : 1) * c->I > 128 * kFp8MaxKC)

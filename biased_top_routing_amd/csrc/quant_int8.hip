@@ -62,7 +62,7 @@ extern "C" moe_status moe_quantize_int8(const void* src_bf16, int32_t n_mat, int
                                         int8_t* dst, float* scales, void* stream) {
   if (n_mat < 0 || rows < 0 || cols <= 0 || cols % 8 || group < 1 || n_mat % group) return MOE_ERR_SHAPE;
   const int64_t n = (int64_t)(n_mat / group) * rows;
-  if (n >= (int64_t)1 << 26) return MOE_ERR_SHAPE;   // (a wavefront a row, in a grid of fewer than 2^32 lanes)
+  if ((n + 3) / 4 >= (int64_t)1 << 24) return MOE_ERR_SHAPE;   // (four rows a workgroup of 256, fewer than 2^32 lanes)
   if (n == 0) return MOE_OK;
   if (!src_bf16 || !dst || !scales) return MOE_ERR_NULL;
   if (misaligned(src_bf16, 16) || misaligned(dst, 8) || misaligned(scales, 4)) return MOE_ERR_UNSUPPORTED;

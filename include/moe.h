@@ -89,7 +89,7 @@ typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_FP8_E4M3 = 2, MOE_MXFP4 = 3, MOE_I
  *  I % 128 == 0, H <= 8192 and max(S, 1)*I <= 8192 (64 scale blocks of K); MXFP4
  *  experts: H % 128 == 0, I % 128 == 0, T*k*max(H, I) and T*max(H, S*I) under 2^36;
  *  INT8 experts: H % 128 == 0, I % 128 == 0, H and max(S, 1)*I under 2^17 (sums in
- *  32 bits), T*(k+1) under 2^26.
+ *  32 bits), ceil(T*k/4) + ceil(T/4) under 2^24.
  */
 typedef struct {
   int32_t T, H, E, G, M, k, S, I;
@@ -412,7 +412,7 @@ moe_status moe_dequantize_fp4(const uint8_t* codes, const uint8_t* scales, int32
  * and ws_gate_up, and S for ws_down.  scale = max|v| / 127, code = the whole number
  * nearest 127 v / max|v| (ties to even): -127 to 127.  A row of zeros has scale 0 and
  * codes 0; one that holds an infinity or a NaN has scale NaN and codes 0.
- * cols must be a multiple of 8, n_mat of group, and n_mat / group * rows below 2^26
+ * cols must be a multiple of 8, n_mat of group, and n_mat / group * rows at most 2^26 - 4
  * (MOE_ERR_SHAPE).  src must be 16-byte aligned, dst 8-byte, scales 4-byte
  * (MOE_ERR_UNSUPPORTED).
  */
