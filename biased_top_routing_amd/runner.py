@@ -49,6 +49,7 @@ def to_device(arr, device="cuda"):
 class MoeLayerGPU:
     norm = residual = graph_residual = codes = code_scale = None
     route_flags = 0
+    scores_there = True      # the affinities of the last batch are in .scores
 
     def __init__(self, cfg, weights, T=None, device="cuda", gather=False, save_gu=False, keep_scores=True, share=None,
                  adds_balance=False, norm=None, eps=1e-6, softmax=False, raw_gates=False):
@@ -187,7 +188,7 @@ class MoeLayerGPU:
         return self.xn
 
     def route(self, x, bias, scores_in=False):
-        keep = self.keep_scores or scores_in
+        keep = self.scores_there = self.keep_scores or scores_in
         flags = self.route_flags & ~L.MOE_SOFTMAX | L.MOE_SCORES_IN if scores_in else self.route_flags
         L.moe_route(self.cfg, x, self.w_router, self.logit_offset, bias, self.scores if keep else None,
                     flags, self.topk_idx, self.topk_w, None if keep else self.ws_route)
@@ -273,6 +274,8 @@ class MoeLayerGPU:
             self._check_rows("x", x)                      # (the norm's input; with a residual that is self.h)
         if self.gather:
             raise ValueError("backward reads the permuted rows x_perm: build the layer with gather=False")
+        if not self.scores_there:
+            raise ValueError("backward reads the affinities: build the layer with keep_scores=True")
         if self.n_tokens is not None and alpha:
             raise ValueError("the balance loss counts every token of the batch: alpha has to be 0 for a padded one")
         if alpha and not self.adds_balance:
@@ -383,5 +386,6 @@ class MoeLayerGPU:
         """One replay of the captured step on the current stream; returns y."""
         self.n_tokens = self.graph_inputs[2]     # backward() then takes the pairs that the graph's batch has
         self.residual = self.graph_residual
+        self.scores_there = self.keep_scores
         self.graph.replay()
         return self.y
