@@ -35,7 +35,7 @@
 //         bits and more, where one bf16 of 8 would put 2^-9 into every gradient):
 //         a slice holds both terms of half its depth of K and W_r's rows, or the
 //         tokens', of that once, so that both meet the same operand registers in
-//         the same accumulators.  T = 16384, E = 256, H = 7168: dW_r 109 us, dx
+//         the same accumulators.  T = 16384, E = 256, H = 7168: dW_r 110 us, dx
 //         121, 1.1 and 1.0 PFLOP/s, where dx stores 470 MB besides; the MFMAs are
 //         busy half the time.  (As products of twice the size, with two sets of
 //         partial sums: dW_r 256 us; a walk over K that passes over the second

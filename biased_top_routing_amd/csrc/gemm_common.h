@@ -29,7 +29,10 @@ constexpr int kNonTemporal = 2;
 constexpr int kBufferWord3 = 0x00020000;
 
 // Raw buffer descriptor over [base, base + bytes), built from wave-uniform
-// values so that it lives in SGPRs.
+// values so that it lives in SGPRs.  The range check compares the lane's offset
+// with what the scalar offset leaves of `bytes` (nothing, where it is larger):
+// no load or store goes past the descriptor, whichever offset would lead there
+// (measured, in registers and to LDS).
 #if defined(__HIP_DEVICE_COMPILE__)   // the descriptor type exists only for the GPU target
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, int bytes) {
   const uint64_t b = reinterpret_cast<uint64_t>(base);

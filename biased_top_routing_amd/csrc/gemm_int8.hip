@@ -238,8 +238,8 @@ __device__ __forceinline__ void gemm_int8_tiles(const Int8Params& p, uint8_t* ld
     left = o.nk1 * o.nexp;
     load_perm(place(++nq));
   };
-  // Load i of PER of the stream's next slice.  (Only offsets that lie inside the descriptor whatever the lane go
-  // through the scalar offset.)
+  // Load i of PER of the stream's next slice.  (Down: rows past the columns' end lie past the descriptor with the last
+  // expert's scalar offset, and inside it, in the next expert's rows, with the others': read, but never stored.)
   struct Stream {                                      // (in scalar registers)
     __amdgpu_buffer_rsrc_t a, w;
     int ak, wk;

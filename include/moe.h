@@ -117,7 +117,7 @@ typedef struct {
  *
  *  x            [T, H] act dtype                 (unused with MOE_SCORES_IN)
  *  w_router     [E, H] act dtype                 (unused with MOE_SCORES_IN)
- *  logit_offset [E] fp32 added to the logits before the sigmoid, or NULL
+ *  logit_offset [E] fp32 added to the logits before the sigmoid or the softmax, or NULL
  *  bias         [E] fp32 routing bias b
  *  scores       [T, E] fp32: output s = sigmoid(x w_router^T + o), or the input
  *               affinities with MOE_SCORES_IN; may be NULL without MOE_SCORES_IN
@@ -445,7 +445,8 @@ moe_status moe_quantize_int8(const void* src_bf16, int32_t n_mat, int32_t rows, 
  *  codes     [T, H] int8 or E4M3 codes out (wgt INT8 or FP8_E4M3, else
  *            MOE_ERR_UNSUPPORTED), or NULL
  *  code_scale [T] (INT8) or [T, H/128] (FP8) fp32 out, with codes
- * Sums are held in fp32.  The codes are those of h * weight before r and before any
+ * Sums are held in fp32: a row whose squares add up to 2^128 and more (magnitudes of
+ * 2^64 / sqrt(H)) has r = 0.  The codes are those of h * weight before r and before any
  * rounding (both formats are free of a row's factor), by the rules of
  * moe_quantize_int8, or of moe_quantize_fp8 with 1 x 128 tiles, and r is in the scales.
  * (A tile of products below 2^-133, the smallest bf16 number, counts as one of zeros.)
@@ -463,6 +464,8 @@ moe_status moe_norm(const moe_cfg* cfg, const int32_t* n_tokens, const void* x, 
  *  dh        [T, H] act dtype: the gradient that reaches h itself, or NULL
  *  dx        [T, H] act dtype out; rows behind the live tokens are zero; may be dy or dh
  *  dweight   [H] fp32 out (summed in a fixed order)
+ * The layer's own backward calls are bf16; with F32 this one serves a caller that has the
+ * rest of an fp32 layer's gradients from elsewhere.
  *  ws, ws_bytes  at least moe_workspace_bytes(cfg, MOE_WS_NORM_BWD)
  */
 moe_status moe_norm_backward(const moe_cfg* cfg, const int32_t* n_tokens, const void* h, const void* weight,
@@ -645,7 +648,10 @@ moe_status moe_route_backward(const moe_cfg* cfg, const void* x, const void* w_r
  *   MOE_GATES_RAW   w_j = scale * s_j:  ds_j = scale * dw_j
  *   MOE_SOFTMAX     dlogit_e = s_e (ds_e - sum_e' s_e' ds_e')
  * Other than moe_route_backward, which rounds dlogit to bf16 for its products, this call
- * carries it as the sum of two bf16 numbers (16 bits and more).
+ * carries it as the sum of two bf16 numbers, off by at most 2^-17 of itself: dx_router and
+ * dw_router are off by some 2.5e-6 of their size, where an fp32 dlogit would leave 4e-7
+ * (dw_router of 16384 tokens: 2e-6), and where its own inputs, gates' gradients of bf16
+ * products, are off by 2^-9 and more.
  *  ws of at least moe_workspace_bytes(cfg, MOE_WS_ROUTE_BWD_SOFTMAX).  x, w_router,
  *  dw_router and ws must be 16-byte aligned, the rest 4-byte (MOE_ERR_UNSUPPORTED); T below
  *  2^23, and T / seq_len * ceil(E / 64) below 2^24 (MOE_ERR_SHAPE).
